@@ -373,6 +373,45 @@ sra_status sra_nm_axpby(const void* a_values, float beta, const void* b_values, 
                         void* out_values, int64_t n_values, int32_t dtype, void* stream);
 
 /*
+ * ckpt_encode / ckpt_decode -- 8-bit activation checkpoints: a layer's input kept for its backward
+ * at 33/32 of a byte per element (SLoPe paperlayer summary, results: the memory of training is
+ * what limits the model).  X [T,K] (bf16 or fp32) is cut along each row into blocks of 32
+ * consecutive columns (the last may be shorter).  A block with largest magnitude a stores the
+ * biased exponent e + 127 of its scale 2^e, with e the smallest integer for which a <= 127 * 2^e,
+ * clamped to [-126, 121] (an all-zero block: -126), and per element the code
+ * q = clamp(round_half_even(x / 2^e), -127, 127).  The decoded value q * 2^e is exact in bf16 and
+ * fp32, so it differs from x by at most 2^(e-1) (2^e at most where the clamp at 127 acts).
+ *   codes: int8 [T,K];  exps: uint8 [T, ceil(K/32)].
+ * The backward calls that take a checkpoint compute exactly what they would compute from the
+ * decoded bf16 activations.
+ */
+sra_status sra_ckpt_encode(const void* X, int32_t dtype, int64_t T, int64_t K, int8_t* codes,
+                           uint8_t* exps, void* stream);
+sra_status sra_ckpt_decode(const int8_t* codes, const uint8_t* exps, int64_t T, int64_t K,
+                           int32_t dtype, void* X, void* stream);
+
+/*
+ * layer_norm -- Y = (X - mean) * rstd * gamma + beta over the rows of X [T,H], the norm ahead of a
+ * projection, and its gradients.  X, gamma, beta, Y, dY, dX have one dtype (bf16 or fp32); mean,
+ * rstd [T], dgamma and dbeta [H] are fp32, as is all arithmetic; every output is rounded once.
+ *   mean = sum(x) / H;  rstd = 1 / sqrt(sum((x - mean)^2) / H + eps)
+ *   dX = rstd * (g - mean(g) - xh * mean(g * xh)) with g = dY * gamma, xh = (X - mean) * rstd;
+ *   dgamma = sum_t dY * xh;  dbeta = sum_t dY
+ * codes / exps: both NULL, or the buffers of a checkpoint (sra_ckpt_encode) of the rounded Y,
+ * written in the same pass (what sra_ckpt_encode(Y) gives, bit for bit).
+ * The backward takes the forward's mean and rstd, and a workspace of sra_layer_norm_bwd_workspace
+ * bytes; its sums over tokens run in a fixed order.  T = 0: the forward is a no-op, the backward
+ * writes zeros to dgamma and dbeta.  eps must be finite and >= 0.  Supported: H <= 16384.
+ */
+sra_status sra_layer_norm_fwd(const void* X, const void* gamma, const void* beta, float eps,
+                              int32_t dtype, int64_t T, int64_t H, void* Y, float* mean,
+                              float* rstd, int8_t* codes, uint8_t* exps, void* stream);
+sra_status sra_layer_norm_bwd_workspace(int64_t T, int64_t H, size_t* bytes /* host */);
+sra_status sra_layer_norm_bwd(const void* dY, const void* X, const void* gamma, const float* mean,
+                              const float* rstd, int32_t dtype, int64_t T, int64_t H, void* dX,
+                              float* dgamma, float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Tuning knobs of the calling thread, for benchmarks and tests (not needed for computing anything;
  * every knob's default is the library's own choice, and results stay within the stated tolerance
  * under any setting).  Returns SRA_ERR_INVALID_ARG for an unknown key or a value out of range.
@@ -424,7 +463,9 @@ enum {
   SRA_KERNEL_SPMM_FFI = 6,     /* bf16 fixed fan-in SpMM (forward Y, backward dX) */
   SRA_KERNEL_FFI_DENSIFY = 7,  /* bf16 fixed fan-in adapter factor expanded to dense rows */
   SRA_KERNEL_WEIGHT_GRAD = 8,  /* bf16 masked weight gradient (sra_masked_weight_grad) */
-  SRA_KERNEL_NM_UPDATE = 9     /* beta A + gamma B on shared-pattern values (sra_nm_axpby) */
+  SRA_KERNEL_NM_UPDATE = 9,    /* beta A + gamma B on shared-pattern values (sra_nm_axpby) */
+  SRA_KERNEL_LAYER_NORM = 10,  /* layer norm forward or backward (not the backward's final sum) */
+  SRA_KERNEL_CKPT = 11         /* 8-bit checkpoint encode or decode */
 };
 
 /*

@@ -27,11 +27,14 @@ EXPORTS = (
     "sra_ffi_tile", "sra_fwd_workspace",
     "sra_sparse_lora_fwd", "sra_bwd_workspace", "sra_sparse_lora_bwd", "sra_sparse_lora_bwd_noalloc",
     "sra_ffa_fwd_workspace", "sra_sparse_lora_fwd_ffa", "sra_ffa_bwd_workspace", "sra_sparse_lora_bwd_ffa",
+    "sra_ckpt_encode", "sra_ckpt_decode",
+    "sra_layer_norm_fwd", "sra_layer_norm_bwd_workspace", "sra_layer_norm_bwd",
     "sra_time_next_kernel", "sra_set_tuning",
 )
 SRA_KERNEL_COMPRESS, SRA_KERNEL_DOUBLE_PRUNE, SRA_KERNEL_SPMM24 = 1, 2, 3
 SRA_KERNEL_ADAPTER, SRA_KERNEL_DECODE24, SRA_KERNEL_SPMM_FFI = 4, 5, 6
 SRA_KERNEL_FFI_DENSIFY, SRA_KERNEL_WEIGHT_GRAD, SRA_KERNEL_NM_UPDATE = 7, 8, 9
+SRA_KERNEL_LAYER_NORM, SRA_KERNEL_CKPT = 10, 11
 
 
 class SraSparse(ctypes.Structure):
@@ -90,6 +93,14 @@ def load(path: str = LIB_PATH):
         "sra_sparse_lora_bwd_ffa": (c_int32, [P, c_void_p, c_void_p, c_int64, c_void_p, P, c_void_p,
                                               c_uint32, c_void_p, c_void_p, c_void_p, c_void_p,
                                               c_void_p, c_size_t, c_void_p]),
+        "sra_ckpt_encode": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
+        "sra_ckpt_decode": (c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_void_p]),
+        "sra_layer_norm_fwd": (c_int32, [c_void_p, c_void_p, c_void_p, c_float, c_int32, c_int64, c_int64,
+                                         c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "sra_layer_norm_bwd_workspace": (c_int32, [c_int64, c_int64, POINTER(c_size_t)]),
+        "sra_layer_norm_bwd": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int64,
+                                         c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                         c_void_p]),
         "sra_time_next_kernel": (c_int32, [c_int32, c_void_p, c_void_p]),
         "sra_set_tuning": (c_int32, [c_int32, c_int32]),
     }

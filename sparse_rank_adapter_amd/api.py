@@ -591,6 +591,127 @@ def ffa_bwd_workspace(P: SparseMatrix, T: int, A: SparseMatrix,
     return n.value
 
 
+CKPT_BLOCK = 32  # columns of a checkpoint that share one scale
+
+
+@dataclass
+class Ckpt8:
+    """8-bit checkpoint of a [T, K] activation: int8 codes [T, K] and uint8 scale exponents
+    [T, ceil(K / 32)]; value = code * 2^(exponent - 127).  `dtype` is that of the activation."""
+    codes: torch.Tensor
+    exps: torch.Tensor
+    dtype: torch.dtype = torch.bfloat16
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _check_ckpt(c: Ckpt8, name: str, shape: tuple | None = None, device=None):
+    if not isinstance(c, Ckpt8):
+        raise TypeError(f"{name} must be a Ckpt8")
+    if c.dtype not in _DT:
+        raise ValueError(f"{name}: dtype {c.dtype} is not bfloat16 or float32")
+    if not isinstance(c.codes, torch.Tensor) or c.codes.dim() != 2:
+        raise ValueError(f"{name}.codes must be a 2-D tensor [T, K]")
+    T, K = shape if shape is not None else tuple(c.codes.shape)
+    _arg(c.codes, f"{name}.codes", (T, K), torch.int8, device)
+    _arg(c.exps, f"{name}.exps", (T, -(-K // CKPT_BLOCK)), torch.uint8, c.codes.device)
+    return T, K
+
+
+def _new_ckpt(T: int, K: int, dtype, device) -> Ckpt8:
+    return Ckpt8(torch.empty((T, K), dtype=torch.int8, device=device),
+                 torch.empty((T, -(-K // CKPT_BLOCK)), dtype=torch.uint8, device=device), dtype)
+
+
+def ckpt8_encode(X: torch.Tensor, out: Ckpt8 | None = None) -> Ckpt8:
+    """The 8-bit checkpoint of X [T, K] (bf16 or fp32), into `out`'s buffers if given."""
+    lib = load()
+    T, K = _mat(X, "X")
+    if out is None:
+        out = _new_ckpt(T, K, X.dtype, X.device)
+    _check_ckpt(out, "out", (T, K), X.device)
+    if out.dtype != X.dtype:
+        raise ValueError(f"out has dtype {out.dtype}, expected {X.dtype}")
+    check("sra_ckpt_encode", lib.sra_ckpt_encode(_p(X), _dt(X), T, K, _p(out.codes), _p(out.exps),
+                                                 _stream(X.device)))
+    return out
+
+
+def ckpt8_decode(c: Ckpt8, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values a checkpoint stands for, in its activation's dtype (exact)."""
+    lib = load()
+    T, K = _check_ckpt(c, "c")
+    if out is None:
+        out = torch.empty((T, K), dtype=c.dtype, device=c.device)
+    _arg(out, "out", (T, K), c.dtype, c.device)
+    check("sra_ckpt_decode", lib.sra_ckpt_decode(_p(c.codes), _p(c.exps), T, K, _dt(out), _p(out),
+                                                 _stream(c.device)))
+    return out
+
+
+def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, eps: float = 1e-5,
+                   ckpt: bool | Ckpt8 = False, Y: torch.Tensor | None = None):
+    """Y = (X - mean) rstd gamma + beta over X's rows.  Returns (Y, mean, rstd, checkpoint): mean and
+    rstd fp32 [T]; the checkpoint of Y, written in the same pass, is None unless ``ckpt`` is true
+    (or a Ckpt8 whose buffers it goes into)."""
+    lib = load()
+    T, H = _mat(X, "X")
+    dev = X.device
+    _arg(gamma, "gamma", (H,), X.dtype, dev)
+    _arg(beta, "beta", (H,), X.dtype, dev)
+    if Y is None:
+        Y = torch.empty_like(X)
+    _arg(Y, "Y", (T, H), X.dtype, dev)
+    c = None
+    if isinstance(ckpt, Ckpt8):
+        c = ckpt
+        if c.dtype != X.dtype:
+            raise ValueError(f"ckpt has dtype {c.dtype}, expected {X.dtype}")
+    elif ckpt:
+        c = _new_ckpt(T, H, X.dtype, dev)
+    if c is not None:
+        _check_ckpt(c, "ckpt", (T, H), dev)
+    mean = torch.empty(T, dtype=torch.float32, device=dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    check("sra_layer_norm_fwd", lib.sra_layer_norm_fwd(
+        _p(X), _p(gamma), _p(beta), float(eps), _dt(X), T, H, _p(Y), _p(mean), _p(rstd),
+        _p(c.codes) if c is not None else None, _p(c.exps) if c is not None else None, _stream(dev)))
+    return Y, mean, rstd, c
+
+
+def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor,
+                   rstd: torch.Tensor, dX: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """Gradients of layer_norm_fwd from its input, mean and rstd.  Returns (dX, dgamma, dbeta), the
+    last two fp32 [H]."""
+    lib = load()
+    T, H = _mat(X, "X")
+    dev = X.device
+    _arg(dY, "dY", (T, H), X.dtype, dev)
+    _arg(gamma, "gamma", (H,), X.dtype, dev)
+    _arg(mean, "mean", (T,), torch.float32, dev)
+    _arg(rstd, "rstd", (T,), torch.float32, dev)
+    if dX is None:
+        dX = torch.empty_like(X)
+    _arg(dX, "dX", (T, H), X.dtype, dev)
+    dgamma = torch.empty(H, dtype=torch.float32, device=dev)
+    dbeta = torch.empty(H, dtype=torch.float32, device=dev)
+    nbytes = ctypes.c_size_t()
+    check("sra_layer_norm_bwd_workspace", lib.sra_layer_norm_bwd_workspace(T, H, ctypes.byref(nbytes)))
+    if ws is None or ws.numel() < nbytes.value:
+        ws = torch.empty(max(1, nbytes.value), dtype=torch.uint8, device=dev)
+    _arg(ws, "ws", (ws.numel(),), torch.uint8, dev)
+    check("sra_layer_norm_bwd", lib.sra_layer_norm_bwd(
+        _p(dY), _p(X), _p(gamma), _p(mean), _p(rstd), _dt(X), T, H, _p(dX), _p(dgamma), _p(dbeta),
+        _p(ws), ws.numel(), _stream(dev)))
+    return dX, dgamma, dbeta
+
+
 _ENGINES = {"smfmac": 0, "dense_mfma": 1}
 
 

@@ -28,6 +28,8 @@ SOURCES = [
     "adapter.hip",
     "spmm_ffi.hip",
     "weight_grad.hip",
+    "ckpt.hip",
+    "layer_norm.hip",
 ]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -369,7 +369,7 @@ sra_status sra_time_next_kernel(int32_t which, void* start, void* stop) {
     g_time_which = 0;
     return SRA_OK;
   }
-  if (which < SRA_KERNEL_COMPRESS || which > SRA_KERNEL_NM_UPDATE)
+  if (which < SRA_KERNEL_COMPRESS || which > SRA_KERNEL_CKPT)
     return fail(SRA_ERR_INVALID_ARG, "unknown kernel class %d", which);
   if (!start || !stop) return fail(SRA_ERR_INVALID_ARG, "start and stop events are required");
   g_time_which = which;
@@ -574,6 +574,88 @@ sra_status sra_nm_axpby(const void* a_values, float beta, const void* b_values, 
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_nm_axpby(dtype, a_values, beta, b_values, gamma, out_values, n_values, s),
                   s, "nm_axpby");
+}
+
+// Shapes and pointers of an 8-bit checkpoint of a T x K matrix.
+static sra_status check_ckpt(const int8_t* codes, const uint8_t* exps, int64_t T, int64_t K) {
+  if (T < 0 || K < 0) return fail(SRA_ERR_INVALID_ARG, "negative shape");
+  SRA_TRY(check_ptr(codes, T > 0 && K > 0, "codes"));
+  return check_ptr(exps, T > 0 && K > 0, "exps");
+}
+
+sra_status sra_ckpt_encode(const void* X, int32_t dtype, int64_t T, int64_t K, int8_t* codes,
+                           uint8_t* exps, void* stream) {
+  SRA_TRY(check_dtype(dtype));
+  SRA_TRY(check_ckpt(codes, exps, T, K));
+  SRA_TRY(check_ptr(X, T > 0 && K > 0, "X"));
+  const hipStream_t s = (hipStream_t)stream;
+  return hip_done(sra::launch_ckpt_encode(dtype, X, T, K, codes, exps, s), s, "ckpt_encode");
+}
+
+sra_status sra_ckpt_decode(const int8_t* codes, const uint8_t* exps, int64_t T, int64_t K,
+                           int32_t dtype, void* X, void* stream) {
+  SRA_TRY(check_dtype(dtype));
+  SRA_TRY(check_ckpt(codes, exps, T, K));
+  SRA_TRY(check_ptr(X, T > 0 && K > 0, "X"));
+  const hipStream_t s = (hipStream_t)stream;
+  return hip_done(sra::launch_ckpt_decode(dtype, codes, exps, T, K, X, s), s, "ckpt_decode");
+}
+
+static sra_status check_ln(int32_t dtype, int64_t T, int64_t H) {
+  SRA_TRY(check_dtype(dtype));
+  if (T < 0 || H < 0) return fail(SRA_ERR_INVALID_ARG, "negative shape");
+  if (!sra::layer_norm_ok(H)) return fail(SRA_ERR_UNSUPPORTED, "layer norm needs H <= 16384 (H = %lld)", (long long)H);
+  if (T > INT32_MAX) return fail(SRA_ERR_UNSUPPORTED, "layer norm needs T < 2^31");
+  return SRA_OK;
+}
+
+sra_status sra_layer_norm_fwd(const void* X, const void* gamma, const void* beta, float eps,
+                              int32_t dtype, int64_t T, int64_t H, void* Y, float* mean,
+                              float* rstd, int8_t* codes, uint8_t* exps, void* stream) {
+  SRA_TRY(check_ln(dtype, T, H));
+  if (!(eps >= 0.f) || eps > 3.0e38f) return fail(SRA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if ((codes == nullptr) != (exps == nullptr))
+    return fail(SRA_ERR_INVALID_ARG, "codes and exps must both be given or both be NULL");
+  const bool any = T > 0 && H > 0;
+  SRA_TRY(check_ptr(X, any, "X"));
+  SRA_TRY(check_ptr(gamma, any, "gamma"));
+  SRA_TRY(check_ptr(beta, any, "beta"));
+  SRA_TRY(check_ptr(Y, any, "Y"));
+  SRA_TRY(check_ptr(mean, any, "mean"));
+  SRA_TRY(check_ptr(rstd, any, "rstd"));
+  if (codes) SRA_TRY(check_ckpt(codes, exps, T, H));
+  const hipStream_t s = (hipStream_t)stream;
+  return hip_done(sra::launch_layer_norm_fwd(dtype, X, gamma, beta, eps, T, H, Y, mean, rstd, codes, exps, s), s,
+                  "layer_norm_fwd");
+}
+
+sra_status sra_layer_norm_bwd_workspace(int64_t T, int64_t H, size_t* bytes) {
+  SRA_TRY(check_ln(SRA_BF16, T, H));
+  if (!bytes) return fail(SRA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = sra::layer_norm_bwd_ws(T, H);
+  return SRA_OK;
+}
+
+sra_status sra_layer_norm_bwd(const void* dY, const void* X, const void* gamma, const float* mean,
+                              const float* rstd, int32_t dtype, int64_t T, int64_t H, void* dX,
+                              float* dgamma, float* dbeta, void* ws, size_t ws_bytes, void* stream) {
+  SRA_TRY(check_ln(dtype, T, H));
+  const bool any = T > 0 && H > 0;
+  SRA_TRY(check_ptr(dY, any, "dY"));
+  SRA_TRY(check_ptr(X, any, "X"));
+  SRA_TRY(check_ptr(gamma, any, "gamma"));
+  SRA_TRY(check_ptr(mean, any, "mean"));
+  SRA_TRY(check_ptr(rstd, any, "rstd"));
+  SRA_TRY(check_ptr(dX, any, "dX"));
+  SRA_TRY(check_ptr(dgamma, H > 0, "dgamma"));
+  SRA_TRY(check_ptr(dbeta, H > 0, "dbeta"));
+  const size_t need = sra::layer_norm_bwd_ws(T, H);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(SRA_ERR_WORKSPACE, "workspace too small: %zu < %zu", ws ? ws_bytes : (size_t)0, need);
+  SRA_TRY(check_ptr(ws, need > 0, "workspace"));
+  const hipStream_t s = (hipStream_t)stream;
+  return hip_done(sra::launch_layer_norm_bwd(dtype, dY, X, gamma, mean, rstd, T, H, dX, dgamma, dbeta, ws, s), s,
+                  "layer_norm_bwd");
 }
 
 sra_status sra_nm_tile_bytes(int64_t rows, int64_t cols, int32_t n, int32_t m, size_t* value_bytes,

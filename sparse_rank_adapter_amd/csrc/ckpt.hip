@@ -1,0 +1,129 @@
+// 8-bit activation checkpoints: X [T][K] kept for the backward as int8 codes [T][K] and one scale
+// exponent per 32 columns [T][ceil(K/32)] (rowvec.h has the code).  Encoding reads X once and
+// writes 33/32 of a byte per element; decoding is the reverse.  Both are bound by HBM.
+//
+// A lane owns VEC consecutive columns, so 32 / VEC neighbouring lanes own a block and find its
+// maximum with lane exchanges, with no LDS.  Rows whose length is a multiple of 32 need no row
+// structure: the call passes them as one long row.  Each thread issues the loads of U vectors
+// before it uses the first.
+#include <algorithm>
+
+#include "rowvec.h"
+
+namespace {
+using namespace sra_row;
+
+constexpr int kThreads = 256, kU = 4;
+
+// grid: (vector tiles of a row, rows in steps of gridDim.y); tile = kThreads * kU vectors
+template <typename E, int VEC>
+__global__ __launch_bounds__(kThreads) void k_ckpt_encode(const E* __restrict__ x, int64_t T, int64_t K,
+                                                          int8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
+  const int64_t nvec = K / VEC, nblk = (K + kCkBlock - 1) / kCkBlock;
+  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kU) + threadIdx.x;
+  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
+    float f[kU][VEC];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int64_t i = i0 + u * kThreads;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) f[u][k] = 0.f;
+      if (i < nvec) RowVec<E, VEC>::load(x + t * K + i * VEC, f[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int64_t i = i0 + u * kThreads;
+      const Coded<VEC> c = ck_encode<VEC>(f[u]);  // lane exchanges: every lane takes part
+      if (i < nvec) {
+        ck_store_codes<VEC>(codes + t * K + i * VEC, c.codes);
+        if ((threadIdx.x & (kCkBlock / VEC - 1)) == 0) exps[t * nblk + i * VEC / kCkBlock] = (uint8_t)c.exp;
+      }
+    }
+  }
+}
+
+template <typename E, int VEC>
+__global__ __launch_bounds__(kThreads) void k_ckpt_decode(const int8_t* __restrict__ codes,
+                                                          const uint8_t* __restrict__ exps, int64_t T, int64_t K,
+                                                          E* __restrict__ x) {
+  const int64_t nvec = K / VEC, nblk = (K + kCkBlock - 1) / kCkBlock;
+  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kU) + threadIdx.x;
+  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
+    uint64_t c[kU];
+    uint32_t e[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int64_t i = i0 + u * kThreads;
+      c[u] = 0;
+      e[u] = 0;
+      if (i < nvec) {
+        c[u] = ck_load_codes<VEC>(codes + t * K + i * VEC);
+        e[u] = exps[t * nblk + i * VEC / kCkBlock];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int64_t i = i0 + u * kThreads;
+      float f[VEC];
+      ck_decode<VEC>(c[u], e[u], f);
+      if (i < nvec) RowVec<E, VEC>::store(x + t * K + i * VEC, f);
+    }
+  }
+}
+
+// rows that are whole blocks follow each other without a gap: one long row
+void flatten(int64_t& T, int64_t& K) {
+  if (K % kCkBlock == 0) {
+    K *= T;
+    T = 1;
+  }
+}
+dim3 grid_of(int64_t T, int64_t nvec) {
+  return dim3((unsigned)((nvec + kThreads * kU - 1) / (kThreads * kU)), (unsigned)std::min<int64_t>(T, 32768));
+}
+
+}  // namespace
+
+namespace sra {
+
+hipError_t launch_ckpt_encode(int dtype, const void* x, int64_t T, int64_t K, int8_t* codes, uint8_t* exps,
+                              hipStream_t s) {
+  if (T <= 0 || K <= 0) return hipSuccess;
+  flatten(T, K);
+  const int vec = row_vec(K);
+  const dim3 grid = grid_of(T, K / vec);
+#define SRA_ENC(E, V) launch(SRA_KERNEL_CKPT, k_ckpt_encode<E, V>, grid, dim3(kThreads), 0, s, (const E*)x, T, K, codes, exps)
+  if (dtype == SRA_BF16) {
+    if (vec == 8) SRA_ENC(uint16_t, 8);
+    else if (vec == 2) SRA_ENC(uint16_t, 2);
+    else SRA_ENC(uint16_t, 1);
+  } else {
+    if (vec == 8) SRA_ENC(float, 8);
+    else if (vec == 2) SRA_ENC(float, 2);
+    else SRA_ENC(float, 1);
+  }
+#undef SRA_ENC
+  return hipGetLastError();
+}
+
+hipError_t launch_ckpt_decode(int dtype, const int8_t* codes, const uint8_t* exps, int64_t T, int64_t K, void* x,
+                              hipStream_t s) {
+  if (T <= 0 || K <= 0) return hipSuccess;
+  flatten(T, K);
+  const int vec = row_vec(K);
+  const dim3 grid = grid_of(T, K / vec);
+#define SRA_DEC(E, V) launch(SRA_KERNEL_CKPT, k_ckpt_decode<E, V>, grid, dim3(kThreads), 0, s, codes, exps, T, K, (E*)x)
+  if (dtype == SRA_BF16) {
+    if (vec == 8) SRA_DEC(uint16_t, 8);
+    else if (vec == 2) SRA_DEC(uint16_t, 2);
+    else SRA_DEC(uint16_t, 1);
+  } else {
+    if (vec == 8) SRA_DEC(float, 8);
+    else if (vec == 2) SRA_DEC(float, 2);
+    else SRA_DEC(float, 1);
+  }
+#undef SRA_DEC
+  return hipGetLastError();
+}
+
+}  // namespace sra

@@ -343,6 +343,23 @@ struct AdapterGradArgs {
   int64_t T, Tp, t_per;
   int r, rp, S;
 };
+// Layer norm over rows (layer_norm.hip), H <= 16384 (layer_norm_ok); codes != nullptr also writes the
+// output's 8-bit checkpoint.  The backward's workspace holds one partial row of dgamma and dbeta
+// per workgroup.
+bool layer_norm_ok(int64_t H);
+size_t layer_norm_bwd_ws(int64_t T, int64_t H);
+hipError_t launch_layer_norm_fwd(int dtype, const void* x, const void* gamma, const void* beta, float eps, int64_t T,
+                                 int64_t H, void* y, float* mean, float* rstd, int8_t* codes, uint8_t* exps,
+                                 hipStream_t s);
+hipError_t launch_layer_norm_bwd(int dtype, const void* dy, const void* x, const void* gamma, const float* mean,
+                                 const float* rstd, int64_t T, int64_t H, void* dx, float* dgamma, float* dbeta,
+                                 void* ws, hipStream_t s);
+// 8-bit activation checkpoints (ckpt.hip): codes [T][K], exps [T][ceil(K/32)]
+hipError_t launch_ckpt_encode(int dtype, const void* x, int64_t T, int64_t K, int8_t* codes, uint8_t* exps,
+                              hipStream_t s);
+hipError_t launch_ckpt_decode(int dtype, const int8_t* codes, const uint8_t* exps, int64_t T, int64_t K, void* x,
+                              hipStream_t s);
+
 bool adapter_grads_ok(const AdapterGrad* g, int n, int64_t T, int r);
 size_t adapter_grads_ws(const AdapterGrad* g, int n, int64_t T, int r);
 hipError_t launch_adapter_grads(const AdapterGrad* g, int n, int64_t T, int r, void* ws,
