@@ -359,6 +359,17 @@ sra_status sra_masked_weight_grad(const sra_sparse* S /* host */, const void* ro
                                   const void* col_act, int64_t T, void* out_values, void* stream);
 
 /*
+ * masked_weight_grad_ckpt -- sra_masked_weight_grad with col_act given as its 8-bit checkpoint
+ * (sra_ckpt_encode; T x S->cols): equal to the call on the decoded bf16 values bit for bit.
+ * The workspace (sra_masked_weight_grad_ckpt_workspace bytes) holds the decoded values.
+ */
+sra_status sra_masked_weight_grad_ckpt_workspace(const sra_sparse* S /* host */, int64_t T,
+                                                 size_t* bytes /* host */);
+sra_status sra_masked_weight_grad_ckpt(const sra_sparse* S /* host */, const void* row_act,
+                                       const int8_t* col_codes, const uint8_t* col_exps, int64_t T,
+                                       void* out_values, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * nm_axpby -- out = beta * A + gamma * B for two compressed matrices that share one N:M pattern,
  * on their value arrays (SLoPe §2.3: a sparse addition of matrices with the same pattern, for
  * weight decay and the update step; §2.1: the mask is fixed, so the metadata stays valid and is
@@ -371,6 +382,42 @@ sra_status sra_masked_weight_grad(const sra_sparse* S /* host */, const void* ro
  */
 sra_status sra_nm_axpby(const void* a_values, float beta, const void* b_values, float gamma,
                         void* out_values, int64_t n_values, int32_t dtype, void* stream);
+
+/*
+ * multi_lora -- one projection shared by the tokens of many requests, each token with the low-rank
+ * adapter of its own request (LoRA as described in "efficient training for the gpu-poor", section
+ * PEFT, on the layer of SLoPe §2.2).  With g = ids[t]:
+ *     forward   U[t] = X[t] A_g^T,  Y[t] = X[t] Ws^T + U[t] B_g^T
+ *     backward  dU[t] = dY[t] B_g,  dX[t] = dY[t] P^T + dU[t] A_g,
+ *               dA_g = sum over g's tokens of dU[t]^T X[t],  dB_g = sum of dY[t]^T U[t]
+ * A [n_adapters, r, K] and B [n_adapters, N, r] hold the adapters (of one rank: smaller ones are
+ * padded with zeros); ids int32 [T], on the device and 4-byte aligned, in any order: requests
+ * whose tokens follow each other run fastest.  A token whose id is outside [0, n_adapters) has no
+ * adapter: its U and dU are zero and its Y and dX are the shared projection alone.
+ * Ws / P: bf16 N:M weights as for sra_sparse_lora_fwd / sra_sparse_lora_bwd (2:4, 1:2 and 2:8,
+ * canonical arrays or the streaming layout); other formats and fp32 are SRA_ERR_UNSUPPORTED.
+ * U_out / U / dU_out [T,r], dA [n_adapters,r,K] and dB [n_adapters,N,r] are fp32; an adapter with
+ * no token gets zero gradients.  Flags as for sra_sparse_lora_bwd.
+ * The backward reads the layer's input from X, or, when X is NULL, from its 8-bit checkpoint
+ * X_codes / X_exps (sra_ckpt_encode); the results equal those from the decoded bf16 values bit for
+ * bit.  It is read for dA, and for U when U is NULL and dB is asked for.  Sums over tokens run in a
+ * fixed order.  T = 0: the forward is a no-op, the backward writes zeros to dA and dB.
+ * Supported: 1 <= r <= 256, 1 <= n_adapters <= 1023, T < 2^26, N * r and K * r (rounded up to 8)
+ * below 2^30.  SRA_TUNE_ENGINE does not apply.
+ */
+sra_status sra_multi_fwd_workspace(const sra_sparse* Ws /* host */, int64_t T, int32_t n_adapters,
+                                   int32_t r, size_t* bytes /* host */);
+sra_status sra_multi_lora_fwd(const sra_sparse* Ws /* host */, const void* X, int64_t T,
+                              const void* A, const void* B, const int32_t* ids, int32_t n_adapters,
+                              int32_t r, void* Y, float* U_out, void* ws, size_t ws_bytes,
+                              void* stream);
+sra_status sra_multi_bwd_workspace(const sra_sparse* P /* host */, int64_t T, int32_t n_adapters,
+                                   int32_t r, uint32_t flags, size_t* bytes /* host */);
+sra_status sra_multi_lora_bwd(const sra_sparse* P /* host */, const void* dY, const void* X,
+                              const int8_t* X_codes, const uint8_t* X_exps, int64_t T,
+                              const float* U, const void* A, const void* B, const int32_t* ids,
+                              int32_t n_adapters, int32_t r, uint32_t flags, void* dX, float* dA,
+                              float* dB, float* dU_out, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * ckpt_encode / ckpt_decode -- 8-bit activation checkpoints: a layer's input kept for its backward

@@ -9,5 +9,5 @@ from .api import (SparseMatrix, bwd_workspace, ffa_bwd_workspace, ffa_fwd_worksp
                   double_prune, ffi_tile, ffi_transpose, fwd_workspace, meta_words, nm_tile, sparse_lora_bwd,
                   sparse_lora_bwd_ffa, sparse_lora_fwd, sparse_lora_fwd_ffa, time_next_kernel,
                   set_tuning, reset_tuning, tuned,
-                  Ckpt8, ckpt8_encode, ckpt8_decode, layer_norm_fwd, layer_norm_bwd,
+                  multi_lora_fwd, multi_lora_bwd, Ckpt8, ckpt8_encode, ckpt8_decode, layer_norm_fwd, layer_norm_bwd,
                   SRA_FMT_NM, SRA_FMT_NM_TILED)

@@ -27,6 +27,8 @@ EXPORTS = (
     "sra_ffi_tile", "sra_fwd_workspace",
     "sra_sparse_lora_fwd", "sra_bwd_workspace", "sra_sparse_lora_bwd", "sra_sparse_lora_bwd_noalloc",
     "sra_ffa_fwd_workspace", "sra_sparse_lora_fwd_ffa", "sra_ffa_bwd_workspace", "sra_sparse_lora_bwd_ffa",
+    "sra_masked_weight_grad_ckpt_workspace", "sra_masked_weight_grad_ckpt",
+    "sra_multi_fwd_workspace", "sra_multi_lora_fwd", "sra_multi_bwd_workspace", "sra_multi_lora_bwd",
     "sra_ckpt_encode", "sra_ckpt_decode",
     "sra_layer_norm_fwd", "sra_layer_norm_bwd_workspace", "sra_layer_norm_bwd",
     "sra_time_next_kernel", "sra_set_tuning",
@@ -93,6 +95,17 @@ def load(path: str = LIB_PATH):
         "sra_sparse_lora_bwd_ffa": (c_int32, [P, c_void_p, c_void_p, c_int64, c_void_p, P, c_void_p,
                                               c_uint32, c_void_p, c_void_p, c_void_p, c_void_p,
                                               c_void_p, c_size_t, c_void_p]),
+        "sra_masked_weight_grad_ckpt_workspace": (c_int32, [P, c_int64, POINTER(c_size_t)]),
+        "sra_masked_weight_grad_ckpt": (c_int32, [P, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
+                                                  c_void_p, c_size_t, c_void_p]),
+        "sra_multi_fwd_workspace": (c_int32, [P, c_int64, c_int32, c_int32, POINTER(c_size_t)]),
+        "sra_multi_lora_fwd": (c_int32, [P, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int32,
+                                         c_int32, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "sra_multi_bwd_workspace": (c_int32, [P, c_int64, c_int32, c_int32, c_uint32, POINTER(c_size_t)]),
+        "sra_multi_lora_bwd": (c_int32, [P, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
+                                         c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_uint32,
+                                         c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                         c_void_p]),
         "sra_ckpt_encode": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
         "sra_ckpt_decode": (c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_void_p]),
         "sra_layer_norm_fwd": (c_int32, [c_void_p, c_void_p, c_void_p, c_float, c_int32, c_int64, c_int64,

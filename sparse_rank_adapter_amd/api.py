@@ -90,6 +90,13 @@ def _check_sparse(S: "SparseMatrix", name: str):
     return dev
 
 
+def _workspace(ws, nbytes: int, dev):
+    """The caller's workspace when it is large enough, else a new one."""
+    if ws is None or ws.numel() < nbytes:
+        return torch.empty(max(1, nbytes), dtype=torch.uint8, device=dev)
+    return _arg(ws, "ws", (ws.numel(),), torch.uint8, dev)
+
+
 def _stream(dev) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
@@ -258,11 +265,12 @@ def compress_pair_tiled(W: torch.Tensor, n: int = 2, m: int = 4, out: tuple | No
     return Ws, P
 
 
-def masked_weight_grad(S: SparseMatrix, row_act: torch.Tensor, col_act: torch.Tensor,
-                       out: torch.Tensor | None = None) -> torch.Tensor:
+def masked_weight_grad(S: SparseMatrix, row_act: torch.Tensor, col_act: torch.Tensor | Ckpt8,
+                       out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of S's stored values: out[row][i] = sum_t row_act[t][row] col_act[t][c_i(row)].
 
     For the forward weight Ws: masked_weight_grad(Ws, dY, X) = (dY^T X) o mask in Ws's value order.
+    ``col_act`` may be an 8-bit checkpoint (Ckpt8); ``ws`` is then its workspace.
     """
     lib = load()
     if S.fmt != SRA_FMT_NM:
@@ -272,11 +280,24 @@ def masked_weight_grad(S: SparseMatrix, row_act: torch.Tensor, col_act: torch.Te
         raise ValueError("row_act must be a 2-D tensor [T, S.rows]")
     T = row_act.shape[0]
     _arg(row_act, "row_act", (T, S.rows), S.dtype, dev)
-    _arg(col_act, "col_act", (T, S.cols), S.dtype, dev)
+    kept = isinstance(col_act, Ckpt8)
+    if kept:
+        _check_ckpt(col_act, "col_act", (T, S.cols), dev)
+    else:
+        _arg(col_act, "col_act", (T, S.cols), S.dtype, dev)
     if out is None:
         out = torch.empty((S.rows, S.cols // S.m * S.n), dtype=S.dtype, device=S.device)
     _arg(out, "out", (S.rows, S.cols // S.m * S.n), S.dtype, dev)
     d = S.desc()
+    if kept:
+        nbytes = ctypes.c_size_t()
+        check("sra_masked_weight_grad_ckpt_workspace",
+              lib.sra_masked_weight_grad_ckpt_workspace(ctypes.byref(d), T, ctypes.byref(nbytes)))
+        ws = _workspace(ws, nbytes.value, dev)
+        check("sra_masked_weight_grad_ckpt", lib.sra_masked_weight_grad_ckpt(
+            ctypes.byref(d), _p(row_act), _p(col_act.codes), _p(col_act.exps), T, _p(out), _p(ws), ws.numel(),
+            _stream(S.device)))
+        return out
     check("sra_masked_weight_grad", lib.sra_masked_weight_grad(ctypes.byref(d), _p(row_act), _p(col_act), T,
                                                                _p(out), _stream(S.device)))
     return out
@@ -591,6 +612,93 @@ def ffa_bwd_workspace(P: SparseMatrix, T: int, A: SparseMatrix,
     return n.value
 
 
+def _multi_args(A, B, ids, T: int, K: int, N: int, dt, dev):
+    """Adapters [n, r, K] and [n, N, r] and the tokens' ids; returns (n, r)."""
+    for t, name in ((A, "A"), (B, "B")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must be a 3-D tensor ([n, r, K] and [n, N, r])")
+    n, r = int(A.shape[0]), int(A.shape[1])
+    _arg(A, "A", (n, r, K), dt, dev)
+    _arg(B, "B", (n, N, r), dt, dev)
+    _arg(ids, "ids", (T,), torch.int32, dev)
+    return n, r
+
+
+def multi_lora_fwd(Ws: SparseMatrix, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor,
+                   Y: torch.Tensor | None = None, U: torch.Tensor | None = None, want_u: bool = True,
+                   ws: torch.Tensor | None = None):
+    """Y[t] = X[t] Ws^T + (X[t] A_g^T) B_g^T with g = ids[t] (an id outside [0, n): no adapter).
+
+    A [n, r, K], B [n, N, r], ids int32 [T].  Returns (Y, U) with U fp32 [T, r] (None when not wanted)."""
+    lib = load()
+    dev = _check_sparse(Ws, "Ws")
+    N, K, dt = Ws.rows, Ws.cols, Ws.dtype
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be a 2-D tensor [T, K]")
+    T = X.shape[0]
+    _arg(X, "X", (T, K), dt, dev)
+    n, r = _multi_args(A, B, ids, T, K, N, dt, dev)
+    if Y is None:
+        Y = torch.empty((T, N), dtype=dt, device=dev)
+    else:
+        _arg(Y, "Y", (T, N), dt, dev)
+    if U is not None:
+        _arg(U, "U", (T, r), torch.float32, dev)
+    elif want_u:
+        U = torch.empty((T, r), dtype=torch.float32, device=dev)
+    d = Ws.desc()
+    nbytes = ctypes.c_size_t()
+    check("sra_multi_fwd_workspace", lib.sra_multi_fwd_workspace(ctypes.byref(d), T, n, r, ctypes.byref(nbytes)))
+    ws = _workspace(ws, nbytes.value, dev)
+    check("sra_multi_lora_fwd", lib.sra_multi_lora_fwd(
+        ctypes.byref(d), _p(X), T, _p(A), _p(B), _p(ids), n, r, _p(Y), _p(U), _p(ws), ws.numel(), _stream(dev)))
+    return Y, U
+
+
+def multi_lora_bwd(P: SparseMatrix, dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, U: torch.Tensor | None,
+                   A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor, dx: bool = True, da: bool = True,
+                   db: bool = True, dx_adapter: bool = True, want_du: bool = False,
+                   ws: torch.Tensor | None = None, out: dict | None = None):
+    """Double-pruned backward of multi_lora_fwd; X may be its 8-bit checkpoint.  Returns a dict with dX,
+    dA [n, r, K] and dB [n, N, r] (and dU when want_du), each only if asked for."""
+    lib = load()
+    dev = _check_sparse(P, "P")
+    K, N, dt = P.rows, P.cols, P.dtype
+    if not isinstance(dY, torch.Tensor) or dY.dim() != 2:
+        raise ValueError("dY must be a 2-D tensor [T, N]")
+    T = dY.shape[0]
+    _arg(dY, "dY", (T, N), dt, dev)
+    n, r = _multi_args(A, B, ids, T, K, N, dt, dev)
+    kept = isinstance(X, Ckpt8)
+    if kept:
+        _check_ckpt(X, "X", (T, K), dev)
+    elif X is not None:
+        _arg(X, "X", (T, K), dt, dev)
+    elif da or (db and U is None):
+        raise ValueError("X is needed for dA, and for dB when U is not given")
+    if U is not None:
+        _arg(U, "U", (T, r), torch.float32, dev)
+    flags = (SRA_GRAD_DX if dx else 0) | (SRA_GRAD_DA if da else 0) | (SRA_GRAD_DB if db else 0)
+    if not dx_adapter:
+        flags |= SRA_DX_NO_ADAPTER
+    out = dict(out or {})
+    for key, wanted, shape, odt in (("dX", dx, (T, K), dt), ("dA", da, (n, r, K), torch.float32),
+                                    ("dB", db, (n, N, r), torch.float32), ("dU", want_du, (T, r), torch.float32)):
+        if out.get(key) is not None:
+            _arg(out[key], f"out['{key}']", shape, odt, dev)
+        elif wanted:
+            out[key] = torch.empty(shape, dtype=odt, device=dev)
+    d = P.desc()
+    nbytes = ctypes.c_size_t()
+    check("sra_multi_bwd_workspace", lib.sra_multi_bwd_workspace(ctypes.byref(d), T, n, r, flags, ctypes.byref(nbytes)))
+    ws = _workspace(ws, nbytes.value, dev)
+    check("sra_multi_lora_bwd", lib.sra_multi_lora_bwd(
+        ctypes.byref(d), _p(dY), None if kept else _p(X), _p(X.codes) if kept else None,
+        _p(X.exps) if kept else None, T, _p(U), _p(A), _p(B), _p(ids), n, r, flags, _p(out.get("dX")),
+        _p(out.get("dA")), _p(out.get("dB")), _p(out.get("dU")), _p(ws), ws.numel(), _stream(dev)))
+    return out
+
+
 CKPT_BLOCK = 32  # columns of a checkpoint that share one scale
 
 
@@ -703,9 +811,7 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor, mean:
     dbeta = torch.empty(H, dtype=torch.float32, device=dev)
     nbytes = ctypes.c_size_t()
     check("sra_layer_norm_bwd_workspace", lib.sra_layer_norm_bwd_workspace(T, H, ctypes.byref(nbytes)))
-    if ws is None or ws.numel() < nbytes.value:
-        ws = torch.empty(max(1, nbytes.value), dtype=torch.uint8, device=dev)
-    _arg(ws, "ws", (ws.numel(),), torch.uint8, dev)
+    ws = _workspace(ws, nbytes.value, dev)
     check("sra_layer_norm_bwd", lib.sra_layer_norm_bwd(
         _p(dY), _p(X), _p(gamma), _p(mean), _p(rstd), _dt(X), T, H, _p(dX), _p(dgamma), _p(dbeta),
         _p(ws), ws.numel(), _stream(dev)))

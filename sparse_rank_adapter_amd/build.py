@@ -28,6 +28,7 @@ SOURCES = [
     "adapter.hip",
     "spmm_ffi.hip",
     "weight_grad.hip",
+    "multi.hip",
     "ckpt.hip",
     "layer_norm.hip",
 ]

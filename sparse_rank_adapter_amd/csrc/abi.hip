@@ -540,8 +540,7 @@ sra_status sra_compress_pair_tiled(const void* W, int32_t dtype, int64_t rows, i
                   s, "compress_pair_tiled");
 }
 
-sra_status sra_masked_weight_grad(const sra_sparse* S, const void* row_act, const void* col_act,
-                                  int64_t T, void* out_values, void* stream) {
+static sra_status check_sddmm(const sra_sparse* S, const void* row_act, int64_t T, const void* out_values) {
   if (!S) return fail(SRA_ERR_INVALID_ARG, "S descriptor is NULL");
   SRA_TRY(check_dtype(S->dtype));
   if (S->format != SRA_FMT_NM) return fail(SRA_ERR_INVALID_ARG, "masked_weight_grad needs a canonical N:M matrix");
@@ -555,10 +554,44 @@ sra_status sra_masked_weight_grad(const sra_sparse* S, const void* row_act, cons
   const bool any = S->rows > 0 && S->cols > 0;
   SRA_TRY(check_ptr(S->meta, any, "meta"));
   SRA_TRY(check_ptr(out_values, any, "out_values"));
-  SRA_TRY(check_ptr(row_act, any && T > 0, "row_act"));
-  SRA_TRY(check_ptr(col_act, any && T > 0, "col_act"));
+  return check_ptr(row_act, any && T > 0, "row_act");
+}
+
+sra_status sra_masked_weight_grad(const sra_sparse* S, const void* row_act, const void* col_act,
+                                  int64_t T, void* out_values, void* stream) {
+  SRA_TRY(check_sddmm(S, row_act, T, out_values));
+  SRA_TRY(check_ptr(col_act, S->rows > 0 && S->cols > 0 && T > 0, "col_act"));
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_sddmm24_bf16((const uint16_t*)row_act, (const uint16_t*)col_act, S->meta,
+                                           is12(S) ? kMeta12To24 : 0u, S->rows, S->cols, T,
+                                           (uint16_t*)out_values, s),
+                  s, "masked_weight_grad");
+}
+
+static sra_status check_ckpt(const int8_t* codes, const uint8_t* exps, int64_t T, int64_t K);
+
+sra_status sra_masked_weight_grad_ckpt_workspace(const sra_sparse* S, int64_t T, size_t* bytes) {
+  if (!S) return fail(SRA_ERR_INVALID_ARG, "S descriptor is NULL");
+  if (T < 0 || S->cols < 0) return fail(SRA_ERR_INVALID_ARG, "negative shape");
+  if (!bytes) return fail(SRA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = (size_t)T * (size_t)S->cols * 2;
+  return SRA_OK;
+}
+
+sra_status sra_masked_weight_grad_ckpt(const sra_sparse* S, const void* row_act, const int8_t* col_codes,
+                                       const uint8_t* col_exps, int64_t T, void* out_values, void* ws,
+                                       size_t ws_bytes, void* stream) {
+  SRA_TRY(check_sddmm(S, row_act, T, out_values));
+  SRA_TRY(check_ckpt(col_codes, col_exps, T, S->rows > 0 ? S->cols : 0));
+  const size_t need = (size_t)T * (size_t)S->cols * 2;
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(SRA_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", need, ws ? ws_bytes : (size_t)0);
+  SRA_TRY(check_ptr(ws, need > 0, "workspace"));
+  const hipStream_t s = (hipStream_t)stream;
+  if (S->rows > 0)
+    SRA_TRY(hip_done(sra::launch_ckpt_decode(SRA_BF16, col_codes, col_exps, T, S->cols, ws, s), s,
+                     "masked_weight_grad decode"));
+  return hip_done(sra::launch_sddmm24_bf16((const uint16_t*)row_act, (const uint16_t*)ws, S->meta,
                                            is12(S) ? kMeta12To24 : 0u, S->rows, S->cols, T,
                                            (uint16_t*)out_values, s),
                   s, "masked_weight_grad");
@@ -1042,6 +1075,292 @@ sra_status sra_sparse_lora_bwd(const sra_sparse* P, const void* dY, const void* 
     SRA_TRY(hip_done(sra::launch_adapter_cols((const uint16_t*)X, T, K, vtdU, 3, r, true, dA, gws, s),
                      s, "bwd dA"));
   return SRA_OK;
+}
+
+// ---------------------------------------------------------------- many adapters
+namespace {
+
+// An N:M weight on the kernels that run it: 1:2 with converted metadata, 2:8 above 16 tokens
+// rewritten as 2:4, both in the workspace at meta_off / v24_off; `out` is then what to run.
+sra_status on24(const sra_sparse* S, int64_t T, uint8_t* wsb, size_t meta_off, size_t v24_off, sra_sparse* out,
+                hipStream_t s) {
+  *out = *S;
+  if (is12(S)) {
+    out->meta = (uint32_t*)(wsb + meta_off);
+    out->n = 2;
+    out->m = 4;
+    return hip_done(sra::launch_meta_or(S->meta, out->meta, (int64_t)(meta_bytes(S) / 4), kMeta12To24, s), s,
+                    "1:2 metadata");
+  }
+  if ((is28(S) || is28t(S)) && !use_dec28(S, T)) {
+    out->format = SRA_FMT_NM;
+    out->values = wsb + v24_off;
+    out->meta = (uint32_t*)(wsb + meta_off);
+    out->n = 2;
+    out->m = 4;
+    return hip_done(sra::launch_nm28_to24((const uint16_t*)S->values, S->meta, S->rows, S->cols,
+                                          (uint16_t*)out->values, out->meta, s, is28t(S)), s, "2:8 as 2:4");
+  }
+  return SRA_OK;
+}
+
+sra_status check_multi(const sra_sparse* S, const char* name, int64_t T, int32_t n, int32_t r) {
+  SRA_TRY(check_sparse(S, name));
+  if (S->format != SRA_FMT_NM && S->format != SRA_FMT_NM_TILED)
+    return fail(SRA_ERR_UNSUPPORTED, "%s: many adapters need an N:M weight", name);
+  if (S->dtype != SRA_BF16) return fail(SRA_ERR_UNSUPPORTED, "%s: many adapters are bf16 only", name);
+  if (T < 0) return fail(SRA_ERR_INVALID_ARG, "T < 0");
+  if (T >= ((int64_t)1 << 26)) return fail(SRA_ERR_UNSUPPORTED, "T = %lld is not below 2^26", (long long)T);
+  if (r < 1 || r > 256) return fail(SRA_ERR_UNSUPPORTED, "rank %d outside [1, 256]", r);
+  if (n < 1) return fail(SRA_ERR_INVALID_ARG, "n_adapters = %d, needs at least 1", n);
+  if (n > sra::multi_max_adapters())
+    return fail(SRA_ERR_UNSUPPORTED, "n_adapters = %d is above %d", n, sra::multi_max_adapters());
+  const int64_t rp = sra::packed_at_ld(r);
+  if (S->rows * rp >= ((int64_t)1 << 30) || S->cols * rp >= ((int64_t)1 << 30))
+    return fail(SRA_ERR_UNSUPPORTED, "%s: N * r and K * r must stay below 2^30", name);
+  return SRA_OK;
+}
+// the shared product itself (forward, or backward with dX)
+sra_status check_multi_product(const sra_sparse* S, int64_t T) {
+  if (S->cols == 0) return fail(SRA_ERR_UNSUPPORTED, "the shared product needs a reduction of at least 32");
+  if (S->format == SRA_FMT_NM_TILED && !is28t(S) && !sra::spmm24_tiled_ok(S->cols, T))
+    return fail(SRA_ERR_UNSUPPORTED, "the streaming 2:4 layout needs a reduction %% 128 == 0 above 16 tokens (T = %lld)",
+                (long long)T);
+  return SRA_OK;
+}
+sra_status check_ids(const int32_t* ids, bool needed) {
+  if (!needed) return SRA_OK;
+  if (!ids) return fail(SRA_ERR_INVALID_ARG, "ids is NULL");
+  if ((uintptr_t)ids & 3) return fail(SRA_ERR_INVALID_ARG, "ids is not 4-byte aligned");
+  return SRA_OK;
+}
+
+struct MultiPlan {
+  size_t u_off = 0, du_off = 0, rows_off = 0, spmm_off = 0, meta_off = 0, v24_off = 0, x_off = 0;
+  size_t gblk_off = 0, perm_off = 0, wt_off = 0, at_off = 0, total = 0;
+};
+void multi_weight_bytes(const sra_sparse* S, int64_t T, Arena* a, MultiPlan* p) {
+  if (is12(S)) p->meta_off = a->take(meta_bytes(S));
+  if ((is28(S) || is28t(S)) && !use_dec28(S, T)) {
+    p->meta_off = a->take(meta_bytes(S));
+    p->v24_off = a->take((size_t)S->rows * (size_t)(S->cols / 2) * 2);
+  }
+  p->spmm_off = a->take(sra::spmm24_multi_ws(S->rows, S->cols, T));
+}
+size_t multi_fwd_plan(const sra_sparse* Ws, int64_t T, int32_t r, bool own_u, MultiPlan* plan) {
+  MultiPlan p;
+  Arena a;
+  if (own_u) p.u_off = a.take((size_t)T * r * 4);
+  p.rows_off = a.take(sra::adapter_rows_ws(T, Ws->cols, r));
+  multi_weight_bytes(Ws, T, &a, &p);
+  p.total = a.used;
+  if (plan) *plan = p;
+  return p.total;
+}
+size_t multi_bwd_plan(const sra_sparse* P, int64_t T, int32_t n, int32_t r, uint32_t flags, bool have_u, bool have_x,
+                      bool have_du, MultiPlan* plan) {
+  MultiPlan p;
+  Arena a;
+  const int64_t K = P->rows, N = P->cols;
+  const bool dx = flags & SRA_GRAD_DX, da = flags & SRA_GRAD_DA, db = flags & SRA_GRAD_DB;
+  const bool need_du = da || have_du || (dx && !(flags & SRA_DX_NO_ADAPTER)), own_u = db && !have_u;
+  size_t rows = 0;
+  if (own_u) {
+    p.u_off = a.take((size_t)T * r * 4);
+    rows = sra::adapter_rows_ws(T, K, r);
+    if (!have_x) p.x_off = a.take((size_t)T * K * 2);  // the decoded checkpoint
+  }
+  if (need_du) {
+    if (!have_du) p.du_off = a.take((size_t)T * r * 4);
+    p.wt_off = a.take((size_t)n * N * r * 2);
+    rows = std::max(rows, sra::adapter_rows_ws(T, N, r));
+  }
+  p.rows_off = a.take(rows);
+  if (dx && !(flags & SRA_DX_NO_ADAPTER)) p.at_off = a.take((size_t)n * K * sra::packed_at_ld(r) * 2);
+  if (da || db) {
+    p.gblk_off = a.take((size_t)(n + 1) * 4);
+    p.perm_off = a.take((size_t)sra::multi_perm_entries(T, n) * 4);
+  }
+  if (dx) multi_weight_bytes(P, T, &a, &p);
+  p.total = a.used;
+  if (plan) *plan = p;
+  return p.total;
+}
+sra_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(SRA_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", need, ws ? ws_bytes : (size_t)0);
+  if (need > 0 && !al16(ws)) return fail(SRA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  return SRA_OK;
+}
+// Y or dX: the shared product with the adapters' epilogue (ep.r = 0: without)
+sra_status multi_product(const sra_sparse* S, const void* act, int64_t T, const sra::Epilogue& ep, void* out, void* ws,
+                         hipStream_t s, const char* what) {
+  if (use_dec28(S, T))
+    return hip_done(sra::launch_decode28_bf16((const uint16_t*)S->values, S->meta, S->rows, S->cols,
+                                              (const uint16_t*)act, T, ep, (uint16_t*)out, s, is28t(S)), s, what);
+  return hip_done(sra::launch_spmm24_multi_bf16(S->format == SRA_FMT_NM_TILED, (const uint16_t*)S->values, S->meta,
+                                                S->rows, S->cols, (const uint16_t*)act, T, ep, (uint16_t*)out, ws, s),
+                  s, what);
+}
+
+}  // namespace
+
+sra_status sra_multi_fwd_workspace(const sra_sparse* Ws, int64_t T, int32_t n_adapters, int32_t r, size_t* bytes) {
+  SRA_TRY(check_multi(Ws, "Ws", T, n_adapters, r));
+  SRA_TRY(check_multi_product(Ws, T));
+  if (!bytes) return fail(SRA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = multi_fwd_plan(Ws, T, r, true, nullptr);
+  return SRA_OK;
+}
+
+sra_status sra_multi_lora_fwd(const sra_sparse* Ws, const void* X, int64_t T, const void* A, const void* B,
+                              const int32_t* ids, int32_t n_adapters, int32_t r, void* Y, float* U_out, void* ws,
+                              size_t ws_bytes, void* stream) {
+  SRA_TRY(check_multi(Ws, "Ws", T, n_adapters, r));
+  SRA_TRY(check_multi_product(Ws, T));
+  const int64_t N = Ws->rows, K = Ws->cols;
+  const bool any = T > 0;
+  SRA_TRY(check_ptr(X, any, "X"));
+  SRA_TRY(check_ptr(A, any, "A"));
+  SRA_TRY(check_ptr(B, any && N > 0, "B"));
+  SRA_TRY(check_ids(ids, any));
+  SRA_TRY(check_ptr(Y, any && N > 0, "Y"));
+  if (U_out) SRA_TRY(check_ptr(U_out, true, "U_out"));
+  MultiPlan plan;
+  multi_fwd_plan(Ws, T, r, U_out == nullptr, &plan);
+  SRA_TRY(check_ws(ws, ws_bytes, plan.total));
+  if (T == 0) return SRA_OK;
+  const hipStream_t s = (hipStream_t)stream;
+  uint8_t* wsb = (uint8_t*)ws;
+  sra_sparse w;
+  SRA_TRY(on24(Ws, T, wsb, plan.meta_off, plan.v24_off, &w, s));
+  sra::Epilogue ep;
+  float* U = U_out ? U_out : (float*)(wsb + plan.u_off);
+  ep.U = U;
+  ep.E = (const uint16_t*)B;
+  ep.e_row_stride = r;
+  ep.e_j_stride = 1;
+  ep.r = r;
+  ep.ai = sra::AdapterIds{ids, N * (int64_t)r, n_adapters};
+  SRA_TRY(hip_done(sra::launch_multi_rows((const uint16_t*)X, T, K, (const uint16_t*)A, K, r,
+                                          sra::AdapterIds{ids, K * (int64_t)r, n_adapters}, U, wsb + plan.rows_off, s),
+                   s, "multi fwd U"));
+  return multi_product(&w, X, T, ep, Y, wsb + plan.spmm_off, s, "multi fwd");
+}
+
+sra_status sra_multi_bwd_workspace(const sra_sparse* P, int64_t T, int32_t n_adapters, int32_t r, uint32_t flags,
+                                   size_t* bytes) {
+  SRA_TRY(check_multi(P, "P", T, n_adapters, r));
+  if (flags & ~15u) return fail(SRA_ERR_INVALID_ARG, "unknown flag bits 0x%x", flags);
+  if (flags & SRA_GRAD_DX) SRA_TRY(check_multi_product(P, T));
+  if (!bytes) return fail(SRA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = multi_bwd_plan(P, T, n_adapters, r, flags, false, false, false, nullptr);
+  return SRA_OK;
+}
+
+sra_status sra_multi_lora_bwd(const sra_sparse* P, const void* dY, const void* X, const int8_t* X_codes,
+                              const uint8_t* X_exps, int64_t T, const float* U, const void* A, const void* B,
+                              const int32_t* ids, int32_t n_adapters, int32_t r, uint32_t flags, void* dX, float* dA,
+                              float* dB, float* dU_out, void* ws, size_t ws_bytes, void* stream) {
+  SRA_TRY(check_multi(P, "P", T, n_adapters, r));
+  if (flags & ~15u) return fail(SRA_ERR_INVALID_ARG, "unknown flag bits 0x%x", flags);
+  if (flags & SRA_GRAD_DX) SRA_TRY(check_multi_product(P, T));
+  const int64_t K = P->rows, N = P->cols;
+  const bool any = T > 0, fdx = flags & SRA_GRAD_DX, fda = flags & SRA_GRAD_DA, fdb = flags & SRA_GRAD_DB;
+  const bool dx_ad = fdx && !(flags & SRA_DX_NO_ADAPTER), own_u = fdb && !U;
+  const bool need_du = dx_ad || fda || dU_out;
+  if (K == 0 || N == 0) return fail(SRA_ERR_UNSUPPORTED, "many adapters need K > 0 and N > 0");
+  SRA_TRY(check_ptr(dY, any && (fdx || need_du || fdb), "dY"));
+  if ((X_codes == nullptr) != (X_exps == nullptr))
+    return fail(SRA_ERR_INVALID_ARG, "X_codes and X_exps must both be given or both be NULL");
+  if (X && X_codes) return fail(SRA_ERR_INVALID_ARG, "X is given both as a tensor and as a checkpoint");
+  if (X_codes) {
+    SRA_TRY(check_ckpt(X_codes, X_exps, T, K));
+  } else {
+    SRA_TRY(check_ptr(X, any && (fda || own_u), "X"));
+  }
+  SRA_TRY(check_ptr(A, any && (dx_ad || own_u), "A"));
+  SRA_TRY(check_ptr(B, any && need_du, "B"));
+  SRA_TRY(check_ids(ids, any && (need_du || fdb)));
+  SRA_TRY(check_ptr(dX, any && fdx, "dX"));
+  SRA_TRY(check_ptr(dA, fda, "dA"));
+  SRA_TRY(check_ptr(dB, fdb, "dB"));
+  if (U) SRA_TRY(check_ptr(U, true, "U"));
+  if (dU_out) SRA_TRY(check_ptr(dU_out, true, "dU_out"));
+  MultiPlan plan;
+  multi_bwd_plan(P, T, n_adapters, r, flags, U != nullptr, X_codes == nullptr, dU_out != nullptr, &plan);
+  SRA_TRY(check_ws(ws, ws_bytes, plan.total));
+  const hipStream_t s = (hipStream_t)stream;
+  if (T == 0) {
+    if (fda) SRA_TRY(hip_done(sra::launch_fill_f32(dA, (int64_t)n_adapters * r * K, 0.f, s), s, "zero dA"));
+    if (fdb) SRA_TRY(hip_done(sra::launch_fill_f32(dB, (int64_t)n_adapters * N * r, 0.f, s), s, "zero dB"));
+    return SRA_OK;
+  }
+  uint8_t* wsb = (uint8_t*)ws;
+  sra::MultiPrep prep;
+  prep.ids = ids;
+  prep.T = T;
+  prep.n = n_adapters;
+  prep.r = r;
+  prep.B = (const uint16_t*)B;
+  prep.N = N;
+  prep.A = (const uint16_t*)A;
+  prep.K = K;
+  if (fda || fdb) {
+    prep.gblk = (int32_t*)(wsb + plan.gblk_off);
+    prep.perm = (int32_t*)(wsb + plan.perm_off);
+  }
+  if (need_du) prep.wt = (uint16_t*)(wsb + plan.wt_off);
+  if (dx_ad) prep.at = (uint16_t*)(wsb + plan.at_off);
+  SRA_TRY(hip_done(sra::launch_multi_prep(prep, s), s, "multi bwd prep"));
+  void* rws = wsb + plan.rows_off;
+  if (own_u) {
+    const uint16_t* x = (const uint16_t*)X;
+    if (!x) {
+      SRA_TRY(hip_done(sra::launch_ckpt_decode(SRA_BF16, X_codes, X_exps, T, K, wsb + plan.x_off, s), s, "multi bwd X"));
+      x = (const uint16_t*)(wsb + plan.x_off);
+    }
+    SRA_TRY(hip_done(sra::launch_multi_rows(x, T, K, (const uint16_t*)A, K, r,
+                                            sra::AdapterIds{ids, K * (int64_t)r, n_adapters},
+                                            (float*)(wsb + plan.u_off), rws, s), s, "multi bwd U"));
+    U = (const float*)(wsb + plan.u_off);
+  }
+  float* dU = dU_out ? dU_out : (float*)(wsb + plan.du_off);
+  if (need_du)
+    SRA_TRY(hip_done(sra::launch_multi_rows((const uint16_t*)dY, T, N, prep.wt, N, r,
+                                            sra::AdapterIds{ids, N * (int64_t)r, n_adapters}, dU, rws, s),
+                     s, "multi bwd dU"));
+  sra::MultiGrad jobs[2];
+  int nj = 0;
+  if (fdb) {
+    jobs[nj].act = (const uint16_t*)dY;
+    jobs[nj].V = U;
+    jobs[nj].out = dB;
+    jobs[nj].M = N;
+    ++nj;
+  }
+  if (fda) {
+    jobs[nj].act = (const uint16_t*)X;
+    jobs[nj].codes = X_codes;
+    jobs[nj].exps = X_exps;
+    jobs[nj].V = dU;
+    jobs[nj].out = dA;
+    jobs[nj].M = K;
+    jobs[nj].out_t = true;
+    ++nj;
+  }
+  SRA_TRY(hip_done(sra::launch_multi_grads(jobs, nj, prep.gblk, prep.perm, n_adapters, r, s), s, "multi bwd dB, dA"));
+  if (!fdx) return SRA_OK;
+  sra_sparse p24;
+  SRA_TRY(on24(P, T, wsb, plan.meta_off, plan.v24_off, &p24, s));
+  sra::Epilogue ep;
+  ep.U = dU;
+  ep.E = prep.at;  // A_g^T rows: E(k, j) = A_g[j][k]
+  ep.e_row_stride = sra::packed_at_ld(r);
+  ep.e_j_stride = 1;
+  ep.r = dx_ad ? r : 0;
+  ep.ai = sra::AdapterIds{ids, K * sra::packed_at_ld(r), n_adapters};
+  return multi_product(&p24, dY, T, ep, dX, wsb + plan.spmm_off, s, "multi bwd dX");
 }
 
 // ---------------------------------------------------------------- fixed-fan-in adapter factor

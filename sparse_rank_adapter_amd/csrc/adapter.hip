@@ -88,15 +88,22 @@ SRA_DEV u32x4 load8(const uint16_t* __restrict__ p, int64_t i, int64_t lim, bool
 // Wave w takes the 32-column steps w, w+4, w+8, ... of its slice, UB steps per batch.
 // When vt is non-null the result is also written as V^T split into three bf16 parts (write_vt3),
 // vt[p][j][t] (rows rp, columns Tp; the zero padding is the caller's), ready for the cols kernel.
+//
+// MA (many adapters): token t takes the weight rows of adapter ids[t], wt + ids[t] * stride, and a
+// token whose id is outside [0, n) gets zeros.  The pass over c runs once for every distinct
+// adapter of the workgroup's tokens (each wave finds the same sequence from the same ids) and a
+// token keeps the sums of its own adapter's pass.  Requests whose tokens follow each other cost
+// one pass nearly everywhere.
 
-template <int JT, int UB>
+template <int JT, int UB, bool MA = false>
 __global__ __launch_bounds__(256) void k_adapter_rows(const uint16_t* __restrict__ act, int64_t T,
                                                       int64_t C, const uint16_t* __restrict__ wt,
                                                       int64_t ldw, int r, int64_t c_per,
                                                       double* __restrict__ part,
                                                       float* __restrict__ out,
                                                       double* __restrict__ out64,
-                                                      uint16_t* __restrict__ vt, int rp, int64_t Tp) {
+                                                      uint16_t* __restrict__ vt, int rp, int64_t Tp,
+                                                      sra::AdapterIds ai = {}) {
   __shared__ double red[3][JT * 4][64];
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, lr = l & 15, lg = l >> 4;
   const int64_t t0 = (int64_t)blockIdx.x * 16, t = t0 + lr;
@@ -151,12 +158,49 @@ __global__ __launch_bounds__(256) void k_adapter_rows(const uint16_t* __restrict
       flush(acc, acc64);
     }
   };
-  if (nb > 0) load(0, fa0, fw0);
-  for (int b = 0; b < nb; b += 2) {
-    if (b + 1 < nb) load(b + 1, fa1, fw1);
-    compute(b, fa0, fw0);
-    if (b + 2 < nb) load(b + 2, fa0, fw0);
-    if (b + 1 < nb) compute(b + 1, fa1, fw1);
+  auto pass = [&] {
+    if (nb > 0) load(0, fa0, fw0);
+    for (int b = 0; b < nb; b += 2) {
+      if (b + 1 < nb) load(b + 1, fa1, fw1);
+      compute(b, fa0, fw0);
+      if (b + 2 < nb) load(b + 2, fa0, fw0);
+      if (b + 1 < nb) compute(b + 1, fa1, fw1);
+    }
+  };
+  if constexpr (MA) {
+    const int id = t_ok ? ai.ids[t] : -1;
+    int idr[4];  // the tokens of this lane's sums
+#pragma unroll
+    for (int e = 0; e < 4; ++e) idr[e] = __shfl(id, 4 * lg + e, 64);
+    double own[JT][4];
+#pragma unroll
+    for (int a = 0; a < JT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) own[a][e] = 0.0;
+    uint32_t todo = (uint32_t)__ballot(id >= 0 && id < ai.n) & 0xffffu;
+    while (todo) {
+      const int g = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+      todo &= ~(uint32_t)__ballot(id == g);
+#pragma unroll
+      for (int a = 0; a < JT; ++a) {
+        const int j = j0 + 16 * a + lr;
+        wrow[a] = wt + (int64_t)g * ai.stride + (int64_t)(j_ok[a] ? j : 0) * ldw;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc64[a][e] = 0.0;
+      }
+      pass();
+#pragma unroll
+      for (int a = 0; a < JT; ++a)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (idr[e] == g) own[a][e] = acc64[a][e];
+    }
+#pragma unroll
+    for (int a = 0; a < JT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc64[a][e] = own[a][e];
+  } else {
+    pass();
   }
   // V^T columns T .. Tp-1 (padding to a multiple of 8) must read as zero in the cols kernel
   if (vt && blockIdx.z == 0 && w == 0) {
@@ -403,10 +447,12 @@ __global__ __launch_bounds__(256) void k_adapter_cols(const uint16_t* __restrict
 // the reduction over workgroups would need a second launch for the sum; with few tokens both
 // launches are latency-bound, so this one reads the token row once per four adapter columns
 // instead.  Needs C % 8 == 0, 16-byte aligned rows (ldw % 8 == 0).
+// With ai.ids, token t takes the rows of adapter ids[t] (zeros when it names none).
 constexpr int kFewJ = 4;
 __global__ __launch_bounds__(256) void k_adapter_rows_few(const uint16_t* __restrict__ act, int64_t C,
                                                          const uint16_t* __restrict__ wt, int64_t ldw,
-                                                         int r, float* __restrict__ out) {
+                                                         int r, float* __restrict__ out,
+                                                         sra::AdapterIds ai) {
   __shared__ double red[kFewJ][256];
   const int tid = threadIdx.x;
   // grid (column groups, tokens): consecutive workgroup ids go to different XCDs, so with a
@@ -415,6 +461,14 @@ __global__ __launch_bounds__(256) void k_adapter_rows_few(const uint16_t* __rest
   const int64_t t = blockIdx.y;
   const int j0 = blockIdx.x * kFewJ;
   const uint16_t* xrow = act + t * C;
+  if (ai.ids) {
+    const int g = ai.ids[t];
+    if (g < 0 || g >= ai.n) {
+      if (tid < kFewJ && j0 + tid < r) out[t * r + j0 + tid] = 0.f;
+      return;
+    }
+    wt += (int64_t)g * ai.stride;
+  }
   double acc[kFewJ] = {0.0, 0.0, 0.0, 0.0};
   // every load of a block of NCH chunks is issued before the first product, so the reduction
   // costs one memory round trip per 256 * NCH chunks instead of one per chunk
@@ -618,7 +672,7 @@ void rows_launch(dim3 grid, hipStream_t s, const uint16_t* act, int64_t T, int64
                  const uint16_t* wt, int64_t ldw, int r, int64_t c_per, double* part, float* out,
                  double* out64, uint16_t* vt, int rp, int64_t Tp) {
   sra::launch(SRA_KERNEL_ADAPTER, k_adapter_rows<JT, UB>, grid, dim3(256), 0, s, act, T, C, wt,
-              ldw, r, c_per, part, out, out64, vt, rp, Tp);
+              ldw, r, c_per, part, out, out64, vt, rp, Tp, sra::AdapterIds{});
 }
 
 template <int JT>
@@ -1036,6 +1090,8 @@ __global__ void k_reduce_grads(sra::AdapterGradArgs ga) {
 // LDS rows are 128 bytes; 16-byte chunk k of row x sits in slot k ^ ((x >> 1) & 7), so the 16 rows
 // of one fragment read spread over the banks.
 // Requires C % 64 == 0, c_per % 64 == 0, ldw % 8 == 0 and 16-byte aligned act / wt.
+// MA: many adapters, one pass over the slice for every distinct adapter of the 128 tokens (as in
+// k_adapter_rows).
 template <int JT>
 struct RowsRing {
   static constexpr int TT = 128, JR = 16 * JT, NW = 8;
@@ -1048,12 +1104,13 @@ struct RowsRing {
 
 SRA_DEV int rows_swz(int x) { return (x >> 1) & 7; }
 
-template <int JT>
+template <int JT, bool MA = false>
 SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T, int64_t C,
                                     const uint16_t* __restrict__ wt, int64_t ldw, int r,
                                     int64_t c_per, double* __restrict__ part,
                                     float* __restrict__ out, double* __restrict__ out64,
-                                    uint16_t* __restrict__ vt, int rp, int64_t Tp) {
+                                    uint16_t* __restrict__ vt, int rp, int64_t Tp,
+                                    sra::AdapterIds ai = {}) {
   using RR = RowsRing<JT>;
   constexpr int NS = RR::NS, L = RR::L, NW = RR::NW;
   __shared__ __attribute__((aligned(16))) uint8_t smem[NS * RR::STAGE];
@@ -1066,8 +1123,11 @@ SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T,
 
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(act + t0 * C + cb), 0, (int)(((T - t0) * C - cb) * 2), 0x00020000);
-  const __amdgpu_buffer_rsrc_t rg = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(wt + (int64_t)j0 * ldw + cb), 0, (int)(((int64_t)(r - j0) * ldw - cb) * 2), 0x00020000);
+  auto weight_rsrc = [&](const uint16_t* w0) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(w0 + (int64_t)j0 * ldw + cb), 0,
+                                             (int)(((int64_t)(r - j0) * ldw - cb) * 2), 0x00020000);
+  };
+  __amdgpu_buffer_rsrc_t rg = weight_rsrc(wt);
   uint32_t a_off[RR::LA], g_off[RR::LG];
   int a_dst[RR::LA], g_dst[RR::LG];
 #pragma unroll
@@ -1136,9 +1196,6 @@ SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T,
   };
 
   constexpr int D = NS - 1;
-#pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (d < n_st) issue(d, d);
   auto step = [&](int st, f32x4 (&cur)[JT], f32x4 (&prev)[JT]) {
     wait_inflight<L, D>(min(D, n_st - st));
     ring_barrier();
@@ -1147,16 +1204,59 @@ SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T,
   };
   // two stages per iteration, so each accumulator set keeps its registers; stage 0 flushes the
   // zero-initialised second set
-  int st = 0;
-  for (; st + 1 < n_st; st += 2) {
-    step(st, acc[0], acc[1]);
-    step(st + 1, acc[1], acc[0]);
-  }
-  if (st < n_st) {
-    step(st, acc[0], acc[1]);
-    to64(acc[0]);
-  } else if (n_st > 0) {
-    to64(acc[1]);
+  auto pass = [&] {
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (d < n_st) issue(d, d);
+    int st = 0;
+    for (; st + 1 < n_st; st += 2) {
+      step(st, acc[0], acc[1]);
+      step(st + 1, acc[1], acc[0]);
+    }
+    if (st < n_st) {
+      step(st, acc[0], acc[1]);
+      to64(acc[0]);
+    } else if (n_st > 0) {
+      to64(acc[1]);
+    }
+  };
+  if constexpr (MA) {
+    const int id0 = t0 + lane < T ? ai.ids[t0 + lane] : -1, id1 = t0 + 64 + lane < T ? ai.ids[t0 + 64 + lane] : -1;
+    int idr[4];  // the tokens of this lane's sums: 16w + 4(l/16) + e
+#pragma unroll
+    for (int e = 0; e < 4; ++e) idr[e] = __shfl(w < 4 ? id0 : id1, 16 * (w & 3) + 4 * q4 + e, 64);
+    double own[JT][4];
+#pragma unroll
+    for (int a = 0; a < JT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) own[a][e] = 0.0;
+    uint64_t todo0 = __ballot(id0 >= 0 && id0 < ai.n), todo1 = __ballot(id1 >= 0 && id1 < ai.n);
+    while (todo0 | todo1) {  // the same sequence in every wave
+      const int g = todo0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(todo0))
+                          : __builtin_amdgcn_readlane(id1, __builtin_ctzll(todo1));
+      todo0 &= ~__ballot(id0 == g);
+      todo1 &= ~__ballot(id1 == g);
+      rg = weight_rsrc(wt + (int64_t)g * ai.stride);
+#pragma unroll
+      for (int a = 0; a < JT; ++a) {
+        acc[1][a] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc64[a][e] = 0.0;
+      }
+      __syncthreads();  // every wave is done with the previous pass's ring
+      pass();
+#pragma unroll
+      for (int a = 0; a < JT; ++a)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (idr[e] == g) own[a][e] = acc64[a][e];
+    }
+#pragma unroll
+    for (int a = 0; a < JT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc64[a][e] = own[a][e];
+  } else {
+    pass();
   }
 
   // D layout: tokens 16w + 4(l/16) + e, column j = 16a + l%16
@@ -1197,6 +1297,14 @@ __global__ __launch_bounds__(512) void k_adapter_rows_ring128(
     int64_t ldw, int r, int64_t c_per, double* __restrict__ part, float* __restrict__ out,
     double* __restrict__ out64, uint16_t* __restrict__ vt, int rp, int64_t Tp) {
   adapter_rows_ring_body<8>(act, T, C, wt, ldw, r, c_per, part, out, out64, vt, rp, Tp);
+}
+// many adapters: fp32 sums out (or fp64 slice partials)
+template <int JT>
+__global__ __launch_bounds__(512) void k_multi_rows_ring(const uint16_t* __restrict__ act, int64_t T, int64_t C,
+                                                         const uint16_t* __restrict__ wt, int64_t ldw, int r,
+                                                         int64_t c_per, double* __restrict__ part,
+                                                         float* __restrict__ out, sra::AdapterIds ai) {
+  adapter_rows_ring_body<JT, true>(act, T, C, wt, ldw, r, c_per, part, out, nullptr, nullptr, 0, 0, ai);
 }
 
 }  // namespace
@@ -1292,7 +1400,7 @@ hipError_t launch_adapter_rows(const uint16_t* act, int64_t T, int64_t C, const 
   }
   if (T <= 16 && !out64 && !vt && C % 8 == 0 && ldw % 8 == 0 && (((uintptr_t)act | (uintptr_t)wt) & 15) == 0) {
     launch(SRA_KERNEL_ADAPTER, k_adapter_rows_few, dim3((unsigned)cdiv(r, kFewJ), (unsigned)T),
-           dim3(256), 0, s, act, C, wt, ldw, r, out);
+           dim3(256), 0, s, act, C, wt, ldw, r, out, AdapterIds{});
     return hipGetLastError();
   }
   const int rp = (int)vt_rows(r);
@@ -1319,6 +1427,42 @@ hipError_t launch_adapter_rows(const uint16_t* act, int64_t T, int64_t C, const 
     default: rows_launch<4, 2>(grid, s, act, T, C, wt, ldw, r, p.c_per, part, out, out64, vt, rp, Tp); break;
   }
   if (p.S > 1) reduce_parts(part, p.S, T, r, out, out64, vt, rp, Tp, s);
+  return hipGetLastError();
+}
+
+// The rows products of many adapters: token t takes weight rows wt + ids[t] * stride.  The same
+// kernels and slices as one adapter's; their workspace is adapter_rows_ws.
+hipError_t launch_multi_rows(const uint16_t* act, int64_t T, int64_t C, const uint16_t* wt, int64_t ldw, int r,
+                             const AdapterIds& ai, float* out, void* ws, hipStream_t s) {
+  if (T == 0 || r == 0) return hipSuccess;
+  if (C == 0 || ai.n == 0) return launch_fill_f32(out, T * r, 0.f, s);
+  if (T <= 16 && C % 8 == 0 && ldw % 8 == 0) {
+    launch(SRA_KERNEL_ADAPTER, k_adapter_rows_few, dim3((unsigned)cdiv(r, kFewJ), (unsigned)T), dim3(256), 0, s,
+           act, C, wt, ldw, r, out, ai);
+    return hipGetLastError();
+  }
+  const RingPlan q = ring_plan(T, C, r);
+  const bool ring = ring_usable(q, act, wt, ldw, r) && ai.stride % 8 == 0;
+  const RowsPlan p = rows_plan(T, C, r);
+  const int S = ring ? q.S : p.S;
+  double* part = S > 1 ? (double*)ws : nullptr;
+  if (ring) {
+    const dim3 grid((unsigned)cdiv(T, 128), (unsigned)cdiv(r, q.jr), (unsigned)S);
+    if (q.jr == 64)
+      launch(SRA_KERNEL_ADAPTER, k_multi_rows_ring<4>, grid, dim3(512), 0, s, act, T, C, wt, ldw, r, q.c_per, part, out, ai);
+    else
+      launch(SRA_KERNEL_ADAPTER, k_multi_rows_ring<8>, grid, dim3(512), 0, s, act, T, C, wt, ldw, r, q.c_per, part, out, ai);
+  } else {
+    const dim3 grid((unsigned)cdiv(T, 16), (unsigned)cdiv(r, 16 * p.jt), (unsigned)S);
+#define SRA_MULTI_ROWS(JT, UB)                                                                                 \
+  launch(SRA_KERNEL_ADAPTER, k_adapter_rows<JT, UB, true>, grid, dim3(256), 0, s, act, T, C, wt, ldw, r, p.c_per, part, \
+         out, (double*)nullptr, (uint16_t*)nullptr, 0, (int64_t)0, ai)
+    if (p.jt == 1) SRA_MULTI_ROWS(1, 4);
+    else if (p.jt == 2) SRA_MULTI_ROWS(2, 4);
+    else SRA_MULTI_ROWS(4, 2);
+#undef SRA_MULTI_ROWS
+  }
+  if (S > 1) reduce_parts(part, S, T, r, out, nullptr, nullptr, 0, 0, s);
   return hipGetLastError();
 }
 

@@ -216,6 +216,14 @@ hipError_t launch_f32_tn(const float* Pf, const double* Pd, int64_t ldp, const f
                          float* Out, hipStream_t s);
 hipError_t launch_fill_f32(float* p, int64_t n, float v, hipStream_t s);
 
+// Which adapter each token takes, of n whose operands lie `stride` elements apart; an id outside
+// [0, n) takes none.
+struct AdapterIds {
+  const int32_t* ids = nullptr;
+  int64_t stride = 0;
+  int n = 0;
+};
+
 // bf16 2:4 SpMM with fused low-rank epilogue:
 //   Out[t][row] = sum_c Act[t][c] * S[row][c] + sum_j U[t][j] * E(row, j)
 struct Epilogue {
@@ -233,6 +241,9 @@ struct Epilogue {
   uint16_t* vt = nullptr;
   int vt_rp = 0;
   int64_t vt_tp = 0;
+  // Many adapters (the *_multi launchers): token t takes E + ids[t] * stride instead of E; U from
+  // memory only (no G).
+  AdapterIds ai;
 };
 // True when launch_spmm24_bf16 for this shape computes the adapter rows U itself (Epilogue::G);
 // the caller then skips the separate U kernel.
@@ -249,6 +260,12 @@ hipError_t launch_spmm_xp_bf16(int nm, bool tiled, const uint16_t* s_vals, const
 hipError_t launch_spmm24_bf16(const uint16_t* s_vals, const uint32_t* s_meta, int64_t R, int64_t C,
                               const uint16_t* act, int64_t T, const Epilogue& ep, uint16_t* out,
                               void* ws, hipStream_t s);
+// The same product with many adapters (Epilogue::ai), any C % 32 == 0; the workspace is
+// spmm24_multi_ws bytes.
+size_t spmm24_multi_ws(int64_t R, int64_t C, int64_t T);
+hipError_t launch_spmm24_multi_bf16(bool tiled, const uint16_t* s_vals, const uint32_t* s_meta, int64_t R,
+                                    int64_t C, const uint16_t* act, int64_t T, const Epilogue& ep,
+                                    uint16_t* out, void* ws, hipStream_t s);
 // the same product with the weight in the streaming layout (sra_nm_tile): any T when C % 128 == 0,
 // else T <= 16 only; ws holds the fp32 partials when the plan splits the reduction (spmm24_ws
 // bytes; without it the product runs unsplit)
@@ -268,6 +285,7 @@ hipError_t launch_nm_tile28_bf16(const uint16_t* s_vals, const uint32_t* s_meta,
 hipError_t launch_decode24_bf16(const uint16_t* s_vals, const uint32_t* s_meta, int64_t R,
                                 int64_t C, const uint16_t* act, int64_t T, const Epilogue& ep,
                                 uint16_t* out, hipStream_t s, bool tiled = false);
+// both decode kernels read Epilogue::ai when its ids are set
 // canonical 2:4 bf16 arrays -> the decode kernel's streaming layout (1 KB blocks per 16-row tile
 // and 64-column step, metadata per tile and 512-column batch)
 void nm_tile_bytes(int64_t R, int64_t C, size_t* value_bytes, size_t* meta_bytes);
@@ -319,6 +337,8 @@ hipError_t launch_adapter_bwd_prep(const uint16_t* B, int64_t N, int r, uint16_t
                                    const uint16_t* A, int64_t K, uint16_t* at, const float* U,
                                    int64_t T, uint16_t* vtU, hipStream_t s);
 size_t adapter_rows_ws(int64_t T, int64_t C, int r);
+hipError_t launch_multi_rows(const uint16_t* act, int64_t T, int64_t C, const uint16_t* wt, int64_t ldw, int r,
+                             const AdapterIds& ai, float* out, void* ws, hipStream_t s);
 hipError_t launch_adapter_rows(const uint16_t* act, int64_t T, int64_t C, const uint16_t* wt,
                                int64_t ldw, int r, float* out, double* out64, uint16_t* vt,
                                void* ws, hipStream_t s);
@@ -343,6 +363,39 @@ struct AdapterGradArgs {
   int64_t T, Tp, t_per;
   int r, rp, S;
 };
+// Gradients of many adapters (multi.hip).  Prep: the tokens sorted by adapter (gblk [n + 1], perm
+// [multi_perm_entries]; gblk == nullptr: not needed), B_g^T as wt [n][r][N] and A_g^T as
+// at [n][K][packed_at_ld(r)] (nullptr: not needed).
+struct MultiPrep {
+  const int32_t* ids = nullptr;
+  int64_t T = 0;
+  int n = 0, r = 0;
+  int32_t* gblk = nullptr;
+  int32_t* perm = nullptr;
+  const uint16_t* B = nullptr;
+  int64_t N = 0;
+  uint16_t* wt = nullptr;
+  const uint16_t* A = nullptr;
+  int64_t K = 0;
+  uint16_t* at = nullptr;
+};
+int multi_max_adapters();
+int64_t multi_perm_entries(int64_t T, int n);
+hipError_t launch_multi_prep(const MultiPrep& p, hipStream_t s);
+// One or two grouped products out_g = sum over g's tokens of act[t][:] V[t][:] (M % 8 == 0): act in
+// bf16, or as a checkpoint (act == nullptr); out [n][M][r], or [n][r][M] when out_t.
+struct MultiGrad {
+  const uint16_t* act = nullptr;
+  const int8_t* codes = nullptr;
+  const uint8_t* exps = nullptr;
+  const float* V = nullptr;
+  float* out = nullptr;
+  int64_t M = 0;
+  bool out_t = false;
+};
+hipError_t launch_multi_grads(const MultiGrad* g, int n_jobs, const int32_t* gblk, const int32_t* perm, int n, int r,
+                              hipStream_t s);
+
 // Layer norm over rows (layer_norm.hip), H <= 16384 (layer_norm_ok); codes != nullptr also writes the
 // output's 8-bit checkpoint.  The backward's workspace holds one partial row of dgamma and dbeta
 // per workgroup.

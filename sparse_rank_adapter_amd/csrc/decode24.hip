@@ -79,7 +79,11 @@ struct DecLds {
 // spare).  finish_tile() adds U E^T to row tile i's sums on v_mfma_f32_16x16x32_bf16 (U as bf16
 // hi + lo) and stores bf16 rows 4q .. 4q+3 of token l16; finish() first sums the NW waves' partial
 // tiles through LDS in wave order (deterministic), and row tile i is finished by wave i % NW.
-template <int FR, int NW, int PF = FR == 4 ? 0 : 2>
+// MA (many adapters): token l16 takes E + ids[token] * stride.  A row tile runs over the distinct
+// adapters of the (at most 16) tokens, kMaChunk at a time so that their E loads are in flight
+// together; an adapter's product takes U with the other adapters' tokens cleared.
+constexpr int kMaChunk = 4;
+template <int FR, int NW, bool MA = false, int PF = MA || FR == 4 ? 0 : 2>
 struct DecodeTail {
   const sra::Epilogue& ep;
   const int64_t R, T, row0;
@@ -87,6 +91,7 @@ struct DecodeTail {
   const bool tok_ok, e_vec, pf;
   u32x4 pf_e[2];
   float pf_u[2][8];
+  int id = -1;  // MA: the token's adapter
 
   SRA_DEV DecodeTail(const sra::Epilogue& ep_, int64_t R_, int64_t T_, int64_t row0_, int w_, int l_)
       : ep(ep_), R(R_), T(T_), row0(row0_), w(w_), l(l_), l16(l_ & 15), q(l_ >> 4), tok_ok(l16 < T_),
@@ -99,6 +104,67 @@ struct DecodeTail {
         load_u(32 * c + 8 * q, pf_u[c]);
       }
     }
+    if constexpr (MA) {
+      if (tok_ok) id = ep.ai.ids[l16];
+      if (id < 0 || id >= ep.ai.n) id = -1;
+    }
+  }
+  // row tile rt of many adapters: y += sum over the adapters
+  SRA_DEV f32x4 multi(f32x4 y, int64_t rt) const {
+    const bool row_ok = rt + l16 < R;
+    const int64_t row = (row_ok ? rt + l16 : 0) * ep.e_row_stride;
+    for (int jj = 0; jj < ep.r; jj += 32) {
+      const int jb = jj + 8 * q;
+      float u[8];
+      load_u(jb, u);
+      union UH { uint16_t h[8]; u32x4 v; bf16x8 b; } uhi, ulo;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) split_bf16(u[e], uhi.h[e], ulo.h[e]);
+      const bool vec = e_vec && jb + 8 <= ep.r;
+      uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xffffu;
+      while (todo) {
+        int g[kMaChunk];
+        u32x4 x[kMaChunk];
+#pragma unroll
+        for (int c = 0; c < kMaChunk; ++c) {
+          g[c] = -2;  // matches no token
+          x[c] = u32x4{0, 0, 0, 0};
+          if (todo) {
+            g[c] = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+            todo &= ~(uint32_t)__ballot(id == g[c]);
+            const uint16_t* E = ep.E + (int64_t)g[c] * ep.ai.stride + row;
+            if (row_ok) {
+              if (vec) {
+                x[c] = *reinterpret_cast<const u32x4*>(E + jb);
+              } else {
+                union { u32x4 v; uint16_t h[8]; } t;
+                t.v = u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (jb + e < ep.r) t.h[e] = E[jb + e];
+                x[c] = t.v;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kMaChunk; ++c) {
+          if (g[c] < 0) break;  // wave-uniform
+          const uint32_t keep = id == g[c] ? ~0u : 0u;
+          UH hi, lo;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            hi.v[k] = uhi.v[k] & keep;
+            lo.v[k] = ulo.v[k] & keep;
+          }
+          union { u32x4 v; bf16x8 b; } e;
+          e.v = x[c];
+          y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e.b, hi.b, y, 0, 0, 0);
+          y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e.b, lo.b, y, 0, 0, 0);
+        }
+      }
+    }
+    return y;
   }
   SRA_DEV u32x4 load_e(int64_t erow, int jb) const {
     union { u32x4 v; uint16_t h[8]; } x;
@@ -136,7 +202,9 @@ struct DecodeTail {
     const int64_t rt = row0 + 16 * i;
     if (rt >= R) return;
     // ---- adapter epilogue: A operand = E rows (row l16, j = 8q..), B operand = U^T (token l16)
-    if (ep.r > 0) {
+    if constexpr (MA) {
+      y = multi(y, rt);
+    } else if (ep.r > 0) {
       const bool first = pf && i == w;  // the prefetched tile
       for (int jj = 0; jj < ep.r; jj += 32) {
         const int jb = jj + 8 * q;
@@ -179,7 +247,7 @@ struct DecodeTail {
 // FR 16-row tiles per workgroup, NW waves splitting each batch's 8 steps (SPW each), OCC
 // workgroups per CU.  (3, 4): 48 rows, 3 per CU; (4, 4): 64 rows; (9, 8): 144 rows, one per CU,
 // which reads the Act block a third as often per weight byte.
-template <int FR, int NW, int OCC, bool TL>
+template <int FR, int NW, int OCC, bool TL, bool MA = false>
 __global__ __launch_bounds__(64 * NW, OCC) void k_decode24(const uint16_t* __restrict__ vals,
                                                           const uint32_t* __restrict__ meta, int64_t R,
                                                           int64_t C, const uint16_t* __restrict__ act,
@@ -283,7 +351,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_decode24(const uint16_t* __res
     }
   };
 
-  DecodeTail<FR, NW> tail(ep, R, T, row0, w, l);
+  DecodeTail<FR, NW, MA> tail(ep, R, T, row0, w, l);
 
   // Ping-pong over register batches; batches past the end are all-zero loads.  sched_barrier
   // keeps the compiler from sinking a batch's loads down to their first use.
@@ -348,7 +416,7 @@ struct Batch28 {
 // batch) block is 2 KB of values, chunk c of lane l at 1024 c + 16 l, then 512 bytes of metadata,
 // lane l's two words at 8 l, so each wave load reads 1 KB (or 512 bytes) contiguously and
 // non-temporally, and rows past R and columns past C hold zeros.
-template <int NW, int FW, int BW, int OCC, bool TL>
+template <int NW, int FW, int BW, int OCC, bool TL, bool MA = false>
 __global__ __launch_bounds__(64 * NW, OCC) void k_decode28(const uint16_t* __restrict__ vals,
                                                           const uint32_t* __restrict__ meta, int64_t R,
                                                           int64_t C, const uint16_t* __restrict__ act,
@@ -463,7 +531,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_decode28(const uint16_t* __res
     }
   };
 
-  DecodeTail<FR, NW, FW == 1 ? 0 : 2> tail(ep, R, T, row0, w, l);
+  DecodeTail<FR, NW, MA, MA || FW == 1 ? 0 : 2> tail(ep, R, T, row0, w, l);
 
   // ping-pong over register batches, as in the 2:4 kernel
   BT b0, b1;
@@ -611,9 +679,15 @@ hipError_t launch_decode24_bf16(const uint16_t* s_vals, const uint32_t* s_meta, 
   }
   if (tuning().decode_rows) fr = tuning().decode_rows;  // 3, 4 or 9 row tiles
   const unsigned grid = (unsigned)((R + 16 * fr - 1) / (16 * fr));
-#define SRA_DECODE_LAUNCH(F, NW, OCC, TLV)                                                     \
-  launch(SRA_KERNEL_DECODE24, k_decode24<F, NW, OCC, TLV>, dim3(grid), dim3(64 * NW), 0, s, s_vals, \
-         s_meta, R, C, act, T, ep, out)
+#define SRA_DECODE_LAUNCH(F, NW, OCC, TLV)                                                            \
+  do {                                                                                                \
+    if (ep.ai.ids)                                                                                    \
+      launch(SRA_KERNEL_DECODE24, k_decode24<F, NW, OCC, TLV, true>, dim3(grid), dim3(64 * NW), 0, s, \
+             s_vals, s_meta, R, C, act, T, ep, out);                                                  \
+    else                                                                                              \
+      launch(SRA_KERNEL_DECODE24, k_decode24<F, NW, OCC, TLV>, dim3(grid), dim3(64 * NW), 0, s,       \
+             s_vals, s_meta, R, C, act, T, ep, out);                                                  \
+  } while (0)
   if (tiled) {
     if (fr == 3) SRA_DECODE_LAUNCH(3, 4, 3, true);
     else if (fr == 4) SRA_DECODE_LAUNCH(4, 4, 3, true);
@@ -648,14 +722,19 @@ hipError_t launch_decode28_bf16(const uint16_t* s_vals, const uint32_t* s_meta, 
   else if (tuning().decode_rows == 3) pick = 3;
   const int rows = 16 * kShapes[pick][0] * kShapes[pick][1];
   const unsigned grid = (unsigned)((R + rows - 1) / rows);
-#define SRA_D28(NWV, FWV, BWV, OCCV)                                                             \
+#define SRA_D28T(NWV, FWV, BWV, OCCV, TLV)                                                         \
   do {                                                                                             \
-    if (tiled)                                                                                     \
-      launch(SRA_KERNEL_DECODE24, k_decode28<NWV, FWV, BWV, OCCV, true>, dim3(grid), dim3(64 * NWV), \
-             0, s, s_vals, s_meta, R, C, act, T, ep, out);                                           \
+    if (ep.ai.ids)                                                                                 \
+      launch(SRA_KERNEL_DECODE24, k_decode28<NWV, FWV, BWV, OCCV, TLV, true>, dim3(grid),          \
+             dim3(64 * NWV), 0, s, s_vals, s_meta, R, C, act, T, ep, out);                         \
     else                                                                                           \
-      launch(SRA_KERNEL_DECODE24, k_decode28<NWV, FWV, BWV, OCCV, false>, dim3(grid), dim3(64 * NWV), \
-             0, s, s_vals, s_meta, R, C, act, T, ep, out);                                           \
+      launch(SRA_KERNEL_DECODE24, k_decode28<NWV, FWV, BWV, OCCV, TLV>, dim3(grid), dim3(64 * NWV), \
+             0, s, s_vals, s_meta, R, C, act, T, ep, out);                                         \
+  } while (0)
+#define SRA_D28(NWV, FWV, BWV, OCCV)                \
+  do {                                              \
+    if (tiled) SRA_D28T(NWV, FWV, BWV, OCCV, true); \
+    else SRA_D28T(NWV, FWV, BWV, OCCV, false);      \
   } while (0)
   // (512-column batches, twice the bytes in flight per wave, measured no faster at the OPT-66B
   // FFN shape: 44.4 / 50.2 us against 44.1 / 49.6 us at T = 1 / 16)
@@ -666,6 +745,7 @@ hipError_t launch_decode28_bf16(const uint16_t* s_vals, const uint32_t* s_meta, 
     default: SRA_D28(3, 1, 256, 4); break;
   }
 #undef SRA_D28
+#undef SRA_D28T
   return hipGetLastError();
 }
 

@@ -71,7 +71,8 @@ struct Tile {
   };
 };
 
-template <int FR, int FT, int WR, int WT>
+// MA: many adapters (Epilogue::ai), one pass of the epilogue per distinct adapter of a wave's tokens.
+template <int FR, int FT, int WR, int WT, bool MA = false>
 __global__ __launch_bounds__(256, (Tile<FR, FT, WR, WT>::OCC)) void k_spmm24(
     const uint16_t* __restrict__ s_vals, const uint32_t* __restrict__ s_meta, int64_t R, int64_t C,
     const uint16_t* __restrict__ act, int64_t T, sra::Epilogue ep, uint16_t* __restrict__ out,
@@ -191,6 +192,28 @@ __global__ __launch_bounds__(256, (Tile<FR, FT, WR, WT>::OCC)) void k_spmm24(
   if (ep.r > 0 && z == 0) {
     const bool e_vec = ep.e_j_stride == 1 && (ep.r & 7) == 0;
     const bool u_vec = (ep.r & 7) == 0;
+    const uint16_t* E = ep.E;
+    int id[FT], cur = 0;
+    uint32_t todo[FT];
+    if constexpr (MA) {
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        const int64_t t = t0 + wt * 32 * FT + j * 32 + li;
+        id[j] = t < T ? ep.ai.ids[t] : -1;
+        todo[j] = (uint32_t)__ballot(id[j] >= 0 && id[j] < ep.ai.n);  // lanes 0 .. 31: the 32 tokens
+      }
+    }
+    auto next = [&]() -> bool {  // the next adapter's E, false when none is left (wave-uniform)
+      cur = -1;
+#pragma unroll
+      for (int j = FT - 1; j >= 0; --j)
+        if (todo[j]) cur = __builtin_amdgcn_readlane(id[j], __builtin_ctz(todo[j]));
+#pragma unroll
+      for (int j = 0; j < FT; ++j) todo[j] &= ~(uint32_t)__ballot(id[j] == cur);
+      if (cur >= 0) E = ep.E + (int64_t)cur * ep.ai.stride;
+      return cur >= 0;
+    };
+    for (bool more = !MA || next(); more; more = MA && next())
     for (int jj = 0; jj < ep.r; jj += 16) {
       const int jb = jj + 8 * g;
       bf16x8 ef[FR];
@@ -201,11 +224,11 @@ __global__ __launch_bounds__(256, (Tile<FR, FT, WR, WT>::OCC)) void k_spmm24(
         x.v = u32x4{0, 0, 0, 0};
         if (row < R) {
           if (e_vec && jb + 8 <= ep.r) {
-            x.v = *reinterpret_cast<const u32x4*>(ep.E + row * ep.e_row_stride + jb);
+            x.v = *reinterpret_cast<const u32x4*>(E + row * ep.e_row_stride + jb);
           } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              if (jb + q < ep.r) x.h[q] = ep.E[row * ep.e_row_stride + (int64_t)(jb + q) * ep.e_j_stride];
+              if (jb + q < ep.r) x.h[q] = E[row * ep.e_row_stride + (int64_t)(jb + q) * ep.e_j_stride];
           }
         }
         ef[i] = x.b;
@@ -216,7 +239,7 @@ __global__ __launch_bounds__(256, (Tile<FR, FT, WR, WT>::OCC)) void k_spmm24(
         float u[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) u[q] = 0.f;
-        if (t < T) {
+        if (t < T && (!MA || id[j] == cur)) {
           const float* up = ep.U + t * ep.r + jb;
           if (u_vec && jb + 8 <= ep.r) {
             const f32x4 a0 = *reinterpret_cast<const f32x4*>(up);
@@ -662,13 +685,13 @@ Plan plan_for(int64_t R, int64_t C, int64_t T) {
   return p;
 }
 
-template <int FR, int FT, int WR, int WT>
+template <int FR, int FT, int WR, int WT, bool MA = false>
 void launch_cfg(const uint16_t* s_vals, const uint32_t* s_meta, int64_t R, int64_t C,
                 const uint16_t* act, int64_t T, const sra::Epilogue& ep, uint16_t* out, float* part,
                 const Plan& p, hipStream_t s) {
   using TL = Tile<FR, FT, WR, WT>;
   const int n_rt = (int)((R + TL::BR - 1) / TL::BR), n_tt = (int)((T + TL::BT - 1) / TL::BT);
-  sra::launch(SRA_KERNEL_SPMM24, k_spmm24<FR, FT, WR, WT>,
+  sra::launch(SRA_KERNEL_SPMM24, k_spmm24<FR, FT, WR, WT, MA>,
               dim3((unsigned)(n_rt * n_tt), (unsigned)p.splits), dim3(256), 0, s, s_vals, s_meta, R,
               C, act, T, ep, out, part, n_rt, n_tt, p.stages_per_split);
 }
@@ -807,6 +830,71 @@ hipError_t launch_spmm24_bf16(const uint16_t* s_vals, const uint32_t* s_meta, in
     default: launch_cfg<2, 2, 2, 2>(s_vals, s_meta, R, C, act, T, ep, out, part, p, s); break;
   }
   if (p.splits > 1) finish_split(p, part, R, T, out, s);
+  return hipGetLastError();
+}
+
+// Many adapters.  The tile follows the one-adapter rule of plan_for on the tile counts: 256x256
+// once those fill the GPU twice, 256x128 once those fill it, else 128x64 (C % 128 == 0, metadata in
+// super-stages) or 256x64; C % 64 == 32 takes the register-staged 128x128.  Few tiles with a long
+// reduction split it (canonical arrays; whole 8-stage super-stages per split).
+namespace {
+struct MultiPlan {
+  int bt;  // tokens per tile: 256, 128 or 64; 0: the register-staged tile
+  Plan p;
+};
+MultiPlan multi_plan(int64_t R, int64_t C, int64_t T, bool tiled) {
+  MultiPlan m{0, Plan{cfg_by_id(3), 1, (int)((C + 63) / 64)}};
+  if (C % 64 != 0) return m;
+  auto tiles = [&](int br, int bt) { return ((R + br - 1) / br) * ((T + bt - 1) / bt); };
+  m.bt = tiles(256, 256) >= 512 ? 256 : tiles(256, 128) >= 240 ? 128 : 64;
+  const int64_t n = tiles(C % 128 == 0 ? 128 : 256, 64);
+  if (m.bt == 64 && !tiled && n < 240) {
+    const int nC = (int)(C / 64);
+    int s = (int)((256 + n - 1) / n);
+    if (s > nC / 8) s = nC / 8;  // keep >= 8 stages per split
+    if (s > 1) {
+      m.p.stages_per_split = ((nC + s - 1) / s + 7) / 8 * 8;
+      m.p.splits = (nC + m.p.stages_per_split - 1) / m.p.stages_per_split;
+    }
+  }
+  return m;
+}
+}  // namespace
+
+size_t spmm24_multi_ws(int64_t R, int64_t C, int64_t T) {
+  if (T <= 16 || R <= 0 || C <= 0) return 0;
+  const MultiPlan m = multi_plan(R, C, T, false);
+  return m.p.splits > 1 ? (size_t)m.p.splits * T * R * sizeof(float) : 0;
+}
+
+hipError_t launch_spmm24_multi_bf16(bool tiled, const uint16_t* s_vals, const uint32_t* s_meta, int64_t R,
+                                    int64_t C, const uint16_t* act, int64_t T, const Epilogue& ep, uint16_t* out,
+                                    void* ws, hipStream_t s) {
+  if (T == 0 || R == 0) return hipSuccess;
+  if (ep.G || !ep.ai.ids || !epilogue_ok(ep, R)) return hipErrorInvalidValue;
+  if (T <= 16) return launch_decode24_bf16(s_vals, s_meta, R, C, act, T, ep, out, s, tiled);
+  if (tiled && C % 128 != 0) return hipErrorInvalidValue;
+  const MultiPlan m = multi_plan(R, C, T, tiled);
+  float* part = m.p.splits > 1 ? (float*)ws : nullptr;
+#define SRA_MA(FR, FT, NS, MS, TLAYV) \
+  launch_q<FR, FT, 4, 2, NS, MS, 0, false, TLAYV, false, 0, 0, true>(s_vals, s_meta, R, C, act, T, ep, out, part, m.p, s)
+  if (tiled) {
+    if (m.bt == 256) SRA_MA(4, 8, 3, 4, true);
+    else if (m.bt == 128) SRA_MA(4, 4, 4, 8, true);
+    else SRA_MA(2, 2, 4, 8, true);
+  } else if (C % 128 == 0) {
+    if (m.bt == 256) SRA_MA(4, 8, 3, 4, false);
+    else if (m.bt == 128) SRA_MA(4, 4, 4, 8, false);
+    else SRA_MA(2, 2, 4, 8, false);
+  } else if (m.bt) {
+    if (m.bt == 256) SRA_MA(4, 8, 3, 0, false);
+    else if (m.bt == 128) SRA_MA(4, 4, 4, 0, false);
+    else SRA_MA(4, 2, 4, 0, false);
+  } else {
+    launch_cfg<2, 2, 2, 2, true>(s_vals, s_meta, R, C, act, T, ep, out, nullptr, m.p, s);
+  }
+#undef SRA_MA
+  if (part) finish_split(m.p, part, R, T, out, s);
   return hipGetLastError();
 }
 

@@ -284,8 +284,10 @@ struct QTile {
 // products; needs MS > 0.
 // FE > 0: s_vals holds the tiled fixed fan-in entries (ent_bytes bytes) and s_meta their list
 // offsets (sra_ffi_tile); C % 64 == 0, no splits.
+// MA: many adapters (Epilogue::ai), U from memory: the epilogue runs over the distinct adapters of
+// each wave's tokens.
 template <int FR, int FT, int WR, int WT, int NS, int MS = 0, int UG = 0, bool DN = false, bool TLAY = false,
-          bool PP = false, int NM = 0, int FE = 0>
+          bool PP = false, int NM = 0, int FE = 0, bool MA = false>
 __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN, NM, FE>::OCC)) void k_spmm24_q(
     const uint16_t* __restrict__ s_vals, const uint32_t* __restrict__ s_meta, int64_t R, int64_t C,
     const uint16_t* __restrict__ act, int64_t T, sra::Epilogue ep, uint16_t* __restrict__ out,
@@ -306,6 +308,7 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
   static_assert(NM == 0 || !DN, "an expanded N:M weight is not a dense one");
   static_assert(NM != 28 || (!TLAY && BR % (32 * NW) == 0), "2:8: canonical arrays, whole transfers");
   static_assert(FE == 0 || (!TLAY && !PP), "fixed fan-in entry lists: their own schedule");
+  static_assert(!MA || (UG == 0 && FE == 0 && NM == 0), "many adapters: 2:4 weights, U from memory");
   __shared__ __attribute__((aligned(16))) uint8_t smem[TL::LDS];
 
   const int tid = threadIdx.x;
@@ -880,13 +883,26 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
   // 16 tokens of a fragment read spread over the banks; each wave splits its fragments into bf16
   // hi + lo itself.
   constexpr bool kStageU = UG == 0 && BT * 512 <= TL::LDS && BT % (2 * NW) == 0;
+  static_assert(!MA || kStageU, "many adapters read U from LDS");
   if constexpr (kStageU) {
   if (ep.r > 0 && z == 0) {
+    // many adapters: the ids of this wave's tokens (token l16 of fragment j) and, per fragment,
+    // the tokens whose adapter is valid
+    int id[MA ? FT : 1];
+    uint32_t valid[MA ? FT : 1];
+    if constexpr (MA) {
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        const int tl = wt * 16 * FT + j * 16 + l16;
+        id[j] = tl < toks_here ? ep.ai.ids[t0 + tl] : -1;
+        valid[j] = (uint32_t)__ballot(id[j] >= 0 && id[j] < ep.ai.n) & 0xffffu;
+      }
+    }
     // E rows are contiguous in j (e_j_stride == 1, checked by the launchers): one 16-byte load
     // per fragment (eight 2-byte ones when rows are not 16-byte aligned) through a resource over
     // E's rows R, so rows past R read as zero; entries past r (the next row's, or padding) are
     // cleared after the load.
-    const __amdgpu_buffer_rsrc_t re = __builtin_amdgcn_make_buffer_rsrc(
+    __amdgpu_buffer_rsrc_t re = __builtin_amdgcn_make_buffer_rsrc(
         (void*)ep.E, 0, (int)(R * ep.e_row_stride * 2), 0x00020000);
     const bool e_al = (ep.e_row_stride & 7) == 0;  // 16-byte aligned fragments
     auto load_e = [&](int64_t row, int j0) {
@@ -927,6 +943,70 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
       wait_vm<0>();
       __syncthreads();
       const int nj = min(128, ep.r - jb0);
+      if constexpr (MA) {
+        // one step per distinct adapter and 32 adapter columns, the next step's E fragments in
+        // flight while a step multiplies; fragments with no token of the adapter are skipped, and
+        // the other tokens' U are cleared
+        uint32_t todo[FT];
+#pragma unroll
+        for (int j = 0; j < FT; ++j) todo[j] = valid[j];
+        auto next_adapter = [&]() {  // wave-uniform; -1 when none is left
+          int g = -1;
+#pragma unroll
+          for (int j = FT - 1; j >= 0; --j)
+            if (todo[j]) g = __builtin_amdgcn_readlane(id[j], __builtin_ctz(todo[j]));
+#pragma unroll
+          for (int j = 0; j < FT; ++j) todo[j] &= ~(uint32_t)__ballot(id[j] == g);
+          return g;
+        };
+        union EF { u32x4 v; bf16x8 b; };
+        EF e[FR], en[FR];
+        auto fetch = [&](int g, int jj, EF (&d)[FR]) {
+          re = __builtin_amdgcn_make_buffer_rsrc((void*)(ep.E + (int64_t)g * ep.ai.stride), 0,
+                                                 (int)(R * ep.e_row_stride * 2), 0x00020000);
+#pragma unroll
+          for (int i = 0; i < FR; ++i) d[i].v = load_e(row0 + wr * 16 * FR + i * 16 + l16, jb0 + jj + 8 * q4);
+        };
+        int g = next_adapter(), jj = 0;
+        if (g >= 0) fetch(g, 0, en);
+        while (g >= 0) {
+#pragma unroll
+          for (int i = 0; i < FR; ++i) e[i] = en[i];
+          int g2 = g, jj2 = jj + 32;
+          if (jj2 >= nj) {
+            g2 = next_adapter();
+            jj2 = 0;
+          }
+          if (g2 >= 0) fetch(g2, jj2, en);
+          const int c0 = (jj + 8 * q4) >> 2;
+#pragma unroll
+          for (int j = 0; j < FT; ++j) {
+            if (((uint32_t)__ballot(id[j] == g) & 0xffffu) == 0) continue;  // wave-uniform
+            const uint32_t keep = id[j] == g ? ~0u : 0u;
+            const int tl = wt * 16 * FT + j * 16 + l16, sw = tl & 31;
+            const f32x4 u0 = *reinterpret_cast<const f32x4*>(smem + tl * 512 + 16 * (c0 ^ sw));
+            const f32x4 u1 = *reinterpret_cast<const f32x4*>(smem + tl * 512 + 16 * ((c0 + 1) ^ sw));
+            union { uint16_t h[8]; uint32_t w[4]; bf16x8 b; } uhi, ulo;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              split_bf16(u0[q], uhi.h[q], ulo.h[q]);
+              split_bf16(u1[q], uhi.h[4 + q], ulo.h[4 + q]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uhi.w[q] &= keep;
+              ulo.w[q] &= keep;
+            }
+#pragma unroll
+            for (int i = 0; i < FR; ++i) {
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, uhi.b, acc[i][j], 0, 0, 0);
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, ulo.b, acc[i][j], 0, 0, 0);
+            }
+          }
+          g = g2;
+          jj = jj2;
+        }
+      } else
       for (int jj = 0; jj < nj; jj += 32) {
         const int c0 = (jj + 8 * q4) >> 2;
         union { u32x4 v; bf16x8 b; } e[FR];
@@ -1135,7 +1215,7 @@ struct Plan {
 };
 
 template <int FR, int FT, int WR, int WT, int NS, int MS = 0, int UG = 0, bool DN = false, bool TLAY = false,
-          bool PP = false, int NM = 0, int FE = 0>
+          bool PP = false, int NM = 0, int FE = 0, bool MA = false>
 void launch_q(const uint16_t* s_vals, const uint32_t* s_meta, int64_t R, int64_t C,
               const uint16_t* act, int64_t T, const sra::Epilogue& ep, uint16_t* out, float* part,
               const Plan& p, hipStream_t s, int which = SRA_KERNEL_SPMM24, uint32_t ent_bytes = 0) {
@@ -1143,7 +1223,7 @@ void launch_q(const uint16_t* s_vals, const uint32_t* s_meta, int64_t R, int64_t
   const int n_rt = (int)((R + TL::BR - 1) / TL::BR), n_tt = (int)((T + TL::BT - 1) / TL::BT);
   const int n = n_rt * n_tt, n_whole = p.tail ? n - n % 256 : -1;
   const dim3 grid = p.tail ? dim3((unsigned)(n_whole + 2 * (n - n_whole))) : dim3((unsigned)n, (unsigned)p.splits);
-  sra::launch(which, k_spmm24_q<FR, FT, WR, WT, NS, MS, UG, DN, TLAY, PP, NM, FE>, grid, dim3(64 * TL::NW), 0, s,
+  sra::launch(which, k_spmm24_q<FR, FT, WR, WT, NS, MS, UG, DN, TLAY, PP, NM, FE, MA>, grid, dim3(64 * TL::NW), 0, s,
               s_vals, s_meta, R, C, act, T, ep, out, part, n_rt, n_tt, p.stages_per_split, n_whole,
               ent_bytes);
 }
