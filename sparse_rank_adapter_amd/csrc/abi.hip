@@ -1137,7 +1137,7 @@ sra_status check_ids(const int32_t* ids, bool needed) {
 
 struct MultiPlan {
   size_t u_off = 0, du_off = 0, rows_off = 0, spmm_off = 0, meta_off = 0, v24_off = 0, x_off = 0;
-  size_t gblk_off = 0, perm_off = 0, wt_off = 0, at_off = 0, total = 0;
+  size_t gblk_off = 0, perm_off = 0, grads_off = 0, wt_off = 0, at_off = 0, total = 0;
 };
 void multi_weight_bytes(const sra_sparse* S, int64_t T, Arena* a, MultiPlan* p) {
   if (is12(S)) p->meta_off = a->take(meta_bytes(S));
@@ -1180,6 +1180,11 @@ size_t multi_bwd_plan(const sra_sparse* P, int64_t T, int32_t n, int32_t r, uint
   if (da || db) {
     p.gblk_off = a.take((size_t)(n + 1) * 4);
     p.perm_off = a.take((size_t)sra::multi_perm_entries(T, n) * 4);
+    sra::MultiGrad jobs[2];
+    int nj = 0;
+    if (db) jobs[nj++].M = N;
+    if (da) jobs[nj++].M = K;
+    p.grads_off = a.take(sra::multi_grads_ws(jobs, nj, T, n, r));
   }
   if (dx) multi_weight_bytes(P, T, &a, &p);
   p.total = a.used;
@@ -1349,7 +1354,8 @@ sra_status sra_multi_lora_bwd(const sra_sparse* P, const void* dY, const void* X
     jobs[nj].out_t = true;
     ++nj;
   }
-  SRA_TRY(hip_done(sra::launch_multi_grads(jobs, nj, prep.gblk, prep.perm, n_adapters, r, s), s, "multi bwd dB, dA"));
+  SRA_TRY(hip_done(sra::launch_multi_grads(jobs, nj, T, prep.gblk, prep.perm, n_adapters, r, wsb + plan.grads_off,
+                                           s), s, "multi bwd dB, dA"));
   if (!fdx) return SRA_OK;
   sra_sparse p24;
   SRA_TRY(on24(P, T, wsb, plan.meta_off, plan.v24_off, &p24, s));

@@ -1220,16 +1220,24 @@ SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T,
       to64(acc[1]);
     }
   };
+  // D layout: tokens 16w + 4(l/16) + e, column j = 16a + l%16
+  auto emit = [&](int a, int e, double s) {
+    const int j = j0 + 16 * a + l16;
+    const int64_t tt = t0 + 16 * w + 4 * q4 + e;
+    if (part) {
+      part[(int64_t)blockIdx.z * T * r + tt * r + j] = s;
+    } else {
+      if (out) out[tt * r + j] = (float)s;
+      if (out64) out64[tt * r + j] = s;
+      if (vt) write_vt3(vt, rp, Tp, j, tt, s);
+    }
+  };
   if constexpr (MA) {
+    // a pass writes the tokens of its adapter (keeping them until the last pass spilled registers)
     const int id0 = t0 + lane < T ? ai.ids[t0 + lane] : -1, id1 = t0 + 64 + lane < T ? ai.ids[t0 + 64 + lane] : -1;
     int idr[4];  // the tokens of this lane's sums: 16w + 4(l/16) + e
 #pragma unroll
     for (int e = 0; e < 4; ++e) idr[e] = __shfl(w < 4 ? id0 : id1, 16 * (w & 3) + 4 * q4 + e, 64);
-    double own[JT][4];
-#pragma unroll
-    for (int a = 0; a < JT; ++a)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) own[a][e] = 0.0;
     uint64_t todo0 = __ballot(id0 >= 0 && id0 < ai.n), todo1 = __ballot(id1 >= 0 && id1 < ai.n);
     while (todo0 | todo1) {  // the same sequence in every wave
       const int g = todo0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(todo0))
@@ -1249,17 +1257,17 @@ SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T,
       for (int a = 0; a < JT; ++a)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (idr[e] == g) own[a][e] = acc64[a][e];
+          if (idr[e] == g && j0 + 16 * a + l16 < r) emit(a, e, acc64[a][e]);
     }
 #pragma unroll
-    for (int a = 0; a < JT; ++a)
+    for (int e = 0; e < 4; ++e)
+      if ((idr[e] < 0 || idr[e] >= ai.n) && t0 + 16 * w + 4 * q4 + e < T)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc64[a][e] = own[a][e];
-  } else {
-    pass();
+        for (int a = 0; a < JT; ++a)
+          if (j0 + 16 * a + l16 < r) emit(a, e, 0.0);
+    return;
   }
-
-  // D layout: tokens 16w + 4(l/16) + e, column j = 16a + l%16
+  pass();
 #pragma unroll
   for (int a = 0; a < JT; ++a) {
     const int j = j0 + 16 * a + l16;
@@ -1274,14 +1282,7 @@ SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T,
           for (int p = 0; p < 3; ++p) vt[((int64_t)p * rp + j) * Tp + tt] = 0;
         continue;
       }
-      const double s = acc64[a][e];
-      if (part) {
-        part[(int64_t)blockIdx.z * T * r + tt * r + j] = s;
-      } else {
-        if (out) out[tt * r + j] = (float)s;
-        if (out64) out64[tt * r + j] = s;
-        if (vt) write_vt3(vt, rp, Tp, j, tt, s);
-      }
+      emit(a, e, acc64[a][e]);
     }
   }
 }

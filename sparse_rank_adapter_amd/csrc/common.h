@@ -393,8 +393,9 @@ struct MultiGrad {
   int64_t M = 0;
   bool out_t = false;
 };
-hipError_t launch_multi_grads(const MultiGrad* g, int n_jobs, const int32_t* gblk, const int32_t* perm, int n, int r,
-                              hipStream_t s);
+size_t multi_grads_ws(const MultiGrad* g, int n_jobs, int64_t T, int n, int r);
+hipError_t launch_multi_grads(const MultiGrad* g, int n_jobs, int64_t T, const int32_t* gblk, const int32_t* perm, int n,
+                              int r, void* ws, hipStream_t s);
 
 // Layer norm over rows (layer_norm.hip), H <= 16384 (layer_norm_ok); codes != nullptr also writes the
 // output's 8-bit checkpoint.  The backward's workspace holds one partial row of dgamma and dbeta

@@ -10,15 +10,24 @@
 //   the other workgroups transpose every B_g (the dU product's operand, contiguous along N) and
 //     every A_g (the dX epilogue's rows of r entries), in 64 x 64 tiles.
 //
-// k_multi_grads: a workgroup owns one adapter, 64 MF columns of dY or X and up to 128 adapter
-// columns, and walks over the adapter's blocks, so an output element is summed by one workgroup in
-// a fixed order and written once: no atomics and no partials.  A 32-token step gathers the tokens'
-// rows into LDS as they lie ([t][m], 16-byte chunks; an 8-bit checkpoint is decoded on the way,
-// exactly) and U or dU as three bf16 parts [part][j][t] that together carry its 24 bits (the sums
-// cancel, so V's rounding would be amplified).  The products are v_mfma_f32_16x16x32_bf16: A
-// operand V^T rows (16-byte LDS reads), B operand Act columns by ds_read_b64_tr_b16, the
-// transposing LDS read.  The next step's rows are in flight (registers) while a step multiplies;
-// two LDS buffers, one barrier per step.
+// The gradients are sums over an adapter's tokens of products of one Act value (dY or X, bf16, or an
+// 8-bit checkpoint decoded on the way, exactly) with one V value (U or dU, fp32, split into three
+// bf16 parts that together carry its 24 bits: the sums cancel, so V's rounding would be amplified).
+// The products are v_mfma_f32_16x16x32_bf16, 32 tokens a step: A operand V^T rows, B operand Act
+// columns by ds_read_b64_tr_b16, the transposing LDS read, from tiles that hold the tokens' gathered
+// rows as they lie ([t][m], swizzled 16-byte chunks).  Sums run in a fixed order; where an adapter's
+// tiles would leave most of the GPU idle, its tokens are cut into slices whose fp32 partials one
+// more launch adds in slice order.
+//
+// Ranks up to 32 (k_multi_grads_few) are bound by reading Act and by latency.  A workgroup owns one
+// adapter and 64 columns; its four waves take every fourth 32-token block, each through its own LDS
+// tile with no barrier, and join their sums at the end, so an adapter's chain of steps is a quarter
+// as long and 16 waves a CU keep loads in flight.  V is read and split by each wave itself.
+//
+// Larger ranks (k_multi_grads) are bound by the matrix cores and by LDS reads of V.  V is split once
+// (k_multi_vt) into tiles of 32 tokens in the sorted order, contiguous per step; a workgroup of
+// eight waves owns 256 columns and 64 or 128 adapter columns (wave: 64 adapter columns by 32 or 64
+// columns), stages both tiles through registers two steps ahead and double-buffers LDS.
 #include <algorithm>
 
 #include "rowvec.h"
@@ -157,7 +166,8 @@ struct GradJob {
   const int8_t* codes;   // its 8-bit checkpoint (act == nullptr)
   const uint8_t* exps;
   const float* V;        // [T][r]
-  float* out;            // [n][r][M] (out_t) or [n][M][r]
+  uint16_t* vt;          // its parts [block][3][rp][32], ranks above 32
+  float* out;            // [n][r][M] (out_t) or [n][M][r]; with slices, partials of slice 0
   int64_t M;
   int mb;                // column tiles
   bool out_t;
@@ -166,155 +176,340 @@ struct GradArgs {
   GradJob job[2];
   const int32_t* gblk;
   const int32_t* perm;
-  int r;
+  int n, r, rp;
+  int S;                 // slices of an adapter's blocks
+  int64_t slice;         // elements from one slice's partials to the next
 };
 
 typedef short v4s __attribute__((ext_vector_type(4)));
 SRA_DEV v4s lds_tr(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
 }
+union Bf8 {
+  __bf16 h[8];
+  u32x4 v;
+  bf16x8 b;
+  v4s half[2];
+};
+// x = a + b + c with bf16 parts (below fp32's rounding; the differences are exact)
+SRA_DEV void split3(float x, __bf16& a, __bf16& b, __bf16& c) {
+  a = (__bf16)x;
+  const float r1 = x - (float)a;
+  b = (__bf16)r1;
+  c = (__bf16)(r1 - (float)b);
+}
+// eight codes of a checkpoint as bf16: q 2^e is exact, so the high halves of the fp32 values are it
+SRA_DEV u32x4 decode8(uint32_t lo, uint32_t hi, uint32_t exp) {
+  float f[8];
+  sra_row::ck_decode<8>((uint64_t)lo | ((uint64_t)hi << 32), exp, f);
+  u32x4 x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = __builtin_amdgcn_perm(__float_as_uint(f[2 * k + 1]), __float_as_uint(f[2 * k]), 0x07060302u);
+  return x;
+}
 
-// chunk swizzle of the Act tile's token row t (8 chunks per row, or 16 and more): over the rows of
+// chunk swizzle of the Act tile's token row t (8 chunks of 16 bytes per row, or 32): over the rows of
 // one transposing read the 32-byte windows spread over the LDS banks
 template <int MT>
 SRA_DEV int act_swz(int t) {
   return MT == 64 ? 2 * (((t >> 1) ^ (t >> 3)) & 3) : 2 * ((t & 3) | (((t >> 3) & 1) << 2));
 }
+// B operand of 16 columns from m0 (a multiple of 16) of an Act tile [32][MT]
+template <int MT>
+SRA_DEV bf16x8 act_frag(const uint8_t* tile, int m0, int l16, int q4) {
+  Bf8 u;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int t = 8 * q4 + 4 * h + (l16 >> 2), col = m0 + 4 * (l16 & 3);
+    u.half[h] = lds_tr(tile + t * (2 * MT) + (((col >> 3) ^ act_swz<MT>(t)) << 4) + (col & 7) * 2);
+  }
+  return u.b;
+}
 
-template <int JT, int MF>
-struct GradTile {
-  static constexpr int JR = 16 * JT, MT = 64 * MF, AROW = MT * 2;
-  static constexpr int A_BYTES = 32 * AROW, V_BYTES = 3 * JR * 64, BUF = A_BYTES + V_BYTES;
-  static constexpr int NA = 32 * MT / 8 / 256;                // 16-byte Act chunks per thread
-  static constexpr int NV = (JR * 4 + 255) / 256;             // (adapter column, 8 tokens) pieces per thread
-};
+// blocks [lo, hi) of slice z of adapter g
+SRA_DEV void slice_of(const GradArgs& ga, int g, int z, int& lo, int& hi) {
+  const int b0 = ga.gblk[g], b1 = ga.gblk[g + 1], per = (b1 - b0 + ga.S - 1) / ga.S;
+  lo = min(b1, b0 + z * per);
+  hi = min(b1, lo + per);
+}
+// D layout: adapter column 4 (l / 16) + e, Act column l % 16
+SRA_DEV void grad_store(const GradArgs& ga, const GradJob& job, int g, int z, int j0, int64_t m0, const f32x4& c, int l16,
+                        int q4) {
+  const int64_t m = m0 + l16;
+  if (m >= job.M) return;
+  float* out = job.out + (int64_t)z * ga.slice;
+  const int j = j0 + 4 * q4;
+  if (!job.out_t) {
+    float* o = out + ((int64_t)g * job.M + m) * ga.r + j;
+    if ((ga.r & 3) == 0 && j + 4 <= ga.r) {
+      *reinterpret_cast<f32x4*>(o) = c;
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (j + e < ga.r) out[job.out_t ? ((int64_t)g * ga.r + j + e) * job.M + m : ((int64_t)g * job.M + m) * ga.r + j + e] = c[e];
+}
 
-template <int JT, int MF>
-__global__ __launch_bounds__(256) void k_multi_grads(GradArgs ga) {
-  using G = GradTile<JT, MF>;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * G::BUF];
-  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, l16 = l & 15, q4 = l >> 4;
+// ---- ranks up to 32
+template <int JT>
+__global__ __launch_bounds__(256) void k_multi_grads_few(GradArgs ga) {
+  constexpr int MT = 64, TILE = 32 * MT * 2;
+  constexpr int RED = 4 * JT * 4 * 64 * 16;  // the waves' sums: [wave][a][f][lane]
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RED > 4 * TILE ? RED : 4 * TILE];
+  const int tid = threadIdx.x, l = tid & 63, l16 = l & 15, q4 = l >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool second = (int)blockIdx.x >= ga.job[0].mb;
-  const GradJob& job = second ? ga.job[1] : ga.job[0];
-  const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * G::MT, M = job.M;
-  const int g = blockIdx.y, j0 = blockIdx.z * G::JR, r = ga.r;
-  const int b0 = ga.gblk[g], b1 = ga.gblk[g + 1];
+  const GradJob job = second ? ga.job[1] : ga.job[0];
+  const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * MT, M = job.M;
+  const int g = blockIdx.y, z = blockIdx.z, r = ga.r;
+  int b0, b1;
+  slice_of(ga, g, z, b0, b1);
   const int64_t nblk = (M + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
+  uint8_t* const tile = lds + w * TILE;
 
-  u32x4 ar[G::NA];       // bf16 chunks, or codes in the low half and the exponent
-  float vr[G::NV][8];
-  auto load = [&](int b) {
-    const int32_t* p = ga.perm + (int64_t)b * 32;
+  // a lane's share of a block: chunk l % 8 of rows l / 8 + 8 i, and V of adapter column l % 16 at the
+  // tokens 8 (l / 16) + e
+  const int c8 = l & 7, r8 = l >> 3;
+  const int64_t mc = m0 + 8 * c8;
+  const bool m_ok = mc < M;  // M % 8 == 0: a chunk is inside a row or past it
+  u32x4 ar[4];
+  float vr[JT][8];
+  auto perm_of = [&](int b) { return b < b1 ? ga.perm[(int64_t)b * 32 + (l & 31)] : -1; };
+  auto load = [&](int p) {  // p: lane l % 32 holds the block's token l % 32
 #pragma unroll
-    for (int i = 0; i < G::NA; ++i) {
-      const int v = tid + 256 * i, t = v / (G::MT / 8), c = v % (G::MT / 8);
-      const int64_t tok = p[t], m = m0 + 8 * c;
+    for (int i = 0; i < 4; ++i) {
+      const int64_t tok = __shfl(p, r8 + 8 * i, 64);
       ar[i] = u32x4{0, 0, 0, 0};
-      if (tok >= 0 && m < M) {  // M % 8 == 0: a chunk is inside a row or past it
+      if (tok >= 0 && m_ok) {
         if (job.act) {
-          ar[i] = *reinterpret_cast<const u32x4*>(job.act + tok * M + m);
+          ar[i] = *reinterpret_cast<const u32x4*>(job.act + tok * M + mc);
         } else {
-          const u32x2 q = *reinterpret_cast<const u32x2*>(job.codes + tok * M + m);
-          ar[i] = u32x4{q[0], q[1], job.exps[tok * nblk + m / sra_row::kCkBlock], 0};
+          const u32x2 q = *reinterpret_cast<const u32x2*>(job.codes + tok * M + mc);
+          ar[i] = u32x4{q[0], q[1], job.exps[tok * nblk + mc / sra_row::kCkBlock], 0};
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < G::NV; ++i) {
-      const int v = tid + 256 * i, j = v % G::JR, t8 = v / G::JR;
+    for (int e = 0; e < 8; ++e) {
+      const int64_t tok = __shfl(p, 8 * q4 + e, 64);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        vr[i][e] = 0.f;
-        if (t8 < 4 && j0 + j < r) {
-          const int64_t tok = p[8 * t8 + e];
-          if (tok >= 0) vr[i][e] = job.V[tok * r + j0 + j];
-        }
+      for (int a = 0; a < JT; ++a) {
+        const int j = 16 * a + l16;
+        vr[a][e] = tok >= 0 && j < r ? job.V[tok * r + j] : 0.f;
       }
     }
   };
-  auto store = [&](uint8_t* buf) {
-#pragma unroll
-    for (int i = 0; i < G::NA; ++i) {
-      const int v = tid + 256 * i, t = v / (G::MT / 8), c = v % (G::MT / 8);
-      u32x4 x = ar[i];
-      if (!job.act) {
-        float f[8];
-        sra_row::ck_decode<8>((uint64_t)ar[i][0] | ((uint64_t)ar[i][1] << 32), ar[i][2], f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)  // exact in bf16: the high halves are the values
-          x[k] = (__float_as_uint(f[2 * k]) >> 16) | (__float_as_uint(f[2 * k + 1]) & 0xffff0000u);
-      }
-      *reinterpret_cast<u32x4*>(buf + t * G::AROW + ((c ^ act_swz<G::MT>(t)) << 4)) = x;
-    }
-    uint8_t* vb = buf + G::A_BYTES;
-#pragma unroll
-    for (int i = 0; i < G::NV; ++i) {
-      const int v = tid + 256 * i, j = v % G::JR, t8 = v / G::JR;
-      if (t8 < 4) {
-        union { uint16_t h[8]; u32x4 v; } p[3];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) split3_bf16(vr[i][e], p[0].h[e], p[1].h[e], p[2].h[e]);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int x = k * G::JR + j;
-          *reinterpret_cast<u32x4*>(vb + x * 64 + ((t8 ^ ((x >> 2) & 3)) << 4)) = p[k].v;
-        }
-      }
-    }
-  };
-
-  f32x4 acc[JT][MF];
+  f32x4 acc[JT][4];
 #pragma unroll
   for (int a = 0; a < JT; ++a)
 #pragma unroll
-    for (int f = 0; f < MF; ++f) acc[a][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int fr = l16 >> 2, fs = l16 & 3;
-  auto compute = [&](const uint8_t* buf) {
-    bf16x8 bf[MF];
+    for (int f = 0; f < 4; ++f) acc[a][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  int p = perm_of(b0 + w), pn = perm_of(b0 + w + 4);
+  if (b0 + w < b1) load(p);
+  for (int b = b0 + w; b < b1; b += 4) {
+    p = pn;
+    pn = perm_of(b + 8);
 #pragma unroll
-    for (int f = 0; f < MF; ++f) {
-      union { v4s h[2]; bf16x8 b; } u;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = 8 * q4 + 4 * h + fr, col = (w * MF + f) * 16 + 4 * fs;
-        u.h[h] = lds_tr(buf + t * G::AROW + (((col >> 3) ^ act_swz<G::MT>(t)) << 4) + (col & 7) * 2);
-      }
-      bf[f] = u.b;
+    for (int i = 0; i < 4; ++i) {
+      const int t = r8 + 8 * i;
+      *reinterpret_cast<u32x4*>(tile + t * (2 * MT) + ((c8 ^ act_swz<MT>(t)) << 4)) =
+          job.act ? ar[i] : decode8(ar[i][0], ar[i][1], ar[i][2]);
     }
-    const uint8_t* vb = buf + G::A_BYTES;
+    Bf8 vf[JT][3];
 #pragma unroll
     for (int a = 0; a < JT; ++a)
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const int x = k * G::JR + 16 * a + l16;
-        const bf16x8 vf = *reinterpret_cast<const bf16x8*>(vb + x * 64 + ((q4 ^ ((x >> 2) & 3)) << 4));
+      for (int e = 0; e < 8; ++e) split3(vr[a][e], vf[a][0].h[e], vf[a][1].h[e], vf[a][2].h[e]);
+    if (b + 4 < b1) load(p);  // in flight while this block multiplies
 #pragma unroll
-        for (int f = 0; f < MF; ++f) acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, bf[f], acc[a][f], 0, 0, 0);
+    for (int f = 0; f < 4; ++f) {
+      const bf16x8 bf = act_frag<MT>(tile, 16 * f, l16, q4);  // this wave's own writes: in order
+#pragma unroll
+      for (int a = 0; a < JT; ++a)
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[a][k].b, bf, acc[a][f], 0, 0, 0);
+    }
+  }
+  // join: wave w finishes column fragment w, adding the waves in order
+  __syncthreads();
+  f32x4* const red = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+  for (int a = 0; a < JT; ++a)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) red[((w * JT + a) * 4 + f) * 64 + l] = acc[a][f];
+  __syncthreads();
+#pragma unroll
+  for (int a = 0; a < JT; ++a) {
+    f32x4 c = red[(a * 4 + w) * 64 + l];
+#pragma unroll
+    for (int k = 1; k < 4; ++k) c += red[((k * JT + a) * 4 + w) * 64 + l];
+    grad_store(ga, job, g, z, 16 * a, m0 + 16 * w, c, l16, q4);
+  }
+}
+
+// ---- ranks above 32
+// V in three parts, in the sorted order: tile b is [3][rp][32] bf16, zeros for padding and for
+// adapter columns past r.  grid: (blocks, jobs)
+__global__ __launch_bounds__(256) void k_multi_vt(GradArgs ga) {
+  const int b = blockIdx.x;
+  if (b >= ga.gblk[ga.n]) return;
+  const GradJob& job = ga.job[blockIdx.y];
+  const int32_t* p = ga.perm + (int64_t)b * 32;
+  uint16_t* vt = job.vt + (int64_t)b * 3 * ga.rp * 32;
+  for (int v = threadIdx.x; v < 4 * ga.rp; v += 256) {
+    const int t8 = v / ga.rp, j = v - t8 * ga.rp;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t tok = p[8 * t8 + e];
+      x[e] = tok >= 0 && j < ga.r ? job.V[tok * ga.r + j] : 0.f;
+    }
+    Bf8 s[3];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split3(x[e], s[0].h[e], s[1].h[e], s[2].h[e]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4*>(vt + ((int64_t)k * ga.rp + j) * 32 + 8 * t8) = s[k].v;
+  }
+}
+
+// WJ = 1: 64 adapter columns, 2: 128.  grid: (column tiles, adapters, adapter column tiles x slices)
+template <int WJ>
+__global__ __launch_bounds__(512) void k_multi_grads(GradArgs ga) {
+  constexpr int MT = 256, JR = 64 * WJ, MF = 2 * WJ;
+  constexpr int A_BYTES = 32 * MT * 2, V_BYTES = 3 * JR * 64, BUF = A_BYTES + V_BYTES;
+  constexpr int NV = (3 * JR * 4 + 511) / 512;  // 16-byte pieces of the V tile per thread
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BUF];
+  const int tid = threadIdx.x, l = tid & 63, l16 = l & 15, q4 = l >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wj = w % WJ, wm = w / WJ;
+  const bool second = (int)blockIdx.x >= ga.job[0].mb;
+  const GradJob job = second ? ga.job[1] : ga.job[0];
+  const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * MT, M = job.M;
+  const int g = blockIdx.y, njt = (ga.r + JR - 1) / JR, j0 = ((int)blockIdx.z % njt) * JR, z = (int)blockIdx.z / njt;
+  int b0, b1;
+  slice_of(ga, g, z, b0, b1);
+  const int64_t nblk = (M + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
+
+  // a thread's share of a step: bf16 chunk tid % 32 of rows tid / 32 and tid / 32 + 16, or 16 codes
+  // tid % 16 of row tid / 16; and NV pieces of the V tile
+  const bool bf = job.act != nullptr;
+  const int t0 = bf ? tid >> 5 : tid >> 4, cc = bf ? tid & 31 : tid & 15;
+  const int64_t mc = m0 + (bf ? 8 : 16) * cc;
+  const bool m_ok = mc < M;  // M % 32 == 0
+  struct Stage {
+    u32x4 a[2], v[NV];
+  };
+  struct Toks {
+    int p0, p1;
+  };
+  auto toks = [&](int b) {
+    Toks t{-1, -1};
+    if (b < b1) {
+      const int32_t* p = ga.perm + (int64_t)b * 32;
+      t.p0 = p[t0];
+      if (bf) t.p1 = p[t0 + 16];
+    }
+    return t;
+  };
+  auto load = [&](int b, const Toks& t, Stage& s) {
+    s.a[0] = s.a[1] = u32x4{0, 0, 0, 0};
+    if (bf) {
+      if (t.p0 >= 0 && m_ok) s.a[0] = *reinterpret_cast<const u32x4*>(job.act + (int64_t)t.p0 * M + mc);
+      if (t.p1 >= 0 && m_ok) s.a[1] = *reinterpret_cast<const u32x4*>(job.act + (int64_t)t.p1 * M + mc);
+    } else if (t.p0 >= 0 && m_ok) {
+      s.a[0] = *reinterpret_cast<const u32x4*>(job.codes + (int64_t)t.p0 * M + mc);
+      s.a[1][0] = job.exps[(int64_t)t.p0 * nblk + mc / sra_row::kCkBlock];
+    }
+    const uint16_t* vt = job.vt + (int64_t)b * 3 * ga.rp * 32;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tid + 512 * i, x = v >> 2, k = x / JR, j = j0 + x % JR;
+      s.v[i] = u32x4{0, 0, 0, 0};
+      if (x < 3 * JR && j < ga.rp) s.v[i] = *reinterpret_cast<const u32x4*>(vt + ((int64_t)k * ga.rp + j) * 32 + 8 * (v & 3));
+    }
+  };
+  auto store = [&](uint8_t* buf, const Stage& s) {
+    if (bf) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = t0 + 16 * i;
+        *reinterpret_cast<u32x4*>(buf + t * (2 * MT) + ((cc ^ act_swz<MT>(t)) << 4)) = s.a[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<u32x4*>(buf + t0 * (2 * MT) + (((2 * cc + i) ^ act_swz<MT>(t0)) << 4)) =
+            decode8(s.a[0][2 * i], s.a[0][2 * i + 1], s.a[1][0]);
+    }
+    uint8_t* vb = buf + A_BYTES;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tid + 512 * i, x = v >> 2;
+      if (x < 3 * JR) *reinterpret_cast<u32x4*>(vb + x * 64 + (((v & 3) ^ ((x >> 2) & 3)) << 4)) = s.v[i];
+    }
+  };
+  f32x4 acc[4][MF];
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int f = 0; f < MF; ++f) acc[a][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const uint8_t* buf) {
+    bf16x8 b[MF];
+#pragma unroll
+    for (int f = 0; f < MF; ++f) b[f] = act_frag<MT>(buf, (wm * MF + f) * 16, l16, q4);
+    const uint8_t* vb = buf + A_BYTES;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int x = k * JR + 64 * wj + 16 * a + l16;
+        const bf16x8 v = *reinterpret_cast<const bf16x8*>(vb + x * 64 + ((q4 ^ ((x >> 2) & 3)) << 4));
+#pragma unroll
+        for (int f = 0; f < MF; ++f) acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[f], acc[a][f], 0, 0, 0);
       }
   };
 
-  if (b0 < b1) load(b0);
-  for (int b = b0; b < b1; ++b) {
-    uint8_t* buf = lds + ((b - b0) & 1) * G::BUF;
-    store(buf);
-    __syncthreads();  // the buffer is written; every wave is done with the other one's last use
-    if (b + 1 < b1) load(b + 1);
+  // step b: its stage goes from registers to LDS, one barrier (every wave is then past its reads of
+  // the other buffer), the loads of step b + 2 are issued into the freed registers, and it multiplies
+  Stage s0, s1;
+  Toks tk = toks(b0);
+  if (b0 < b1) load(b0, tk, s0);
+  tk = toks(b0 + 1);
+  if (b0 + 1 < b1) load(b0 + 1, tk, s1);
+  tk = toks(b0 + 2);
+  auto step = [&](int b, Stage& s, uint8_t* buf) {
+    store(buf, s);
+    __syncthreads();
+    const Toks next = toks(b + 3);
+    if (b + 2 < b1) load(b + 2, tk, s);
+    tk = next;
     compute(buf);
+  };
+  int b = b0;
+  for (; b + 1 < b1; b += 2) {
+    step(b, s0, lds);
+    step(b + 1, s1, lds + BUF);
   }
+  if (b < b1) step(b, s0, lds);
 
-  // D layout: adapter column 4 (l / 16) + e of fragment a, Act column l % 16 of fragment f
 #pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    const int64_t m = m0 + (w * MF + f) * 16 + l16;
-    if (m >= M) continue;
+  for (int a = 0; a < 4; ++a)
 #pragma unroll
-    for (int a = 0; a < JT; ++a)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = j0 + 16 * a + 4 * q4 + e;
-        if (j < r) job.out[job.out_t ? ((int64_t)g * r + j) * M + m : ((int64_t)g * M + m) * r + j] = acc[a][f][e];
-      }
-  }
+    for (int f = 0; f < MF; ++f)
+      grad_store(ga, job, g, z, j0 + 64 * wj + 16 * a, m0 + (wm * MF + f) * 16, acc[a][f], l16, q4);
+}
+
+// out[i] = sum of the S slices' partials in slice order; both jobs' outputs one after the other
+__global__ void k_multi_join(const float* __restrict__ part, int64_t slice, int S, int64_t n0, int64_t n1,
+                             float* __restrict__ out0, float* __restrict__ out1) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n0 + n1) return;
+  float s = part[i];
+  for (int k = 1; k < S; ++k) s += part[(int64_t)k * slice + i];
+  if (i < n0) out0[i] = s;
+  else out1[i - n0] = s;
 }
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -349,43 +544,84 @@ hipError_t launch_multi_prep(const MultiPrep& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_multi_grads(const MultiGrad* g, int n_jobs, const int32_t* gblk, const int32_t* perm, int n, int r,
-                              hipStream_t s) {
+namespace {
+struct GradPlan {
+  bool few;
+  int mt, wj, S, njt;
+  int64_t vt, slice;  // bytes of one job's V parts, elements of one slice's partials
+};
+// Slices so that about 512 (few: four waves each) or 256 workgroups run, of at least 8 blocks of a
+// batch spread evenly over the adapters.
+GradPlan grad_plan(const MultiGrad* g, int n_jobs, int64_t T, int n, int r) {
+  GradPlan p{};
+  p.few = r <= 32;
+  p.mt = p.few ? 64 : 256;
+  p.wj = r <= 64 ? 1 : 2;
+  p.njt = p.few ? 1 : (int)cdiv64(r, 64 * p.wj);
+  int64_t tiles = 0;
+  for (int i = 0; i < n_jobs; ++i) {
+    tiles += cdiv64(g[i].M, p.mt);
+    p.slice += (int64_t)n * r * g[i].M;
+  }
+  const int64_t wg = tiles * n * p.njt;
+  int64_t S = wg > 0 ? (p.few ? 512 : 256) / wg : 1;
+  S = std::min<int64_t>(S, cdiv64(cdiv64(T, 32), n) / 8);
+  p.S = (int)std::max<int64_t>(1, S);
+  p.vt = p.few ? 0 : multi_perm_entries(T, n) * 3 * cdiv64(r, 16) * 16 * 2;
+  return p;
+}
+}  // namespace
+
+size_t multi_grads_ws(const MultiGrad* g, int n_jobs, int64_t T, int n, int r) {
+  const GradPlan p = grad_plan(g, n_jobs, T, n, r);
+  return (size_t)(((p.vt + 255) / 256 * 256) * n_jobs + (p.S > 1 ? p.S * p.slice * 4 : 0));
+}
+
+hipError_t launch_multi_grads(const MultiGrad* g, int n_jobs, int64_t T, const int32_t* gblk, const int32_t* perm, int n,
+                              int r, void* ws, hipStream_t s) {
   if (n_jobs <= 0 || r <= 0 || n <= 0) return hipSuccess;
+  const GradPlan p = grad_plan(g, n_jobs, T, n, r);
   GradArgs ga{};
   ga.gblk = gblk;
   ga.perm = perm;
+  ga.n = n;
   ga.r = r;
-  int64_t cols = 0;
-  for (int i = 0; i < n_jobs; ++i) cols += g[i].M;
-  const int jt = r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8;
-  const bool wide = cdiv64(cols, 128) * n >= 512;
-  const int mt = wide ? 128 : 64;
-  int64_t mb = 0;
+  ga.rp = (int)(cdiv64(r, 16) * 16);
+  ga.S = p.S;
+  ga.slice = p.slice;
+  uint8_t* at = (uint8_t*)ws;
+  int64_t mb = 0, done = 0;
+  float* part = (float*)(at + (p.vt + 255) / 256 * 256 * n_jobs);
   for (int i = 0; i < n_jobs; ++i) {
     GradJob& j = ga.job[i];
     j.act = g[i].act;
     j.codes = g[i].codes;
     j.exps = g[i].exps;
     j.V = g[i].V;
-    j.out = g[i].out;
+    j.vt = (uint16_t*)at;
+    at += (p.vt + 255) / 256 * 256;
+    j.out = p.S > 1 ? part + done : g[i].out;
+    done += (int64_t)n * r * g[i].M;
     j.M = g[i].M;
-    j.mb = (int)cdiv64(g[i].M, mt);
+    j.mb = (int)cdiv64(g[i].M, p.mt);
     j.out_t = g[i].out_t;
     mb += j.mb;
   }
   if (mb == 0) return hipSuccess;
-  const dim3 grid((unsigned)mb, (unsigned)n, (unsigned)cdiv64(r, 16 * jt));
-#define SRA_MG(JT)                                                                                    \
-  do {                                                                                                \
-    if (wide) launch(SRA_KERNEL_ADAPTER, k_multi_grads<JT, 2>, grid, dim3(256), 0, s, ga);             \
-    else launch(SRA_KERNEL_ADAPTER, k_multi_grads<JT, 1>, grid, dim3(256), 0, s, ga);                  \
-  } while (0)
-  if (jt == 1) SRA_MG(1);
-  else if (jt == 2) SRA_MG(2);
-  else if (jt == 4) SRA_MG(4);
-  else SRA_MG(8);
-#undef SRA_MG
+  const dim3 grid((unsigned)mb, (unsigned)n, (unsigned)(p.njt * p.S));
+  if (p.few) {
+    if (r <= 16) launch(SRA_KERNEL_ADAPTER, k_multi_grads_few<1>, grid, dim3(256), 0, s, ga);
+    else launch(SRA_KERNEL_ADAPTER, k_multi_grads_few<2>, grid, dim3(256), 0, s, ga);
+  } else {
+    hipLaunchKernelGGL(k_multi_vt, dim3((unsigned)(multi_perm_entries(T, n) / 32), (unsigned)n_jobs), dim3(256), 0, s, ga);
+    if (p.wj == 1) launch(SRA_KERNEL_ADAPTER, k_multi_grads<1>, grid, dim3(512), 0, s, ga);
+    else launch(SRA_KERNEL_ADAPTER, k_multi_grads<2>, grid, dim3(512), 0, s, ga);
+  }
+  if (p.S > 1) {
+    const int64_t n0 = (int64_t)n * r * g[0].M, n1 = n_jobs > 1 ? (int64_t)n * r * g[1].M : 0;
+    hipLaunchKernelGGL(k_multi_join, dim3((unsigned)cdiv64(n0 + n1, 256)), dim3(256), 0, s, part, p.slice, p.S, n0, n1,
+                       g[0].out, n_jobs > 1 ? g[1].out : nullptr);
+  }
   return hipGetLastError();
 }
 

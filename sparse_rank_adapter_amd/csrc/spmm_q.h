@@ -946,7 +946,26 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
       if constexpr (MA) {
         // one step per distinct adapter and 32 adapter columns, the next step's E fragments in
         // flight while a step multiplies; fragments with no token of the adapter are skipped, and
-        // the other tokens' U are cleared
+        // the other tokens' U are cleared.  U is split once per workgroup, in place (an fp32 word
+        // becomes hi | lo << 16): by every wave of a token column and for every adapter, the split
+        // took longer than the products
+        const int cs = nj > 64 ? 5 : nj > 32 ? 4 : nj > 16 ? 3 : 2;  // 2^cs chunks of 4 hold the nj columns
+        for (int i = tid; i < BT << cs; i += 64 * NW) {
+          const int tok = i >> cs, c = (i & ((1 << cs) - 1)) ^ (tok & 31);
+          u32x4* const p = reinterpret_cast<u32x4*>(smem + tok * 512 + c * 16);
+          const u32x4 v = *p;
+          u32x4 o;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float x = __uint_as_float(v[q]);
+            union { __bf16 b; uint16_t h; } hi, lo;
+            hi.b = (__bf16)x;
+            lo.b = (__bf16)(x - bf16_to_f32(hi.h));
+            o[q] = (uint32_t)hi.h | ((uint32_t)lo.h << 16);
+          }
+          *p = o;
+        }
+        __syncthreads();
         uint32_t todo[FT];
 #pragma unroll
         for (int j = 0; j < FT; ++j) todo[j] = valid[j];
@@ -984,18 +1003,15 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
             if (((uint32_t)__ballot(id[j] == g) & 0xffffu) == 0) continue;  // wave-uniform
             const uint32_t keep = id[j] == g ? ~0u : 0u;
             const int tl = wt * 16 * FT + j * 16 + l16, sw = tl & 31;
-            const f32x4 u0 = *reinterpret_cast<const f32x4*>(smem + tl * 512 + 16 * (c0 ^ sw));
-            const f32x4 u1 = *reinterpret_cast<const f32x4*>(smem + tl * 512 + 16 * ((c0 + 1) ^ sw));
-            union { uint16_t h[8]; uint32_t w[4]; bf16x8 b; } uhi, ulo;
+            const u32x4 u0 = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * (c0 ^ sw));
+            const u32x4 u1 = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * ((c0 + 1) ^ sw));
+            union { uint32_t w[4]; bf16x8 b; } uhi, ulo;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              split_bf16(u0[q], uhi.h[q], ulo.h[q]);
-              split_bf16(u1[q], uhi.h[4 + q], ulo.h[4 + q]);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uhi.w[q] &= keep;
-              ulo.w[q] &= keep;
+            for (int q = 0; q < 2; ++q) {  // low halves of two words, and their high halves
+              uhi.w[q] = __builtin_amdgcn_perm(u0[2 * q + 1], u0[2 * q], 0x05040100u) & keep;
+              ulo.w[q] = __builtin_amdgcn_perm(u0[2 * q + 1], u0[2 * q], 0x07060302u) & keep;
+              uhi.w[2 + q] = __builtin_amdgcn_perm(u1[2 * q + 1], u1[2 * q], 0x05040100u) & keep;
+              ulo.w[2 + q] = __builtin_amdgcn_perm(u1[2 * q + 1], u1[2 * q], 0x07060302u) & keep;
             }
 #pragma unroll
             for (int i = 0; i < FR; ++i) {
