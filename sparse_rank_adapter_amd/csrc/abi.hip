@@ -1147,11 +1147,11 @@ void multi_weight_bytes(const sra_sparse* S, int64_t T, Arena* a, MultiPlan* p) 
   }
   p->spmm_off = a->take(sra::spmm24_multi_ws(S->rows, S->cols, T));
 }
-size_t multi_fwd_plan(const sra_sparse* Ws, int64_t T, int32_t r, bool own_u, MultiPlan* plan) {
+size_t multi_fwd_plan(const sra_sparse* Ws, int64_t T, int32_t n, int32_t r, bool own_u, MultiPlan* plan) {
   MultiPlan p;
   Arena a;
   if (own_u) p.u_off = a.take((size_t)T * r * 4);
-  p.rows_off = a.take(sra::adapter_rows_ws(T, Ws->cols, r));
+  p.rows_off = a.take(sra::multi_rows_ws(T, Ws->cols, n, r));
   multi_weight_bytes(Ws, T, &a, &p);
   p.total = a.used;
   if (plan) *plan = p;
@@ -1167,18 +1167,18 @@ size_t multi_bwd_plan(const sra_sparse* P, int64_t T, int32_t n, int32_t r, uint
   size_t rows = 0;
   if (own_u) {
     p.u_off = a.take((size_t)T * r * 4);
-    rows = sra::adapter_rows_ws(T, K, r);
+    rows = sra::multi_rows_ws(T, K, n, r);
     if (!have_x) p.x_off = a.take((size_t)T * K * 2);  // the decoded checkpoint
   }
   if (need_du) {
     if (!have_du) p.du_off = a.take((size_t)T * r * 4);
-    p.wt_off = a.take((size_t)n * N * r * 2);
-    rows = std::max(rows, sra::adapter_rows_ws(T, N, r));
+    if (!sra::multi_rows_w_t(T, N, r)) p.wt_off = a.take((size_t)n * N * r * 2);
+    rows = std::max(rows, sra::multi_rows_ws(T, N, n, r));
   }
   p.rows_off = a.take(rows);
   if (dx && !(flags & SRA_DX_NO_ADAPTER)) p.at_off = a.take((size_t)n * K * sra::packed_at_ld(r) * 2);
   if (da || db) {
-    p.gblk_off = a.take((size_t)(n + 1) * 4);
+    p.gblk_off = a.take((size_t)(2 * n + 1) * 4);  // block starts, then the adapters' order
     p.perm_off = a.take((size_t)sra::multi_perm_entries(T, n) * 4);
     sra::MultiGrad jobs[2];
     int nj = 0;
@@ -1214,7 +1214,7 @@ sra_status sra_multi_fwd_workspace(const sra_sparse* Ws, int64_t T, int32_t n_ad
   SRA_TRY(check_multi(Ws, "Ws", T, n_adapters, r));
   SRA_TRY(check_multi_product(Ws, T));
   if (!bytes) return fail(SRA_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = multi_fwd_plan(Ws, T, r, true, nullptr);
+  *bytes = multi_fwd_plan(Ws, T, n_adapters, r, true, nullptr);
   return SRA_OK;
 }
 
@@ -1232,7 +1232,7 @@ sra_status sra_multi_lora_fwd(const sra_sparse* Ws, const void* X, int64_t T, co
   SRA_TRY(check_ptr(Y, any && N > 0, "Y"));
   if (U_out) SRA_TRY(check_ptr(U_out, true, "U_out"));
   MultiPlan plan;
-  multi_fwd_plan(Ws, T, r, U_out == nullptr, &plan);
+  multi_fwd_plan(Ws, T, n_adapters, r, U_out == nullptr, &plan);
   SRA_TRY(check_ws(ws, ws_bytes, plan.total));
   if (T == 0) return SRA_OK;
   const hipStream_t s = (hipStream_t)stream;
@@ -1246,10 +1246,11 @@ sra_status sra_multi_lora_fwd(const sra_sparse* Ws, const void* X, int64_t T, co
   ep.e_row_stride = r;
   ep.e_j_stride = 1;
   ep.r = r;
-  ep.ai = sra::AdapterIds{ids, N * (int64_t)r, n_adapters};
-  SRA_TRY(hip_done(sra::launch_multi_rows((const uint16_t*)X, T, K, (const uint16_t*)A, K, r,
-                                          sra::AdapterIds{ids, K * (int64_t)r, n_adapters}, U, wsb + plan.rows_off, s),
-                   s, "multi fwd U"));
+  ep.ai.ids = ids;
+  ep.ai.stride = N * (int64_t)r;
+  ep.ai.n = n_adapters;
+  SRA_TRY(hip_done(sra::launch_multi_rows((const uint16_t*)X, T, K, (const uint16_t*)A, false, r, ids, n_adapters, U,
+                                          wsb + plan.rows_off, s), s, "multi fwd U"));
   return multi_product(&w, X, T, ep, Y, wsb + plan.spmm_off, s, "multi fwd");
 }
 
@@ -1315,7 +1316,8 @@ sra_status sra_multi_lora_bwd(const sra_sparse* P, const void* dY, const void* X
     prep.gblk = (int32_t*)(wsb + plan.gblk_off);
     prep.perm = (int32_t*)(wsb + plan.perm_off);
   }
-  if (need_du) prep.wt = (uint16_t*)(wsb + plan.wt_off);
+  const bool b_t = sra::multi_rows_w_t(T, N, r);  // the dU product reads B_g as it lies
+  if (need_du && !b_t) prep.wt = (uint16_t*)(wsb + plan.wt_off);
   if (dx_ad) prep.at = (uint16_t*)(wsb + plan.at_off);
   SRA_TRY(hip_done(sra::launch_multi_prep(prep, s), s, "multi bwd prep"));
   void* rws = wsb + plan.rows_off;
@@ -1325,16 +1327,14 @@ sra_status sra_multi_lora_bwd(const sra_sparse* P, const void* dY, const void* X
       SRA_TRY(hip_done(sra::launch_ckpt_decode(SRA_BF16, X_codes, X_exps, T, K, wsb + plan.x_off, s), s, "multi bwd X"));
       x = (const uint16_t*)(wsb + plan.x_off);
     }
-    SRA_TRY(hip_done(sra::launch_multi_rows(x, T, K, (const uint16_t*)A, K, r,
-                                            sra::AdapterIds{ids, K * (int64_t)r, n_adapters},
+    SRA_TRY(hip_done(sra::launch_multi_rows(x, T, K, (const uint16_t*)A, false, r, ids, n_adapters,
                                             (float*)(wsb + plan.u_off), rws, s), s, "multi bwd U"));
     U = (const float*)(wsb + plan.u_off);
   }
   float* dU = dU_out ? dU_out : (float*)(wsb + plan.du_off);
   if (need_du)
-    SRA_TRY(hip_done(sra::launch_multi_rows((const uint16_t*)dY, T, N, prep.wt, N, r,
-                                            sra::AdapterIds{ids, N * (int64_t)r, n_adapters}, dU, rws, s),
-                     s, "multi bwd dU"));
+    SRA_TRY(hip_done(sra::launch_multi_rows((const uint16_t*)dY, T, N, b_t ? (const uint16_t*)B : prep.wt, b_t, r, ids,
+                                            n_adapters, dU, rws, s), s, "multi bwd dU"));
   sra::MultiGrad jobs[2];
   int nj = 0;
   if (fdb) {
@@ -1365,7 +1365,9 @@ sra_status sra_multi_lora_bwd(const sra_sparse* P, const void* dY, const void* X
   ep.e_row_stride = sra::packed_at_ld(r);
   ep.e_j_stride = 1;
   ep.r = dx_ad ? r : 0;
-  ep.ai = sra::AdapterIds{ids, K * sra::packed_at_ld(r), n_adapters};
+  ep.ai.ids = ids;
+  ep.ai.stride = K * sra::packed_at_ld(r);
+  ep.ai.n = n_adapters;
   return multi_product(&p24, dY, T, ep, dX, wsb + plan.spmm_off, s, "multi bwd dX");
 }
 

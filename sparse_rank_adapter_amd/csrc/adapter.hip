@@ -92,8 +92,10 @@ SRA_DEV u32x4 load8(const uint16_t* __restrict__ p, int64_t i, int64_t lim, bool
 // MA (many adapters): token t takes the weight rows of adapter ids[t], wt + ids[t] * stride, and a
 // token whose id is outside [0, n) gets zeros.  The pass over c runs once for every distinct
 // adapter of the workgroup's tokens (each wave finds the same sequence from the same ids) and a
-// token keeps the sums of its own adapter's pass.  Requests whose tokens follow each other cost
-// one pass nearly everywhere.
+// token keeps the sums of its own adapter's pass.  The grid holds ai.passes workgroups per tile and
+// slice (blockIdx.z = slice + S * pass): the first passes - 1 take one distinct adapter each, the
+// last the rest, so a tile where many short requests meet does not run them one after another.
+// Requests whose tokens follow each other cost one pass nearly everywhere.
 
 template <int JT, int UB, bool MA = false>
 __global__ __launch_bounds__(256) void k_adapter_rows(const uint16_t* __restrict__ act, int64_t T,
@@ -108,7 +110,8 @@ __global__ __launch_bounds__(256) void k_adapter_rows(const uint16_t* __restrict
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, lr = l & 15, lg = l >> 4;
   const int64_t t0 = (int64_t)blockIdx.x * 16, t = t0 + lr;
   const int j0 = blockIdx.y * 16 * JT;
-  const int64_t cb = (int64_t)blockIdx.z * c_per, ce = min(C, cb + c_per);
+  const int S = MA ? (int)gridDim.z / ai.passes : 0, z = MA ? (int)blockIdx.z % S : (int)blockIdx.z;
+  const int64_t cb = (int64_t)z * c_per, ce = min(C, cb + c_per);
   const int64_t nsteps = (ce - cb + 31) / 32;
   const int nb = (int)((nsteps + 4 * UB - 1) / (4 * UB));  // batches (same count for every wave)
   const bool a_vec = (C & 7) == 0, w_vec = (ldw & 7) == 0;
@@ -167,20 +170,26 @@ __global__ __launch_bounds__(256) void k_adapter_rows(const uint16_t* __restrict
       if (b + 1 < nb) compute(b + 1, fa1, fw1);
     }
   };
+  uint32_t mine = 0xfu;  // MA: which of this lane's four tokens this workgroup writes
   if constexpr (MA) {
+    const int my = (int)blockIdx.z / S, last = ai.passes - 1;
     const int id = t_ok ? ai.ids[t] : -1;
     int idr[4];  // the tokens of this lane's sums
 #pragma unroll
     for (int e = 0; e < 4; ++e) idr[e] = __shfl(id, 4 * lg + e, 64);
     double own[JT][4];
+    mine = 0;
 #pragma unroll
-    for (int a = 0; a < JT; ++a)
+    for (int e = 0; e < 4; ++e) {
+      if (my == 0 && (idr[e] < 0 || idr[e] >= ai.n)) mine |= 1u << e;  // no adapter: zeros, by the first pass
 #pragma unroll
-      for (int e = 0; e < 4; ++e) own[a][e] = 0.0;
+      for (int a = 0; a < JT; ++a) own[a][e] = 0.0;
+    }
     uint32_t todo = (uint32_t)__ballot(id >= 0 && id < ai.n) & 0xffffu;
-    while (todo) {
+    for (int k = 0; todo; ++k) {
       const int g = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
       todo &= ~(uint32_t)__ballot(id == g);
+      if (min(k, last) != my) continue;
 #pragma unroll
       for (int a = 0; a < JT; ++a) {
         const int j = j0 + 16 * a + lr;
@@ -190,15 +199,18 @@ __global__ __launch_bounds__(256) void k_adapter_rows(const uint16_t* __restrict
       }
       pass();
 #pragma unroll
-      for (int a = 0; a < JT; ++a)
+      for (int e = 0; e < 4; ++e)
+        if (idr[e] == g) {
+          mine |= 1u << e;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (idr[e] == g) own[a][e] = acc64[a][e];
+          for (int a = 0; a < JT; ++a) own[a][e] = acc64[a][e];
+        }
     }
 #pragma unroll
     for (int a = 0; a < JT; ++a)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc64[a][e] = own[a][e];
+    if (__ballot(mine != 0) == 0) return;  // the same in every wave: before any barrier
   } else {
     pass();
   }
@@ -238,10 +250,10 @@ __global__ __launch_bounds__(256) void k_adapter_rows(const uint16_t* __restrict
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t tt = t0 + 4 * lg + e;
-      if (tt >= T) continue;
+      if (tt >= T || !(mine & (1u << e))) continue;
       const double s = acc64[a][e];
       if (part) {
-        part[(int64_t)blockIdx.z * T * r + tt * r + j] = s;
+        part[(int64_t)z * T * r + tt * r + j] = s;
       } else {
         if (out) out[tt * r + j] = (float)s;
         if (out64) out64[tt * r + j] = s;
@@ -1090,8 +1102,6 @@ __global__ void k_reduce_grads(sra::AdapterGradArgs ga) {
 // LDS rows are 128 bytes; 16-byte chunk k of row x sits in slot k ^ ((x >> 1) & 7), so the 16 rows
 // of one fragment read spread over the banks.
 // Requires C % 64 == 0, c_per % 64 == 0, ldw % 8 == 0 and 16-byte aligned act / wt.
-// MA: many adapters, one pass over the slice for every distinct adapter of the 128 tokens (as in
-// k_adapter_rows).
 template <int JT>
 struct RowsRing {
   static constexpr int TT = 128, JR = 16 * JT, NW = 8;
@@ -1104,13 +1114,12 @@ struct RowsRing {
 
 SRA_DEV int rows_swz(int x) { return (x >> 1) & 7; }
 
-template <int JT, bool MA = false>
+template <int JT>
 SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T, int64_t C,
                                     const uint16_t* __restrict__ wt, int64_t ldw, int r,
                                     int64_t c_per, double* __restrict__ part,
                                     float* __restrict__ out, double* __restrict__ out64,
-                                    uint16_t* __restrict__ vt, int rp, int64_t Tp,
-                                    sra::AdapterIds ai = {}) {
+                                    uint16_t* __restrict__ vt, int rp, int64_t Tp) {
   using RR = RowsRing<JT>;
   constexpr int NS = RR::NS, L = RR::L, NW = RR::NW;
   __shared__ __attribute__((aligned(16))) uint8_t smem[NS * RR::STAGE];
@@ -1123,11 +1132,8 @@ SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T,
 
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(act + t0 * C + cb), 0, (int)(((T - t0) * C - cb) * 2), 0x00020000);
-  auto weight_rsrc = [&](const uint16_t* w0) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)(w0 + (int64_t)j0 * ldw + cb), 0,
-                                             (int)(((int64_t)(r - j0) * ldw - cb) * 2), 0x00020000);
-  };
-  __amdgpu_buffer_rsrc_t rg = weight_rsrc(wt);
+  const __amdgpu_buffer_rsrc_t rg = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(wt + (int64_t)j0 * ldw + cb), 0, (int)(((int64_t)(r - j0) * ldw - cb) * 2), 0x00020000);
   uint32_t a_off[RR::LA], g_off[RR::LG];
   int a_dst[RR::LA], g_dst[RR::LG];
 #pragma unroll
@@ -1196,6 +1202,9 @@ SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T,
   };
 
   constexpr int D = NS - 1;
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (d < n_st) issue(d, d);
   auto step = [&](int st, f32x4 (&cur)[JT], f32x4 (&prev)[JT]) {
     wait_inflight<L, D>(min(D, n_st - st));
     ring_barrier();
@@ -1204,70 +1213,19 @@ SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T,
   };
   // two stages per iteration, so each accumulator set keeps its registers; stage 0 flushes the
   // zero-initialised second set
-  auto pass = [&] {
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (d < n_st) issue(d, d);
-    int st = 0;
-    for (; st + 1 < n_st; st += 2) {
-      step(st, acc[0], acc[1]);
-      step(st + 1, acc[1], acc[0]);
-    }
-    if (st < n_st) {
-      step(st, acc[0], acc[1]);
-      to64(acc[0]);
-    } else if (n_st > 0) {
-      to64(acc[1]);
-    }
-  };
-  // D layout: tokens 16w + 4(l/16) + e, column j = 16a + l%16
-  auto emit = [&](int a, int e, double s) {
-    const int j = j0 + 16 * a + l16;
-    const int64_t tt = t0 + 16 * w + 4 * q4 + e;
-    if (part) {
-      part[(int64_t)blockIdx.z * T * r + tt * r + j] = s;
-    } else {
-      if (out) out[tt * r + j] = (float)s;
-      if (out64) out64[tt * r + j] = s;
-      if (vt) write_vt3(vt, rp, Tp, j, tt, s);
-    }
-  };
-  if constexpr (MA) {
-    // a pass writes the tokens of its adapter (keeping them until the last pass spilled registers)
-    const int id0 = t0 + lane < T ? ai.ids[t0 + lane] : -1, id1 = t0 + 64 + lane < T ? ai.ids[t0 + 64 + lane] : -1;
-    int idr[4];  // the tokens of this lane's sums: 16w + 4(l/16) + e
-#pragma unroll
-    for (int e = 0; e < 4; ++e) idr[e] = __shfl(w < 4 ? id0 : id1, 16 * (w & 3) + 4 * q4 + e, 64);
-    uint64_t todo0 = __ballot(id0 >= 0 && id0 < ai.n), todo1 = __ballot(id1 >= 0 && id1 < ai.n);
-    while (todo0 | todo1) {  // the same sequence in every wave
-      const int g = todo0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(todo0))
-                          : __builtin_amdgcn_readlane(id1, __builtin_ctzll(todo1));
-      todo0 &= ~__ballot(id0 == g);
-      todo1 &= ~__ballot(id1 == g);
-      rg = weight_rsrc(wt + (int64_t)g * ai.stride);
-#pragma unroll
-      for (int a = 0; a < JT; ++a) {
-        acc[1][a] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc64[a][e] = 0.0;
-      }
-      __syncthreads();  // every wave is done with the previous pass's ring
-      pass();
-#pragma unroll
-      for (int a = 0; a < JT; ++a)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (idr[e] == g && j0 + 16 * a + l16 < r) emit(a, e, acc64[a][e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if ((idr[e] < 0 || idr[e] >= ai.n) && t0 + 16 * w + 4 * q4 + e < T)
-#pragma unroll
-        for (int a = 0; a < JT; ++a)
-          if (j0 + 16 * a + l16 < r) emit(a, e, 0.0);
-    return;
+  int st = 0;
+  for (; st + 1 < n_st; st += 2) {
+    step(st, acc[0], acc[1]);
+    step(st + 1, acc[1], acc[0]);
   }
-  pass();
+  if (st < n_st) {
+    step(st, acc[0], acc[1]);
+    to64(acc[0]);
+  } else if (n_st > 0) {
+    to64(acc[1]);
+  }
+
+  // D layout: tokens 16w + 4(l/16) + e, column j = 16a + l%16
 #pragma unroll
   for (int a = 0; a < JT; ++a) {
     const int j = j0 + 16 * a + l16;
@@ -1282,7 +1240,14 @@ SRA_DEV void adapter_rows_ring_body(const uint16_t* __restrict__ act, int64_t T,
           for (int p = 0; p < 3; ++p) vt[((int64_t)p * rp + j) * Tp + tt] = 0;
         continue;
       }
-      emit(a, e, acc64[a][e]);
+      const double s = acc64[a][e];
+      if (part) {
+        part[(int64_t)blockIdx.z * T * r + tt * r + j] = s;
+      } else {
+        if (out) out[tt * r + j] = (float)s;
+        if (out64) out64[tt * r + j] = s;
+        if (vt) write_vt3(vt, rp, Tp, j, tt, s);
+      }
     }
   }
 }
@@ -1298,14 +1263,6 @@ __global__ __launch_bounds__(512) void k_adapter_rows_ring128(
     int64_t ldw, int r, int64_t c_per, double* __restrict__ part, float* __restrict__ out,
     double* __restrict__ out64, uint16_t* __restrict__ vt, int rp, int64_t Tp) {
   adapter_rows_ring_body<8>(act, T, C, wt, ldw, r, c_per, part, out, out64, vt, rp, Tp);
-}
-// many adapters: fp32 sums out (or fp64 slice partials)
-template <int JT>
-__global__ __launch_bounds__(512) void k_multi_rows_ring(const uint16_t* __restrict__ act, int64_t T, int64_t C,
-                                                         const uint16_t* __restrict__ wt, int64_t ldw, int r,
-                                                         int64_t c_per, double* __restrict__ part,
-                                                         float* __restrict__ out, sra::AdapterIds ai) {
-  adapter_rows_ring_body<JT, true>(act, T, C, wt, ldw, r, c_per, part, out, nullptr, nullptr, 0, 0, ai);
 }
 
 }  // namespace
@@ -1431,39 +1388,30 @@ hipError_t launch_adapter_rows(const uint16_t* act, int64_t T, int64_t C, const 
   return hipGetLastError();
 }
 
-// The rows products of many adapters: token t takes weight rows wt + ids[t] * stride.  The same
-// kernels and slices as one adapter's; their workspace is adapter_rows_ws.
-hipError_t launch_multi_rows(const uint16_t* act, int64_t T, int64_t C, const uint16_t* wt, int64_t ldw, int r,
-                             const AdapterIds& ai, float* out, void* ws, hipStream_t s) {
-  if (T == 0 || r == 0) return hipSuccess;
-  if (C == 0 || ai.n == 0) return launch_fill_f32(out, T * r, 0.f, s);
+// The rows products of many adapters on the small tiles: token t takes weight rows wt + ids[t] *
+// stride.  The same kernels and slices as one adapter's.
+size_t multi_rows_small_ws(int64_t T, int64_t C, int r) {
+  return T <= 0 || C <= 0 || r <= 0 ? 0 : rows_plan(T, C, r).part_bytes;
+}
+hipError_t launch_multi_rows_small(const uint16_t* act, int64_t T, int64_t C, const uint16_t* wt, int64_t ldw, int r,
+                                   AdapterIds ai, float* out, void* ws, hipStream_t s) {
   if (T <= 16 && C % 8 == 0 && ldw % 8 == 0) {
     launch(SRA_KERNEL_ADAPTER, k_adapter_rows_few, dim3((unsigned)cdiv(r, kFewJ), (unsigned)T), dim3(256), 0, s,
            act, C, wt, ldw, r, out, ai);
     return hipGetLastError();
   }
-  const RingPlan q = ring_plan(T, C, r);
-  const bool ring = ring_usable(q, act, wt, ldw, r) && ai.stride % 8 == 0;
   const RowsPlan p = rows_plan(T, C, r);
-  const int S = ring ? q.S : p.S;
-  double* part = S > 1 ? (double*)ws : nullptr;
-  if (ring) {
-    const dim3 grid((unsigned)cdiv(T, 128), (unsigned)cdiv(r, q.jr), (unsigned)S);
-    if (q.jr == 64)
-      launch(SRA_KERNEL_ADAPTER, k_multi_rows_ring<4>, grid, dim3(512), 0, s, act, T, C, wt, ldw, r, q.c_per, part, out, ai);
-    else
-      launch(SRA_KERNEL_ADAPTER, k_multi_rows_ring<8>, grid, dim3(512), 0, s, act, T, C, wt, ldw, r, q.c_per, part, out, ai);
-  } else {
-    const dim3 grid((unsigned)cdiv(T, 16), (unsigned)cdiv(r, 16 * p.jt), (unsigned)S);
+  double* part = p.S > 1 ? (double*)ws : nullptr;
+  ai.passes = ai.n < 4 ? ai.n : 4;
+  const dim3 grid((unsigned)cdiv(T, 16), (unsigned)cdiv(r, 16 * p.jt), (unsigned)(p.S * ai.passes));
 #define SRA_MULTI_ROWS(JT, UB)                                                                                 \
   launch(SRA_KERNEL_ADAPTER, k_adapter_rows<JT, UB, true>, grid, dim3(256), 0, s, act, T, C, wt, ldw, r, p.c_per, part, \
          out, (double*)nullptr, (uint16_t*)nullptr, 0, (int64_t)0, ai)
-    if (p.jt == 1) SRA_MULTI_ROWS(1, 4);
-    else if (p.jt == 2) SRA_MULTI_ROWS(2, 4);
-    else SRA_MULTI_ROWS(4, 2);
+  if (p.jt == 1) SRA_MULTI_ROWS(1, 4);
+  else if (p.jt == 2) SRA_MULTI_ROWS(2, 4);
+  else SRA_MULTI_ROWS(4, 2);
 #undef SRA_MULTI_ROWS
-  }
-  if (S > 1) reduce_parts(part, S, T, r, out, nullptr, nullptr, 0, 0, s);
+  if (p.S > 1) reduce_parts(part, p.S, T, r, out, nullptr, nullptr, 0, 0, s);
   return hipGetLastError();
 }
 

@@ -222,6 +222,7 @@ struct AdapterIds {
   const int32_t* ids = nullptr;
   int64_t stride = 0;
   int n = 0;
+  int passes = 1;  // rows kernels: workgroups that share a tile's distinct adapters
 };
 
 // bf16 2:4 SpMM with fused low-rank epilogue:
@@ -337,8 +338,9 @@ hipError_t launch_adapter_bwd_prep(const uint16_t* B, int64_t N, int r, uint16_t
                                    const uint16_t* A, int64_t K, uint16_t* at, const float* U,
                                    int64_t T, uint16_t* vtU, hipStream_t s);
 size_t adapter_rows_ws(int64_t T, int64_t C, int r);
-hipError_t launch_multi_rows(const uint16_t* act, int64_t T, int64_t C, const uint16_t* wt, int64_t ldw, int r,
-                             const AdapterIds& ai, float* out, void* ws, hipStream_t s);
+size_t multi_rows_small_ws(int64_t T, int64_t C, int r);
+hipError_t launch_multi_rows_small(const uint16_t* act, int64_t T, int64_t C, const uint16_t* wt, int64_t ldw, int r,
+                                   AdapterIds ai, float* out, void* ws, hipStream_t s);
 hipError_t launch_adapter_rows(const uint16_t* act, int64_t T, int64_t C, const uint16_t* wt,
                                int64_t ldw, int r, float* out, double* out64, uint16_t* vt,
                                void* ws, hipStream_t s);
@@ -382,6 +384,13 @@ struct MultiPrep {
 int multi_max_adapters();
 int64_t multi_perm_entries(int64_t T, int n);
 hipError_t launch_multi_prep(const MultiPrep& p, hipStream_t s);
+// Out[t][j] = sum_c act[t][c] W_g[j][c], g = ids[t] (zeros for a token without an adapter), W_g at
+// w + g * r * C as [r][C], or as [C][r] when w_t (only where multi_rows_w_t says so: else the caller
+// packs the transpose).
+bool multi_rows_w_t(int64_t T, int64_t C, int r);
+size_t multi_rows_ws(int64_t T, int64_t C, int n, int r);
+hipError_t launch_multi_rows(const uint16_t* act, int64_t T, int64_t C, const uint16_t* w, bool w_t, int r,
+                             const int32_t* ids, int n, float* out, void* ws, hipStream_t s);
 // One or two grouped products out_g = sum over g's tokens of act[t][:] V[t][:] (M % 8 == 0): act in
 // bf16, or as a checkpoint (act == nullptr); out [n][M][r], or [n][r][M] when out_t.
 struct MultiGrad {

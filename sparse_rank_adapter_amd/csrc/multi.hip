@@ -6,7 +6,9 @@
 // k_multi_prep, one launch for what the products need from ids, A and B:
 //   workgroup 0 sorts the tokens by adapter (a stable counting sort, so sums run in token order):
 //     adapter g's tokens fill blocks gblk[g] .. gblk[g+1]-1 of 32 entries of perm, the last block
-//     of each adapter padded with -1; tokens with no adapter are left out;
+//     of each adapter padded with ~(its last token), a negative number, so that padding loads the
+//     adapter's own data (its V is cleared); tokens with no adapter are left out; order holds the
+//     adapters by falling block count (up to 64 of them), so that the longest start first;
 //   the other workgroups transpose every B_g (the dU product's operand, contiguous along N) and
 //     every A_g (the dX epilogue's rows of r entries), in 64 x 64 tiles.
 //
@@ -40,7 +42,7 @@ struct PrepArgs {
   const int32_t* ids;  // nullptr: no sort
   int64_t T;
   int n;
-  int32_t* gblk;
+  int32_t* gblk;       // [n + 1], then the order [n]
   int32_t* perm;
   const uint16_t* B;  // [n][N][r] -> wt [n][r][N]; nullptr: none
   int64_t N;
@@ -55,6 +57,7 @@ struct SortLds {
   int hist[kPrepWaves][kMaxAdapters + 1];
   int base[kMaxAdapters + 1];
   int wsum[kPrepWaves];
+  int total;
 };
 struct TileLds {
   uint16_t t[64][66];
@@ -66,7 +69,7 @@ union PrepLds {
 
 SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
-  for (int i = tid; i < kPrepWaves * (kMaxAdapters + 1); i += kPrepThreads) (&s.hist[0][0])[i] = 0;
+  for (int i = l; i < a.n; i += 64) s.hist[w][i] = 0;  // wave w's own row
   __syncthreads();
   // wave w takes tokens [w * chunk, (w + 1) * chunk)
   const int64_t chunk = ((a.T + kPrepWaves - 1) / kPrepWaves + 63) / 64 * 64;
@@ -96,13 +99,24 @@ SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
   __syncthreads();
   for (int i = 0; i < w; ++i) incl += s.wsum[i];
   const int first = incl - blocks;
+  if (tid == kPrepThreads - 1) s.total = incl;
   if (tid < a.n) {
     s.base[tid] = first;
     a.gblk[tid] = first;
     if (tid == a.n - 1) a.gblk[a.n] = incl;
-    for (int p = cnt; p < 32 * blocks; ++p) a.perm[(int64_t)first * 32 + p] = -1;
   }
   __syncthreads();
+  if (tid < a.n) {
+    int rank = tid;
+    if (a.n <= 64) {  // by falling block count, ties by index (the bases' differences are the counts)
+      rank = 0;
+      for (int i = 0; i < a.n; ++i) {
+        const int b = (i + 1 < a.n ? s.base[i + 1] : s.total) - s.base[i];
+        rank += b > blocks || (b == blocks && i < tid);
+      }
+    }
+    a.gblk[a.n + 1 + rank] = tid;
+  }
   volatile int* const at = s.hist[w];  // this wave's running positions (only this wave uses them)
   for (int64_t t0 = lo; t0 < hi; t0 += 64) {
     const int64_t t = t0 + l;
@@ -118,12 +132,42 @@ SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
       if (l == lead) at[cur] = start + __popcll(same);
     }
   }
+  __syncthreads();  // this workgroup's perm is written (a barrier orders its own global writes)
+  if (tid < a.n && cnt < 32 * blocks) {
+    int32_t* const p = a.perm + (int64_t)first * 32;
+    const int32_t pad = ~p[cnt - 1];
+    for (int i = cnt; i < 32 * blocks; ++i) p[i] = pad;
+  }
 }
 
-// dst[y][x] = src[x][y] for one 64 x 64 tile (X x Y source, dst rows of stride ld)
+// dst[y][x] = src[x][y] for one 64 x 64 tile (X x Y source, dst rows of stride ld), 16 bytes a lane on
+// both sides where the rows allow (X, Y and ld multiples of 8: the matrices' bases are 16-byte aligned)
 SRA_DEV void transpose64(const uint16_t* __restrict__ src, int64_t X, int64_t Y, uint16_t* __restrict__ dst, int64_t ld,
                          int64_t x0, int64_t y0, TileLds& s) {
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  const bool vec = ((X | Y | ld) & 7) == 0;
+  const int tid = threadIdx.x;
+  if (vec) {
+    if (tid < 512) {
+      const int i = tid >> 3, c = tid & 7;
+      const int64_t x = x0 + i, y = y0 + 8 * c;
+      union { u32x4 v; uint32_t w[4]; } u;
+      u.v = u32x4{0, 0, 0, 0};
+      if (x < X && y < Y) u.v = *reinterpret_cast<const u32x4*>(src + x * Y + y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t*>(&s.t[i][8 * c + 2 * k]) = u.w[k];
+    }
+    __syncthreads();
+    if (tid < 512) {
+      const int i = tid >> 3, c = tid & 7;  // row y0 + i, columns x0 + 8 c ..
+      const int64_t y = y0 + i, x = x0 + 8 * c;
+      union { u32x4 v; uint16_t h[8]; } u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u.h[k] = s.t[8 * c + k][i];
+      if (y < Y && x < X) *reinterpret_cast<u32x4*>(dst + y * ld + x) = u.v;
+    }
+    return;
+  }
+  const int tx = tid & 63, ty = tid >> 6;
 #pragma unroll
   for (int k = 0; k < 64 / kPrepWaves; ++k) {
     const int i = ty + kPrepWaves * k;
@@ -262,7 +306,7 @@ __global__ __launch_bounds__(256) void k_multi_grads_few(GradArgs ga) {
   const bool second = (int)blockIdx.x >= ga.job[0].mb;
   const GradJob job = second ? ga.job[1] : ga.job[0];
   const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * MT, M = job.M;
-  const int g = blockIdx.y, z = blockIdx.z, r = ga.r;
+  const int g = ga.gblk[ga.n + 1 + blockIdx.y], z = blockIdx.z, r = ga.r;
   int b0, b1;
   slice_of(ga, g, z, b0, b1);
   const int64_t nblk = (M + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
@@ -271,32 +315,33 @@ __global__ __launch_bounds__(256) void k_multi_grads_few(GradArgs ga) {
   // a lane's share of a block: chunk l % 8 of rows l / 8 + 8 i, and V of adapter column l % 16 at the
   // tokens 8 (l / 16) + e
   const int c8 = l & 7, r8 = l >> 3;
-  const int64_t mc = m0 + 8 * c8;
-  const bool m_ok = mc < M;  // M % 8 == 0: a chunk is inside a row or past it
+  const int64_t mc = min(m0 + 8 * c8, M - 8);  // past the row: any columns, their sums are not stored
   u32x4 ar[4];
   float vr[JT][8];
-  auto perm_of = [&](int b) { return b < b1 ? ga.perm[(int64_t)b * 32 + (l & 31)] : -1; };
-  auto load = [&](int p) {  // p: lane l % 32 holds the block's token l % 32
+  auto perm_of = [&](int b) { return ga.perm[(int64_t)min(b, b1 - 1) * 32 + (l & 31)]; };
+  auto load = [&](int p) {  // p: lane l % 32 holds the block's token l % 32 (~token: padding)
+    const int tk = p ^ (p >> 31);
+    if (job.act) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t tok = __shfl(p, r8 + 8 * i, 64);
-      ar[i] = u32x4{0, 0, 0, 0};
-      if (tok >= 0 && m_ok) {
-        if (job.act) {
-          ar[i] = *reinterpret_cast<const u32x4*>(job.act + tok * M + mc);
-        } else {
-          const u32x2 q = *reinterpret_cast<const u32x2*>(job.codes + tok * M + mc);
-          ar[i] = u32x4{q[0], q[1], job.exps[tok * nblk + mc / sra_row::kCkBlock], 0};
-        }
+      for (int i = 0; i < 4; ++i)
+        ar[i] = *reinterpret_cast<const u32x4*>(job.act + (int64_t)__shfl(tk, r8 + 8 * i, 64) * M + mc);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t tok = __shfl(tk, r8 + 8 * i, 64);
+        const u32x2 q = *reinterpret_cast<const u32x2*>(job.codes + tok * M + mc);
+        ar[i] = u32x4{q[0], q[1], job.exps[tok * nblk + mc / sra_row::kCkBlock], 0};
       }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t tok = __shfl(p, 8 * q4 + e, 64);
+      const int q = __shfl(p, 8 * q4 + e, 64);
+      const int64_t tok = q ^ (q >> 31);
 #pragma unroll
       for (int a = 0; a < JT; ++a) {
         const int j = 16 * a + l16;
-        vr[a][e] = tok >= 0 && j < r ? job.V[tok * r + j] : 0.f;
+        const float v = job.V[tok * r + min(j, r - 1)];
+        vr[a][e] = q >= 0 && j < r ? v : 0.f;
       }
     }
   };
@@ -306,8 +351,12 @@ __global__ __launch_bounds__(256) void k_multi_grads_few(GradArgs ga) {
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[a][f] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  int p = perm_of(b0 + w), pn = perm_of(b0 + w + 4);
-  if (b0 + w < b1) load(p);
+  int p = 0, pn = 0;
+  if (b0 + w < b1) {
+    p = perm_of(b0 + w);
+    pn = perm_of(b0 + w + 4);
+    load(p);
+  }
   for (int b = b0 + w; b < b1; b += 4) {
     p = pn;
     pn = perm_of(b + 8);
@@ -351,104 +400,112 @@ __global__ __launch_bounds__(256) void k_multi_grads_few(GradArgs ga) {
 }
 
 // ---- ranks above 32
+template <int N>
+SRA_DEV void wait_vm_all() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+SRA_DEV void lds_dma(__amdgpu_buffer_rsrc_t rs, uint8_t* block, uint32_t off, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)block, 16, off, soff, 0, 0);
+}
+
 // V in three parts, in the sorted order: tile b is [3][rp][32] bf16, zeros for padding and for
-// adapter columns past r.  grid: (blocks, jobs)
+// adapter columns past r; 64 adapter columns per workgroup, gathered along r and written in whole
+// lines through LDS.  grid: (blocks, jobs, 64-column parts)
 __global__ __launch_bounds__(256) void k_multi_vt(GradArgs ga) {
-  const int b = blockIdx.x;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[3 * 64 * 32];
+  const int b = blockIdx.x, jb = blockIdx.z * 64, nj = min(64, ga.rp - jb);
   if (b >= ga.gblk[ga.n]) return;
   const GradJob& job = ga.job[blockIdx.y];
   const int32_t* p = ga.perm + (int64_t)b * 32;
+  const int jl = threadIdx.x & 63, j = jb + jl, t8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Bf8 s[3];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int q = p[8 * t8 + e];
+    const float v = job.V[(int64_t)(q ^ (q >> 31)) * ga.r + min(j, ga.r - 1)];
+    split3(q >= 0 && j < ga.r ? v : 0.f, s[0].h[e], s[1].h[e], s[2].h[e]);
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k)  // 16-byte piece t8 of row (k, jl), pieces swizzled against bank conflicts
+    *reinterpret_cast<u32x4*>(lds + ((k * 64 + jl) * 4 + (t8 ^ ((jl >> 2) & 3))) * 8) = s[k].v;
+  __syncthreads();
   uint16_t* vt = job.vt + (int64_t)b * 3 * ga.rp * 32;
-  for (int v = threadIdx.x; v < 4 * ga.rp; v += 256) {
-    const int t8 = v / ga.rp, j = v - t8 * ga.rp;
-    float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t tok = p[8 * t8 + e];
-      x[e] = tok >= 0 && j < ga.r ? job.V[tok * ga.r + j] : 0.f;
-    }
-    Bf8 s[3];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) split3(x[e], s[0].h[e], s[1].h[e], s[2].h[e]);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4*>(vt + ((int64_t)k * ga.rp + j) * 32 + 8 * t8) = s[k].v;
+  for (int k = 0; k < 3; ++k) {
+    const int row = threadIdx.x >> 2, c = threadIdx.x & 3;
+    if (row < nj)
+      *reinterpret_cast<u32x4*>(vt + ((int64_t)k * ga.rp + jb + row) * 32 + 8 * c) =
+          *reinterpret_cast<const u32x4*>(lds + ((k * 64 + row) * 4 + (c ^ ((row >> 2) & 3))) * 8);
   }
 }
 
-// WJ = 1: 64 adapter columns, 2: 128.  grid: (column tiles, adapters, adapter column tiles x slices)
+// WJ = 1: 64 adapter columns, 2: 128.  grid: (column tiles, adapters, adapter column tiles x slices).
+// The V tile goes to LDS by buffer -> LDS transfers, Act through registers (a checkpoint is decoded
+// there), both one step ahead; at most 128 registers and 80 KB of LDS, so two workgroups share a CU
+// and one's loads, LDS writes and barrier run under the other's products.
 template <int WJ>
-__global__ __launch_bounds__(512) void k_multi_grads(GradArgs ga) {
+__global__ __launch_bounds__(512, 4) void k_multi_grads(GradArgs ga) {
   constexpr int MT = 256, JR = 64 * WJ, MF = 2 * WJ;
   constexpr int A_BYTES = 32 * MT * 2, V_BYTES = 3 * JR * 64, BUF = A_BYTES + V_BYTES;
-  constexpr int NV = (3 * JR * 4 + 511) / 512;  // 16-byte pieces of the V tile per thread
+  constexpr int NV = V_BYTES / 1024;  // 1 KB transfers: 12 or 24
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BUF];
   const int tid = threadIdx.x, l = tid & 63, l16 = l & 15, q4 = l >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wj = w % WJ, wm = w / WJ;
   const bool second = (int)blockIdx.x >= ga.job[0].mb;
-  const GradJob job = second ? ga.job[1] : ga.job[0];
+  const GradJob& job = ga.job[second ? 1 : 0];
   const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * MT, M = job.M;
-  const int g = blockIdx.y, njt = (ga.r + JR - 1) / JR, j0 = ((int)blockIdx.z % njt) * JR, z = (int)blockIdx.z / njt;
+  const int g = ga.gblk[ga.n + 1 + blockIdx.y], njt = (ga.r + JR - 1) / JR, j0 = ((int)blockIdx.z % njt) * JR,
+            z = (int)blockIdx.z / njt;
   int b0, b1;
   slice_of(ga, g, z, b0, b1);
-  const int64_t nblk = (M + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
 
   // a thread's share of a step: bf16 chunk tid % 32 of rows tid / 32 and tid / 32 + 16, or 16 codes
-  // tid % 16 of row tid / 16; and NV pieces of the V tile
+  // tid % 16 of row tid / 16.  Every load is unconditional: columns past the row read its last ones
+  // (not stored), padding reads the adapter's last token (V is zero there).
   const bool bf = job.act != nullptr;
   const int t0 = bf ? tid >> 5 : tid >> 4, cc = bf ? tid & 31 : tid & 15;
-  const int64_t mc = m0 + (bf ? 8 : 16) * cc;
-  const bool m_ok = mc < M;  // M % 32 == 0
-  struct Stage {
-    u32x4 a[2], v[NV];
-  };
-  struct Toks {
-    int p0, p1;
-  };
+  const int64_t mc = min(m0 + (bf ? 8 : 16) * cc, M - (bf ? 8 : 16));
+  const uint8_t* const col = bf ? reinterpret_cast<const uint8_t*>(job.act + mc) : reinterpret_cast<const uint8_t*>(job.codes + mc);
+  const int64_t rowb = bf ? 2 * M : M, nblk = (M + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
+  const uint8_t* const ecol = job.exps + mc / sra_row::kCkBlock;
+  u32x4 a0, a1;
+  int p0, p1;
   auto toks = [&](int b) {
-    Toks t{-1, -1};
-    if (b < b1) {
-      const int32_t* p = ga.perm + (int64_t)b * 32;
-      t.p0 = p[t0];
-      if (bf) t.p1 = p[t0 + 16];
-    }
-    return t;
+    const int32_t* p = ga.perm + (int64_t)min(b, b1 - 1) * 32;
+    p0 = p[t0];
+    p1 = p[(t0 + 16) & 31];
   };
-  auto load = [&](int b, const Toks& t, Stage& s) {
-    s.a[0] = s.a[1] = u32x4{0, 0, 0, 0};
-    if (bf) {
-      if (t.p0 >= 0 && m_ok) s.a[0] = *reinterpret_cast<const u32x4*>(job.act + (int64_t)t.p0 * M + mc);
-      if (t.p1 >= 0 && m_ok) s.a[1] = *reinterpret_cast<const u32x4*>(job.act + (int64_t)t.p1 * M + mc);
-    } else if (t.p0 >= 0 && m_ok) {
-      s.a[0] = *reinterpret_cast<const u32x4*>(job.codes + (int64_t)t.p0 * M + mc);
-      s.a[1][0] = job.exps[(int64_t)t.p0 * nblk + mc / sra_row::kCkBlock];
-    }
-    const uint16_t* vt = job.vt + (int64_t)b * 3 * ga.rp * 32;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = tid + 512 * i, x = v >> 2, k = x / JR, j = j0 + x % JR;
-      s.v[i] = u32x4{0, 0, 0, 0};
-      if (x < 3 * JR && j < ga.rp) s.v[i] = *reinterpret_cast<const u32x4*>(vt + ((int64_t)k * ga.rp + j) * 32 + 8 * (v & 3));
-    }
+  auto load_act = [&]() {
+    const int64_t q0 = p0 ^ (p0 >> 31), q1 = p1 ^ (p1 >> 31);
+    a0 = *reinterpret_cast<const u32x4*>(col + q0 * rowb);
+    if (bf) a1 = *reinterpret_cast<const u32x4*>(col + q1 * rowb);
+    else a1[0] = ecol[q0 * nblk];
   };
-  auto store = [&](uint8_t* buf, const Stage& s) {
-    if (bf) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = t0 + 16 * i;
-        *reinterpret_cast<u32x4*>(buf + t * (2 * MT) + ((cc ^ act_swz<MT>(t)) << 4)) = s.a[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<u32x4*>(buf + t0 * (2 * MT) + (((2 * cc + i) ^ act_swz<MT>(t0)) << 4)) =
-            decode8(s.a[0][2 * i], s.a[0][2 * i + 1], s.a[1][0]);
+  auto store_act = [&](uint8_t* buf) {
+    u32x4 x0 = a0, x1 = a1;
+    if (!bf) {
+      x0 = decode8(a0[0], a0[1], a1[0]);
+      x1 = decode8(a0[2], a0[3], a1[0]);
     }
-    uint8_t* vb = buf + A_BYTES;
+    const int r1 = bf ? t0 + 16 : t0, c0 = bf ? cc : 2 * cc, c1 = bf ? cc : 2 * cc + 1;
+    *reinterpret_cast<u32x4*>(buf + t0 * (2 * MT) + ((c0 ^ act_swz<MT>(t0)) << 4)) = x0;
+    *reinterpret_cast<u32x4*>(buf + r1 * (2 * MT) + ((c1 ^ act_swz<MT>(r1)) << 4)) = x1;
+  };
+  // V: transfer k of 16 rows of 64 bytes; rows past rp read as zeros or another part's (not stored)
+  const int vtile = 3 * ga.rp * 64;
+  uint32_t v_off[(NV + 7) / 8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = tid + 512 * i, x = v >> 2;
-      if (x < 3 * JR) *reinterpret_cast<u32x4*>(vb + x * 64 + (((v & 3) ^ ((x >> 2) & 3)) << 4)) = s.v[i];
-    }
+  for (int i = 0; i < (NV + 7) / 8; ++i) {
+    const int x = 16 * (8 * i + w) + (l >> 2), c = (l & 3) ^ ((x >> 2) & 3), k = x / JR, j = j0 + x % JR;
+    v_off[i] = (uint32_t)((k * ga.rp + j) * 64 + 16 * c);
+  }
+  auto issue_v = [&](int b, uint8_t* buf) {
+    const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(job.vt + (int64_t)b * 3 * ga.rp * 32), 0, vtile, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < (NV + 7) / 8; ++i)
+      if (8 * i + 8 <= NV || 8 * i + w < NV) lds_dma(rv, buf + A_BYTES + (8 * i + w) * 1024, v_off[i], 0);
   };
   f32x4 acc[4][MF];
 #pragma unroll
@@ -471,28 +528,27 @@ __global__ __launch_bounds__(512) void k_multi_grads(GradArgs ga) {
       }
   };
 
-  // step b: its stage goes from registers to LDS, one barrier (every wave is then past its reads of
-  // the other buffer), the loads of step b + 2 are issued into the freed registers, and it multiplies
-  Stage s0, s1;
-  Toks tk = toks(b0);
-  if (b0 < b1) load(b0, tk, s0);
-  tk = toks(b0 + 1);
-  if (b0 + 1 < b1) load(b0 + 1, tk, s1);
-  tk = toks(b0 + 2);
-  auto step = [&](int b, Stage& s, uint8_t* buf) {
-    store(buf, s);
-    __syncthreads();
-    const Toks next = toks(b + 3);
-    if (b + 2 < b1) load(b + 2, tk, s);
-    tk = next;
-    compute(buf);
-  };
-  int b = b0;
-  for (; b + 1 < b1; b += 2) {
-    step(b, s0, lds);
-    step(b + 1, s1, lds + BUF);
+  // step b: its Act goes from registers to LDS, one barrier (every wave is then past its reads of
+  // the other buffer, and step b's transfers have landed), the loads of step b + 1 are issued, and
+  // it multiplies
+  if (b0 < b1) {
+    toks(b0);
+    load_act();
+    issue_v(b0, lds);
+    toks(b0 + 1);
   }
-  if (b < b1) step(b, s0, lds);
+  for (int b = b0; b < b1; ++b) {
+    uint8_t* const buf = lds + ((b - b0) & 1) * BUF;
+    store_act(buf);
+    wait_vm_all<0>();
+    __syncthreads();
+    if (b + 1 < b1) {
+      load_act();
+      issue_v(b + 1, lds + ((b + 1 - b0) & 1) * BUF);
+      toks(b + 2);
+    }
+    compute(buf);
+  }
 
 #pragma unroll
   for (int a = 0; a < 4; ++a)
@@ -512,6 +568,163 @@ __global__ void k_multi_join(const float* __restrict__ part, int64_t slice, int 
   else out1[i - n0] = s;
 }
 
+// ------------------------------------------------------------------------------------ rows
+// Out[t][j] = sum_c act[t][c] W_g[j][c] for ranks above 32: a workgroup owns 128 tokens and JR
+// adapter columns over a slice of c, in 64-column stages; both operands stream through a two-stage
+// LDS ring filled by buffer -> LDS transfers.  64 KB of LDS and at most 128 registers, so two
+// workgroups share a CU and one's transfers run under the other's products.  Eight waves: four of
+// 32 tokens by two of JR / 2 adapter columns.
+// TW: the weight is given as [C][r] (B_g as it lies) and its stage [64][JR] is read with the
+// transposing LDS read; else as [r][C].
+// A tile whose tokens take several adapters runs one pass per distinct adapter and writes the tokens
+// of that adapter after it; the grid holds `passes` workgroups per tile (as k_adapter_rows), the last
+// of them taking what the others leave.
+template <int JR, bool TW>
+__global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restrict__ act, int64_t T, int64_t C,
+                                                       const uint16_t* __restrict__ wgt, int r, int64_t c_per, int S,
+                                                       float* __restrict__ part, float* __restrict__ out,
+                                                       sra::AdapterIds ai) {
+  constexpr int A_BYTES = 128 * 128, G_BYTES = JR * 128, STAGE = A_BYTES + G_BYTES, JW = JR / 32;
+  constexpr int LA = A_BYTES / 8192, LG = G_BYTES / 8192;  // 1 KB transfers per wave
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wt = w & 3, wj = w >> 2;
+  // workgroups go to the 8 XCDs in turn: XCD x takes an eighth of the (slice, adapter column tile,
+  // token tile) list in one piece, so the token tiles that read the same weight slice share its L2
+  const int n_tt = (int)((T + 127) / 128), n_jt = (r + JR - 1) / JR, n_wg = n_tt * n_jt * S;
+  const int my = (int)blockIdx.x / n_wg, last = ai.passes - 1;
+  const int id = (int)blockIdx.x % n_wg, xcd = id & 7, per = n_wg >> 3, rem = n_wg & 7;
+  const int lin = xcd * per + min(xcd, rem) + (id >> 3);
+  const int64_t t0 = (int64_t)(lin % n_tt) * 128;
+  const int j0 = lin / n_tt % n_jt * JR, z = lin / n_tt / n_jt;
+  const int64_t cb = (int64_t)z * c_per, ce = min(C, cb + c_per);
+  const int n_st = (int)((ce - cb) / 64), toks = (int)min((int64_t)128, T - t0);
+
+  const __amdgpu_buffer_rsrc_t ra =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(act + t0 * C + cb), 0, (int)((toks * C - cb) * 2), 0x00020000);
+  auto swz = [](int x) { return (x >> 1) & 7; };
+  uint32_t a_off[LA], g_off[LG];
+#pragma unroll
+  for (int k = 0; k < LA; ++k) {  // 8 rows of 128 bytes
+    const int x = 8 * (k * 8 + w) + (lane >> 3), c = (lane & 7) ^ swz(x);
+    a_off[k] = (uint32_t)((x * C + c * 8) * 2);
+  }
+#pragma unroll
+  for (int k = 0; k < LG; ++k) {
+    const int b = k * 8 + w;
+    if constexpr (TW) {  // rows of JR columns; columns past r lie past the buffer's end
+      constexpr int CH = JR / 8;
+      const int x = (64 / CH) * b + lane / CH, c = (lane % CH) ^ act_swz<JR>(x);
+      g_off[k] = (uint32_t)((x * r + j0 + 8 * c) * 2) | ((uint32_t)(j0 + 8 * c >= r) << 31);
+    } else {
+      const int x = 8 * b + (lane >> 3), c = (lane & 7) ^ swz(x);
+      g_off[k] = (uint32_t)((x * C + c * 8) * 2);
+    }
+  }
+  auto weight = [&](int g) {
+    const uint16_t* w0 = wgt + (int64_t)g * r * C;
+    const int64_t first = TW ? cb * r : (int64_t)j0 * C + cb, len = TW ? (C - cb) * r : (r - j0) * C - cb;
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(w0 + first), 0, (int)(len * 2), 0x00020000);
+  };
+  __amdgpu_buffer_rsrc_t rg = weight(0);
+
+  f32x4 acc[2][JW];
+  auto pass = [&] {
+    auto issue = [&](int st) {
+      uint8_t* base = lds + (st & 1) * STAGE;
+#pragma unroll
+      for (int k = 0; k < LA; ++k)
+        lds_dma(ra, base + (k * 8 + w) * 1024, a_off[k], st * 128);
+#pragma unroll
+      for (int k = 0; k < LG; ++k)
+        lds_dma(rg, base + A_BYTES + (k * 8 + w) * 1024, g_off[k], TW ? st * 128 * r : st * 128);
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int a = 0; a < JW; ++a) acc[i][a] = f32x4{0.f, 0.f, 0.f, 0.f};
+    __syncthreads();  // every wave is done with the previous pass's stages
+    if (n_st > 0) issue(0);
+    for (int st = 0; st < n_st; ++st) {
+      wait_vm_all<0>();
+      ring_barrier();  // stage st is in LDS, stage st - 1 consumed
+      if (st + 1 < n_st) issue(st + 1);
+      const uint8_t* A = lds + (st & 1) * STAGE;
+      const uint8_t* G = A + A_BYTES;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int k = 4 * ks + q4;
+        bf16x8 af[2], gf[JW];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int x = 32 * wt + 16 * i + l16;
+          af[i] = *reinterpret_cast<const bf16x8*>(A + x * 128 + ((k ^ swz(x)) << 4));
+        }
+#pragma unroll
+        for (int a = 0; a < JW; ++a) {
+          const int j = 16 * (JW * wj + a);
+          if constexpr (TW) {
+            Bf8 u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int t = 32 * ks + 8 * q4 + 4 * h + (l16 >> 2), col = j + 4 * (l16 & 3);
+              u.half[h] = lds_tr(G + t * (2 * JR) + (((col >> 3) ^ act_swz<JR>(t)) << 4) + (col & 7) * 2);
+            }
+            gf[a] = u.b;
+          } else {
+            const int x = j + l16;
+            gf[a] = *reinterpret_cast<const bf16x8*>(G + x * 128 + ((k ^ swz(x)) << 4));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int a = 0; a < JW; ++a) acc[i][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], gf[a], acc[i][a], 0, 0, 0);
+      }
+    }
+  };
+  // D layout: token 32 wt + 16 i + 4 (l / 16) + e, adapter column 16 (JW wj + a) + l % 16
+  float* const dst = part ? part + (int64_t)z * T * r : out;
+  int idr[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = 32 * wt + 16 * i + 4 * q4 + e;
+      idr[i][e] = t < toks ? ai.ids[t0 + t] : -1;
+      if (my == 0 && t < toks && (idr[i][e] < 0 || idr[i][e] >= ai.n)) {  // no adapter: zeros
+#pragma unroll
+        for (int a = 0; a < JW; ++a) {
+          const int j = j0 + 16 * (JW * wj + a) + l16;
+          if (j < r) dst[(t0 + t) * r + j] = 0.f;
+        }
+      }
+    }
+  const int id0 = lane < toks ? ai.ids[t0 + lane] : -1, id1 = 64 + lane < toks ? ai.ids[t0 + 64 + lane] : -1;
+  uint64_t todo0 = __ballot(id0 >= 0 && id0 < ai.n), todo1 = __ballot(id1 >= 0 && id1 < ai.n);
+  for (int k = 0; todo0 | todo1; ++k) {  // the same sequence in every wave
+    const int g = todo0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(todo0))
+                        : __builtin_amdgcn_readlane(id1, __builtin_ctzll(todo1));
+    todo0 &= ~__ballot(id0 == g);
+    todo1 &= ~__ballot(id1 == g);
+    if (min(k, last) != my) continue;
+    rg = weight(g);
+    pass();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (idr[i][e] == g) {
+          const int64_t t = t0 + 32 * wt + 16 * i + 4 * q4 + e;
+#pragma unroll
+          for (int a = 0; a < JW; ++a) {
+            const int j = j0 + 16 * (JW * wj + a) + l16;
+            if (j < r) dst[t * r + j] = acc[i][a][e];
+          }
+        }
+  }
+}
+
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
@@ -520,6 +733,65 @@ namespace sra {
 
 int multi_max_adapters() { return kMaxAdapters; }
 int64_t multi_perm_entries(int64_t T, int n) { return 32 * (T / 32 + std::min<int64_t>(n, T)); }
+
+namespace {
+// The 128-token tiles: ranks above 32 with at least two tiles and whole 64-column stages; slices of
+// the reduction (at least 4 stages) for about 512 workgroups, two per CU.
+struct RowsPlan {
+  bool ring;
+  int jr, S;
+  int64_t c_per;
+};
+RowsPlan multi_rows_plan(int64_t T, int64_t C, int r) {
+  RowsPlan p{};
+  p.ring = r > 32 && T >= 256 && C > 0 && C % 64 == 0 && C < ((int64_t)1 << 23);  // 32-bit offsets in 128 rows
+  p.jr = r <= 64 ? 64 : 128;
+  p.S = 1;
+  if (!p.ring) return p;
+  int64_t S = 512 / (cdiv64(T, 128) * cdiv64(r, p.jr));
+  S = std::min<int64_t>(S, C / 256);
+  S = std::max<int64_t>(S, 1);
+  p.c_per = cdiv64(cdiv64(C, S), 64) * 64;
+  p.S = (int)cdiv64(C, p.c_per);
+  return p;
+}
+}  // namespace
+
+bool multi_rows_w_t(int64_t T, int64_t C, int r) { return multi_rows_plan(T, C, r).ring && r % 8 == 0; }
+size_t multi_rows_ws(int64_t T, int64_t C, int n, int r) {
+  const RowsPlan p = multi_rows_plan(T, C, r);
+  if (p.ring) return p.S > 1 ? (size_t)p.S * T * r * sizeof(float) : 0;
+  return multi_rows_small_ws(T, C, r);
+}
+hipError_t launch_multi_rows(const uint16_t* act, int64_t T, int64_t C, const uint16_t* w, bool w_t, int r,
+                             const int32_t* ids, int n, float* out, void* ws, hipStream_t s) {
+  if (T == 0 || r == 0) return hipSuccess;
+  if (C == 0) return launch_fill_f32(out, T * r, 0.f, s);
+  AdapterIds ai;
+  ai.ids = ids;
+  ai.stride = (int64_t)r * C;
+  ai.n = n;
+  const RowsPlan p = multi_rows_plan(T, C, r);
+  if (!p.ring) return w_t ? hipErrorInvalidValue : launch_multi_rows_small(act, T, C, w, C, r, ai, out, ws, s);
+  if (w_t && r % 8 != 0) return hipErrorInvalidValue;
+  ai.passes = n < 8 ? n : 8;
+  float* part = p.S > 1 ? (float*)ws : nullptr;
+  const dim3 grid((unsigned)(cdiv64(T, 128) * cdiv64(r, p.jr) * p.S * ai.passes));
+#define SRA_MR(JR, TWV) \
+  launch(SRA_KERNEL_ADAPTER, k_multi_rows<JR, TWV>, grid, dim3(512), 0, s, act, T, C, w, r, p.c_per, p.S, part, out, ai)
+  if (p.jr == 64) {
+    if (w_t) SRA_MR(64, true);
+    else SRA_MR(64, false);
+  } else {
+    if (w_t) SRA_MR(128, true);
+    else SRA_MR(128, false);
+  }
+#undef SRA_MR
+  if (p.S > 1)
+    hipLaunchKernelGGL(k_multi_join, dim3((unsigned)cdiv64(T * r, 256)), dim3(256), 0, s, part, T * r, p.S, T * r, (int64_t)0,
+                       out, (float*)nullptr);
+  return hipGetLastError();
+}
 
 hipError_t launch_multi_prep(const MultiPrep& p, hipStream_t s) {
   PrepArgs a{};
@@ -613,7 +885,8 @@ hipError_t launch_multi_grads(const MultiGrad* g, int n_jobs, int64_t T, const i
     if (r <= 16) launch(SRA_KERNEL_ADAPTER, k_multi_grads_few<1>, grid, dim3(256), 0, s, ga);
     else launch(SRA_KERNEL_ADAPTER, k_multi_grads_few<2>, grid, dim3(256), 0, s, ga);
   } else {
-    hipLaunchKernelGGL(k_multi_vt, dim3((unsigned)(multi_perm_entries(T, n) / 32), (unsigned)n_jobs), dim3(256), 0, s, ga);
+    hipLaunchKernelGGL(k_multi_vt, dim3((unsigned)(multi_perm_entries(T, n) / 32), (unsigned)n_jobs, (unsigned)cdiv64(r, 64)),
+                       dim3(256), 0, s, ga);
     if (p.wj == 1) launch(SRA_KERNEL_ADAPTER, k_multi_grads<1>, grid, dim3(512), 0, s, ga);
     else launch(SRA_KERNEL_ADAPTER, k_multi_grads<2>, grid, dim3(512), 0, s, ga);
   }

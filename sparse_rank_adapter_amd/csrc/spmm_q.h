@@ -898,6 +898,7 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
         valid[j] = (uint32_t)__ballot(id[j] >= 0 && id[j] < ep.ai.n) & 0xffffu;
       }
     }
+    uint32_t todo[MA ? FT : 1];
     // E rows are contiguous in j (e_j_stride == 1, checked by the launchers): one 16-byte load
     // per fragment (eight 2-byte ones when rows are not 16-byte aligned) through a resource over
     // E's rows R, so rows past R read as zero; entries past r (the next row's, or padding) are
@@ -923,6 +924,43 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
     };
     const __amdgpu_buffer_rsrc_t ru = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(ep.U + t0 * ep.r), 0, toks_here * ep.r * 4, 0x00020000);
+    // many adapters: the steps (adapter, 32 columns) come in chunks of CH whose E fragments are in
+    // flight together (the largest wave tile has registers for two steps)
+    constexpr int CH = MA ? (FR * FT >= 32 ? 2 : 4) : 1;
+    union EF { u32x4 v; bf16x8 b; };
+    EF en[CH][MA ? FR : 1];
+    int ga[CH], ja[CH], g_at = -1, j_at = 0;
+    auto next_adapter = [&]() {  // wave-uniform; -1 when none is left
+      int g = -1;
+      if constexpr (MA) {
+#pragma unroll
+        for (int j = FT - 1; j >= 0; --j)
+          if (todo[j]) g = __builtin_amdgcn_readlane(id[j], __builtin_ctz(todo[j]));
+#pragma unroll
+        for (int j = 0; j < FT; ++j) todo[j] &= ~(uint32_t)__ballot(id[j] == g);
+      }
+      return g;
+    };
+    auto fetch_chunk = [&](int jb0, int nj) {  // the next CH steps (ga = -1 past the last)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        ga[c] = g_at;
+        ja[c] = j_at;
+        if constexpr (MA) {
+          if (g_at >= 0) {
+            re = __builtin_amdgcn_make_buffer_rsrc((void*)(ep.E + (int64_t)g_at * ep.ai.stride), 0,
+                                                   (int)(R * ep.e_row_stride * 2), 0x00020000);
+#pragma unroll
+            for (int i = 0; i < FR; ++i) en[c][i].v = load_e(row0 + wr * 16 * FR + i * 16 + l16, jb0 + j_at + 8 * q4);
+            j_at += 32;
+            if (j_at >= nj) {
+              g_at = next_adapter();
+              j_at = 0;
+            }
+          }
+        }
+      }
+    };
     for (int jb0 = 0; jb0 < ep.r; jb0 += 128) {
       __syncthreads();  // the operand ring (or the previous block's U) is no longer read
       if ((ep.r & 3) == 0) {
@@ -940,12 +978,18 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
           bdma(ru, smem + b * 256, 4, j < ep.r ? (uint32_t)((tok * ep.r + j) * 4) : 0x80000000u, 0);
         }
       }
-      wait_vm<0>();
-      __syncthreads();
       const int nj = min(128, ep.r - jb0);
       if constexpr (MA) {
-        // one step per distinct adapter and 32 adapter columns, the next step's E fragments in
-        // flight while a step multiplies; fragments with no token of the adapter are skipped, and
+#pragma unroll
+        for (int j = 0; j < FT; ++j) todo[j] = valid[j];
+        g_at = next_adapter();
+        j_at = 0;
+        fetch_chunk(jb0, nj);
+      }
+      wait_vm<0>();
+      __syncthreads();
+      if constexpr (MA) {
+        // one step per distinct adapter and 32 adapter columns; fragments with no token of the adapter are skipped, and
         // the other tokens' U are cleared.  U is split once per workgroup, in place (an fp32 word
         // becomes hi | lo << 16): by every wave of a token column and for every adapter, the split
         // took longer than the products
@@ -966,37 +1010,12 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
           *p = o;
         }
         __syncthreads();
-        uint32_t todo[FT];
+        while (ga[0] >= 0) {
 #pragma unroll
-        for (int j = 0; j < FT; ++j) todo[j] = valid[j];
-        auto next_adapter = [&]() {  // wave-uniform; -1 when none is left
-          int g = -1;
-#pragma unroll
-          for (int j = FT - 1; j >= 0; --j)
-            if (todo[j]) g = __builtin_amdgcn_readlane(id[j], __builtin_ctz(todo[j]));
-#pragma unroll
-          for (int j = 0; j < FT; ++j) todo[j] &= ~(uint32_t)__ballot(id[j] == g);
-          return g;
-        };
-        union EF { u32x4 v; bf16x8 b; };
-        EF e[FR], en[FR];
-        auto fetch = [&](int g, int jj, EF (&d)[FR]) {
-          re = __builtin_amdgcn_make_buffer_rsrc((void*)(ep.E + (int64_t)g * ep.ai.stride), 0,
-                                                 (int)(R * ep.e_row_stride * 2), 0x00020000);
-#pragma unroll
-          for (int i = 0; i < FR; ++i) d[i].v = load_e(row0 + wr * 16 * FR + i * 16 + l16, jb0 + jj + 8 * q4);
-        };
-        int g = next_adapter(), jj = 0;
-        if (g >= 0) fetch(g, 0, en);
-        while (g >= 0) {
-#pragma unroll
-          for (int i = 0; i < FR; ++i) e[i] = en[i];
-          int g2 = g, jj2 = jj + 32;
-          if (jj2 >= nj) {
-            g2 = next_adapter();
-            jj2 = 0;
-          }
-          if (g2 >= 0) fetch(g2, jj2, en);
+          for (int ch = 0; ch < CH; ++ch) {
+          const int g = ga[ch], jj = ja[ch];
+          if (g < 0) break;  // wave-uniform
+          const EF (&e)[FR] = en[ch];
           const int c0 = (jj + 8 * q4) >> 2;
 #pragma unroll
           for (int j = 0; j < FT; ++j) {
@@ -1019,8 +1038,8 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
               acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, ulo.b, acc[i][j], 0, 0, 0);
             }
           }
-          g = g2;
-          jj = jj2;
+          }
+          fetch_chunk(jb0, nj);
         }
       } else
       for (int jj = 0; jj < nj; jj += 32) {
