@@ -925,7 +925,10 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
     const __amdgpu_buffer_rsrc_t ru = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(ep.U + t0 * ep.r), 0, toks_here * ep.r * 4, 0x00020000);
     // many adapters: the steps (adapter, 32 columns) come in chunks of CH whose E fragments are in
-    // flight together (the largest wave tile has registers for two steps)
+    // flight together (the largest wave tile has registers for two steps).  The loads are bare:
+    // clearing the entries past r right after each load made every load wait for itself (36.3 us
+    // against 23.1 at OPT-350M fc1 where 16 adapters meet in each 128-token tile), so that happens at
+    // the products.
     constexpr int CH = MA ? (FR * FT >= 32 ? 2 : 4) : 1;
     union EF { u32x4 v; bf16x8 b; };
     EF en[CH][MA ? FR : 1];
@@ -950,8 +953,15 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
           if (g_at >= 0) {
             re = __builtin_amdgcn_make_buffer_rsrc((void*)(ep.E + (int64_t)g_at * ep.ai.stride), 0,
                                                    (int)(R * ep.e_row_stride * 2), 0x00020000);
+            if (e_al) {
 #pragma unroll
-            for (int i = 0; i < FR; ++i) en[c][i].v = load_e(row0 + wr * 16 * FR + i * 16 + l16, jb0 + j_at + 8 * q4);
+              for (int i = 0; i < FR; ++i)
+                en[c][i].v = __builtin_amdgcn_raw_buffer_load_b128(
+                    re, (uint32_t)(((row0 + wr * 16 * FR + i * 16 + l16) * ep.e_row_stride + jb0 + j_at + 8 * q4) * 2), 0, 0);
+            } else {
+#pragma unroll
+              for (int i = 0; i < FR; ++i) en[c][i].v = load_e(row0 + wr * 16 * FR + i * 16 + l16, jb0 + j_at + 8 * q4);
+            }
             j_at += 32;
             if (j_at >= nj) {
               g_at = next_adapter();
@@ -1015,7 +1025,15 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
           for (int ch = 0; ch < CH; ++ch) {
           const int g = ga[ch], jj = ja[ch];
           if (g < 0) break;  // wave-uniform
-          const EF (&e)[FR] = en[ch];
+          EF (&e)[FR] = en[ch];
+          if (jb0 + jj + 32 > ep.r) {  // entries past r: another row's
+            const int left = ep.r - (jb0 + jj + 8 * q4);  // of this lane's eight
+#pragma unroll
+            for (int i = 0; i < FR; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                e[i].v[q] &= left >= 2 * q + 2 ? ~0u : left == 2 * q + 1 ? 0xffffu : 0u;
+          }
           const int c0 = (jj + 8 * q4) >> 2;
 #pragma unroll
           for (int j = 0; j < FT; ++j) {
