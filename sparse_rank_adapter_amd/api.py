@@ -8,6 +8,7 @@ from __future__ import annotations
 import ctypes
 from contextlib import contextmanager
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -26,7 +27,7 @@ def _dt(t: torch.Tensor) -> int:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _dev(t: torch.Tensor, name: str = "tensor", device=None):
@@ -34,7 +35,7 @@ def _dev(t: torch.Tensor, name: str = "tensor", device=None):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
-    if device is not None and t.device != torch.device(device):
+    if device is not None and t.device != device and t.device != torch.device(device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -45,6 +46,9 @@ def _arg(t, name: str, shape: tuple, dtype: torch.dtype, device=None, min_numel:
     """Check one tensor argument before anything reaches the library: shape (or, with
     ``min_numel``, at least that many elements), dtype, device and contiguity.  Shape and dtype
     are checked first so that a wrong call is reported the same way with or without a GPU."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.is_contiguous() and (device is None or t.device == device)):
+        return t  # the usual case in one pass; what fails it is named below
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if min_numel:
@@ -97,8 +101,14 @@ def _workspace(ws, nbytes: int, dev):
     return _arg(ws, "ws", (ws.numel(),), torch.uint8, dev)
 
 
-def _stream(dev) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(dev) -> int:
+    """The device's current stream as a hipStream_t."""
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 @dataclass
@@ -118,20 +128,15 @@ class SparseMatrix:
     nnz: int = 0
 
     def desc(self) -> SraSparse:
-        d = SraSparse()
-        d.format, d.dtype, d.rows, d.cols = self.fmt, _DT[self.dtype], self.rows, self.cols
-        d.n, d.m, d.k, d.nnz = self.n, self.m, self.k, self.nnz
-        d.values = self.values.data_ptr() if self.values is not None else None
-        d.meta = self.meta.data_ptr() if self.meta is not None else None
-        d.index = self.index.data_ptr() if self.index is not None else None
-        d.row_ptr = self.row_ptr.data_ptr() if self.row_ptr is not None else None
-        return d
+        return SraSparse(self.fmt, _DT[self.dtype], self.rows, self.cols, self.n, self.m, self.k, self.nnz,
+                         _p(self.values), _p(self.meta), _p(self.index), _p(self.row_ptr))
 
     @property
     def device(self):
         return self.values.device
 
 
+@lru_cache(maxsize=1024)
 def meta_words(cols: int, n: int = 2, m: int = 4) -> int:
     return int(load().sra_nm_meta_words(cols, n, m))
 
@@ -142,7 +147,7 @@ def _mat(W, name: str):
         raise ValueError(f"{name} must be a 2-D tensor")
     _dt(W)
     _dev(W, name)
-    return tuple(int(x) for x in W.shape)
+    return tuple(W.shape)
 
 
 def _check_out_nm(S: "SparseMatrix", name: str, like: torch.Tensor, rows: int, cols: int, n: int, m: int):
@@ -236,6 +241,7 @@ def nm_tile(Ws: SparseMatrix, out: SparseMatrix | None = None) -> SparseMatrix:
     return out
 
 
+@lru_cache(maxsize=1024)
 def tile_bytes(rows: int, cols: int, n: int = 2, m: int = 4) -> tuple:
     """(value bytes, metadata bytes) of the streaming layout of a rows x cols N:M matrix."""
     vb, mb = ctypes.c_size_t(), ctypes.c_size_t()
@@ -624,6 +630,28 @@ def _multi_args(A, B, ids, T: int, K: int, N: int, dt, dev):
     return n, r
 
 
+# Workspace sizes of the calls below depend on the shapes alone, so each is asked for once.  The size
+# queries validate the descriptor's pointers but do not read them: any aligned address will do.
+@lru_cache(maxsize=1024)
+def _multi_bytes(fmt: int, dt: int, rows: int, cols: int, nn: int, mm: int, T: int, n: int, r: int,
+                 flags: int | None) -> int:
+    d = SraSparse(fmt, dt, rows, cols, nn, mm, 0, 0, 1 << 12, 1 << 12, None, None)
+    nbytes = ctypes.c_size_t()
+    if flags is None:
+        check("sra_multi_fwd_workspace", load().sra_multi_fwd_workspace(ctypes.byref(d), T, n, r, ctypes.byref(nbytes)))
+    else:
+        check("sra_multi_bwd_workspace", load().sra_multi_bwd_workspace(ctypes.byref(d), T, n, r, flags,
+                                                                        ctypes.byref(nbytes)))
+    return nbytes.value
+
+
+@lru_cache(maxsize=1024)
+def _ln_bwd_bytes(T: int, H: int) -> int:
+    nbytes = ctypes.c_size_t()
+    check("sra_layer_norm_bwd_workspace", load().sra_layer_norm_bwd_workspace(T, H, ctypes.byref(nbytes)))
+    return nbytes.value
+
+
 def multi_lora_fwd(Ws: SparseMatrix, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor,
                    Y: torch.Tensor | None = None, U: torch.Tensor | None = None, want_u: bool = True,
                    ws: torch.Tensor | None = None):
@@ -647,9 +675,7 @@ def multi_lora_fwd(Ws: SparseMatrix, X: torch.Tensor, A: torch.Tensor, B: torch.
     elif want_u:
         U = torch.empty((T, r), dtype=torch.float32, device=dev)
     d = Ws.desc()
-    nbytes = ctypes.c_size_t()
-    check("sra_multi_fwd_workspace", lib.sra_multi_fwd_workspace(ctypes.byref(d), T, n, r, ctypes.byref(nbytes)))
-    ws = _workspace(ws, nbytes.value, dev)
+    ws = _workspace(ws, _multi_bytes(Ws.fmt, _DT[dt], N, K, Ws.n, Ws.m, T, n, r, None), dev)
     check("sra_multi_lora_fwd", lib.sra_multi_lora_fwd(
         ctypes.byref(d), _p(X), T, _p(A), _p(B), _p(ids), n, r, _p(Y), _p(U), _p(ws), ws.numel(), _stream(dev)))
     return Y, U
@@ -689,9 +715,7 @@ def multi_lora_bwd(P: SparseMatrix, dY: torch.Tensor, X: torch.Tensor | Ckpt8 | 
         elif wanted:
             out[key] = torch.empty(shape, dtype=odt, device=dev)
     d = P.desc()
-    nbytes = ctypes.c_size_t()
-    check("sra_multi_bwd_workspace", lib.sra_multi_bwd_workspace(ctypes.byref(d), T, n, r, flags, ctypes.byref(nbytes)))
-    ws = _workspace(ws, nbytes.value, dev)
+    ws = _workspace(ws, _multi_bytes(P.fmt, _DT[dt], K, N, P.n, P.m, T, n, r, flags), dev)
     check("sra_multi_lora_bwd", lib.sra_multi_lora_bwd(
         ctypes.byref(d), _p(dY), None if kept else _p(X), _p(X.codes) if kept else None,
         _p(X.exps) if kept else None, T, _p(U), _p(A), _p(B), _p(ids), n, r, flags, _p(out.get("dX")),
@@ -809,9 +833,7 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor, mean:
     _arg(dX, "dX", (T, H), X.dtype, dev)
     dgamma = torch.empty(H, dtype=torch.float32, device=dev)
     dbeta = torch.empty(H, dtype=torch.float32, device=dev)
-    nbytes = ctypes.c_size_t()
-    check("sra_layer_norm_bwd_workspace", lib.sra_layer_norm_bwd_workspace(T, H, ctypes.byref(nbytes)))
-    ws = _workspace(ws, nbytes.value, dev)
+    ws = _workspace(ws, _ln_bwd_bytes(T, H), dev)
     check("sra_layer_norm_bwd", lib.sra_layer_norm_bwd(
         _p(dY), _p(X), _p(gamma), _p(mean), _p(rstd), _dt(X), T, H, _p(dX), _p(dgamma), _p(dbeta),
         _p(ws), ws.numel(), _stream(dev)))

@@ -8,7 +8,7 @@
 // Both are bound by HBM: the forward reads and writes each element once, the backward reads two
 // tensors and writes one.  A workgroup holds a whole row in registers (EPT elements a thread, as
 // vectors of VEC), so the variance is summed from the deviations with no second read.
-// All sums are fp32.
+// Terms are summed in fp32 within a thread (8 or 16 of them) and in fp64 over the threads.
 //
 // The backward's workgroups walk over rows (gridDim.x apart): a thread keeps its columns, so its
 // parts of dgamma and dbeta stay in registers until the end, are written as one partial row per
@@ -21,31 +21,58 @@
 namespace {
 using namespace sra_row;
 
-template <int N>
-SRA_DEV void wave_sum(float (&v)[N]) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1)
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], d, 64);
+// Sum over the wave in fp64 by DPP row shifts and broadcasts (lane 63 ends with it), the same value in
+// every lane, with no LDS round trips (lane exchanges through LDS: 52 us against 48-50 at 8192 x 5120);
+// fp32 sums here moved the statistics by enough to flip over half as many codes of a checkpoint again.
+template <int CTRL, int ROWS>
+SRA_DEV double dpp_add(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+  return x + __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
 }
-// Sum over the workgroup (up to 16 waves), the same value in every thread.  `red` is LDS that no
-// wave still reads: calls alternate between two areas, so one barrier each is enough.
+SRA_DEV double wave_sum(double x) {
+  x = dpp_add<0x111, 0xf>(x);  // row_shr 1, 2, 4, 8: lane 15 of each row of 16 holds the row's sum
+  x = dpp_add<0x112, 0xf>(x);
+  x = dpp_add<0x114, 0xf>(x);
+  x = dpp_add<0x118, 0xf>(x);
+  x = dpp_add<0x142, 0xa>(x);  // row_bcast 15 into rows 1 and 3
+  x = dpp_add<0x143, 0xc>(x);  // row_bcast 31 into rows 2 and 3
+  const uint64_t u = (uint64_t)__double_as_longlong(x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  return __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
+}
+// Sums over the workgroup (up to 16 waves, added in fp64), the same values in every thread.  `red` is
+// LDS that no wave still reads: calls alternate between two areas, so one barrier each is enough.
 template <int N>
-SRA_DEV void block_sum(float (&v)[N], float* red) {
-  wave_sum<N>(v);
+SRA_DEV void block_sum(const float (&v)[N], double (&out)[N], double* red) {
+  double s[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) s[k] = wave_sum((double)v[k]);
   const int nw = blockDim.x >> 6;
-  if (nw == 1) return;
+  if (nw == 1) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) out[k] = s[k];
+    return;
+  }
   const int w = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) red[w * N + k] = v[k];
+    for (int k = 0; k < N; ++k) red[w * N + k] = s[k];
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = 0.f;
+  for (int k = 0; k < N; ++k) out[k] = 0.0;
   for (int i = 0; i < nw; ++i)
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += red[i * N + k];
+    for (int k = 0; k < N; ++k) out[k] += red[i * N + k];
+}
+
+// sum of N terms as a tree
+template <int N>
+SRA_DEV float tree_sum(const float* v) {
+  if constexpr (N == 1) return v[0];
+  else return tree_sum<N / 2>(v) + tree_sum<N - N / 2>(v + N / 2);
 }
 
 // one workgroup per row
@@ -55,34 +82,38 @@ __global__ __launch_bounds__(EPT == 8 ? 256 : 1024) void k_ln_fwd(const E* __res
                                                  float* __restrict__ mean, float* __restrict__ rstd,
                                                  int8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
   constexpr int V = EPT / VEC;
-  __shared__ float red[2][16];
+  __shared__ double red[2][16];
   const int64_t t = blockIdx.x;
   const int nvec = (int)(H / VEC), nt = blockDim.x;
   float f[V][VEC];
-  float s[1] = {0.f};
+  float part[1] = {0.f};
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int i = threadIdx.x + v * nt;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) f[v][k] = 0.f;
     if (i < nvec) RowVec<E, VEC>::load(x + t * H + (int64_t)i * VEC, f[v]);
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) s[0] += f[v][k];
+    part[0] += tree_sum<VEC>(f[v]);
   }
-  block_sum<1>(s, red[0]);
-  const float mu = s[0] / (float)H;
-  float q[1] = {0.f};
+  double s[1];
+  block_sum<1>(part, s, red[0]);
+  const double inv_h = 1.0 / (double)H;
+  const float mu = (float)(s[0] * inv_h);
+  part[0] = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const bool in = threadIdx.x + v * nt < nvec;
+    float sq[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
       f[v][k] = in ? f[v][k] - mu : 0.f;
-      q[0] += f[v][k] * f[v][k];
+      sq[k] = f[v][k] * f[v][k];
     }
+    part[0] += tree_sum<VEC>(sq);
   }
-  block_sum<1>(q, red[1]);
-  const float rs = 1.f / sqrtf(q[0] / (float)H + eps);
+  double q[1];
+  block_sum<1>(part, q, red[1]);
+  const float rs = 1.f / sqrtf((float)(q[0] * inv_h) + eps);
   if (threadIdx.x == 0) {
     mean[t] = mu;
     rstd[t] = rs;
@@ -119,13 +150,14 @@ __global__ __launch_bounds__(EPT == 8 ? 256 : 1024) void k_ln_bwd(const E* __res
                                                  const float* __restrict__ rstd, int64_t T, int64_t H,
                                                  E* __restrict__ dx, float* __restrict__ part) {
   constexpr int V = EPT / VEC;
-  __shared__ float red[2][2 * 16];
+  __shared__ double red[2][2 * 16];
   const int nvec = (int)(H / VEC), nt = blockDim.x;
   float dg[V][VEC], db[V][VEC];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) dg[v][k] = db[v][k] = 0.f;
+  const double inv_h = 1.0 / (double)H;
   int flip = 0;
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x, flip ^= 1) {
     const float mu = mean[t], rs = rstd[t];
@@ -150,8 +182,9 @@ __global__ __launch_bounds__(EPT == 8 ? 256 : 1024) void k_ln_bwd(const E* __res
         }
       }
     }
-    block_sum<2>(s, red[flip]);
-    const float a = s[0] / (float)H, b = s[1] / (float)H;
+    double m[2];
+    block_sum<2>(s, m, red[flip]);
+    const float a = (float)(m[0] * inv_h), b = (float)(m[1] * inv_h);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = threadIdx.x + v * nt;
@@ -181,12 +214,20 @@ __global__ __launch_bounds__(1024) void k_ln_params(const float* __restrict__ pa
   __shared__ float red[16][64];
   const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t col = (int64_t)blockIdx.x * 64 + c;
+  constexpr int U = 8;  // loads in flight: the partials are few and the launch is bound by their latency
   float s = 0.f;
-  if (col < 2 * H)
-    for (int p = w; p < P; p += 16) s += part[(int64_t)p * 2 * H + col];
+  const float* src = part + min(col, 2 * H - 1);
+  for (int p = w; p < P; p += 16 * U) {
+    float v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = src[(int64_t)min(p + 16 * u, P - 1) * 2 * H];
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += p + 16 * u < P ? v[u] : 0.f;
+  }
   red[w][c] = s;
   __syncthreads();
   if (w == 0 && col < 2 * H) {
+#pragma unroll
     for (int i = 1; i < 16; ++i) s += red[i][c];
     if (col < H) dgamma[col] = s;
     else dbeta[col - H] = s;
