@@ -1178,7 +1178,7 @@ size_t multi_bwd_plan(const sra_sparse* P, int64_t T, int32_t n, int32_t r, uint
   p.rows_off = a.take(rows);
   if (dx && !(flags & SRA_DX_NO_ADAPTER)) p.at_off = a.take((size_t)n * K * sra::packed_at_ld(r) * 2);
   if (da || db) {
-    p.gblk_off = a.take((size_t)(2 * n + 1) * 4);  // block starts, then the adapters' order
+    p.gblk_off = a.take(sra::multi_groups_bytes(n));
     p.perm_off = a.take((size_t)sra::multi_perm_entries(T, n) * 4);
     sra::MultiGrad jobs[2];
     int nj = 0;

@@ -1402,7 +1402,7 @@ hipError_t launch_multi_rows_small(const uint16_t* act, int64_t T, int64_t C, co
   }
   const RowsPlan p = rows_plan(T, C, r);
   double* part = p.S > 1 ? (double*)ws : nullptr;
-  ai.passes = ai.n < 4 ? ai.n : 4;
+  ai.passes = ai.n < 8 ? ai.n : 8;
   const dim3 grid((unsigned)cdiv(T, 16), (unsigned)cdiv(r, 16 * p.jt), (unsigned)(p.S * ai.passes));
 #define SRA_MULTI_ROWS(JT, UB)                                                                                 \
   launch(SRA_KERNEL_ADAPTER, k_adapter_rows<JT, UB, true>, grid, dim3(256), 0, s, act, T, C, wt, ldw, r, p.c_per, part, \

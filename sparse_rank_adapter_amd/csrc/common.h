@@ -365,8 +365,8 @@ struct AdapterGradArgs {
   int64_t T, Tp, t_per;
   int r, rp, S;
 };
-// Gradients of many adapters (multi.hip).  Prep: the tokens sorted by adapter (gblk [n + 1], perm
-// [multi_perm_entries]; gblk == nullptr: not needed), B_g^T as wt [n][r][N] and A_g^T as
+// Gradients of many adapters (multi.hip).  Prep: the tokens sorted by adapter (gblk of
+// multi_groups_bytes, perm [multi_perm_entries]; gblk == nullptr: not needed), B_g^T as wt [n][r][N] and A_g^T as
 // at [n][K][packed_at_ld(r)] (nullptr: not needed).
 struct MultiPrep {
   const int32_t* ids = nullptr;
@@ -382,6 +382,7 @@ struct MultiPrep {
   uint16_t* at = nullptr;
 };
 int multi_max_adapters();
+size_t multi_groups_bytes(int n);
 int64_t multi_perm_entries(int64_t T, int n);
 hipError_t launch_multi_prep(const MultiPrep& p, hipStream_t s);
 // Out[t][j] = sum_c act[t][c] W_g[j][c], g = ids[t] (zeros for a token without an adapter), W_g at

@@ -5,10 +5,9 @@
 //
 // k_multi_prep, one launch for what the products need from ids, A and B:
 //   workgroup 0 sorts the tokens by adapter (a stable counting sort, so sums run in token order):
-//     adapter g's tokens fill blocks gblk[g] .. gblk[g+1]-1 of 32 entries of perm, the last block
-//     of each adapter padded with ~(its last token), a negative number, so that padding loads the
-//     adapter's own data (its V is cleared); tokens with no adapter are left out; order holds the
-//     adapters by falling block count (up to 64 of them), so that the longest start first;
+//     each adapter's tokens fill blocks of 32 entries of perm, the last block padded with ~(its last token), a negative number, so that padding loads the
+//     adapter's own data (its V is cleared); tokens with no adapter are left out; the adapters' list
+//     runs by falling block count (up to 64 adapters), so that the longest start first;
 //   the other workgroups transpose every B_g (the dU product's operand, contiguous along N) and
 //     every A_g (the dX epilogue's rows of r entries), in 64 x 64 tiles.
 //
@@ -22,9 +21,9 @@
 // more launch adds in slice order.
 //
 // Ranks up to 32 (k_multi_grads_few) are bound by reading Act and by latency.  A workgroup owns one
-// adapter and 64 columns; its four waves take every fourth 32-token block, each through its own LDS
-// tile with no barrier, and join their sums at the end, so an adapter's chain of steps is a quarter
-// as long and 16 waves a CU keep loads in flight.  V is read and split by each wave itself.
+// adapter and 64 columns; its NW waves take every NW-th 32-token block, each through its own LDS
+// tile with no barrier, and join their sums at the end, so an adapter's chain of steps is 1 / NW as
+// long and 16 waves a CU keep loads in flight.  V is read and split by each wave itself.
 //
 // Larger ranks (k_multi_grads) are bound by the matrix cores and by LDS reads of V.  V is split once
 // (k_multi_vt) into tiles of 32 tokens in the sorted order, contiguous per step; a workgroup of
@@ -42,7 +41,8 @@ struct PrepArgs {
   const int32_t* ids;  // nullptr: no sort
   int64_t T;
   int n;
-  int32_t* gblk;       // [n + 1], then the order [n]
+  int32_t* gblk;       // gblk[n]: the block count; then, 16-byte aligned, per adapter in falling order
+                       // of its blocks {adapter, first block, end, 0}
   int32_t* perm;
   const uint16_t* B;  // [n][N][r] -> wt [n][r][N]; nullptr: none
   int64_t N;
@@ -53,9 +53,13 @@ struct PrepArgs {
   int r, b_tiles, a_tiles;  // 64 x 64 tiles per adapter
 };
 
+// offset (entries) of the adapters' list after gblk [n + 1], 16-byte aligned
+__host__ __device__ inline int group_list(int n) { return (n + 1 + 3) / 4 * 4; }
+
 struct SortLds {
   int hist[kPrepWaves][kMaxAdapters + 1];
   int base[kMaxAdapters + 1];
+  int last[kMaxAdapters + 1];  // the adapter's last token
   int wsum[kPrepWaves];
   int total;
 };
@@ -70,22 +74,38 @@ union PrepLds {
 SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
   for (int i = l; i < a.n; i += 64) s.hist[w][i] = 0;  // wave w's own row
+  if (tid < a.n) s.last[tid] = 0;
   __syncthreads();
   // wave w takes tokens [w * chunk, (w + 1) * chunk)
   const int64_t chunk = ((a.T + kPrepWaves - 1) / kPrepWaves + 63) / 64 * 64;
   const int64_t lo = w * chunk, hi = min(a.T, lo + chunk);
-  for (int64_t t = lo + l; t < hi; t += 64) {
-    const int g = a.ids[t];
-    if (g >= 0 && g < a.n) atomicAdd(&s.hist[w][g], 1);  // LDS counts: the order does not matter
+  constexpr int KEEP = 8;  // ids of the wave's first tokens stay in registers for the second walk
+  int kept[KEEP];
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    const int64_t t = lo + 64 * k + l;
+    kept[k] = t < hi ? a.ids[t] : -1;
   }
+  auto count = [&](int g, int64_t t) {  // LDS integers: the order does not matter
+    if (g >= 0 && g < a.n) {
+      atomicAdd(&s.hist[w][g], 1);
+      atomicMax(&s.last[g], (int)t);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) count(kept[k], lo + 64 * k + l);
+  for (int64_t t = lo + 64 * KEEP + l; t < hi; t += 64) count(a.ids[t], t);
   __syncthreads();
   // thread g: where each wave's tokens of adapter g start, and the adapter's blocks
   int cnt = 0, blocks = 0;
   if (tid < a.n) {
+    int c[kPrepWaves];
+#pragma unroll
+    for (int i = 0; i < kPrepWaves; ++i) c[i] = s.hist[i][tid];
+#pragma unroll
     for (int i = 0; i < kPrepWaves; ++i) {
-      const int c = s.hist[i][tid];
       s.hist[i][tid] = cnt;
-      cnt += c;
+      cnt += c[i];
     }
     blocks = (cnt + 31) / 32;
   }
@@ -102,8 +122,9 @@ SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
   if (tid == kPrepThreads - 1) s.total = incl;
   if (tid < a.n) {
     s.base[tid] = first;
-    a.gblk[tid] = first;
     if (tid == a.n - 1) a.gblk[a.n] = incl;
+    const int pad = ~s.last[tid];
+    for (int i = cnt; i < 32 * blocks; ++i) a.perm[(int64_t)first * 32 + i] = pad;
   }
   __syncthreads();
   if (tid < a.n) {
@@ -115,12 +136,10 @@ SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
         rank += b > blocks || (b == blocks && i < tid);
       }
     }
-    a.gblk[a.n + 1 + rank] = tid;
+    reinterpret_cast<int4*>(a.gblk + group_list(a.n))[rank] = int4{tid, first, first + blocks, 0};
   }
   volatile int* const at = s.hist[w];  // this wave's running positions (only this wave uses them)
-  for (int64_t t0 = lo; t0 < hi; t0 += 64) {
-    const int64_t t = t0 + l;
-    const int g = t < hi ? a.ids[t] : -1;
+  auto place = [&](int g, int64_t t) {
     uint64_t todo = __ballot(g >= 0 && g < a.n);
     while (todo) {
       const int lead = __builtin_ctzll(todo);
@@ -131,13 +150,11 @@ SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
       if (g == cur) a.perm[(int64_t)s.base[cur] * 32 + start + __popcll(same & ((1ull << l) - 1))] = (int32_t)t;
       if (l == lead) at[cur] = start + __popcll(same);
     }
-  }
-  __syncthreads();  // this workgroup's perm is written (a barrier orders its own global writes)
-  if (tid < a.n && cnt < 32 * blocks) {
-    int32_t* const p = a.perm + (int64_t)first * 32;
-    const int32_t pad = ~p[cnt - 1];
-    for (int i = cnt; i < 32 * blocks; ++i) p[i] = pad;
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k)
+    if (lo + 64 * k < hi) place(kept[k], lo + 64 * k + l);
+  for (int64_t t0 = lo + 64 * KEEP; t0 < hi; t0 += 64) place(t0 + l < hi ? a.ids[t0 + l] : -1, t0 + l);
 }
 
 // dst[y][x] = src[x][y] for one 64 x 64 tile (X x Y source, dst rows of stride ld), 16 bytes a lane on
@@ -270,11 +287,13 @@ SRA_DEV bf16x8 act_frag(const uint8_t* tile, int m0, int l16, int q4) {
   return u.b;
 }
 
-// blocks [lo, hi) of slice z of adapter g
-SRA_DEV void slice_of(const GradArgs& ga, int g, int z, int& lo, int& hi) {
-  const int b0 = ga.gblk[g], b1 = ga.gblk[g + 1], per = (b1 - b0 + ga.S - 1) / ga.S;
-  lo = min(b1, b0 + z * per);
-  hi = min(b1, lo + per);
+// the k-th adapter of the list (the longest first) and the blocks [lo, hi) of its slice z
+SRA_DEV int slice_of(const GradArgs& ga, int k, int z, int& lo, int& hi) {
+  const int4 e = reinterpret_cast<const int4*>(ga.gblk + group_list(ga.n))[k];
+  const int per = (e.z - e.y + ga.S - 1) / ga.S;
+  lo = min(e.z, e.y + z * per);
+  hi = min(e.z, lo + per);
+  return e.x;
 }
 // D layout: adapter column 4 (l / 16) + e, Act column l % 16
 SRA_DEV void grad_store(const GradArgs& ga, const GradJob& job, int g, int z, int j0, int64_t m0, const f32x4& c, int l16,
@@ -296,19 +315,19 @@ SRA_DEV void grad_store(const GradArgs& ga, const GradJob& job, int g, int z, in
 }
 
 // ---- ranks up to 32
-template <int JT>
-__global__ __launch_bounds__(256) void k_multi_grads_few(GradArgs ga) {
+template <int JT, int NW>
+__global__ __launch_bounds__(64 * NW) void k_multi_grads_few(GradArgs ga) {
   constexpr int MT = 64, TILE = 32 * MT * 2;
-  constexpr int RED = 4 * JT * 4 * 64 * 16;  // the waves' sums: [wave][a][f][lane]
-  __shared__ __attribute__((aligned(16))) uint8_t lds[RED > 4 * TILE ? RED : 4 * TILE];
+  constexpr int RED = NW * JT * 4 * 64 * 16;  // the waves' sums: [wave][a][f][lane]
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RED > NW * TILE ? RED : NW * TILE];
   const int tid = threadIdx.x, l = tid & 63, l16 = l & 15, q4 = l >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool second = (int)blockIdx.x >= ga.job[0].mb;
   const GradJob job = second ? ga.job[1] : ga.job[0];
   const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * MT, M = job.M;
-  const int g = ga.gblk[ga.n + 1 + blockIdx.y], z = blockIdx.z, r = ga.r;
+  const int z = blockIdx.z, r = ga.r;
   int b0, b1;
-  slice_of(ga, g, z, b0, b1);
+  const int g = slice_of(ga, blockIdx.y, z, b0, b1);
   const int64_t nblk = (M + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
   uint8_t* const tile = lds + w * TILE;
 
@@ -354,12 +373,12 @@ __global__ __launch_bounds__(256) void k_multi_grads_few(GradArgs ga) {
   int p = 0, pn = 0;
   if (b0 + w < b1) {
     p = perm_of(b0 + w);
-    pn = perm_of(b0 + w + 4);
+    pn = perm_of(b0 + w + NW);
     load(p);
   }
-  for (int b = b0 + w; b < b1; b += 4) {
+  for (int b = b0 + w; b < b1; b += NW) {
     p = pn;
-    pn = perm_of(b + 8);
+    pn = perm_of(b + 2 * NW);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = r8 + 8 * i;
@@ -371,7 +390,7 @@ __global__ __launch_bounds__(256) void k_multi_grads_few(GradArgs ga) {
     for (int a = 0; a < JT; ++a)
 #pragma unroll
       for (int e = 0; e < 8; ++e) split3(vr[a][e], vf[a][0].h[e], vf[a][1].h[e], vf[a][2].h[e]);
-    if (b + 4 < b1) load(p);  // in flight while this block multiplies
+    if (b + NW < b1) load(p);  // in flight while this block multiplies
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       const bf16x8 bf = act_frag<MT>(tile, 16 * f, l16, q4);  // this wave's own writes: in order
@@ -382,7 +401,7 @@ __global__ __launch_bounds__(256) void k_multi_grads_few(GradArgs ga) {
           acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[a][k].b, bf, acc[a][f], 0, 0, 0);
     }
   }
-  // join: wave w finishes column fragment w, adding the waves in order
+  // join: fragment i = (a, f) is finished by wave i % NW, adding the waves in order
   __syncthreads();
   f32x4* const red = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
@@ -390,12 +409,12 @@ __global__ __launch_bounds__(256) void k_multi_grads_few(GradArgs ga) {
 #pragma unroll
     for (int f = 0; f < 4; ++f) red[((w * JT + a) * 4 + f) * 64 + l] = acc[a][f];
   __syncthreads();
+  for (int i = w; i < 4 * JT; i += NW) {
+    const int a = i >> 2, f = i & 3;
+    f32x4 c = red[i * 64 + l];
 #pragma unroll
-  for (int a = 0; a < JT; ++a) {
-    f32x4 c = red[(a * 4 + w) * 64 + l];
-#pragma unroll
-    for (int k = 1; k < 4; ++k) c += red[((k * JT + a) * 4 + w) * 64 + l];
-    grad_store(ga, job, g, z, 16 * a, m0 + 16 * w, c, l16, q4);
+    for (int k = 1; k < NW; ++k) c += red[(k * JT * 4 + i) * 64 + l];
+    grad_store(ga, job, g, z, 16 * a, m0 + 16 * f, c, l16, q4);
   }
 }
 
@@ -455,10 +474,9 @@ __global__ __launch_bounds__(512, 4) void k_multi_grads(GradArgs ga) {
   const bool second = (int)blockIdx.x >= ga.job[0].mb;
   const GradJob& job = ga.job[second ? 1 : 0];
   const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * MT, M = job.M;
-  const int g = ga.gblk[ga.n + 1 + blockIdx.y], njt = (ga.r + JR - 1) / JR, j0 = ((int)blockIdx.z % njt) * JR,
-            z = (int)blockIdx.z / njt;
+  const int njt = (ga.r + JR - 1) / JR, j0 = ((int)blockIdx.z % njt) * JR, z = (int)blockIdx.z / njt;
   int b0, b1;
-  slice_of(ga, g, z, b0, b1);
+  const int g = slice_of(ga, blockIdx.y, z, b0, b1);
 
   // a thread's share of a step: bf16 chunk tid % 32 of rows tid / 32 and tid / 32 + 16, or 16 codes
   // tid % 16 of row tid / 16.  Every load is unconditional: columns past the row read its last ones
@@ -570,11 +588,12 @@ __global__ void k_multi_join(const float* __restrict__ part, int64_t slice, int 
 
 // ------------------------------------------------------------------------------------ rows
 // Out[t][j] = sum_c act[t][c] W_g[j][c] for ranks above 32: a workgroup owns 128 tokens and JR
-// adapter columns over a slice of c, in 64-column stages; both operands stream through a two-stage
-// LDS ring filled by buffer -> LDS transfers.  64 KB of LDS and at most 128 registers, so two
-// workgroups share a CU and one's transfers run under the other's products.  Eight waves: four of
-// 32 tokens by two of JR / 2 adapter columns.
-// TW: the weight is given as [C][r] (B_g as it lies) and its stage [64][JR] is read with the
+// adapter columns over a slice of c, in 64-column stages (whole 128-byte lines of every row; five
+// stages of 32 columns took 164 us where two of 64 took 133, OPT-13B's dU at 8 slices); both operands stream
+// through an LDS ring of NS stages filled by buffer -> LDS transfers.  At most 80 KB of LDS and 128
+// registers, so two workgroups share a CU and one's transfers run under the other's products.
+// Eight waves: four of 32 tokens by two of JR / 2 adapter columns.
+// TW: the weight is given as [C][r] (B_g as it lies) and its stage [SC][JR] is read with the
 // transposing LDS read; else as [r][C].
 // A tile whose tokens take several adapters runs one pass per distinct adapter and writes the tokens
 // of that adapter after it; the grid holds `passes` workgroups per tile (as k_adapter_rows), the last
@@ -584,9 +603,11 @@ __global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restric
                                                        const uint16_t* __restrict__ wgt, int r, int64_t c_per, int S,
                                                        float* __restrict__ part, float* __restrict__ out,
                                                        sra::AdapterIds ai) {
-  constexpr int A_BYTES = 128 * 128, G_BYTES = JR * 128, STAGE = A_BYTES + G_BYTES, JW = JR / 32;
-  constexpr int LA = A_BYTES / 8192, LG = G_BYTES / 8192;  // 1 KB transfers per wave
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
+  constexpr int SC = 64, NS = JR == 128 ? 2 : 3, D = NS - 1;
+  constexpr int RB = 2 * SC, CH = SC / 8;  // bytes and 16-byte chunks of a row of a stage
+  constexpr int A_BYTES = 128 * RB, G_BYTES = JR * RB, STAGE = A_BYTES + G_BYTES, JW = JR / 32;
+  constexpr int LA = A_BYTES / 8192, LG = G_BYTES / 8192, L = LA + LG;  // 1 KB transfers per wave
+  __shared__ __attribute__((aligned(16))) uint8_t lds[NS * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wt = w & 3, wj = w >> 2;
   // workgroups go to the 8 XCDs in turn: XCD x takes an eighth of the (slice, adapter column tile,
@@ -598,26 +619,26 @@ __global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restric
   const int64_t t0 = (int64_t)(lin % n_tt) * 128;
   const int j0 = lin / n_tt % n_jt * JR, z = lin / n_tt / n_jt;
   const int64_t cb = (int64_t)z * c_per, ce = min(C, cb + c_per);
-  const int n_st = (int)((ce - cb) / 64), toks = (int)min((int64_t)128, T - t0);
+  const int n_st = (int)((ce - cb) / SC), toks = (int)min((int64_t)128, T - t0);
 
   const __amdgpu_buffer_rsrc_t ra =
       __builtin_amdgcn_make_buffer_rsrc((void*)(act + t0 * C + cb), 0, (int)((toks * C - cb) * 2), 0x00020000);
   auto swz = [](int x) { return (x >> 1) & 7; };
   uint32_t a_off[LA], g_off[LG];
 #pragma unroll
-  for (int k = 0; k < LA; ++k) {  // 8 rows of 128 bytes
-    const int x = 8 * (k * 8 + w) + (lane >> 3), c = (lane & 7) ^ swz(x);
+  for (int k = 0; k < LA; ++k) {  // 1024 / RB rows a transfer
+    const int x = (1024 / RB) * (k * 8 + w) + lane / CH, c = (lane % CH) ^ swz(x);
     a_off[k] = (uint32_t)((x * C + c * 8) * 2);
   }
 #pragma unroll
   for (int k = 0; k < LG; ++k) {
     const int b = k * 8 + w;
     if constexpr (TW) {  // rows of JR columns; columns past r lie past the buffer's end
-      constexpr int CH = JR / 8;
-      const int x = (64 / CH) * b + lane / CH, c = (lane % CH) ^ act_swz<JR>(x);
+      constexpr int GH = JR / 8;
+      const int x = (64 / GH) * b + lane / GH, c = (lane % GH) ^ act_swz<JR>(x);
       g_off[k] = (uint32_t)((x * r + j0 + 8 * c) * 2) | ((uint32_t)(j0 + 8 * c >= r) << 31);
     } else {
-      const int x = 8 * b + (lane >> 3), c = (lane & 7) ^ swz(x);
+      const int x = (1024 / RB) * b + lane / CH, c = (lane % CH) ^ swz(x);
       g_off[k] = (uint32_t)((x * C + c * 8) * 2);
     }
   }
@@ -631,34 +652,38 @@ __global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restric
   f32x4 acc[2][JW];
   auto pass = [&] {
     auto issue = [&](int st) {
-      uint8_t* base = lds + (st & 1) * STAGE;
+      uint8_t* base = lds + (st % NS) * STAGE;
 #pragma unroll
-      for (int k = 0; k < LA; ++k)
-        lds_dma(ra, base + (k * 8 + w) * 1024, a_off[k], st * 128);
+      for (int k = 0; k < LA; ++k) lds_dma(ra, base + (k * 8 + w) * 1024, a_off[k], st * RB);
 #pragma unroll
       for (int k = 0; k < LG; ++k)
-        lds_dma(rg, base + A_BYTES + (k * 8 + w) * 1024, g_off[k], TW ? st * 128 * r : st * 128);
+        lds_dma(rg, base + A_BYTES + (k * 8 + w) * 1024, g_off[k], TW ? st * RB * r : st * RB);
     };
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int a = 0; a < JW; ++a) acc[i][a] = f32x4{0.f, 0.f, 0.f, 0.f};
     __syncthreads();  // every wave is done with the previous pass's stages
-    if (n_st > 0) issue(0);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (d < n_st) issue(d);
     for (int st = 0; st < n_st; ++st) {
-      wait_vm_all<0>();
-      ring_barrier();  // stage st is in LDS, stage st - 1 consumed
-      if (st + 1 < n_st) issue(st + 1);
-      const uint8_t* A = lds + (st & 1) * STAGE;
+      // stage st has landed when at most the later stages' transfers are outstanding
+      const int later = n_st - 1 - st;
+      if (D > 1 && later >= D - 1) wait_vm_all<(D - 1) * L>();
+      else wait_vm_all<0>();
+      ring_barrier();  // every wave's part of stage st is in LDS, stage st - 1 consumed
+      if (st + D < n_st) issue(st + D);
+      const uint8_t* A = lds + (st % NS) * STAGE;
       const uint8_t* G = A + A_BYTES;
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
+      for (int ks = 0; ks < SC / 32; ++ks) {
         const int k = 4 * ks + q4;
         bf16x8 af[2], gf[JW];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int x = 32 * wt + 16 * i + l16;
-          af[i] = *reinterpret_cast<const bf16x8*>(A + x * 128 + ((k ^ swz(x)) << 4));
+          af[i] = *reinterpret_cast<const bf16x8*>(A + x * RB + ((k ^ swz(x)) << 4));
         }
 #pragma unroll
         for (int a = 0; a < JW; ++a) {
@@ -673,7 +698,7 @@ __global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restric
             gf[a] = u.b;
           } else {
             const int x = j + l16;
-            gf[a] = *reinterpret_cast<const bf16x8*>(G + x * 128 + ((k ^ swz(x)) << 4));
+            gf[a] = *reinterpret_cast<const bf16x8*>(G + x * RB + ((k ^ swz(x)) << 4));
           }
         }
 #pragma unroll
@@ -732,23 +757,28 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 namespace sra {
 
 int multi_max_adapters() { return kMaxAdapters; }
+size_t multi_groups_bytes(int n) { return (size_t)(group_list(n) + 4 * n) * 4; }
 int64_t multi_perm_entries(int64_t T, int n) { return 32 * (T / 32 + std::min<int64_t>(n, T)); }
 
 namespace {
-// The 128-token tiles: ranks above 32 with at least two tiles and whole 64-column stages; slices of
-// the reduction (at least 4 stages) for about 512 workgroups, two per CU.
+// The 128-token tiles: ranks above 32 with at least two tiles and whole 64-column stages.  Slices of
+// the reduction (at least 4 stages) for about 512 workgroups, two per CU, with one adapter, and 256
+// with several, whose further passes then run beside the first ones.  Measured at OPT-13B's dU (64
+// tiles, r 128), 4 / 8 / 16 slices: one adapter 104 / 90 / 113 us, 8 adapters in 15 requests 124 /
+// 141 / 153 us.
 struct RowsPlan {
   bool ring;
   int jr, S;
   int64_t c_per;
 };
-RowsPlan multi_rows_plan(int64_t T, int64_t C, int r) {
+RowsPlan multi_rows_plan(int64_t T, int64_t C, int n, int r) {
   RowsPlan p{};
   p.ring = r > 32 && T >= 256 && C > 0 && C % 64 == 0 && C < ((int64_t)1 << 23);  // 32-bit offsets in 128 rows
   p.jr = r <= 64 ? 64 : 128;
   p.S = 1;
   if (!p.ring) return p;
-  int64_t S = 512 / (cdiv64(T, 128) * cdiv64(r, p.jr));
+  const int64_t tiles = cdiv64(T, 128);
+  int64_t S = (n > 1 ? 256 : 512) / (tiles * cdiv64(r, p.jr));
   S = std::min<int64_t>(S, C / 256);
   S = std::max<int64_t>(S, 1);
   p.c_per = cdiv64(cdiv64(C, S), 64) * 64;
@@ -757,9 +787,9 @@ RowsPlan multi_rows_plan(int64_t T, int64_t C, int r) {
 }
 }  // namespace
 
-bool multi_rows_w_t(int64_t T, int64_t C, int r) { return multi_rows_plan(T, C, r).ring && r % 8 == 0; }
+bool multi_rows_w_t(int64_t T, int64_t C, int r) { return multi_rows_plan(T, C, 1, r).ring && r % 8 == 0; }
 size_t multi_rows_ws(int64_t T, int64_t C, int n, int r) {
-  const RowsPlan p = multi_rows_plan(T, C, r);
+  const RowsPlan p = multi_rows_plan(T, C, n, r);
   if (p.ring) return p.S > 1 ? (size_t)p.S * T * r * sizeof(float) : 0;
   return multi_rows_small_ws(T, C, r);
 }
@@ -771,7 +801,7 @@ hipError_t launch_multi_rows(const uint16_t* act, int64_t T, int64_t C, const ui
   ai.ids = ids;
   ai.stride = (int64_t)r * C;
   ai.n = n;
-  const RowsPlan p = multi_rows_plan(T, C, r);
+  const RowsPlan p = multi_rows_plan(T, C, n, r);
   if (!p.ring) return w_t ? hipErrorInvalidValue : launch_multi_rows_small(act, T, C, w, C, r, ai, out, ws, s);
   if (w_t && r % 8 != 0) return hipErrorInvalidValue;
   ai.passes = n < 8 ? n : 8;
@@ -882,8 +912,8 @@ hipError_t launch_multi_grads(const MultiGrad* g, int n_jobs, int64_t T, const i
   if (mb == 0) return hipSuccess;
   const dim3 grid((unsigned)mb, (unsigned)n, (unsigned)(p.njt * p.S));
   if (p.few) {
-    if (r <= 16) launch(SRA_KERNEL_ADAPTER, k_multi_grads_few<1>, grid, dim3(256), 0, s, ga);
-    else launch(SRA_KERNEL_ADAPTER, k_multi_grads_few<2>, grid, dim3(256), 0, s, ga);
+    if (r <= 16) launch(SRA_KERNEL_ADAPTER, k_multi_grads_few<1, 8>, grid, dim3(512), 0, s, ga);
+    else launch(SRA_KERNEL_ADAPTER, k_multi_grads_few<2, 4>, grid, dim3(256), 0, s, ga);
   } else {
     hipLaunchKernelGGL(k_multi_vt, dim3((unsigned)(multi_perm_entries(T, n) / 32), (unsigned)n_jobs, (unsigned)cdiv64(r, 64)),
                        dim3(256), 0, s, ga);
