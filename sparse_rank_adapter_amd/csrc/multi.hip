@@ -5,8 +5,8 @@
 //
 // k_multi_prep, one launch for what the products need from ids, A and B:
 //   workgroup 0 sorts the tokens by adapter (a stable counting sort, so sums run in token order):
-//     each adapter's tokens fill blocks of 32 entries of perm, the last block padded with ~(its last token), a negative number, so that padding loads the
-//     adapter's own data (its V is cleared); tokens with no adapter are left out; the adapters' list
+//     each adapter's tokens fill blocks of 32 entries of perm, the last block padded with -1 (loads
+//     there read token 0 and are cleared); tokens with no adapter are left out; the adapters' list
 //     runs by falling block count (up to 64 adapters), so that the longest start first;
 //   the other workgroups transpose every B_g (the dU product's operand, contiguous along N) and
 //     every A_g (the dX epilogue's rows of r entries), in 64 x 64 tiles.
@@ -59,7 +59,6 @@ __host__ __device__ inline int group_list(int n) { return (n + 1 + 3) / 4 * 4; }
 struct SortLds {
   int hist[kPrepWaves][kMaxAdapters + 1];
   int base[kMaxAdapters + 1];
-  int last[kMaxAdapters + 1];  // the adapter's last token
   int wsum[kPrepWaves];
   int total;
 };
@@ -74,27 +73,23 @@ union PrepLds {
 SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
   for (int i = l; i < a.n; i += 64) s.hist[w][i] = 0;  // wave w's own row
-  if (tid < a.n) s.last[tid] = 0;
   __syncthreads();
   // wave w takes tokens [w * chunk, (w + 1) * chunk)
   const int64_t chunk = ((a.T + kPrepWaves - 1) / kPrepWaves + 63) / 64 * 64;
   const int64_t lo = w * chunk, hi = min(a.T, lo + chunk);
-  constexpr int KEEP = 8;  // ids of the wave's first tokens stay in registers for the second walk
+  constexpr int KEEP = 4;  // ids of the wave's first tokens stay in registers for the second walk
   int kept[KEEP];
 #pragma unroll
   for (int k = 0; k < KEEP; ++k) {
     const int64_t t = lo + 64 * k + l;
     kept[k] = t < hi ? a.ids[t] : -1;
   }
-  auto count = [&](int g, int64_t t) {  // LDS integers: the order does not matter
-    if (g >= 0 && g < a.n) {
-      atomicAdd(&s.hist[w][g], 1);
-      atomicMax(&s.last[g], (int)t);
-    }
+  auto count = [&](int g) {  // LDS integers: the order does not matter
+    if (g >= 0 && g < a.n) atomicAdd(&s.hist[w][g], 1);
   };
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k) count(kept[k], lo + 64 * k + l);
-  for (int64_t t = lo + 64 * KEEP + l; t < hi; t += 64) count(a.ids[t], t);
+  for (int k = 0; k < KEEP; ++k) count(kept[k]);
+  for (int64_t t = lo + 64 * KEEP + l; t < hi; t += 64) count(a.ids[t]);
   __syncthreads();
   // thread g: where each wave's tokens of adapter g start, and the adapter's blocks
   int cnt = 0, blocks = 0;
@@ -123,8 +118,7 @@ SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
   if (tid < a.n) {
     s.base[tid] = first;
     if (tid == a.n - 1) a.gblk[a.n] = incl;
-    const int pad = ~s.last[tid];
-    for (int i = cnt; i < 32 * blocks; ++i) a.perm[(int64_t)first * 32 + i] = pad;
+    for (int i = cnt; i < 32 * blocks; ++i) a.perm[(int64_t)first * 32 + i] = -1;
   }
   __syncthreads();
   if (tid < a.n) {
@@ -337,31 +331,35 @@ __global__ __launch_bounds__(64 * NW) void k_multi_grads_few(GradArgs ga) {
   const int64_t mc = min(m0 + 8 * c8, M - 8);  // past the row: any columns, their sums are not stored
   u32x4 ar[4];
   float vr[JT][8];
+  uint32_t a_ok = 0, v_ok = 0;  // bit: the row (token) is no padding.  Clearing waits for the data, so it
+                                // happens where the data is used, not where it is loaded
   auto perm_of = [&](int b) { return ga.perm[(int64_t)min(b, b1 - 1) * 32 + (l & 31)]; };
-  auto load = [&](int p) {  // p: lane l % 32 holds the block's token l % 32 (~token: padding)
-    const int tk = p ^ (p >> 31);
+  auto load = [&](int p) {  // p: lane l % 32 holds the block's token l % 32 (-1: padding)
+    a_ok = v_ok = 0;
+    int64_t tok[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = __shfl(p, r8 + 8 * i, 64);
+      a_ok |= (uint32_t)(q >= 0) << i;
+      tok[i] = max(q, 0);
+    }
     if (job.act) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        ar[i] = *reinterpret_cast<const u32x4*>(job.act + (int64_t)__shfl(tk, r8 + 8 * i, 64) * M + mc);
+      for (int i = 0; i < 4; ++i) ar[i] = *reinterpret_cast<const u32x4*>(job.act + tok[i] * M + mc);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t tok = __shfl(tk, r8 + 8 * i, 64);
-        const u32x2 q = *reinterpret_cast<const u32x2*>(job.codes + tok * M + mc);
-        ar[i] = u32x4{q[0], q[1], job.exps[tok * nblk + mc / sra_row::kCkBlock], 0};
+        const u32x2 q = *reinterpret_cast<const u32x2*>(job.codes + tok[i] * M + mc);
+        ar[i] = u32x4{q[0], q[1], job.exps[tok[i] * nblk + mc / sra_row::kCkBlock], 0};
       }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int q = __shfl(p, 8 * q4 + e, 64);
-      const int64_t tok = q ^ (q >> 31);
+      v_ok |= (uint32_t)(q >= 0) << e;
+      const float* v = job.V + (int64_t)max(q, 0) * r;
 #pragma unroll
-      for (int a = 0; a < JT; ++a) {
-        const int j = 16 * a + l16;
-        const float v = job.V[tok * r + min(j, r - 1)];
-        vr[a][e] = q >= 0 && j < r ? v : 0.f;
-      }
+      for (int a = 0; a < JT; ++a) vr[a][e] = v[min(16 * a + l16, r - 1)];
     }
   };
   f32x4 acc[JT][4];
@@ -382,14 +380,16 @@ __global__ __launch_bounds__(64 * NW) void k_multi_grads_few(GradArgs ga) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = r8 + 8 * i;
+      const u32x4 x = job.act ? ar[i] : decode8(ar[i][0], ar[i][1], ar[i][2]);
       *reinterpret_cast<u32x4*>(tile + t * (2 * MT) + ((c8 ^ act_swz<MT>(t)) << 4)) =
-          job.act ? ar[i] : decode8(ar[i][0], ar[i][1], ar[i][2]);
+          (a_ok >> i) & 1u ? x : u32x4{0, 0, 0, 0};
     }
     Bf8 vf[JT][3];
 #pragma unroll
     for (int a = 0; a < JT; ++a)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) split3(vr[a][e], vf[a][0].h[e], vf[a][1].h[e], vf[a][2].h[e]);
+      for (int e = 0; e < 8; ++e)
+        split3((v_ok >> e) & 1u && 16 * a + l16 < r ? vr[a][e] : 0.f, vf[a][0].h[e], vf[a][1].h[e], vf[a][2].h[e]);
     if (b + NW < b1) load(p);  // in flight while this block multiplies
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
@@ -439,12 +439,16 @@ __global__ __launch_bounds__(256) void k_multi_vt(GradArgs ga) {
   const int32_t* p = ga.perm + (int64_t)b * 32;
   const int jl = threadIdx.x & 63, j = jb + jl, t8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Bf8 s[3];
+  float x[8];
+  uint32_t ok = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int q = p[8 * t8 + e];
-    const float v = job.V[(int64_t)(q ^ (q >> 31)) * ga.r + min(j, ga.r - 1)];
-    split3(q >= 0 && j < ga.r ? v : 0.f, s[0].h[e], s[1].h[e], s[2].h[e]);
+    x[e] = job.V[(int64_t)max(q, 0) * ga.r + min(j, ga.r - 1)];
+    ok |= (uint32_t)(q >= 0 && j < ga.r) << e;
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) split3((ok >> e) & 1u ? x[e] : 0.f, s[0].h[e], s[1].h[e], s[2].h[e]);
 #pragma unroll
   for (int k = 0; k < 3; ++k)  // 16-byte piece t8 of row (k, jl), pieces swizzled against bank conflicts
     *reinterpret_cast<u32x4*>(lds + ((k * 64 + jl) * 4 + (t8 ^ ((jl >> 2) & 3))) * 8) = s[k].v;
@@ -480,7 +484,7 @@ __global__ __launch_bounds__(512, 4) void k_multi_grads(GradArgs ga) {
 
   // a thread's share of a step: bf16 chunk tid % 32 of rows tid / 32 and tid / 32 + 16, or 16 codes
   // tid % 16 of row tid / 16.  Every load is unconditional: columns past the row read its last ones
-  // (not stored), padding reads the adapter's last token (V is zero there).
+  // (not stored), padding reads token 0 and is cleared on the way to LDS.
   const bool bf = job.act != nullptr;
   const int t0 = bf ? tid >> 5 : tid >> 4, cc = bf ? tid & 31 : tid & 15;
   const int64_t mc = min(m0 + (bf ? 8 : 16) * cc, M - (bf ? 8 : 16));
@@ -489,13 +493,16 @@ __global__ __launch_bounds__(512, 4) void k_multi_grads(GradArgs ga) {
   const uint8_t* const ecol = job.exps + mc / sra_row::kCkBlock;
   u32x4 a0, a1;
   int p0, p1;
+  uint32_t ok0 = 0, ok1 = 0;  // all ones: the rows of a0 / a1 are no padding
   auto toks = [&](int b) {
     const int32_t* p = ga.perm + (int64_t)min(b, b1 - 1) * 32;
     p0 = p[t0];
     p1 = p[(t0 + 16) & 31];
   };
   auto load_act = [&]() {
-    const int64_t q0 = p0 ^ (p0 >> 31), q1 = p1 ^ (p1 >> 31);
+    const int64_t q0 = max(p0, 0), q1 = max(p1, 0);
+    ok0 = ~(uint32_t)(p0 >> 31);
+    ok1 = bf ? ~(uint32_t)(p1 >> 31) : ok0;
     a0 = *reinterpret_cast<const u32x4*>(col + q0 * rowb);
     if (bf) a1 = *reinterpret_cast<const u32x4*>(col + q1 * rowb);
     else a1[0] = ecol[q0 * nblk];
@@ -505,6 +512,11 @@ __global__ __launch_bounds__(512, 4) void k_multi_grads(GradArgs ga) {
     if (!bf) {
       x0 = decode8(a0[0], a0[1], a1[0]);
       x1 = decode8(a0[2], a0[3], a1[0]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x0[k] &= ok0;
+      x1[k] &= ok1;
     }
     const int r1 = bf ? t0 + 16 : t0, c0 = bf ? cc : 2 * cc, c1 = bf ? cc : 2 * cc + 1;
     *reinterpret_cast<u32x4*>(buf + t0 * (2 * MT) + ((c0 ^ act_swz<MT>(t0)) << 4)) = x0;
