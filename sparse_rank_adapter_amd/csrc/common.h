@@ -119,6 +119,47 @@ SRA_DEV void ring_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// Transposing LDS reads (ds_read_b64_tr_b16) of several MFMA fragments and their wait in one block.
+// The compiler puts a wait for every outstanding transfer in front of the builtin form when
+// buffer -> LDS transfers are in flight (it cannot tell their targets apart), which emptied the
+// rings each stage; ordinary LDS reads do not suffer so.  A fragment is two reads, rows t and t + 4 of a
+// tile: for addresses a[k] (LDS byte offsets), out[k] = (a[k] + OFF, a[k] + OFF + H).
+typedef __attribute__((address_space(3))) const uint8_t* lds_cptr_t;
+SRA_DEV uint32_t lds_offset(const uint8_t* p) { return (uint32_t)(uintptr_t)(lds_cptr_t)p; }
+union TrFrag {
+  u32x2 h[2];
+  bf16x8 b;
+};
+template <int OFF, int H>
+SRA_DEV void lds_tr_frags(const uint32_t (&a)[1], TrFrag (&o)[1]) {
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %2 offset:%3\n\tds_read_b64_tr_b16 %1, %2 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(o[0].h[0]), "=&v"(o[0].h[1])
+      : "v"(a[0]), "n"(OFF), "n"(OFF + H)
+      : "memory");
+}
+template <int OFF, int H>
+SRA_DEV void lds_tr_frags(const uint32_t (&a)[2], TrFrag (&o)[2]) {
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %4 offset:%6\n\tds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+      "ds_read_b64_tr_b16 %2, %5 offset:%6\n\tds_read_b64_tr_b16 %3, %5 offset:%7\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(o[0].h[0]), "=&v"(o[0].h[1]), "=&v"(o[1].h[0]), "=&v"(o[1].h[1])
+      : "v"(a[0]), "v"(a[1]), "n"(OFF), "n"(OFF + H)
+      : "memory");
+}
+template <int OFF, int H>
+SRA_DEV void lds_tr_frags(const uint32_t (&a)[4], TrFrag (&o)[4]) {
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %2, %9 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %4, %10 offset:%12\n\tds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %6, %11 offset:%12\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(o[0].h[0]), "=&v"(o[0].h[1]), "=&v"(o[1].h[0]), "=&v"(o[1].h[1]), "=&v"(o[2].h[0]), "=&v"(o[2].h[1]),
+        "=&v"(o[3].h[0]), "=&v"(o[3].h[1])
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(OFF), "n"(OFF + H)
+      : "memory");
+}
+
 // ---- host-side launchers implemented in the kernel sources (internal C++ linkage)
 namespace sra {
 

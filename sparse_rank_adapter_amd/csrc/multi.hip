@@ -263,11 +263,12 @@ SRA_DEV u32x4 decode8(uint32_t lo, uint32_t hi, uint32_t exp) {
   return x;
 }
 
-// chunk swizzle of the Act tile's token row t (8 chunks of 16 bytes per row, or 32): over the rows of
-// one transposing read the 32-byte windows spread over the LDS banks
+// chunk swizzle of a tile's row t (8 chunks of 16 bytes per row, or 16 and more): over the rows of one
+// transposing read the 32-byte windows spread over the LDS banks.  Bit 2 of t is not used, so the two
+// reads of a fragment, four rows apart, have one swizzle (and so have rows 32 apart).
 template <int MT>
 SRA_DEV int act_swz(int t) {
-  return MT == 64 ? 2 * (((t >> 1) ^ (t >> 3)) & 3) : 2 * ((t & 3) | (((t >> 3) & 1) << 2));
+  return MT == 64 ? 2 * (((t >> 1) & 1) | (((t >> 3) & 1) << 1)) : 2 * ((t & 3) | (((t >> 3) & 1) << 2));
 }
 // B operand of 16 columns from m0 (a multiple of 16) of an Act tile [32][MT]
 template <int MT>
@@ -465,14 +466,15 @@ __global__ __launch_bounds__(256) void k_multi_vt(GradArgs ga) {
 
 // WJ = 1: 64 adapter columns, 2: 128.  grid: (column tiles, adapters, adapter column tiles x slices).
 // The V tile goes to LDS by buffer -> LDS transfers, Act through registers (a checkpoint is decoded
-// there), both one step ahead; at most 128 registers and 80 KB of LDS, so two workgroups share a CU
-// and one's loads, LDS writes and barrier run under the other's products.
+// there), both two steps ahead: with one step ahead and two workgroups per CU every step waited for
+// its loads (192 us; 131 us with the loads taken out, and as much with the products taken out).
 template <int WJ>
-__global__ __launch_bounds__(512, 4) void k_multi_grads(GradArgs ga) {
+__global__ __launch_bounds__(512, 2) void k_multi_grads(GradArgs ga) {
   constexpr int MT = 256, JR = 64 * WJ, MF = 2 * WJ;
-  constexpr int A_BYTES = 32 * MT * 2, V_BYTES = 3 * JR * 64, BUF = A_BYTES + V_BYTES;
+  constexpr int A_BYTES = 32 * MT * 2, V_BYTES = 3 * JR * 64;
   constexpr int NV = V_BYTES / 1024;  // 1 KB transfers: 12 or 24
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BUF];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * A_BYTES + 3 * V_BYTES];
+  uint8_t* const vlds = lds + 2 * A_BYTES;
   const int tid = threadIdx.x, l = tid & 63, l16 = l & 15, q4 = l >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wj = w % WJ, wm = w / WJ;
   const bool second = (int)blockIdx.x >= ga.job[0].mb;
@@ -490,33 +492,38 @@ __global__ __launch_bounds__(512, 4) void k_multi_grads(GradArgs ga) {
   const int64_t mc = min(m0 + (bf ? 8 : 16) * cc, M - (bf ? 8 : 16));
   const uint8_t* const col = bf ? reinterpret_cast<const uint8_t*>(job.act + mc) : reinterpret_cast<const uint8_t*>(job.codes + mc);
   const int64_t rowb = bf ? 2 * M : M, nblk = (M + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
-  const uint8_t* const ecol = job.exps + mc / sra_row::kCkBlock;
-  u32x4 a0, a1;
-  int p0, p1;
-  uint32_t ok0 = 0, ok1 = 0;  // all ones: the rows of a0 / a1 are no padding
+  // (bf16: the exponent's load stays, one per step for either kind, and reads Act's first byte)
+  const uint8_t* const ecol = bf ? reinterpret_cast<const uint8_t*>(job.act) : job.exps + mc / sra_row::kCkBlock;
+  struct Act {
+    u32x4 a0, a1;
+    uint32_t e;         // checkpoint: the scale's exponent
+    uint32_t ok0, ok1;  // all ones: the rows of a0 / a1 are no padding
+  };
+  struct Toks {
+    int p0, p1;
+  };
   auto toks = [&](int b) {
     const int32_t* p = ga.perm + (int64_t)min(b, b1 - 1) * 32;
-    p0 = p[t0];
-    p1 = p[(t0 + 16) & 31];
+    return Toks{p[t0], p[(t0 + 16) & 31]};
   };
-  auto load_act = [&]() {
-    const int64_t q0 = max(p0, 0), q1 = max(p1, 0);
-    ok0 = ~(uint32_t)(p0 >> 31);
-    ok1 = bf ? ~(uint32_t)(p1 >> 31) : ok0;
-    a0 = *reinterpret_cast<const u32x4*>(col + q0 * rowb);
-    if (bf) a1 = *reinterpret_cast<const u32x4*>(col + q1 * rowb);
-    else a1[0] = ecol[q0 * nblk];
+  auto load_act = [&](const Toks& t, Act& s) {
+    const int64_t q0 = max(t.p0, 0), q1 = max(t.p1, 0);
+    s.ok0 = ~(uint32_t)(t.p0 >> 31);
+    s.ok1 = bf ? ~(uint32_t)(t.p1 >> 31) : s.ok0;
+    s.a0 = *reinterpret_cast<const u32x4*>(col + q0 * rowb);
+    s.a1 = *reinterpret_cast<const u32x4*>(col + (bf ? q1 : q0) * rowb);  // (checkpoint: the same line again)
+    s.e = ecol[bf ? 0 : q0 * nblk];
   };
-  auto store_act = [&](uint8_t* buf) {
-    u32x4 x0 = a0, x1 = a1;
+  auto store_act = [&](uint8_t* buf, const Act& s) {
+    u32x4 x0 = s.a0, x1 = s.a1;
     if (!bf) {
-      x0 = decode8(a0[0], a0[1], a1[0]);
-      x1 = decode8(a0[2], a0[3], a1[0]);
+      x0 = decode8(s.a0[0], s.a0[1], s.e);
+      x1 = decode8(s.a0[2], s.a0[3], s.e);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      x0[k] &= ok0;
-      x1[k] &= ok1;
+      x0[k] &= s.ok0;
+      x1[k] &= s.ok1;
     }
     const int r1 = bf ? t0 + 16 : t0, c0 = bf ? cc : 2 * cc, c1 = bf ? cc : 2 * cc + 1;
     *reinterpret_cast<u32x4*>(buf + t0 * (2 * MT) + ((c0 ^ act_swz<MT>(t0)) << 4)) = x0;
@@ -530,23 +537,29 @@ __global__ __launch_bounds__(512, 4) void k_multi_grads(GradArgs ga) {
     const int x = 16 * (8 * i + w) + (l >> 2), c = (l & 3) ^ ((x >> 2) & 3), k = x / JR, j = j0 + x % JR;
     v_off[i] = (uint32_t)((k * ga.rp + j) * 64 + 16 * c);
   }
-  auto issue_v = [&](int b, uint8_t* buf) {
+  auto issue_v = [&](int b) {
+    uint8_t* const buf = vlds + (b - b0) % 3 * V_BYTES;
     const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(job.vt + (int64_t)b * 3 * ga.rp * 32), 0, vtile, 0x00020000);
+        (void*)(job.vt + (int64_t)min(b, b1 - 1) * 3 * ga.rp * 32), 0, vtile, 0x00020000);
 #pragma unroll
     for (int i = 0; i < (NV + 7) / 8; ++i)
-      if (8 * i + 8 <= NV || 8 * i + w < NV) lds_dma(rv, buf + A_BYTES + (8 * i + w) * 1024, v_off[i], 0);
+      if (8 * i + 8 <= NV || 8 * i + w < NV) lds_dma(rv, buf + (8 * i + w) * 1024, v_off[i], 0);
   };
   f32x4 acc[4][MF];
 #pragma unroll
   for (int a = 0; a < 4; ++a)
 #pragma unroll
     for (int f = 0; f < MF; ++f) acc[a][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](const uint8_t* buf) {
-    bf16x8 b[MF];
+  uint32_t act_addr[MF];  // this wave's fragments of an Act tile (rows t and t + 4 share their swizzle)
 #pragma unroll
-    for (int f = 0; f < MF; ++f) b[f] = act_frag<MT>(buf, (wm * MF + f) * 16, l16, q4);
-    const uint8_t* vb = buf + A_BYTES;
+  for (int f = 0; f < MF; ++f) {
+    const int t = 8 * q4 + (l16 >> 2), m = (wm * MF + f) * 16 + 4 * (l16 & 3);
+    act_addr[f] = lds_offset(lds) + t * (2 * MT) + (((m >> 3) ^ act_swz<MT>(t)) << 4) + (m & 7) * 2;
+  }
+  auto compute = [&](bool odd, const uint8_t* vb) {
+    TrFrag b[MF];
+    if (odd) lds_tr_frags<A_BYTES, 8 * MT>(act_addr, b);
+    else lds_tr_frags<0, 8 * MT>(act_addr, b);
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -554,31 +567,46 @@ __global__ __launch_bounds__(512, 4) void k_multi_grads(GradArgs ga) {
         const int x = k * JR + 64 * wj + 16 * a + l16;
         const bf16x8 v = *reinterpret_cast<const bf16x8*>(vb + x * 64 + ((q4 ^ ((x >> 2) & 3)) << 4));
 #pragma unroll
-        for (int f = 0; f < MF; ++f) acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[f], acc[a][f], 0, 0, 0);
+        for (int f = 0; f < MF; ++f) acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[f].b, acc[a][f], 0, 0, 0);
       }
   };
 
-  // step b: its Act goes from registers to LDS, one barrier (every wave is then past its reads of
-  // the other buffer, and step b's transfers have landed), the loads of step b + 1 are issued, and
-  // it multiplies
+  // Step b: its Act goes from registers to LDS; its transfers have landed when at most what step
+  // b + 1 issued is outstanding (two loads of tokens, three of Act, the V transfers); one barrier, after
+  // which every wave is past step b - 1's reads, so the loads of step b + 2 may go to its buffers;
+  // then it multiplies.  Loads past the last block repeat it, so every step issues the same number.
+  Act s0, s1;
+  Toks tk{0, 0};
   if (b0 < b1) {
-    toks(b0);
-    load_act();
-    issue_v(b0, lds);
-    toks(b0 + 1);
+    const Toks ta = toks(b0), tb = toks(b0 + 1);
+    tk = toks(b0 + 2);
+    load_act(ta, s0);
+    issue_v(b0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_act(tb, s1);
+    issue_v(b0 + 1);
+    __builtin_amdgcn_sched_barrier(0);
   }
-  for (int b = b0; b < b1; ++b) {
-    uint8_t* const buf = lds + ((b - b0) & 1) * BUF;
-    store_act(buf);
-    wait_vm_all<0>();
-    __syncthreads();
-    if (b + 1 < b1) {
-      load_act();
-      issue_v(b + 1, lds + ((b + 1 - b0) & 1) * BUF);
-      toks(b + 2);
-    }
-    compute(buf);
+  auto step = [&](int b, Act& s, uint8_t* buf) {
+    store_act(buf, s);
+    if (NV % 8 == 0 || w < NV % 8) wait_vm_all<2 + 3 + (NV + 7) / 8>();
+    else wait_vm_all<2 + 3 + NV / 8>();
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // lgkmcnt(0): this wave's LDS writes are done
+    ring_barrier();
+    const Toks next = toks(b + 3);
+    load_act(tk, s);
+    issue_v(b + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    tk = next;
+    compute(buf != lds, vlds + (b - b0) % 3 * V_BYTES);
+  };
+  int b = b0;
+  for (; b + 1 < b1; b += 2) {
+    step(b, s0, lds);
+    step(b + 1, s1, lds + A_BYTES);
   }
+  if (b < b1) step(b, s0, lds);
+  wait_vm_all<0>();  // the repeated transfers land before this workgroup gives its LDS back
 
 #pragma unroll
   for (int a = 0; a < 4; ++a)
@@ -661,6 +689,15 @@ __global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restric
   };
   __amdgpu_buffer_rsrc_t rg = weight(0);
 
+  // TW: this wave's fragments (16 adapter columns each) of a stage's [SC][JR] tile; rows t and t + 4
+  // share their swizzle, and so do k steps 32 rows apart
+  uint32_t tr_addr[JW];
+#pragma unroll
+  for (int a = 0; a < JW; ++a) {
+    const int t = 8 * q4 + (l16 >> 2), col = 16 * (JW * wj + a) + 4 * (l16 & 3);
+    tr_addr[a] = lds_offset(lds) + A_BYTES + t * (2 * JR) + (((col >> 3) ^ act_swz<JR>(t)) << 4) + (col & 7) * 2;
+  }
+
   f32x4 acc[2][JW];
   auto pass = [&] {
     auto issue = [&](int st) {
@@ -697,19 +734,19 @@ __global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restric
           const int x = 32 * wt + 16 * i + l16;
           af[i] = *reinterpret_cast<const bf16x8*>(A + x * RB + ((k ^ swz(x)) << 4));
         }
+        if constexpr (TW) {
+          uint32_t at[JW];
+          TrFrag fr[JW];
 #pragma unroll
-        for (int a = 0; a < JW; ++a) {
-          const int j = 16 * (JW * wj + a);
-          if constexpr (TW) {
-            Bf8 u;
+          for (int a = 0; a < JW; ++a) at[a] = tr_addr[a] + (st % NS) * STAGE;
+          if (ks == 0) lds_tr_frags<0, 8 * JR>(at, fr);
+          else lds_tr_frags<64 * JR, 8 * JR>(at, fr);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int t = 32 * ks + 8 * q4 + 4 * h + (l16 >> 2), col = j + 4 * (l16 & 3);
-              u.half[h] = lds_tr(G + t * (2 * JR) + (((col >> 3) ^ act_swz<JR>(t)) << 4) + (col & 7) * 2);
-            }
-            gf[a] = u.b;
-          } else {
-            const int x = j + l16;
+          for (int a = 0; a < JW; ++a) gf[a] = fr[a].b;
+        } else {
+#pragma unroll
+          for (int a = 0; a < JW; ++a) {
+            const int x = 16 * (JW * wj + a) + l16;
             gf[a] = *reinterpret_cast<const bf16x8*>(G + x * RB + ((k ^ swz(x)) << 4));
           }
         }
