@@ -160,6 +160,17 @@ SRA_DEV void lds_tr_frags(const uint32_t (&a)[4], TrFrag (&o)[4]) {
       : "memory");
 }
 
+// the same for fragments whose two halves have their own addresses a[2 k], a[2 k + 1]
+template <int OFF>
+SRA_DEV void lds_tr_reads(const uint32_t (&a)[4], TrFrag (&o)[2]) {
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %4 offset:%8\n\tds_read_b64_tr_b16 %1, %5 offset:%8\n\t"
+      "ds_read_b64_tr_b16 %2, %6 offset:%8\n\tds_read_b64_tr_b16 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(o[0].h[0]), "=&v"(o[0].h[1]), "=&v"(o[1].h[0]), "=&v"(o[1].h[1])
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(OFF)
+      : "memory");
+}
+
 // ---- host-side launchers implemented in the kernel sources (internal C++ linkage)
 namespace sra {
 

@@ -11,7 +11,8 @@
 // only its stored half leaves.  The reduction (tokens) runs along the rows of both operands in
 // memory, while an MFMA lane needs 8 consecutive reduction elements.  Each 64-token stage is copied
 // as it lies (rows of tokens) from global memory to LDS by buffer -> LDS transfers into a three-
-// stage ring, and the fragments are read with ds_read_b64_tr_b16, gfx950's transposing LDS read:
+// stage ring, and the fragments are read with ds_read_b64_tr_b16, gfx950's transposing LDS read
+// (in blocks with their own wait, see lds_tr_frags: the builtin form drained the ring every stage):
 // within a group of 16 lanes, lane i receives element i % 4 of the 8-byte pieces addressed by lanes
 // i / 4 + 4 r (r = 0..3).  So lane j (r = j / 4, s = j % 4) of lane group g addresses row
 // t = 8 g + 4 h + r and columns m0 + 4 s .. +3, and lane i gets column m0 + i at tokens
@@ -27,21 +28,25 @@
 
 namespace {
 
-constexpr int SD_BM = 64, SD_BC = 128, SD_BT = 64;  // rows, logical columns, tokens per stage
-constexpr int SD_NS = 3;                            // ring stages
-constexpr int SD_AROW = SD_BM * 2, SD_BROW = SD_BC * 2;        // bytes per token row of each tile
-constexpr int SD_ASTG = SD_BT * SD_AROW, SD_BSTG = SD_BT * SD_BROW;
-constexpr int SD_STAGE = SD_ASTG + SD_BSTG;                    // 24 KB
-constexpr int SD_DLD = SD_BC + 4;                              // LDS row stride of the fp32 block
-constexpr int SD_LA = SD_ASTG / (1024 * 4), SD_LB = SD_BSTG / (1024 * 4);  // 1 KB transfers per wave
-static_assert(SD_BM * SD_DLD * 4 <= SD_NS * SD_STAGE, "the output block fits over the ring");
+constexpr int SD_BC = 128, SD_BT = 64;       // logical columns, tokens per stage
+constexpr int SD_NS = 3;                     // ring stages
+constexpr int SD_BROW = SD_BC * 2;           // bytes per token row of the column tile
+constexpr int SD_BSTG = SD_BT * SD_BROW;
+constexpr int SD_DLD = SD_BC + 4;            // LDS row stride of the fp32 block
+// BM rows per workgroup of BM / 16 waves
+template <int BM>
+struct SdTile {
+  static constexpr int NW = BM / 16, AROW = BM * 2, ASTG = SD_BT * AROW, STAGE = ASTG + SD_BSTG;  // 24 or 32 KB
+  static constexpr int LA = ASTG / (1024 * NW), LB = SD_BSTG / (1024 * NW);  // 1 KB transfers per wave
+  static_assert(BM * SD_DLD * 4 <= SD_NS * STAGE, "the output block fits over the ring");
+};
 
 typedef __attribute__((address_space(3))) void* sd_lds_t;
-typedef short sd_v4s __attribute__((ext_vector_type(4)));
 
 // chunk swizzles (16-byte chunks, even values keep chunk pairs together): over the 16 rows one
 // transposing read touches, the 32-byte windows land in 8 distinct bank windows, twice each
-SRA_DEV int swz_a(int t) { return 2 * (((t >> 1) ^ (t >> 3)) & 3); }
+template <int BM>
+SRA_DEV int swz_a(int t) { return BM == 64 ? 2 * (((t >> 1) ^ (t >> 3)) & 3) : 2 * ((t & 3) | (((t >> 3) & 1) << 2)); }
 SRA_DEV int swz_b(int t) { return 2 * ((t & 3) | (((t >> 3) & 1) << 2)); }
 
 SRA_DEV void sd_dma(__amdgpu_buffer_rsrc_t rs, uint8_t* lds_block, uint32_t voff, int soff) {
@@ -52,19 +57,22 @@ SRA_DEV void sd_wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
-// half of an MFMA fragment (4 tokens of 16 rows or columns) by one transposing read
-SRA_DEV sd_v4s sd_tr(const uint8_t* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) sd_v4s*)p);
-}
-
-__global__ __launch_bounds__(256, 2) void k_sddmm24(const uint16_t* __restrict__ ra,
+template <int BM>
+__global__ __launch_bounds__(4 * BM, 2) void k_sddmm24(const uint16_t* __restrict__ ra,
                                                     const uint16_t* __restrict__ ca,
                                                     const uint32_t* __restrict__ meta, uint32_t meta_or,
                                                     int64_t R, int64_t C, int64_t T,
                                                     uint16_t* __restrict__ out) {
+  using TL = SdTile<BM>;
+  constexpr int SD_AROW = TL::AROW, SD_ASTG = TL::ASTG, SD_STAGE = TL::STAGE, SD_LA = TL::LA, SD_LB = TL::LB, NW = TL::NW;
   __shared__ __attribute__((aligned(16))) uint8_t lds[SD_NS * SD_STAGE];
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, l16 = l & 15, q4 = l >> 4;
-  const int64_t c0 = (int64_t)blockIdx.x * SD_BC, r0 = (int64_t)blockIdx.y * SD_BM;
+  // workgroups go to the 8 XCDs in turn: XCD x takes an eighth of the tiles in one piece (columns
+  // fastest), so its L2 holds a band of row_act instead of all of it
+  const int n_ct = (int)((C + SD_BC - 1) / SD_BC), n_wg = (int)gridDim.x;
+  const int xcd = blockIdx.x & 7, per = n_wg >> 3, rem = n_wg & 7;
+  const int lin = xcd * per + min(xcd, rem) + (int)(blockIdx.x >> 3);
+  const int64_t c0 = (int64_t)(lin % n_ct) * SD_BC, r0 = (int64_t)(lin / n_ct) * BM;
   const int nst = (int)((T + SD_BT - 1) / SD_BT);
 
   // buffer resources based at the tile's first column; rows past T are past the range (zeros),
@@ -73,19 +81,20 @@ __global__ __launch_bounds__(256, 2) void k_sddmm24(const uint16_t* __restrict__
       (void*)(ra + r0), (short)0, (int)((T * R - r0) * 2), 0x00020000);
   const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(ca + c0), (short)0, (int)((T * C - c0) * 2), 0x00020000);
-  // transfer k of this wave: A block q = k * 4 + w covers tile rows 8q .. 8q+7 (lane: row 8q + l/8,
-  // physical chunk l % 8); B block q covers rows 4q .. 4q+3 (row 4q + l/16, chunk l % 16).  The
-  // lane fetches the logical chunk that its slot holds under the swizzle.
+  // transfer k of this wave: A block q = k * NW + w covers 512 / BM tile rows (BM / 8 chunks each); B
+  // block q covers rows 4q .. 4q+3 (row 4q + l/16, chunk l % 16).  The lane fetches the logical
+  // chunk that its slot holds under the swizzle.
   uint32_t a_off[SD_LA], b_off[SD_LB];
 #pragma unroll
   for (int k = 0; k < SD_LA; ++k) {
-    const int q = k * 4 + w, t = 8 * q + (l >> 3), lc = (l & 7) ^ swz_a(t);
+    constexpr int CH = BM / 8;
+    const int q = k * NW + w, t = (64 / CH) * q + l / CH, lc = (l % CH) ^ swz_a<BM>(t);
     const bool in = r0 + 8 * lc < R;
     a_off[k] = (uint32_t)((t * R + 8 * lc) * 2) | ((uint32_t)!in << 31);
   }
 #pragma unroll
   for (int k = 0; k < SD_LB; ++k) {
-    const int q = k * 4 + w, t = 4 * q + (l >> 4), lc = (l & 15) ^ swz_b(t);
+    const int q = k * NW + w, t = 4 * q + (l >> 4), lc = (l & 15) ^ swz_b(t);
     const bool in = c0 + 8 * lc < C;
     b_off[k] = (uint32_t)((t * C + 8 * lc) * 2) | ((uint32_t)!in << 31);
   }
@@ -93,27 +102,33 @@ __global__ __launch_bounds__(256, 2) void k_sddmm24(const uint16_t* __restrict__
     uint8_t* base = lds + buf * SD_STAGE;
     const int soff_a = (int)((int64_t)st * SD_BT * R * 2), soff_b = (int)((int64_t)st * SD_BT * C * 2);
 #pragma unroll
-    for (int k = 0; k < SD_LA; ++k) sd_dma(rsa, base + (k * 4 + w) * 1024, a_off[k], soff_a);
+    for (int k = 0; k < SD_LA; ++k) sd_dma(rsa, base + (k * NW + w) * 1024, a_off[k], soff_a);
 #pragma unroll
-    for (int k = 0; k < SD_LB; ++k) sd_dma(rsb, base + SD_ASTG + (k * 4 + w) * 1024, b_off[k], soff_b);
-  };
-
-  // fragment read addresses: lane (group g = q4, j = l16: r = j/4, s = j%4), half h, K-step kk
-  const int fr = l16 >> 2, fs = l16 & 3;
-  auto frag = [&](const uint8_t* tile, int rowb, bool is_a, int m0, int kk) {
-    union { sd_v4s h[2]; bf16x8 v; } u;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = 32 * kk + 8 * q4 + 4 * h + fr, col = m0 + 4 * fs;
-      const int pc = (col >> 3) ^ (is_a ? swz_a(t) : swz_b(t));
-      u.h[h] = sd_tr(tile + t * rowb + pc * 16 + (col & 7) * 2);
-    }
-    return u.v;
+    for (int k = 0; k < SD_LB; ++k) sd_dma(rsb, base + SD_ASTG + (k * NW + w) * 1024, b_off[k], soff_b);
   };
 
   // wave w: rows 32 (w / 2) .. +31 (two row fragments) against columns 64 (w % 2) .. +63 (four
   // column fragments): six fragment reads per 32-token step for eight products
   const int wr = 32 * (w >> 1), wc = 64 * (w & 1);
+  // fragment read addresses: lane (group g = q4, j = l16: r = j/4, s = j%4) reads row 8 g + 4 h + r of
+  // the step for half h.  The column tile's swizzle is the same for both halves, the 64-row tile's is
+  // not; a step of 32 tokens further down both are the same again.
+  const int fr = l16 >> 2, fs = l16 & 3;
+  uint32_t a_addr[2][2], b_addr[4];  // [half][fragment]
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int col = wr + 16 * i + 4 * fs;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = 8 * q4 + 4 * h + fr;
+      a_addr[h][i] = lds_offset(lds) + t * SD_AROW + (((col >> 3) ^ swz_a<BM>(t)) << 4) + (col & 7) * 2;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int t = 8 * q4 + fr, col = wc + 16 * j + 4 * fs;
+    b_addr[j] = lds_offset(lds) + SD_ASTG + t * SD_BROW + (((col >> 3) ^ swz_b(t)) << 4) + (col & 7) * 2;
+  }
   f32x4 d[2][4];
   double acc[2][4][4];
 #pragma unroll
@@ -133,16 +148,25 @@ __global__ __launch_bounds__(256, 2) void k_sddmm24(const uint16_t* __restrict__
         for (int e = 0; e < 4; ++e) acc[i][j][e] += (double)d[i][j][e];
   };
   auto compute = [&](int buf) {
-    const uint8_t* at = lds + buf * SD_STAGE;
-    const uint8_t* bt = at + SD_ASTG;
+    const uint32_t base = (uint32_t)(buf * SD_STAGE);
+    const uint32_t aa[4] = {a_addr[0][0] + base, a_addr[1][0] + base, a_addr[0][1] + base, a_addr[1][1] + base};
+    const uint32_t ba[4] = {b_addr[0] + base, b_addr[1] + base, b_addr[2] + base, b_addr[3] + base};
     flush();
 #pragma unroll
     for (int kk = 0; kk < SD_BT / 32; ++kk) {
+      TrFrag af[2], bf[4];
+      if (kk == 0) {
+        lds_tr_reads<0>(aa, af);
+        lds_tr_frags<0, 4 * SD_BROW>(ba, bf);
+      } else {
+        lds_tr_reads<32 * SD_AROW>(aa, af);
+        lds_tr_frags<32 * SD_BROW, 4 * SD_BROW>(ba, bf);
+      }
       bf16x8 a[2], b[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) a[i] = frag(at, SD_AROW, true, wr + 16 * i, kk);
+      for (int i = 0; i < 2; ++i) a[i] = af[i].b;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = frag(bt, SD_BROW, false, wc + 16 * j, kk);
+      for (int j = 0; j < 4; ++j) b[j] = bf[j].b;
       __builtin_amdgcn_sched_barrier(0);  // every read of the step ahead of its products
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -270,9 +294,15 @@ hipError_t launch_sddmm24_bf16(const uint16_t* row_act, const uint16_t* col_act,
   if (R <= 0 || C <= 0) return hipSuccess;
   if (R % 8 != 0 || C % 32 != 0) return hipErrorInvalidValue;
   if (!sddmm24_fits(R, C, T)) return hipErrorInvalidValue;  // 32-bit buffer offsets
-  const dim3 grid((unsigned)((C + SD_BC - 1) / SD_BC), (unsigned)((R + SD_BM - 1) / SD_BM));
-  launch(SRA_KERNEL_WEIGHT_GRAD, k_sddmm24, grid, dim3(256), 0, s, row_act, col_act, meta, meta_or, R, C,
-         T, out);
+  // 128 rows per workgroup (one per CU) once those fill the GPU: the transfers to LDS bound the kernel,
+  // and this tile moves a third less per product; 64 rows (two per CU) below that
+  const int64_t ct = (C + SD_BC - 1) / SD_BC;
+  if (ct * ((R + 127) / 128) >= 256)
+    launch(SRA_KERNEL_WEIGHT_GRAD, k_sddmm24<128>, dim3((unsigned)(ct * ((R + 127) / 128))), dim3(512), 0, s, row_act,
+           col_act, meta, meta_or, R, C, T, out);
+  else
+    launch(SRA_KERNEL_WEIGHT_GRAD, k_sddmm24<64>, dim3((unsigned)(ct * ((R + 63) / 64))), dim3(256), 0, s, row_act,
+           col_act, meta, meta_or, R, C, T, out);
   return hipGetLastError();
 }
 
