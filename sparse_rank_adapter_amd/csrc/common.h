@@ -119,57 +119,42 @@ SRA_DEV void ring_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Transposing LDS reads (ds_read_b64_tr_b16) of several MFMA fragments and their wait in one block.
-// The compiler puts a wait for every outstanding transfer in front of the builtin form when
-// buffer -> LDS transfers are in flight (it cannot tell their targets apart), which emptied the
-// rings each stage; ordinary LDS reads do not suffer so.  A fragment is two reads, rows t and t + 4 of a
-// tile: for addresses a[k] (LDS byte offsets), out[k] = (a[k] + OFF, a[k] + OFF + H).
+// 16-byte buffer -> LDS transfers (lane i's bytes land at block + 16 i) for kernels that also use the
+// transposing LDS reads (ds_read_b64_tr_b16).  With the builtin transfer the compiler puts a wait for
+// every outstanding transfer in front of each transposing read (it cannot tell their targets apart),
+// which empties a ring at every stage; issued from here they are not seen, so the kernel itself waits
+// for the stage it reads.  The compiler's own vmcnt waits stay right: transfers it does not count only make
+// them wait longer.  No register is written, and addresses are read at issue.
+typedef int32_t dma_rsrc_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) const uint8_t* lds_cptr_t;
 SRA_DEV uint32_t lds_offset(const uint8_t* p) { return (uint32_t)(uintptr_t)(lds_cptr_t)p; }
+SRA_DEV dma_rsrc_t dma_rsrc(const void* base, uint32_t bytes) {  // uniform; offsets past `bytes` read zeros
+  const uint64_t b = (uint64_t)(uintptr_t)base;
+  dma_rsrc_t r;
+  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32) & 0xffff);
+  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
+  r[3] = 0x00020000;
+  return r;
+}
+SRA_DEV void lds_dma(const dma_rsrc_t& rs, uint32_t block, uint32_t off, int soff) {
+  // the nops cover what the compiler would insert around its own form: one wait state after M0 is
+  // written, five after a vector instruction writes a scalar register that the transfer reads.  M0 is
+  // reserved: nothing else in a kernel that uses this may depend on it (no builtin transfer).
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane((int)block)), "v"(off), "s"(rs), "s"(soff)
+               : "memory");
+}
+typedef short tr_v4s __attribute__((ext_vector_type(4)));
+// half of an MFMA fragment by one transposing read
+SRA_DEV tr_v4s lds_tr(const uint8_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tr_v4s*)p);
+}
 union TrFrag {
-  u32x2 h[2];
+  tr_v4s h[2];
   bf16x8 b;
 };
-template <int OFF, int H>
-SRA_DEV void lds_tr_frags(const uint32_t (&a)[1], TrFrag (&o)[1]) {
-  asm volatile(
-      "ds_read_b64_tr_b16 %0, %2 offset:%3\n\tds_read_b64_tr_b16 %1, %2 offset:%4\n\ts_waitcnt lgkmcnt(0)"
-      : "=&v"(o[0].h[0]), "=&v"(o[0].h[1])
-      : "v"(a[0]), "n"(OFF), "n"(OFF + H)
-      : "memory");
-}
-template <int OFF, int H>
-SRA_DEV void lds_tr_frags(const uint32_t (&a)[2], TrFrag (&o)[2]) {
-  asm volatile(
-      "ds_read_b64_tr_b16 %0, %4 offset:%6\n\tds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
-      "ds_read_b64_tr_b16 %2, %5 offset:%6\n\tds_read_b64_tr_b16 %3, %5 offset:%7\n\ts_waitcnt lgkmcnt(0)"
-      : "=&v"(o[0].h[0]), "=&v"(o[0].h[1]), "=&v"(o[1].h[0]), "=&v"(o[1].h[1])
-      : "v"(a[0]), "v"(a[1]), "n"(OFF), "n"(OFF + H)
-      : "memory");
-}
-template <int OFF, int H>
-SRA_DEV void lds_tr_frags(const uint32_t (&a)[4], TrFrag (&o)[4]) {
-  asm volatile(
-      "ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
-      "ds_read_b64_tr_b16 %2, %9 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
-      "ds_read_b64_tr_b16 %4, %10 offset:%12\n\tds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
-      "ds_read_b64_tr_b16 %6, %11 offset:%12\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\ts_waitcnt lgkmcnt(0)"
-      : "=&v"(o[0].h[0]), "=&v"(o[0].h[1]), "=&v"(o[1].h[0]), "=&v"(o[1].h[1]), "=&v"(o[2].h[0]), "=&v"(o[2].h[1]),
-        "=&v"(o[3].h[0]), "=&v"(o[3].h[1])
-      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(OFF), "n"(OFF + H)
-      : "memory");
-}
-
-// the same for fragments whose two halves have their own addresses a[2 k], a[2 k + 1]
-template <int OFF>
-SRA_DEV void lds_tr_reads(const uint32_t (&a)[4], TrFrag (&o)[2]) {
-  asm volatile(
-      "ds_read_b64_tr_b16 %0, %4 offset:%8\n\tds_read_b64_tr_b16 %1, %5 offset:%8\n\t"
-      "ds_read_b64_tr_b16 %2, %6 offset:%8\n\tds_read_b64_tr_b16 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
-      : "=&v"(o[0].h[0]), "=&v"(o[0].h[1]), "=&v"(o[1].h[0]), "=&v"(o[1].h[1])
-      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(OFF)
-      : "memory");
-}
 
 // ---- host-side launchers implemented in the kernel sources (internal C++ linkage)
 namespace sra {

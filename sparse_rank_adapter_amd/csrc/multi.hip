@@ -236,15 +236,11 @@ struct GradArgs {
   int64_t slice;         // elements from one slice's partials to the next
 };
 
-typedef short v4s __attribute__((ext_vector_type(4)));
-SRA_DEV v4s lds_tr(const uint8_t* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
-}
 union Bf8 {
   __bf16 h[8];
   u32x4 v;
   bf16x8 b;
-  v4s half[2];
+  tr_v4s half[2];
 };
 // x = a + b + c with bf16 parts (below fp32's rounding; the differences are exact)
 SRA_DEV void split3(float x, __bf16& a, __bf16& b, __bf16& c) {
@@ -424,11 +420,6 @@ template <int N>
 SRA_DEV void wait_vm_all() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-SRA_DEV void lds_dma(__amdgpu_buffer_rsrc_t rs, uint8_t* block, uint32_t off, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)block, 16, off, soff, 0, 0);
-}
-
 // V in three parts, in the sorted order: tile b is [3][rp][32] bf16, zeros for padding and for
 // adapter columns past r; 64 adapter columns per workgroup, gathered along r and written in whole
 // lines through LDS.  grid: (blocks, jobs, 64-column parts)
@@ -538,9 +529,8 @@ __global__ __launch_bounds__(512, 2) void k_multi_grads(GradArgs ga) {
     v_off[i] = (uint32_t)((k * ga.rp + j) * 64 + 16 * c);
   }
   auto issue_v = [&](int b) {
-    uint8_t* const buf = vlds + (b - b0) % 3 * V_BYTES;
-    const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(job.vt + (int64_t)min(b, b1 - 1) * 3 * ga.rp * 32), 0, vtile, 0x00020000);
+    const uint32_t buf = lds_offset(vlds) + (b - b0) % 3 * V_BYTES;
+    const dma_rsrc_t rv = dma_rsrc(job.vt + (int64_t)min(b, b1 - 1) * 3 * ga.rp * 32, (uint32_t)vtile);
 #pragma unroll
     for (int i = 0; i < (NV + 7) / 8; ++i)
       if (8 * i + 8 <= NV || 8 * i + w < NV) lds_dma(rv, buf + (8 * i + w) * 1024, v_off[i], 0);
@@ -550,16 +540,10 @@ __global__ __launch_bounds__(512, 2) void k_multi_grads(GradArgs ga) {
   for (int a = 0; a < 4; ++a)
 #pragma unroll
     for (int f = 0; f < MF; ++f) acc[a][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint32_t act_addr[MF];  // this wave's fragments of an Act tile (rows t and t + 4 share their swizzle)
+  auto compute = [&](const uint8_t* buf, const uint8_t* vb) {
+    bf16x8 b[MF];
 #pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    const int t = 8 * q4 + (l16 >> 2), m = (wm * MF + f) * 16 + 4 * (l16 & 3);
-    act_addr[f] = lds_offset(lds) + t * (2 * MT) + (((m >> 3) ^ act_swz<MT>(t)) << 4) + (m & 7) * 2;
-  }
-  auto compute = [&](bool odd, const uint8_t* vb) {
-    TrFrag b[MF];
-    if (odd) lds_tr_frags<A_BYTES, 8 * MT>(act_addr, b);
-    else lds_tr_frags<0, 8 * MT>(act_addr, b);
+    for (int f = 0; f < MF; ++f) b[f] = act_frag<MT>(buf, (wm * MF + f) * 16, l16, q4);
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -567,7 +551,7 @@ __global__ __launch_bounds__(512, 2) void k_multi_grads(GradArgs ga) {
         const int x = k * JR + 64 * wj + 16 * a + l16;
         const bf16x8 v = *reinterpret_cast<const bf16x8*>(vb + x * 64 + ((q4 ^ ((x >> 2) & 3)) << 4));
 #pragma unroll
-        for (int f = 0; f < MF; ++f) acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[f].b, acc[a][f], 0, 0, 0);
+        for (int f = 0; f < MF; ++f) acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[f], acc[a][f], 0, 0, 0);
       }
   };
 
@@ -598,7 +582,7 @@ __global__ __launch_bounds__(512, 2) void k_multi_grads(GradArgs ga) {
     issue_v(b + 2);
     __builtin_amdgcn_sched_barrier(0);
     tk = next;
-    compute(buf != lds, vlds + (b - b0) % 3 * V_BYTES);
+    compute(buf, vlds + (b - b0) % 3 * V_BYTES);
   };
   int b = b0;
   for (; b + 1 < b1; b += 2) {
@@ -661,8 +645,7 @@ __global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restric
   const int64_t cb = (int64_t)z * c_per, ce = min(C, cb + c_per);
   const int n_st = (int)((ce - cb) / SC), toks = (int)min((int64_t)128, T - t0);
 
-  const __amdgpu_buffer_rsrc_t ra =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(act + t0 * C + cb), 0, (int)((toks * C - cb) * 2), 0x00020000);
+  const dma_rsrc_t ra = dma_rsrc(act + t0 * C + cb, (uint32_t)((toks * C - cb) * 2));
   auto swz = [](int x) { return (x >> 1) & 7; };
   uint32_t a_off[LA], g_off[LG];
 #pragma unroll
@@ -685,23 +668,23 @@ __global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restric
   auto weight = [&](int g) {
     const uint16_t* w0 = wgt + (int64_t)g * r * C;
     const int64_t first = TW ? cb * r : (int64_t)j0 * C + cb, len = TW ? (C - cb) * r : (r - j0) * C - cb;
-    return __builtin_amdgcn_make_buffer_rsrc((void*)(w0 + first), 0, (int)(len * 2), 0x00020000);
+    return dma_rsrc(w0 + first, (uint32_t)(len * 2));
   };
-  __amdgpu_buffer_rsrc_t rg = weight(0);
+  dma_rsrc_t rg = weight(0);
 
   // TW: this wave's fragments (16 adapter columns each) of a stage's [SC][JR] tile; rows t and t + 4
   // share their swizzle, and so do k steps 32 rows apart
-  uint32_t tr_addr[JW];
+  const uint8_t* tr_at[JW];
 #pragma unroll
   for (int a = 0; a < JW; ++a) {
     const int t = 8 * q4 + (l16 >> 2), col = 16 * (JW * wj + a) + 4 * (l16 & 3);
-    tr_addr[a] = lds_offset(lds) + A_BYTES + t * (2 * JR) + (((col >> 3) ^ act_swz<JR>(t)) << 4) + (col & 7) * 2;
+    tr_at[a] = lds + A_BYTES + t * (2 * JR) + (((col >> 3) ^ act_swz<JR>(t)) << 4) + (col & 7) * 2;
   }
 
   f32x4 acc[2][JW];
   auto pass = [&] {
     auto issue = [&](int st) {
-      uint8_t* base = lds + (st % NS) * STAGE;
+      const uint32_t base = lds_offset(lds) + (st % NS) * STAGE;
 #pragma unroll
       for (int k = 0; k < LA; ++k) lds_dma(ra, base + (k * 8 + w) * 1024, a_off[k], st * RB);
 #pragma unroll
@@ -735,14 +718,13 @@ __global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restric
           af[i] = *reinterpret_cast<const bf16x8*>(A + x * RB + ((k ^ swz(x)) << 4));
         }
         if constexpr (TW) {
-          uint32_t at[JW];
-          TrFrag fr[JW];
 #pragma unroll
-          for (int a = 0; a < JW; ++a) at[a] = tr_addr[a] + (st % NS) * STAGE;
-          if (ks == 0) lds_tr_frags<0, 8 * JR>(at, fr);
-          else lds_tr_frags<64 * JR, 8 * JR>(at, fr);
+          for (int a = 0; a < JW; ++a) {
+            TrFrag u;
 #pragma unroll
-          for (int a = 0; a < JW; ++a) gf[a] = fr[a].b;
+            for (int h = 0; h < 2; ++h) u.h[h] = lds_tr(tr_at[a] + (st % NS) * STAGE + (32 * ks + 4 * h) * 2 * JR);
+            gf[a] = u.b;
+          }
         } else {
 #pragma unroll
           for (int a = 0; a < JW; ++a) {

@@ -7,12 +7,12 @@
 // order: the weight gradient of SLoPe's sparse training (SLoPe paperlayer summary, §2.1 -- the mask
 // is fixed, only stored entries learn; §2.3 -- both compressed forms are kept).
 //
-// Design: the dense 64 x 128 block of RowAct^T ColAct is computed with v_mfma_f32_16x16x32_bf16 and
+// Design: a dense 64 x 128 or 128 x 128 block of RowAct^T ColAct is computed with v_mfma_f32_16x16x32_bf16 and
 // only its stored half leaves.  The reduction (tokens) runs along the rows of both operands in
 // memory, while an MFMA lane needs 8 consecutive reduction elements.  Each 64-token stage is copied
 // as it lies (rows of tokens) from global memory to LDS by buffer -> LDS transfers into a three-
 // stage ring, and the fragments are read with ds_read_b64_tr_b16, gfx950's transposing LDS read
-// (in blocks with their own wait, see lds_tr_frags: the builtin form drained the ring every stage):
+// (the transfers are issued so that those reads do not wait for all of them, see lds_dma):
 // within a group of 16 lanes, lane i receives element i % 4 of the 8-byte pieces addressed by lanes
 // i / 4 + 4 r (r = 0..3).  So lane j (r = j / 4, s = j % 4) of lane group g addresses row
 // t = 8 g + 4 h + r and columns m0 + 4 s .. +3, and lane i gets column m0 + i at tokens
@@ -41,7 +41,6 @@ struct SdTile {
   static_assert(BM * SD_DLD * 4 <= SD_NS * STAGE, "the output block fits over the ring");
 };
 
-typedef __attribute__((address_space(3))) void* sd_lds_t;
 
 // chunk swizzles (16-byte chunks, even values keep chunk pairs together): over the 16 rows one
 // transposing read touches, the 32-byte windows land in 8 distinct bank windows, twice each
@@ -49,9 +48,6 @@ template <int BM>
 SRA_DEV int swz_a(int t) { return BM == 64 ? 2 * (((t >> 1) ^ (t >> 3)) & 3) : 2 * ((t & 3) | (((t >> 3) & 1) << 2)); }
 SRA_DEV int swz_b(int t) { return 2 * ((t & 3) | (((t >> 3) & 1) << 2)); }
 
-SRA_DEV void sd_dma(__amdgpu_buffer_rsrc_t rs, uint8_t* lds_block, uint32_t voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (sd_lds_t)lds_block, 16, voff, soff, 0, 0);
-}
 template <int N>
 SRA_DEV void sd_wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
@@ -67,20 +63,14 @@ __global__ __launch_bounds__(4 * BM, 2) void k_sddmm24(const uint16_t* __restric
   constexpr int SD_AROW = TL::AROW, SD_ASTG = TL::ASTG, SD_STAGE = TL::STAGE, SD_LA = TL::LA, SD_LB = TL::LB, NW = TL::NW;
   __shared__ __attribute__((aligned(16))) uint8_t lds[SD_NS * SD_STAGE];
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, l16 = l & 15, q4 = l >> 4;
-  // workgroups go to the 8 XCDs in turn: XCD x takes an eighth of the tiles in one piece (columns
-  // fastest), so its L2 holds a band of row_act instead of all of it
-  const int n_ct = (int)((C + SD_BC - 1) / SD_BC), n_wg = (int)gridDim.x;
-  const int xcd = blockIdx.x & 7, per = n_wg >> 3, rem = n_wg & 7;
-  const int lin = xcd * per + min(xcd, rem) + (int)(blockIdx.x >> 3);
-  const int64_t c0 = (int64_t)(lin % n_ct) * SD_BC, r0 = (int64_t)(lin / n_ct) * BM;
+  // (grouping the tiles by XCD, as bands of rows or as 8 x 8 blocks, measured no faster)
+  const int64_t c0 = (int64_t)blockIdx.x * SD_BC, r0 = (int64_t)blockIdx.y * BM;
   const int nst = (int)((T + SD_BT - 1) / SD_BT);
 
   // buffer resources based at the tile's first column; rows past T are past the range (zeros),
   // columns past R or C get an offset with bit 31 set (past the range too)
-  const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(ra + r0), (short)0, (int)((T * R - r0) * 2), 0x00020000);
-  const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(ca + c0), (short)0, (int)((T * C - c0) * 2), 0x00020000);
+  const dma_rsrc_t rsa = dma_rsrc(ra + r0, (uint32_t)((T * R - r0) * 2));
+  const dma_rsrc_t rsb = dma_rsrc(ca + c0, (uint32_t)((T * C - c0) * 2));
   // transfer k of this wave: A block q = k * NW + w covers 512 / BM tile rows (BM / 8 chunks each); B
   // block q covers rows 4q .. 4q+3 (row 4q + l/16, chunk l % 16).  The lane fetches the logical
   // chunk that its slot holds under the swizzle.
@@ -99,12 +89,12 @@ __global__ __launch_bounds__(4 * BM, 2) void k_sddmm24(const uint16_t* __restric
     b_off[k] = (uint32_t)((t * C + 8 * lc) * 2) | ((uint32_t)!in << 31);
   }
   auto issue = [&](int st, int buf) {
-    uint8_t* base = lds + buf * SD_STAGE;
+    const uint32_t base = lds_offset(lds) + (uint32_t)(buf * SD_STAGE);
     const int soff_a = (int)((int64_t)st * SD_BT * R * 2), soff_b = (int)((int64_t)st * SD_BT * C * 2);
 #pragma unroll
-    for (int k = 0; k < SD_LA; ++k) sd_dma(rsa, base + (k * NW + w) * 1024, a_off[k], soff_a);
+    for (int k = 0; k < SD_LA; ++k) lds_dma(rsa, base + (k * NW + w) * 1024, a_off[k], soff_a);
 #pragma unroll
-    for (int k = 0; k < SD_LB; ++k) sd_dma(rsb, base + SD_ASTG + (k * NW + w) * 1024, b_off[k], soff_b);
+    for (int k = 0; k < SD_LB; ++k) lds_dma(rsb, base + SD_ASTG + (k * NW + w) * 1024, b_off[k], soff_b);
   };
 
   // wave w: rows 32 (w / 2) .. +31 (two row fragments) against columns 64 (w % 2) .. +63 (four
@@ -114,20 +104,21 @@ __global__ __launch_bounds__(4 * BM, 2) void k_sddmm24(const uint16_t* __restric
   // the step for half h.  The column tile's swizzle is the same for both halves, the 64-row tile's is
   // not; a step of 32 tokens further down both are the same again.
   const int fr = l16 >> 2, fs = l16 & 3;
-  uint32_t a_addr[2][2], b_addr[4];  // [half][fragment]
+  const uint8_t* a_at[2][2];  // [fragment][half]
+  const uint8_t* b_at[4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int col = wr + 16 * i + 4 * fs;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int t = 8 * q4 + 4 * h + fr;
-      a_addr[h][i] = lds_offset(lds) + t * SD_AROW + (((col >> 3) ^ swz_a<BM>(t)) << 4) + (col & 7) * 2;
+      a_at[i][h] = lds + t * SD_AROW + (((col >> 3) ^ swz_a<BM>(t)) << 4) + (col & 7) * 2;
     }
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int t = 8 * q4 + fr, col = wc + 16 * j + 4 * fs;
-    b_addr[j] = lds_offset(lds) + SD_ASTG + t * SD_BROW + (((col >> 3) ^ swz_b(t)) << 4) + (col & 7) * 2;
+    b_at[j] = lds + SD_ASTG + t * SD_BROW + (((col >> 3) ^ swz_b(t)) << 4) + (col & 7) * 2;
   }
   f32x4 d[2][4];
   double acc[2][4][4];
@@ -148,33 +139,29 @@ __global__ __launch_bounds__(4 * BM, 2) void k_sddmm24(const uint16_t* __restric
         for (int e = 0; e < 4; ++e) acc[i][j][e] += (double)d[i][j][e];
   };
   auto compute = [&](int buf) {
-    const uint32_t base = (uint32_t)(buf * SD_STAGE);
-    const uint32_t aa[4] = {a_addr[0][0] + base, a_addr[1][0] + base, a_addr[0][1] + base, a_addr[1][1] + base};
-    const uint32_t ba[4] = {b_addr[0] + base, b_addr[1] + base, b_addr[2] + base, b_addr[3] + base};
-    flush();
+    const int base = buf * SD_STAGE;
+    TrFrag a[2][2], b[2][4];  // both 32-token steps' fragments, read ahead of the sums and the products
 #pragma unroll
     for (int kk = 0; kk < SD_BT / 32; ++kk) {
-      TrFrag af[2], bf[4];
-      if (kk == 0) {
-        lds_tr_reads<0>(aa, af);
-        lds_tr_frags<0, 4 * SD_BROW>(ba, bf);
-      } else {
-        lds_tr_reads<32 * SD_AROW>(aa, af);
-        lds_tr_frags<32 * SD_BROW, 4 * SD_BROW>(ba, bf);
-      }
-      bf16x8 a[2], b[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) a[i] = af[i].b;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = bf[j].b;
-      __builtin_amdgcn_sched_barrier(0);  // every read of the step ahead of its products
+        for (int h = 0; h < 2; ++h) a[kk][i].h[h] = lds_tr(a_at[i][h] + base + 32 * kk * SD_AROW);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) b[kk][j].h[h] = lds_tr(b_at[j] + base + (32 * kk + 4 * h) * SD_BROW);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    flush();
+#pragma unroll
+    for (int kk = 0; kk < SD_BT / 32; ++kk)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          d[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], kk ? d[i][j] : f32x4{0.f, 0.f, 0.f, 0.f},
-                                                            0, 0, 0);
-    }
+          d[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[kk][i].b, b[kk][j].b,
+                                                            kk ? d[i][j] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
   };
 
   // ring: stage c sits in buffer c % NS; NS - 1 stages are in flight ahead of the products
@@ -294,15 +281,15 @@ hipError_t launch_sddmm24_bf16(const uint16_t* row_act, const uint16_t* col_act,
   if (R <= 0 || C <= 0) return hipSuccess;
   if (R % 8 != 0 || C % 32 != 0) return hipErrorInvalidValue;
   if (!sddmm24_fits(R, C, T)) return hipErrorInvalidValue;  // 32-bit buffer offsets
-  // 128 rows per workgroup (one per CU) once those fill the GPU: the transfers to LDS bound the kernel,
-  // and this tile moves a third less per product; 64 rows (two per CU) below that
-  const int64_t ct = (C + SD_BC - 1) / SD_BC;
+  // 128 rows per workgroup (one per CU) once those fill the GPU, else 64 (two per CU): 35.9 against 39.8 us
+  // at 2048 tokens of 4096 x 1024, 2.68-2.90 against 2.80-2.90 ms at 8192 tokens of 20480 x 5120
+  const unsigned ct = (unsigned)((C + SD_BC - 1) / SD_BC);
   if (ct * ((R + 127) / 128) >= 256)
-    launch(SRA_KERNEL_WEIGHT_GRAD, k_sddmm24<128>, dim3((unsigned)(ct * ((R + 127) / 128))), dim3(512), 0, s, row_act,
-           col_act, meta, meta_or, R, C, T, out);
+    launch(SRA_KERNEL_WEIGHT_GRAD, k_sddmm24<128>, dim3(ct, (unsigned)((R + 127) / 128)), dim3(512), 0, s, row_act, col_act,
+           meta, meta_or, R, C, T, out);
   else
-    launch(SRA_KERNEL_WEIGHT_GRAD, k_sddmm24<64>, dim3((unsigned)(ct * ((R + 63) / 64))), dim3(256), 0, s, row_act,
-           col_act, meta, meta_or, R, C, T, out);
+    launch(SRA_KERNEL_WEIGHT_GRAD, k_sddmm24<64>, dim3(ct, (unsigned)((R + 63) / 64)), dim3(256), 0, s, row_act, col_act,
+           meta, meta_or, R, C, T, out);
   return hipGetLastError();
 }
 
