@@ -398,6 +398,8 @@ sra_status sra_nm_axpby(const void* a_values, float beta, const void* b_values, 
  * canonical arrays or the streaming layout); other formats and fp32 are SRA_ERR_UNSUPPORTED.
  * U_out / U / dU_out [T,r], dA [n_adapters,r,K] and dB [n_adapters,N,r] are fp32; an adapter with
  * no token gets zero gradients.  Flags as for sra_sparse_lora_bwd.
+ * Requests stay apart: infinities or NaN in one adapter, or in its tokens, change nothing for other
+ * adapters' tokens and gradients.
  * The backward reads the layer's input from X, or, when X is NULL, from its 8-bit checkpoint
  * X_codes / X_exps (sra_ckpt_encode); the results equal those from the decoded bf16 values bit for
  * bit.  It is read for dA, and for U when U is NULL and dB is asked for.  Sums over tokens run in a

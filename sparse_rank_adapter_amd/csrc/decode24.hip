@@ -81,7 +81,9 @@ struct DecLds {
 // tiles through LDS in wave order (deterministic), and row tile i is finished by wave i % NW.
 // MA (many adapters): token l16 takes E + ids[token] * stride.  A row tile runs over the distinct
 // adapters of the (at most 16) tokens, kMaChunk at a time so that their E loads are in flight
-// together; an adapter's product takes U with the other adapters' tokens cleared.
+// together; each adapter's products are added to all tokens' sums and kept for its own tokens (a
+// selection, not a product with zeros: nothing in one adapter, an infinity say, reaches another's tokens,
+// and a token's result has the same bits whatever its neighbours take).
 constexpr int kMaChunk = 4;
 template <int FR, int NW, bool MA = false, int PF = MA || FR == 4 ? 0 : 2>
 struct DecodeTail {
@@ -117,7 +119,7 @@ struct DecodeTail {
       const int jb = jj + 8 * q;
       float u[8];
       load_u(jb, u);
-      union UH { uint16_t h[8]; u32x4 v; bf16x8 b; } uhi, ulo;
+      union UH { uint16_t h[8]; bf16x8 b; } uhi, ulo;
 #pragma unroll
       for (int e = 0; e < 8; ++e) split_bf16(u[e], uhi.h[e], ulo.h[e]);
       const bool vec = e_vec && jb + 8 <= ep.r;
@@ -150,17 +152,12 @@ struct DecodeTail {
 #pragma unroll
         for (int c = 0; c < kMaChunk; ++c) {
           if (g[c] < 0) break;  // wave-uniform
-          const uint32_t keep = id == g[c] ? ~0u : 0u;
-          UH hi, lo;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            hi.v[k] = uhi.v[k] & keep;
-            lo.v[k] = ulo.v[k] & keep;
-          }
           union { u32x4 v; bf16x8 b; } e;
           e.v = x[c];
-          y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e.b, hi.b, y, 0, 0, 0);
-          y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e.b, lo.b, y, 0, 0, 0);
+          f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e.b, uhi.b, y, 0, 0, 0);
+          t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e.b, ulo.b, t, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = id == g[c] ? t[k] : y[k];
         }
       }
     }

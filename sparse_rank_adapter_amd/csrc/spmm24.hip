@@ -239,7 +239,7 @@ __global__ __launch_bounds__(256, (Tile<FR, FT, WR, WT>::OCC)) void k_spmm24(
         float u[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) u[q] = 0.f;
-        if (t < T && (!MA || id[j] == cur)) {
+        if (t < T) {
           const float* up = ep.U + t * ep.r + jb;
           if (u_vec && jb + 8 <= ep.r) {
             const f32x4 a0 = *reinterpret_cast<const f32x4*>(up);
@@ -258,6 +258,20 @@ __global__ __launch_bounds__(256, (Tile<FR, FT, WR, WT>::OCC)) void k_spmm24(
         union { uint16_t h[8]; bf16x8 b; } hi, lo;
 #pragma unroll
         for (int q = 0; q < 8; ++q) split_bf16(u[q], hi.h[q], lo.h[q]);
+        if constexpr (MA) {  // an adapter's products go to its own tokens only, by selection
+          const uint32_t here = (uint32_t)__ballot(id[j] == cur);  // lanes 0 .. 31: the 32 tokens
+          if (here == 0) continue;
+          if (here != ~0u) {
+#pragma unroll
+            for (int i = 0; i < FR; ++i) {
+              f32x16 t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ef[i], hi.b, acc[i][j], 0, 0, 0);
+              t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ef[i], lo.b, t, 0, 0, 0);
+#pragma unroll
+              for (int q = 0; q < 16; ++q) acc[i][j][q] = id[j] == cur ? t[q] : acc[i][j][q];
+            }
+            continue;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < FR; ++i) {
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ef[i], hi.b, acc[i][j], 0, 0, 0);

@@ -999,10 +999,12 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
       wait_vm<0>();
       __syncthreads();
       if constexpr (MA) {
-        // one step per distinct adapter and 32 adapter columns; fragments with no token of the adapter are skipped, and
-        // the other tokens' U are cleared.  U is split once per workgroup, in place (an fp32 word
-        // becomes hi | lo << 16): by every wave of a token column and for every adapter, the split
-        // took longer than the products
+        // one step per distinct adapter and 32 adapter columns.  A fragment whose tokens all take the
+        // adapter adds its products in place, one with none skips them, and a mixed one keeps them
+        // for the adapter's tokens only (a selection, not a product with zeros: nothing in one adapter
+        // reaches another's tokens, whose bits do not depend on their neighbours either).  U is split once per workgroup, in place (an fp32 word becomes
+        // hi | lo << 16): by every wave of a token column and for every adapter, the split took longer
+        // than the products
         const int cs = nj > 64 ? 5 : nj > 32 ? 4 : nj > 16 ? 3 : 2;  // 2^cs chunks of 4 hold the nj columns
         for (int i = tid; i < BT << cs; i += 64 * NW) {
           const int tok = i >> cs, c = (i & ((1 << cs) - 1)) ^ (tok & 31);
@@ -1037,23 +1039,33 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
           const int c0 = (jj + 8 * q4) >> 2;
 #pragma unroll
           for (int j = 0; j < FT; ++j) {
-            if (((uint32_t)__ballot(id[j] == g) & 0xffffu) == 0) continue;  // wave-uniform
-            const uint32_t keep = id[j] == g ? ~0u : 0u;
+            const uint32_t here = (uint32_t)__ballot(id[j] == g) & 0xffffu;
+            if (here == 0) continue;  // wave-uniform, as is the choice below
             const int tl = wt * 16 * FT + j * 16 + l16, sw = tl & 31;
             const u32x4 u0 = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * (c0 ^ sw));
             const u32x4 u1 = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * ((c0 + 1) ^ sw));
             union { uint32_t w[4]; bf16x8 b; } uhi, ulo;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {  // low halves of two words, and their high halves
-              uhi.w[q] = __builtin_amdgcn_perm(u0[2 * q + 1], u0[2 * q], 0x05040100u) & keep;
-              ulo.w[q] = __builtin_amdgcn_perm(u0[2 * q + 1], u0[2 * q], 0x07060302u) & keep;
-              uhi.w[2 + q] = __builtin_amdgcn_perm(u1[2 * q + 1], u1[2 * q], 0x05040100u) & keep;
-              ulo.w[2 + q] = __builtin_amdgcn_perm(u1[2 * q + 1], u1[2 * q], 0x07060302u) & keep;
+              uhi.w[q] = __builtin_amdgcn_perm(u0[2 * q + 1], u0[2 * q], 0x05040100u);
+              ulo.w[q] = __builtin_amdgcn_perm(u0[2 * q + 1], u0[2 * q], 0x07060302u);
+              uhi.w[2 + q] = __builtin_amdgcn_perm(u1[2 * q + 1], u1[2 * q], 0x05040100u);
+              ulo.w[2 + q] = __builtin_amdgcn_perm(u1[2 * q + 1], u1[2 * q], 0x07060302u);
             }
+            if (here == 0xffffu) {
 #pragma unroll
-            for (int i = 0; i < FR; ++i) {
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, uhi.b, acc[i][j], 0, 0, 0);
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, ulo.b, acc[i][j], 0, 0, 0);
+              for (int i = 0; i < FR; ++i) {
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, uhi.b, acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, ulo.b, acc[i][j], 0, 0, 0);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < FR; ++i) {
+                f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, uhi.b, acc[i][j], 0, 0, 0);
+                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, ulo.b, t, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][j][q] = id[j] == g ? t[q] : acc[i][j][q];
+              }
             }
           }
           }

@@ -245,3 +245,43 @@ def test_masked_weight_grad_from_checkpoint(gpu, T, R, C, fmt):
     col = (i // S.n) * S.m + pos
     w, mag = np.take_along_axis(D, col, 1), np.take_along_axis(M, col, 1)
     assert np.all(np.abs(f64(got) - w) <= BF * np.abs(w) + 70 * U24 * mag)
+
+
+@pytest.mark.parametrize("T,K,N", [(12, 128, 96), (150, 128, 96), (150, 96, 64), (300, 256, 256)])
+def test_one_request_cannot_reach_another(gpu, T, K, N):
+    """Infinities and NaN in one adapter, or in one adapter's tokens, leave every other token's results and
+    every other adapter's gradients as they were."""
+    g = torch.Generator().manual_seed(T + K)
+    r, n = 40 if T == 300 else 8, 4
+    S, _ = weight(N, K, 2, 4, g, gpu)
+    P, _ = weight(K, N, 2, 4, g, gpu)
+    X = torch.randn(T, K, generator=g).bfloat16().to(gpu)
+    dY = torch.randn(T, N, generator=g).bfloat16().to(gpu)
+    A = (torch.randn(n, r, K, generator=g) * 0.05).bfloat16().to(gpu)
+    B = (torch.randn(n, N, r, generator=g) * 0.05).bfloat16().to(gpu)
+    ids = make_ids("mixed", T, n, g).to(gpu)
+    others = ids != 2
+    keep = [0, 1, 3]
+    Y, U = sra.multi_lora_fwd(S, X, A, B, ids)
+    want = sra.multi_lora_bwd(P, dY, X, U, A, B, ids)
+
+    A2, B2 = A.clone(), B.clone()
+    A2[2, 1] = float("nan")
+    B2[2, ::3] = float("inf")
+    Yb, Ub = sra.multi_lora_fwd(S, X, A2, B2, ids)
+    got = sra.multi_lora_bwd(P, dY, X, Ub, A2, B2, ids)
+    assert torch.equal(Yb[others], Y[others]) and torch.equal(Ub[others], U[others])
+    assert not torch.isfinite(Yb[~others]).all()
+    assert torch.equal(got["dX"][others], want["dX"][others])
+    for k in ("dA", "dB"):
+        assert torch.equal(got[k][keep], want[k][keep]), k
+
+    X2, dY2 = X.clone(), dY.clone()
+    X2[~others] = float("nan")
+    dY2[~others] = float("inf")
+    Yb, Ub = sra.multi_lora_fwd(S, X2, A, B, ids)
+    got = sra.multi_lora_bwd(P, dY2, X2, Ub, A, B, ids)
+    assert torch.equal(Yb[others], Y[others]) and torch.equal(Ub[others], U[others])
+    assert torch.equal(got["dX"][others], want["dX"][others])
+    for k in ("dA", "dB"):
+        assert torch.equal(got[k][keep], want[k][keep]), k
