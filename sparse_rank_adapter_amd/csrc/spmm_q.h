@@ -924,8 +924,8 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
     };
     const __amdgpu_buffer_rsrc_t ru = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(ep.U + t0 * ep.r), 0, toks_here * ep.r * 4, 0x00020000);
-    // many adapters: the steps (adapter, 32 columns) come in chunks of CH whose E fragments are in
-    // flight together (the largest wave tile has registers for two steps).  The loads are bare:
+    // many adapters: the E fragments of CH steps (adapter, 32 columns) are in flight together, a step's
+    // slot refilled once its products are out (the largest wave tile has registers for two steps).  The loads are bare:
     // clearing the entries past r right after each load made every load wait for itself (36.3 us
     // against 23.1 at OPT-350M fc1 where 16 adapters meet in each 128-token tile), so that happens at
     // the products.
@@ -944,29 +944,26 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
       }
       return g;
     };
-    auto fetch_chunk = [&](int jb0, int nj) {  // the next CH steps (ga = -1 past the last)
+    auto fetch = [&](int c, int jb0, int nj) {  // the next step into slot c (ga = -1 past the last)
+      ga[c] = g_at;
+      ja[c] = j_at;
+      if constexpr (MA) {
+        if (g_at >= 0) {
+          re = __builtin_amdgcn_make_buffer_rsrc((void*)(ep.E + (int64_t)g_at * ep.ai.stride), 0,
+                                                 (int)(R * ep.e_row_stride * 2), 0x00020000);
+          if (e_al) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        ga[c] = g_at;
-        ja[c] = j_at;
-        if constexpr (MA) {
-          if (g_at >= 0) {
-            re = __builtin_amdgcn_make_buffer_rsrc((void*)(ep.E + (int64_t)g_at * ep.ai.stride), 0,
-                                                   (int)(R * ep.e_row_stride * 2), 0x00020000);
-            if (e_al) {
+            for (int i = 0; i < FR; ++i)
+              en[c][i].v = __builtin_amdgcn_raw_buffer_load_b128(
+                  re, (uint32_t)(((row0 + wr * 16 * FR + i * 16 + l16) * ep.e_row_stride + jb0 + j_at + 8 * q4) * 2), 0, 0);
+          } else {
 #pragma unroll
-              for (int i = 0; i < FR; ++i)
-                en[c][i].v = __builtin_amdgcn_raw_buffer_load_b128(
-                    re, (uint32_t)(((row0 + wr * 16 * FR + i * 16 + l16) * ep.e_row_stride + jb0 + j_at + 8 * q4) * 2), 0, 0);
-            } else {
-#pragma unroll
-              for (int i = 0; i < FR; ++i) en[c][i].v = load_e(row0 + wr * 16 * FR + i * 16 + l16, jb0 + j_at + 8 * q4);
-            }
-            j_at += 32;
-            if (j_at >= nj) {
-              g_at = next_adapter();
-              j_at = 0;
-            }
+            for (int i = 0; i < FR; ++i) en[c][i].v = load_e(row0 + wr * 16 * FR + i * 16 + l16, jb0 + j_at + 8 * q4);
+          }
+          j_at += 32;
+          if (j_at >= nj) {
+            g_at = next_adapter();
+            j_at = 0;
           }
         }
       }
@@ -994,7 +991,8 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
         for (int j = 0; j < FT; ++j) todo[j] = valid[j];
         g_at = next_adapter();
         j_at = 0;
-        fetch_chunk(jb0, nj);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) fetch(c, jb0, nj);
       }
       wait_vm<0>();
       __syncthreads();
@@ -1002,24 +1000,25 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
         // one step per distinct adapter and 32 adapter columns.  A fragment whose tokens all take the
         // adapter adds its products in place, one with none skips them, and a mixed one keeps them
         // for the adapter's tokens only (a selection, not a product with zeros: nothing in one adapter
-        // reaches another's tokens, whose bits do not depend on their neighbours either).  U is split once per workgroup, in place (an fp32 word becomes
-        // hi | lo << 16): by every wave of a token column and for every adapter, the split took longer
-        // than the products
-        const int cs = nj > 64 ? 5 : nj > 32 ? 4 : nj > 16 ? 3 : 2;  // 2^cs chunks of 4 hold the nj columns
+        // reaches another's tokens, whose bits do not depend on their neighbours either).  U is split
+        // once per workgroup, in place (32 bytes of eight fp32 become eight bf16 parts and eight bf16
+        // rests): by every wave of a token column and for every adapter, the split took longer than
+        // the products
+        const int cs = nj > 64 ? 4 : nj > 32 ? 3 : nj > 16 ? 2 : 1;  // 2^cs groups of 8 hold the nj columns
         for (int i = tid; i < BT << cs; i += 64 * NW) {
-          const int tok = i >> cs, c = (i & ((1 << cs) - 1)) ^ (tok & 31);
-          u32x4* const p = reinterpret_cast<u32x4*>(smem + tok * 512 + c * 16);
-          const u32x4 v = *p;
-          u32x4 o;
+          const int tok = i >> cs, c = (2 * (i & ((1 << cs) - 1))) ^ (tok & 31);
+          u32x4* const p0 = reinterpret_cast<u32x4*>(smem + tok * 512 + c * 16);
+          u32x4* const p1 = reinterpret_cast<u32x4*>(smem + tok * 512 + (c ^ 1) * 16);
+          const u32x4 v0 = *p0, v1 = *p1;
+          union { u32x4 v; __bf16 b[8]; uint16_t h[8]; } hi, lo;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float x = __uint_as_float(v[q]);
-            union { __bf16 b; uint16_t h; } hi, lo;
-            hi.b = (__bf16)x;
-            lo.b = (__bf16)(x - bf16_to_f32(hi.h));
-            o[q] = (uint32_t)hi.h | ((uint32_t)lo.h << 16);
+          for (int q = 0; q < 8; ++q) {
+            const float x = __uint_as_float(q < 4 ? v0[q & 3] : v1[q & 3]);
+            hi.b[q] = (__bf16)x;
+            lo.b[q] = (__bf16)(x - bf16_to_f32(hi.h[q]));
           }
-          *p = o;
+          *p0 = hi.v;
+          *p1 = lo.v;
         }
         __syncthreads();
         while (ga[0] >= 0) {
@@ -1042,16 +1041,9 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
             const uint32_t here = (uint32_t)__ballot(id[j] == g) & 0xffffu;
             if (here == 0) continue;  // wave-uniform, as is the choice below
             const int tl = wt * 16 * FT + j * 16 + l16, sw = tl & 31;
-            const u32x4 u0 = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * (c0 ^ sw));
-            const u32x4 u1 = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * ((c0 + 1) ^ sw));
-            union { uint32_t w[4]; bf16x8 b; } uhi, ulo;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {  // low halves of two words, and their high halves
-              uhi.w[q] = __builtin_amdgcn_perm(u0[2 * q + 1], u0[2 * q], 0x05040100u);
-              ulo.w[q] = __builtin_amdgcn_perm(u0[2 * q + 1], u0[2 * q], 0x07060302u);
-              uhi.w[2 + q] = __builtin_amdgcn_perm(u1[2 * q + 1], u1[2 * q], 0x05040100u);
-              ulo.w[2 + q] = __builtin_amdgcn_perm(u1[2 * q + 1], u1[2 * q], 0x07060302u);
-            }
+            EF uhi, ulo;
+            uhi.v = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * (c0 ^ sw));
+            ulo.v = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * ((c0 + 1) ^ sw));
             if (here == 0xffffu) {
 #pragma unroll
               for (int i = 0; i < FR; ++i) {
@@ -1068,8 +1060,8 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
               }
             }
           }
+          fetch(ch, jb0, nj);
           }
-          fetch_chunk(jb0, nj);
         }
       } else
       for (int jj = 0; jj < nj; jj += 32) {
