@@ -145,8 +145,9 @@ def _mat(W, name: str):
     """A dense 2-D input matrix (bf16 or fp32, on the GPU, contiguous); returns its shape."""
     if not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
-    _dt(W)
-    _dev(W, name)
+    if W.dtype not in _DT or not (W.is_cuda and W.is_contiguous()):
+        _dt(W)
+        _dev(W, name)
     return tuple(W.shape)
 
 
@@ -620,10 +621,11 @@ def ffa_bwd_workspace(P: SparseMatrix, T: int, A: SparseMatrix,
 
 def _multi_args(A, B, ids, T: int, K: int, N: int, dt, dev):
     """Adapters [n, r, K] and [n, N, r] and the tokens' ids; returns (n, r)."""
-    for t, name in ((A, "A"), (B, "B")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            raise ValueError(f"{name} must be a 3-D tensor ([n, r, K] and [n, N, r])")
-    n, r = int(A.shape[0]), int(A.shape[1])
+    if not isinstance(A, torch.Tensor) or A.dim() != 3:
+        raise ValueError("A must be a 3-D tensor [n, r, K]")
+    if not isinstance(B, torch.Tensor) or B.dim() != 3:
+        raise ValueError("B must be a 3-D tensor [n, N, r]")
+    n, r, _ = A.shape
     _arg(A, "A", (n, r, K), dt, dev)
     _arg(B, "B", (n, N, r), dt, dev)
     _arg(ids, "ids", (T,), torch.int32, dev)
@@ -674,10 +676,10 @@ def multi_lora_fwd(Ws: SparseMatrix, X: torch.Tensor, A: torch.Tensor, B: torch.
         _arg(U, "U", (T, r), torch.float32, dev)
     elif want_u:
         U = torch.empty((T, r), dtype=torch.float32, device=dev)
-    d = Ws.desc()
     ws = _workspace(ws, _multi_bytes(Ws.fmt, _DT[dt], N, K, Ws.n, Ws.m, T, n, r, None), dev)
     check("sra_multi_lora_fwd", lib.sra_multi_lora_fwd(
-        ctypes.byref(d), _p(X), T, _p(A), _p(B), _p(ids), n, r, _p(Y), _p(U), _p(ws), ws.numel(), _stream(dev)))
+        ctypes.byref(Ws.desc()), X.data_ptr(), T, A.data_ptr(), B.data_ptr(), ids.data_ptr(), n, r, Y.data_ptr(), _p(U),
+        ws.data_ptr(), ws.numel(), _stream(dev)))
     return Y, U
 
 
@@ -799,7 +801,8 @@ def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, eps
     _arg(beta, "beta", (H,), X.dtype, dev)
     if Y is None:
         Y = torch.empty_like(X)
-    _arg(Y, "Y", (T, H), X.dtype, dev)
+    else:
+        _arg(Y, "Y", (T, H), X.dtype, dev)
     c = None
     if isinstance(ckpt, Ckpt8):
         c = ckpt
@@ -807,13 +810,15 @@ def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, eps
             raise ValueError(f"ckpt has dtype {c.dtype}, expected {X.dtype}")
     elif ckpt:
         c = _new_ckpt(T, H, X.dtype, dev)
+    codes = exps = None
     if c is not None:
         _check_ckpt(c, "ckpt", (T, H), dev)
+        codes, exps = c.codes.data_ptr(), c.exps.data_ptr()
     mean = torch.empty(T, dtype=torch.float32, device=dev)
     rstd = torch.empty(T, dtype=torch.float32, device=dev)
     check("sra_layer_norm_fwd", lib.sra_layer_norm_fwd(
-        _p(X), _p(gamma), _p(beta), float(eps), _dt(X), T, H, _p(Y), _p(mean), _p(rstd),
-        _p(c.codes) if c is not None else None, _p(c.exps) if c is not None else None, _stream(dev)))
+        X.data_ptr(), gamma.data_ptr(), beta.data_ptr(), float(eps), _DT[X.dtype], T, H, Y.data_ptr(), mean.data_ptr(),
+        rstd.data_ptr(), codes, exps, _stream(dev)))
     return Y, mean, rstd, c
 
 
@@ -830,13 +835,14 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor, mean:
     _arg(rstd, "rstd", (T,), torch.float32, dev)
     if dX is None:
         dX = torch.empty_like(X)
-    _arg(dX, "dX", (T, H), X.dtype, dev)
+    else:
+        _arg(dX, "dX", (T, H), X.dtype, dev)
     dgamma = torch.empty(H, dtype=torch.float32, device=dev)
     dbeta = torch.empty(H, dtype=torch.float32, device=dev)
     ws = _workspace(ws, _ln_bwd_bytes(T, H), dev)
     check("sra_layer_norm_bwd", lib.sra_layer_norm_bwd(
-        _p(dY), _p(X), _p(gamma), _p(mean), _p(rstd), _dt(X), T, H, _p(dX), _p(dgamma), _p(dbeta),
-        _p(ws), ws.numel(), _stream(dev)))
+        dY.data_ptr(), X.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _DT[X.dtype], T, H,
+        dX.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)))
     return dX, dgamma, dbeta
 
 
