@@ -9,7 +9,7 @@
 //     there read token 0 and are cleared); tokens with no adapter are left out; the adapters' list
 //     runs by falling block count (up to 64 adapters), so that the longest start first;
 //   the other workgroups transpose every B_g (the dU product's operand, contiguous along N) and
-//     every A_g (the dX epilogue's rows of r entries), in 64 x 64 tiles.
+//     every A_g (the dX epilogue's rows of r entries), in tiles of 8192 elements.
 //
 // The gradients are sums over an adapter's tokens of products of one Act value (dY or X, bf16, or an
 // 8-bit checkpoint decoded on the way, exactly) with one V value (U or dU, fp32, split into three
@@ -50,7 +50,7 @@ struct PrepArgs {
   const uint16_t* A;  // [n][r][K] -> at [n][K][lda]; nullptr: none
   int64_t K, lda;
   uint16_t* at;
-  int r, b_tiles, a_tiles;  // 64 x 64 tiles per adapter
+  int r, b_tiles, a_tiles;  // tiles per adapter
 };
 
 // offset (entries) of the adapters' list after gblk [n + 1], 16-byte aligned
@@ -60,36 +60,64 @@ struct SortLds {
   int hist[kPrepWaves][kMaxAdapters + 1];
   int base[kMaxAdapters + 1];
   int wsum[kPrepWaves];
-  int total;
 };
+// 512 x (16 + 2), the largest of the tile shapes with their padding
 struct TileLds {
-  uint16_t t[64][66];
+  uint16_t t[512 * 18];
 };
 union PrepLds {
   SortLds s;
   TileLds t;
 };
 
+// The lanes of a wave that name the same adapter: the number of them and this lane's place among
+// them (g < 0: none).
+struct Match {
+  int count, place;
+};
+SRA_DEV Match match_adapter(int g, int l) {
+  Match m{0, 0};
+  uint64_t todo = __ballot(g >= 0);
+  while (todo) {
+    const int lead = __builtin_ctzll(todo);
+    const uint64_t same = __ballot(g == __builtin_amdgcn_readlane(g, lead));
+    todo &= ~same;
+    if ((same >> l) & 1) m = {(int)__popcll(same), (int)__popcll(same & ((1ull << l) - 1))};
+  }
+  return m;
+}
 SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
-  for (int i = l; i < a.n; i += 64) s.hist[w][i] = 0;  // wave w's own row
-  __syncthreads();
   // wave w takes tokens [w * chunk, (w + 1) * chunk)
   const int64_t chunk = ((a.T + kPrepWaves - 1) / kPrepWaves + 63) / 64 * 64;
   const int64_t lo = w * chunk, hi = min(a.T, lo + chunk);
-  constexpr int KEEP = 4;  // ids of the wave's first tokens stay in registers for the second walk
-  int kept[KEEP];
-#pragma unroll
-  for (int k = 0; k < KEEP; ++k) {
-    const int64_t t = lo + 64 * k + l;
-    kept[k] = t < hi ? a.ids[t] : -1;
-  }
-  auto count = [&](int g) {  // LDS integers: the order does not matter
-    if (g >= 0 && g < a.n) atomicAdd(&s.hist[w][g], 1);
+  constexpr int KEEP = 4;  // the wave's first tokens are walked once: adapter and place stay in registers
+  int kept[KEEP], at[KEEP];
+  auto load_id = [&](int64_t t) {
+    const int g = t < hi ? a.ids[t] : -1;
+    return g < a.n ? g : -1;
   };
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k) count(kept[k]);
-  for (int64_t t = lo + 64 * KEEP + l; t < hi; t += 64) count(a.ids[t]);
+  for (int k = 0; k < KEEP; ++k) kept[k] = load_id(lo + 64 * k + l);
+  volatile int* const mine = s.hist[w];  // this wave's counts: only this wave uses them until the barrier
+  for (int i = l; i < a.n; i += 64) mine[i] = 0;
+  // this wave's tokens of the same adapter before the lane's: one LDS round trip for 64 tokens
+  auto take = [&](int g) {
+    const Match m = match_adapter(g, l);
+    int before = 0;
+    if (g >= 0) before = mine[g];
+    if (g >= 0 && m.place == 0) mine[g] = before + m.count;
+    return before + m.place;
+  };
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    at[k] = 0;
+    if (lo + 64 * k < hi) at[k] = take(kept[k]);
+  }
+  for (int64_t t0 = lo + 64 * KEEP; t0 < hi; t0 += 64) {  // counted here, placed by the second walk
+    const int g = load_id(t0 + l);
+    if (g >= 0) atomicAdd(&s.hist[w][g], 1);  // LDS integers: the order does not matter
+  }
   __syncthreads();
   // thread g: where each wave's tokens of adapter g start, and the adapter's blocks
   int cnt = 0, blocks = 0;
@@ -112,87 +140,98 @@ SRA_DEV void sort_tokens(const PrepArgs& a, SortLds& s) {
   }
   if (l == 63) s.wsum[w] = incl;
   __syncthreads();
-  for (int i = 0; i < w; ++i) incl += s.wsum[i];
+  int sums[kPrepWaves];
+#pragma unroll
+  for (int i = 0; i < kPrepWaves; ++i) sums[i] = s.wsum[i];
+#pragma unroll
+  for (int i = 0; i < kPrepWaves; ++i) incl += i < w ? sums[i] : 0;
   const int first = incl - blocks;
-  if (tid == kPrepThreads - 1) s.total = incl;
   if (tid < a.n) {
     s.base[tid] = first;
     if (tid == a.n - 1) a.gblk[a.n] = incl;
-    for (int i = cnt; i < 32 * blocks; ++i) a.perm[(int64_t)first * 32 + i] = -1;
   }
   __syncthreads();
-  if (tid < a.n) {
-    int rank = tid;
-    if (a.n <= 64) {  // by falling block count, ties by index (the bases' differences are the counts)
-      rank = 0;
-      for (int i = 0; i < a.n; ++i) {
-        const int b = (i + 1 < a.n ? s.base[i + 1] : s.total) - s.base[i];
-        rank += b > blocks || (b == blocks && i < tid);
-      }
-    }
-    reinterpret_cast<int4*>(a.gblk + group_list(a.n))[rank] = int4{tid, first, first + blocks, 0};
-  }
-  volatile int* const at = s.hist[w];  // this wave's running positions (only this wave uses them)
-  auto place = [&](int g, int64_t t) {
-    uint64_t todo = __ballot(g >= 0 && g < a.n);
-    while (todo) {
-      const int lead = __builtin_ctzll(todo);
-      const int cur = __builtin_amdgcn_readlane(g, lead);
-      const uint64_t same = __ballot(g == cur);
-      todo &= ~same;
-      const int start = at[cur];
-      if (g == cur) a.perm[(int64_t)s.base[cur] * 32 + start + __popcll(same & ((1ull << l) - 1))] = (int32_t)t;
-      if (l == lead) at[cur] = start + __popcll(same);
-    }
-  };
+  int start[KEEP];
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) start[k] = kept[k] >= 0 ? s.base[kept[k]] * 32 + s.hist[w][kept[k]] : 0;
 #pragma unroll
   for (int k = 0; k < KEEP; ++k)
-    if (lo + 64 * k < hi) place(kept[k], lo + 64 * k + l);
-  for (int64_t t0 = lo + 64 * KEEP; t0 < hi; t0 += 64) place(t0 + l < hi ? a.ids[t0 + l] : -1, t0 + l);
+    if (kept[k] >= 0) a.perm[start[k] + at[k]] = (int32_t)(lo + 64 * k + l);
+  if (a.n > 64) {
+    if (tid < a.n) reinterpret_cast<int4*>(a.gblk + group_list(a.n))[tid] = int4{tid, first, first + blocks, 0};
+  } else if (w == 0) {  // by falling block count, ties by index
+    int rank = 0;
+    for (int i = 0; i < a.n; ++i) {
+      const int b = __builtin_amdgcn_readlane(blocks, i);
+      rank += b > blocks || (b == blocks && i < tid);
+    }
+    if (tid < a.n) reinterpret_cast<int4*>(a.gblk + group_list(a.n))[rank] = int4{tid, first, first + blocks, 0};
+  }
+  if (tid < a.n)
+    for (int i = cnt; i < 32 * blocks; ++i) a.perm[(int64_t)first * 32 + i] = -1;
+  if (lo + 64 * KEEP >= hi) return;
+  // the wave's later tokens: its counts become running places, which start behind the kept tokens
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    const Match m = match_adapter(kept[k], l);
+    if (kept[k] >= 0 && m.place == 0) mine[kept[k]] = mine[kept[k]] + m.count;
+  }
+  for (int64_t t0 = lo + 64 * KEEP; t0 < hi; t0 += 64) {
+    const int g = load_id(t0 + l), p = take(g);
+    if (g >= 0) a.perm[s.base[g] * 32 + p] = (int32_t)(t0 + l);
+  }
 }
 
-// dst[y][x] = src[x][y] for one 64 x 64 tile (X x Y source, dst rows of stride ld), 16 bytes a lane on
-// both sides where the rows allow (X, Y and ld multiples of 8: the matrices' bases are 16-byte aligned)
-SRA_DEV void transpose64(const uint16_t* __restrict__ src, int64_t X, int64_t Y, uint16_t* __restrict__ dst, int64_t ld,
-                         int64_t x0, int64_t y0, TileLds& s) {
-  const bool vec = ((X | Y | ld) & 7) == 0;
-  const int tid = threadIdx.x;
-  if (vec) {
-    if (tid < 512) {
-      const int i = tid >> 3, c = tid & 7;
+// dst[y][x] = src[x][y] for one tile of 2^lx by 2^ly (X x Y source, dst rows of stride ld), 16 bytes a
+// lane on both sides where the rows allow (X, Y and ld multiples of 8: the matrices' bases are 16-byte
+// aligned).  A tile has 8192 elements whatever its shape, one load and one store a thread: tiles of
+// 64 x 64 left three quarters of the lanes idle at rank 16.
+SRA_DEV void transpose_tile(const uint16_t* __restrict__ src, int64_t X, int64_t Y, uint16_t* __restrict__ dst, int64_t ld,
+                            int lx, int ly, int64_t x0, int64_t y0, TileLds& s) {
+  const int tid = threadIdx.x, pitch = (1 << ly) + 2;
+  // chunk i of 1024 -> (row, chunk of the row): eight chunks (128 bytes) of a row, then the rows, so that
+  // the gathering reads spread over the banks
+  auto place = [](int i, int lrows, int lchunks, int& row, int& c) {
+    const int lc = min(lchunks, 3);
+    c = (i & ((1 << lc) - 1)) | (i >> (lrows + lc) << lc);
+    row = (i >> lc) & ((1 << lrows) - 1);
+  };
+  if (((X | Y | ld) & 7) == 0) {
+    int i, c;
+    place(tid, lx, ly - 3, i, c);
+    {
       const int64_t x = x0 + i, y = y0 + 8 * c;
       union { u32x4 v; uint32_t w[4]; } u;
       u.v = u32x4{0, 0, 0, 0};
       if (x < X && y < Y) u.v = *reinterpret_cast<const u32x4*>(src + x * Y + y);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t*>(&s.t[i][8 * c + 2 * k]) = u.w[k];
+      for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t*>(&s.t[i * pitch + 8 * c + 2 * k]) = u.w[k];
     }
     __syncthreads();
-    if (tid < 512) {
-      const int i = tid >> 3, c = tid & 7;  // row y0 + i, columns x0 + 8 c ..
-      const int64_t y = y0 + i, x = x0 + 8 * c;
-      union { u32x4 v; uint16_t h[8]; } u;
+    place(tid, ly, lx - 3, i, c);  // row y0 + i, columns x0 + 8 c ..
+    const int64_t y = y0 + i, x = x0 + 8 * c;
+    union { u32x4 v; uint16_t h[8]; } u;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u.h[k] = s.t[8 * c + k][i];
-      if (y < Y && x < X) *reinterpret_cast<u32x4*>(dst + y * ld + x) = u.v;
-    }
+    for (int k = 0; k < 8; ++k) u.h[k] = s.t[(8 * c + k) * pitch + i];
+    if (y < Y && x < X) *reinterpret_cast<u32x4*>(dst + y * ld + x) = u.v;
     return;
   }
-  const int tx = tid & 63, ty = tid >> 6;
 #pragma unroll
-  for (int k = 0; k < 64 / kPrepWaves; ++k) {
-    const int i = ty + kPrepWaves * k;
-    const int64_t x = x0 + i, y = y0 + tx;
-    s.t[i][tx] = (x < X && y < Y) ? src[x * Y + y] : (uint16_t)0;
+  for (int k = 0; k < 8; ++k) {
+    const int e = tid + kPrepThreads * k, i = e >> ly, j = e & ((1 << ly) - 1);
+    const int64_t x = x0 + i, y = y0 + j;
+    s.t[i * pitch + j] = (x < X && y < Y) ? src[x * Y + y] : (uint16_t)0;
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 64 / kPrepWaves; ++k) {
-    const int i = ty + kPrepWaves * k;
-    const int64_t y = y0 + i, x = x0 + tx;
-    if (y < Y && x < X) dst[y * ld + x] = s.t[tx][i];
+  for (int k = 0; k < 8; ++k) {
+    const int e = tid + kPrepThreads * k, i = e >> lx, j = e & ((1 << lx) - 1);
+    const int64_t y = y0 + i, x = x0 + j;
+    if (y < Y && x < X) dst[y * ld + x] = s.t[j * pitch + i];
   }
 }
+// a tile's extent along the rank, as a power of two: 2^13 elements lie in one
+__host__ __device__ inline int tile_lr(int r) { return r <= 16 ? 4 : r <= 32 ? 5 : 6; }
 
 __global__ __launch_bounds__(kPrepThreads) void k_multi_prep(PrepArgs a) {
   __shared__ PrepLds lds;
@@ -205,13 +244,15 @@ __global__ __launch_bounds__(kPrepThreads) void k_multi_prep(PrepArgs a) {
     --b;
   }
   const int64_t nb = (int64_t)a.n * a.b_tiles;
+  const int lr = tile_lr(a.r), lm = 13 - lr;
+  const int64_t rt = (a.r + (1 << lr) - 1) >> lr;  // tiles along the rank
   if (b < nb) {
-    const int64_t g = b / a.b_tiles, i = b % a.b_tiles, yt = (a.r + 63) / 64;
-    transpose64(a.B + g * a.N * a.r, a.N, a.r, a.wt + g * a.N * a.r, a.N, i / yt * 64, i % yt * 64, lds.t);
+    const int64_t g = b / a.b_tiles, i = b % a.b_tiles;
+    transpose_tile(a.B + g * a.N * a.r, a.N, a.r, a.wt + g * a.N * a.r, a.N, lm, lr, i / rt << lm, i % rt << lr, lds.t);
   } else {
     b -= nb;
-    const int64_t g = b / a.a_tiles, i = b % a.a_tiles, xt = (a.r + 63) / 64;
-    transpose64(a.A + g * a.r * a.K, a.r, a.K, a.at + g * a.K * a.lda, a.lda, i % xt * 64, i / xt * 64, lds.t);
+    const int64_t g = b / a.a_tiles, i = b % a.a_tiles;
+    transpose_tile(a.A + g * a.r * a.K, a.r, a.K, a.at + g * a.K * a.lda, a.lda, lr, lm, i % rt << lr, i / rt << lm, lds.t);
   }
 }
 
@@ -869,8 +910,10 @@ hipError_t launch_multi_prep(const MultiPrep& p, hipStream_t s) {
   a.lda = packed_at_ld(p.r);
   a.at = p.at;
   a.r = p.r;
-  a.b_tiles = p.wt ? (int)(cdiv64(p.N, 64) * cdiv64(p.r, 64)) : 0;
-  a.a_tiles = p.at ? (int)(cdiv64(p.K, 64) * cdiv64(p.r, 64)) : 0;
+  const int lr = tile_lr(p.r), lm = 13 - lr;
+  const int64_t rt = cdiv64(p.r, 1 << lr);
+  a.b_tiles = p.wt ? (int)(cdiv64(p.N, 1 << lm) * rt) : 0;
+  a.a_tiles = p.at ? (int)(cdiv64(p.K, 1 << lm) * rt) : 0;
   const int64_t blocks = (a.ids ? 1 : 0) + (int64_t)p.n * (a.b_tiles + a.a_tiles);
   if (blocks == 0) return hipSuccess;
   hipLaunchKernelGGL(k_multi_prep, dim3((unsigned)blocks), dim3(kPrepThreads), 0, s, a);

@@ -142,6 +142,13 @@ def test_many_adapters(gpu):
     run(gpu, 1500, 64, 32, 4, 700, "mixed")
 
 
+@pytest.mark.parametrize("n", [5, 70])
+@pytest.mark.parametrize("kind", ["mixed", "requests"])
+def test_long_batches(gpu, n, kind):
+    """More tokens than the sort's workgroup keeps in registers."""
+    run(gpu, 9001, 64, 32, 4, n, kind)
+
+
 def test_one_adapter_equals_the_layer(gpu):
     """With one adapter for every token, the outputs of the one-adapter layer to rounding."""
     S, P, X, dY, A, B, di, U, res = run(gpu, 96, 128, 64, 8, 1, "one")
