@@ -6,6 +6,10 @@
 // maximum with lane exchanges, with no LDS.  Rows whose length is a multiple of 32 need no row
 // structure: the call passes them as one long row.  Each thread issues the loads of U vectors
 // before it uses the first.
+//
+// Measured at 8192 x 20480 in bf16 (509 MB each way): encoding 111 us, 4.6 TB/s; decoding 77 us, 6.6
+// TB/s, its codes still in the Infinity Cache where it follows the encoding (a copy of 2 GiB
+// reaches 4.9 TB/s).
 #include <algorithm>
 
 #include "rowvec.h"

@@ -10,6 +10,9 @@
 //     runs by falling block count (up to 64 adapters), so that the longest start first;
 //   the other workgroups transpose every B_g (the dU product's operand, contiguous along N) and
 //     every A_g (the dX epilogue's rows of r entries), in tiles of 8192 elements.
+//   It is bound by the sort's chain of dependent steps at small sizes (5.3 us: 2047 tokens, 12 adapters,
+//   rank 16, K + N = 5120) and by HBM at large ones (13.7 us for the 105 MB that 8 adapters of rank 128
+//   and K + N = 25600 read and write).
 //
 // The gradients are sums over an adapter's tokens of products of one Act value (dY or X, bf16, or an
 // 8-bit checkpoint decoded on the way, exactly) with one V value (U or dU, fp32, split into three
@@ -23,12 +26,17 @@
 // Ranks up to 32 (k_multi_grads_few) are bound by reading Act and by latency.  A workgroup owns one
 // adapter and 64 columns; its NW waves take every NW-th 32-token block, each through its own LDS
 // tile with no barrier, and join their sums at the end, so an adapter's chain of steps is 1 / NW as
-// long and 16 waves a CU keep loads in flight.  V is read and split by each wave itself.
+// long and 16 waves a CU keep loads in flight.  V is read and split by each wave itself.  10 us for dA
+// and dB of 2047 tokens, 12 adapters, rank 16, K = 4096, N = 1024: 21 MB of Act at 2.1 TB/s, bound by
+// the longest adapter's chain of steps.
 //
 // Larger ranks (k_multi_grads) are bound by the matrix cores and by LDS reads of V.  V is split once
 // (k_multi_vt) into tiles of 32 tokens in the sorted order, contiguous per step; a workgroup of
 // eight waves owns 256 columns and 64 or 128 adapter columns (wave: 64 adapter columns by 32 or 64
-// columns), stages both tiles through registers two steps ahead and double-buffers LDS.
+// columns), has both tiles two steps ahead and double-buffers LDS.  182 us for 8192 tokens, 8
+// adapters, rank 128, K = 5120 (a checkpoint), N = 20480: 161 GFLOP of the three parts at 0.88
+// PFLOP/s, where a large bf16 matrix product reaches 1.34; the matrix cores are busy for 40% of the
+// cycles and the 800 workgroups take unequal shares of the tokens.
 #include <algorithm>
 
 #include "rowvec.h"
@@ -640,7 +648,8 @@ __global__ __launch_bounds__(512, 2) void k_multi_grads(GradArgs ga) {
       grad_store(ga, job, g, z, j0 + 64 * wj + 16 * a, m0 + (wm * MF + f) * 16, acc[a][f], l16, q4);
 }
 
-// out[i] = sum of the S slices' partials in slice order; both jobs' outputs one after the other
+// out[i] = sum of the S slices' partials in slice order; both jobs' outputs one after the other (5.5 us
+// for the slices of U or dU at 8192 tokens, rank 128)
 __global__ void k_multi_join(const float* __restrict__ part, int64_t slice, int S, int64_t n0, int64_t n1,
                              float* __restrict__ out0, float* __restrict__ out1) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -663,6 +672,9 @@ __global__ void k_multi_join(const float* __restrict__ part, int64_t slice, int 
 // A tile whose tokens take several adapters runs one pass per distinct adapter and writes the tokens
 // of that adapter after it; the grid holds `passes` workgroups per tile (as k_adapter_rows), the last
 // of them taking what the others leave.
+// Bound by the transfers' latency into LDS: 36 us for U of 8192 tokens at K = 5120, rank 128, 8
+// adapters in 15 requests (84 MB of X, 2.3 TB/s) and 112 us for dU at N = 20480 (336 MB of dY, 3.0
+// TB/s, where a copy reaches 4.9).
 template <int JR, bool TW>
 __global__ __launch_bounds__(512, 4) void k_multi_rows(const uint16_t* __restrict__ act, int64_t T, int64_t C,
                                                        const uint16_t* __restrict__ wgt, int r, int64_t c_per, int S,
