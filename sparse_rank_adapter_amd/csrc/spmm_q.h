@@ -925,14 +925,24 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
     const __amdgpu_buffer_rsrc_t ru = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(ep.U + t0 * ep.r), 0, toks_here * ep.r * 4, 0x00020000);
     // many adapters: the E fragments of CH steps (adapter, 32 columns) are in flight together, a step's
-    // slot refilled once its products are out (the largest wave tile has registers for two steps).  The loads are bare:
-    // clearing the entries past r right after each load made every load wait for itself (36.3 us
-    // against 23.1 at OPT-350M fc1 where 16 adapters meet in each 128-token tile), so that happens at
-    // the products.
-    constexpr int CH = MA ? (FR * FT >= 32 ? 2 : 4) : 1;
+    // slot refilled once its products are out (the largest wave tile has registers for two steps).
+    // The loads are bare: clearing the entries past r right after each load made every load wait for
+    // itself (36.3 us against 23.1 at OPT-350M fc1 where 16 adapters met in each 128-token tile, before
+    // other steps), so that happens at the products.  With 16 adapters a tile the kernel takes 25.7 us now,
+    // with one 22.4: a step costs about 150 instructions beside its products.
+    constexpr int CH = MA ? (FR * FT >= 32 ? 2 : 6) : 1;
     union EF { u32x4 v; bf16x8 b; };
     EF en[CH][MA ? FR : 1];
     int ga[CH], ja[CH], g_at = -1, j_at = 0;
+    uint32_t e_off[MA ? FR : 1];
+    u32x4 e_keep;  // of this lane's eight entries, those before r in r's last 32 columns
+    if constexpr (MA) {
+      const int left = ep.r - ((ep.r - 1) / 32 * 32 + 8 * q4);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) e_keep[q] = left >= 2 * q + 2 ? ~0u : left == 2 * q + 1 ? 0xffffu : 0u;
+#pragma unroll
+      for (int i = 0; i < FR; ++i) e_off[i] = (uint32_t)(((row0 + wr * 16 * FR + i * 16 + l16) * ep.e_row_stride + 8 * q4) * 2);
+    }
     auto next_adapter = [&]() {  // wave-uniform; -1 when none is left
       int g = -1;
       if constexpr (MA) {
@@ -944,27 +954,23 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
       }
       return g;
     };
-    auto fetch = [&](int c, int jb0, int nj) {  // the next step into slot c (ga = -1 past the last)
+    // The next step into slot c (ga = -1 past the last; nothing is loaded then: empty loads that would let
+    // the compiler count what is in flight cost more, 26.2 against 25.6 us at OPT-350M fc1's mixed batch).
+    // Rows that are not 16-byte aligned are loaded at the products.
+    auto fetch = [&](int c, int jb0, int nj) {
       ga[c] = g_at;
       ja[c] = j_at;
       if constexpr (MA) {
-        if (g_at >= 0) {
-          re = __builtin_amdgcn_make_buffer_rsrc((void*)(ep.E + (int64_t)g_at * ep.ai.stride), 0,
-                                                 (int)(R * ep.e_row_stride * 2), 0x00020000);
-          if (e_al) {
+        if (g_at < 0) return;
+        const __amdgpu_buffer_rsrc_t rg = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(ep.E + (int64_t)g_at * ep.ai.stride), 0, e_al ? (int)(R * ep.e_row_stride * 2) : 0, 0x00020000);
 #pragma unroll
-            for (int i = 0; i < FR; ++i)
-              en[c][i].v = __builtin_amdgcn_raw_buffer_load_b128(
-                  re, (uint32_t)(((row0 + wr * 16 * FR + i * 16 + l16) * ep.e_row_stride + jb0 + j_at + 8 * q4) * 2), 0, 0);
-          } else {
-#pragma unroll
-            for (int i = 0; i < FR; ++i) en[c][i].v = load_e(row0 + wr * 16 * FR + i * 16 + l16, jb0 + j_at + 8 * q4);
-          }
-          j_at += 32;
-          if (j_at >= nj) {
-            g_at = next_adapter();
-            j_at = 0;
-          }
+        for (int i = 0; i < FR; ++i)
+          en[c][i].v = __builtin_amdgcn_raw_buffer_load_b128(rg, e_off[i], e_al ? (uint32_t)(2 * (jb0 + j_at)) : 0u, 0);
+        j_at += 32;
+        if (j_at >= nj) {
+          g_at = next_adapter();
+          j_at = 0;
         }
       }
     };
@@ -997,13 +1003,13 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
       wait_vm<0>();
       __syncthreads();
       if constexpr (MA) {
-        // one step per distinct adapter and 32 adapter columns.  A fragment whose tokens all take the
-        // adapter adds its products in place, one with none skips them, and a mixed one keeps them
-        // for the adapter's tokens only (a selection, not a product with zeros: nothing in one adapter
-        // reaches another's tokens, whose bits do not depend on their neighbours either).  U is split
-        // once per workgroup, in place (32 bytes of eight fp32 become eight bf16 parts and eight bf16
-        // rests): by every wave of a token column and for every adapter, the split took longer than
-        // the products
+        // one step per distinct adapter and 32 adapter columns.  A fragment with no token of the adapter is
+        // skipped; the others keep the products for the adapter's tokens only (a selection, not a product
+        // with zeros: nothing in one adapter reaches another's tokens, whose bits do not depend on their
+        // neighbours either; a separate path for fragments of one adapter cost as many register moves as
+        // the selection).  U is split once per workgroup, in place (32 bytes of eight fp32 become eight bf16
+        // parts and eight bf16 rests): by every wave of a token column and for every adapter, the split
+        // took longer than the products
         const int cs = nj > 64 ? 4 : nj > 32 ? 3 : nj > 16 ? 2 : 1;  // 2^cs groups of 8 hold the nj columns
         for (int i = tid; i < BT << cs; i += 64 * NW) {
           const int tok = i >> cs, c = (2 * (i & ((1 << cs) - 1))) ^ (tok & 31);
@@ -1027,37 +1033,30 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
           const int g = ga[ch], jj = ja[ch];
           if (g < 0) break;  // wave-uniform
           EF (&e)[FR] = en[ch];
+          if (!e_al) {
+            re = __builtin_amdgcn_make_buffer_rsrc((void*)(ep.E + (int64_t)g * ep.ai.stride), 0,
+                                                   (int)(R * ep.e_row_stride * 2), 0x00020000);
+#pragma unroll
+            for (int i = 0; i < FR; ++i) e[i].v = load_e(row0 + wr * 16 * FR + i * 16 + l16, jb0 + jj + 8 * q4);
+          }
           if (jb0 + jj + 32 > ep.r) {  // entries past r: another row's
-            const int left = ep.r - (jb0 + jj + 8 * q4);  // of this lane's eight
 #pragma unroll
-            for (int i = 0; i < FR; ++i)
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                e[i].v[q] &= left >= 2 * q + 2 ? ~0u : left == 2 * q + 1 ? 0xffffu : 0u;
+            for (int i = 0; i < FR; ++i) e[i].v &= e_keep;
           }
           const int c0 = (jj + 8 * q4) >> 2;
 #pragma unroll
           for (int j = 0; j < FT; ++j) {
-            const uint32_t here = (uint32_t)__ballot(id[j] == g) & 0xffffu;
-            if (here == 0) continue;  // wave-uniform, as is the choice below
+            if (((uint32_t)__ballot(id[j] == g) & 0xffffu) == 0) continue;  // wave-uniform
             const int tl = wt * 16 * FT + j * 16 + l16, sw = tl & 31;
             EF uhi, ulo;
             uhi.v = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * (c0 ^ sw));
             ulo.v = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * ((c0 + 1) ^ sw));
-            if (here == 0xffffu) {
 #pragma unroll
-              for (int i = 0; i < FR; ++i) {
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, uhi.b, acc[i][j], 0, 0, 0);
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, ulo.b, acc[i][j], 0, 0, 0);
-              }
-            } else {
+            for (int i = 0; i < FR; ++i) {
+              f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, uhi.b, acc[i][j], 0, 0, 0);
+              t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, ulo.b, t, 0, 0, 0);
 #pragma unroll
-              for (int i = 0; i < FR; ++i) {
-                f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, uhi.b, acc[i][j], 0, 0, 0);
-                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e[i].b, ulo.b, t, 0, 0, 0);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[i][j][q] = id[j] == g ? t[q] : acc[i][j][q];
-              }
+              for (int q = 0; q < 4; ++q) acc[i][j][q] = id[j] == g ? t[q] : acc[i][j][q];
             }
           }
           fetch(ch, jb0, nj);
