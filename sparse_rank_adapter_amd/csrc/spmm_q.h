@@ -886,19 +886,27 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
   static_assert(!MA || kStageU, "many adapters read U from LDS");
   if constexpr (kStageU) {
   if (ep.r > 0 && z == 0) {
-    // many adapters: the ids of this wave's tokens (token l16 of fragment j) and, per fragment,
-    // the tokens whose adapter is valid
-    int id[MA ? FT : 1];
-    uint32_t valid[MA ? FT : 1];
+    // many adapters: the ids of this wave's tokens, token l16 of fragment j in id[j] and again, four
+    // fragments to a word, lane 16 k + i that of token i of fragment 4 w + k, so that one ballot finds an
+    // adapter's tokens (-1: no adapter)
+    constexpr int IW = MA ? (FT + 3) / 4 : 1;
+    int id[MA ? FT : 1], idw[IW];
     if constexpr (MA) {
 #pragma unroll
       for (int j = 0; j < FT; ++j) {
         const int tl = wt * 16 * FT + j * 16 + l16;
         id[j] = tl < toks_here ? ep.ai.ids[t0 + tl] : -1;
-        valid[j] = (uint32_t)__ballot(id[j] >= 0 && id[j] < ep.ai.n) & 0xffffu;
+        if (id[j] >= ep.ai.n) id[j] = -1;
+      }
+#pragma unroll
+      for (int w = 0; w < IW; ++w) {
+        idw[w] = -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (4 * w + k < FT) idw[w] = q4 == k ? id[4 * w + k] : idw[w];
       }
     }
-    uint32_t todo[MA ? FT : 1];
+    uint64_t todo[IW], same_at[IW];
     // E rows are contiguous in j (e_j_stride == 1, checked by the launchers): one 16-byte load
     // per fragment (eight 2-byte ones when rows are not 16-byte aligned) through a resource over
     // E's rows R, so rows past R read as zero; entries past r (the next row's, or padding) are
@@ -934,6 +942,7 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
     union EF { u32x4 v; bf16x8 b; };
     EF en[CH][MA ? FR : 1];
     int ga[CH], ja[CH], g_at = -1, j_at = 0;
+    uint64_t same[CH][IW];  // the slots' tokens
     uint32_t e_off[MA ? FR : 1];
     u32x4 e_keep;  // of this lane's eight entries, those before r in r's last 32 columns
     if constexpr (MA) {
@@ -947,10 +956,13 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
       int g = -1;
       if constexpr (MA) {
 #pragma unroll
-        for (int j = FT - 1; j >= 0; --j)
-          if (todo[j]) g = __builtin_amdgcn_readlane(id[j], __builtin_ctz(todo[j]));
+        for (int w = IW - 1; w >= 0; --w)
+          if (todo[w]) g = __builtin_amdgcn_readlane(idw[w], __builtin_ctzll(todo[w]));
 #pragma unroll
-        for (int j = 0; j < FT; ++j) todo[j] &= ~(uint32_t)__ballot(id[j] == g);
+        for (int w = 0; w < IW; ++w) {
+          same_at[w] = __ballot(idw[w] == g);
+          todo[w] &= ~same_at[w];
+        }
       }
       return g;
     };
@@ -962,6 +974,8 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
       ja[c] = j_at;
       if constexpr (MA) {
         if (g_at < 0) return;
+#pragma unroll
+        for (int w = 0; w < IW; ++w) same[c][w] = same_at[w];
         const __amdgpu_buffer_rsrc_t rg = __builtin_amdgcn_make_buffer_rsrc(
             (void*)(ep.E + (int64_t)g_at * ep.ai.stride), 0, e_al ? (int)(R * ep.e_row_stride * 2) : 0, 0x00020000);
 #pragma unroll
@@ -994,7 +1008,7 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
       const int nj = min(128, ep.r - jb0);
       if constexpr (MA) {
 #pragma unroll
-        for (int j = 0; j < FT; ++j) todo[j] = valid[j];
+        for (int w = 0; w < IW; ++w) todo[w] = __ballot(idw[w] >= 0);
         g_at = next_adapter();
         j_at = 0;
 #pragma unroll
@@ -1046,7 +1060,7 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
           const int c0 = (jj + 8 * q4) >> 2;
 #pragma unroll
           for (int j = 0; j < FT; ++j) {
-            if (((uint32_t)__ballot(id[j] == g) & 0xffffu) == 0) continue;  // wave-uniform
+            if (((uint32_t)(same[ch][j / 4] >> (16 * (j % 4))) & 0xffffu) == 0) continue;  // wave-uniform
             const int tl = wt * 16 * FT + j * 16 + l16, sw = tl & 31;
             EF uhi, ulo;
             uhi.v = *reinterpret_cast<const u32x4*>(smem + tl * 512 + 16 * (c0 ^ sw));
