@@ -149,6 +149,24 @@ def test_long_batches(gpu, n, kind):
     run(gpu, 9001, 64, 32, 4, n, kind)
 
 
+@pytest.mark.parametrize("T", [32, 33, 34, 64, 100, 255, 256, 257])
+@pytest.mark.parametrize("r", [4, 24, 64])
+def test_single_tokens_of_many_adapters(gpu, T, r):
+    """Batches whose tokens each take an adapter of their own choice: the order of the work, not the results,
+    depends on them."""
+    run(gpu, T, 128, 96, r, 40, "mixed")
+    g = torch.Generator().manual_seed(T)
+    S, _ = weight(96, 128, 2, 4, g, gpu)
+    X = torch.randn(T, 128, generator=g).bfloat16().to(gpu)
+    A = (torch.randn(40, r, 128, generator=g) * 0.05).bfloat16().to(gpu)
+    B = (torch.randn(40, 96, r, generator=g) * 0.05).bfloat16().to(gpu)
+    ids = make_ids("mixed", T, 40, g).to(gpu)
+    Y, U = sra.multi_lora_fwd(S, X, A, B, ids)
+    order = torch.argsort(ids, stable=True)
+    Ys, Us = sra.multi_lora_fwd(S, X[order].contiguous(), A, B, ids[order].contiguous())
+    assert torch.equal(U[order], Us) and torch.equal(Y[order], Ys)
+
+
 def test_one_adapter_equals_the_layer(gpu):
     """With one adapter for every token, the outputs of the one-adapter layer to rounding."""
     S, P, X, dY, A, B, di, U, res = run(gpu, 96, 128, 64, 8, 1, "one")
