@@ -888,7 +888,11 @@ hipError_t launch_multi_rows(const uint16_t* act, int64_t T, int64_t C, const ui
   const RowsPlan p = multi_rows_plan(T, C, n, r);
   if (!p.ring) return w_t ? hipErrorInvalidValue : launch_multi_rows_small(act, T, C, w, C, r, ai, out, ws, s);
   if (w_t && r % 8 != 0) return hipErrorInvalidValue;
-  ai.passes = n < 8 ? n : 8;
+  // eight workgroups share a tile's adapters, and up to 32 as long as the grid stays at 1024: 256 / 512 tokens
+  // of 32 adapters side by side, C = N = 4096, r = 64: forward 67 / 101 us where eight took 100 / 107 (one
+  // adapter: 41 / 42 and 39 / 41)
+  const int64_t wgs = cdiv64(T, 128) * cdiv64(r, p.jr) * p.S;
+  ai.passes = (int)std::min<int64_t>(n, std::max<int64_t>(8, std::min<int64_t>(32, 1024 / wgs)));
   float* part = p.S > 1 ? (float*)ws : nullptr;
   const dim3 grid((unsigned)(cdiv64(T, 128) * cdiv64(r, p.jr) * p.S * ai.passes));
 #define SRA_MR(JR, TWV) \
