@@ -849,20 +849,23 @@ hipError_t launch_spmm24_bf16(const uint16_t* s_vals, const uint32_t* s_meta, in
 
 // Many adapters.  The tile follows the one-adapter rule of plan_for on the tile counts: 256x256
 // once those fill the GPU twice, 256x128 once those fill it, else 128x64 (C % 128 == 0, metadata in
-// super-stages) or 256x64; C % 64 == 32 takes the register-staged 128x128.  Few tiles with a long
-// reduction split it (canonical arrays; whole 8-stage super-stages per split).
+// super-stages) or 256x64; C % 64 == 32 takes the register-staged 128x128.  Up to 128 tiles
+// split a long reduction (whole 8-stage super-stages per split, so a split of the streaming layout starts
+// on a metadata block) into about 256 workgroups, and the splits share the adapters: forward of 64
+// tokens of 32 adapters, streaming layout, r = 16, whole / split: K = N = 4096 40.3 / 27.0 us, K = 8192,
+// N = 16384 (128 tiles) 63.1 / 48.2; with 160 tiles (K = 5120, N = 20480) 54.4 / 57.1.
 namespace {
 struct MultiPlan {
   int bt;  // tokens per tile: 256, 128 or 64; 0: the register-staged tile
   Plan p;
 };
-MultiPlan multi_plan(int64_t R, int64_t C, int64_t T, bool tiled) {
+MultiPlan multi_plan(int64_t R, int64_t C, int64_t T) {
   MultiPlan m{0, Plan{cfg_by_id(3), 1, (int)((C + 63) / 64)}};
   if (C % 64 != 0) return m;
   auto tiles = [&](int br, int bt) { return ((R + br - 1) / br) * ((T + bt - 1) / bt); };
   m.bt = tiles(256, 256) >= 512 ? 256 : tiles(256, 128) >= 240 ? 128 : 64;
   const int64_t n = tiles(C % 128 == 0 ? 128 : 256, 64);
-  if (m.bt == 64 && !tiled && n < 240) {
+  if (m.bt == 64 && n <= 128) {
     const int nC = (int)(C / 64);
     int s = (int)((256 + n - 1) / n);
     if (s > nC / 8) s = nC / 8;  // keep >= 8 stages per split
@@ -877,7 +880,7 @@ MultiPlan multi_plan(int64_t R, int64_t C, int64_t T, bool tiled) {
 
 size_t spmm24_multi_ws(int64_t R, int64_t C, int64_t T) {
   if (T <= 16 || R <= 0 || C <= 0) return 0;
-  const MultiPlan m = multi_plan(R, C, T, false);
+  const MultiPlan m = multi_plan(R, C, T);
   return m.p.splits > 1 ? (size_t)m.p.splits * T * R * sizeof(float) : 0;
 }
 
@@ -888,7 +891,7 @@ hipError_t launch_spmm24_multi_bf16(bool tiled, const uint16_t* s_vals, const ui
   if (ep.G || !ep.ai.ids || !epilogue_ok(ep, R)) return hipErrorInvalidValue;
   if (T <= 16) return launch_decode24_bf16(s_vals, s_meta, R, C, act, T, ep, out, s, tiled);
   if (tiled && C % 128 != 0) return hipErrorInvalidValue;
-  const MultiPlan m = multi_plan(R, C, T, tiled);
+  const MultiPlan m = multi_plan(R, C, T);
   float* part = m.p.splits > 1 ? (float*)ws : nullptr;
 #define SRA_MA(FR, FT, NS, MS, TLAYV) \
   launch_q<FR, FT, 4, 2, NS, MS, 0, false, TLAYV, false, 0, 0, true>(s_vals, s_meta, R, C, act, T, ep, out, part, m.p, s)

@@ -873,7 +873,7 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
     __syncthreads();
   }
 
-  // ---- fused low-rank epilogue (first split only), dense v_mfma_f32_16x16x32_bf16:
+  // ---- fused low-rank epilogue (first split only; many adapters: each split its share), dense v_mfma_f32_16x16x32_bf16:
   //      A operand = E rows (lane: row l%16, j = 8(l/16)..+7), B operand = U^T (token l%16)
   // With U from memory, the tile's U rows go through LDS once per 128 adapter columns (LDS-DMA
   // when r % 4 == 0, no registers held), so each U element crosses from L2 once per workgroup
@@ -885,7 +885,7 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
   constexpr bool kStageU = UG == 0 && BT * 512 <= TL::LDS && BT % (2 * NW) == 0;
   static_assert(!MA || kStageU, "many adapters read U from LDS");
   if constexpr (kStageU) {
-  if (ep.r > 0 && z == 0) {
+  if (ep.r > 0 && (MA || z == 0)) {
     // many adapters: the ids of this wave's tokens, token l16 of fragment j in id[j] and again, four
     // fragments to a word, lane 16 k + i that of token i of fragment 4 w + k, so that one ballot finds an
     // adapter's tokens (-1: no adapter)
@@ -897,6 +897,9 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
         const int tl = wt * 16 * FT + j * 16 + l16;
         id[j] = tl < toks_here ? ep.ai.ids[t0 + tl] : -1;
         if (id[j] >= ep.ai.n) id[j] = -1;
+        // the splits of the reduction share the adapters, by their numbers: a token's sums do not depend on
+        // what its neighbours take
+        if (gridDim.y > 1 && id[j] >= 0 && (uint32_t)id[j] % gridDim.y != (uint32_t)z) id[j] = -1;
       }
 #pragma unroll
       for (int w = 0; w < IW; ++w) {
