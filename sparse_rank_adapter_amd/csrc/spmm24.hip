@@ -29,6 +29,8 @@
 
 
 
+#include <algorithm>
+
 #include "common.h"
 #include "spmm_q.h"
 
@@ -188,8 +190,8 @@ __global__ __launch_bounds__(256, (Tile<FR, FT, WR, WT>::OCC)) void k_spmm24(
     }
   }
 
-  // ---- fused low-rank epilogue (first split only): acc += E(rows, :) U(tokens, :)^T
-  if (ep.r > 0 && z == 0) {
+  // ---- fused low-rank epilogue (first split only; many adapters: each split its share): acc += E(rows, :) U(tokens, :)^T
+  if (ep.r > 0 && (MA || z == 0)) {
     const bool e_vec = ep.e_j_stride == 1 && (ep.r & 7) == 0;
     const bool u_vec = (ep.r & 7) == 0;
     const uint16_t* E = ep.E;
@@ -200,7 +202,8 @@ __global__ __launch_bounds__(256, (Tile<FR, FT, WR, WT>::OCC)) void k_spmm24(
       for (int j = 0; j < FT; ++j) {
         const int64_t t = t0 + wt * 32 * FT + j * 32 + li;
         id[j] = t < T ? ep.ai.ids[t] : -1;
-        todo[j] = (uint32_t)__ballot(id[j] >= 0 && id[j] < ep.ai.n);  // lanes 0 .. 31: the 32 tokens
+        if (id[j] >= ep.ai.n || (gridDim.y > 1 && id[j] >= 0 && (uint32_t)id[j] % gridDim.y != (uint32_t)z)) id[j] = -1;
+        todo[j] = (uint32_t)__ballot(id[j] >= 0);  // lanes 0 .. 31: the 32 tokens
       }
     }
     auto next = [&]() -> bool {  // the next adapter's E, false when none is left (wave-uniform)
@@ -861,8 +864,20 @@ struct MultiPlan {
 };
 MultiPlan multi_plan(int64_t R, int64_t C, int64_t T) {
   MultiPlan m{0, Plan{cfg_by_id(3), 1, (int)((C + 63) / 64)}};
-  if (C % 64 != 0) return m;
   auto tiles = [&](int br, int bt) { return ((R + br - 1) / br) * ((T + bt - 1) / bt); };
+  // the register-staged tile has two workgroups to a CU and no transfers in flight over a stage, so it splits
+  // down to two stages: forward of 752 tokens, K = 6432, N = 1248, r = 64 147 -> 58 us; of 28 tokens of 18
+  // adapters, K = 544, N = 2880, r = 128 88 -> 45 us
+  if (C % 64 != 0) {
+    const int64_t t = tiles(128, 128);
+    const int nC = (int)((C + 63) / 64);
+    const int s = t > 0 && t <= 256 ? std::min((int)(512 / t), nC / 2) : 1;
+    if (s > 1) {
+      m.p.stages_per_split = (nC + s - 1) / s;
+      m.p.splits = (nC + m.p.stages_per_split - 1) / m.p.stages_per_split;
+    }
+    return m;
+  }
   m.bt = tiles(256, 256) >= 512 ? 256 : tiles(256, 128) >= 240 ? 128 : 64;
   const int64_t n = tiles(C % 128 == 0 ? 128 : 256, 64);
   if (m.bt == 64 && n <= 128) {
@@ -908,7 +923,7 @@ hipError_t launch_spmm24_multi_bf16(bool tiled, const uint16_t* s_vals, const ui
     else if (m.bt == 128) SRA_MA(4, 4, 4, 0, false);
     else SRA_MA(4, 2, 4, 0, false);
   } else {
-    launch_cfg<2, 2, 2, 2, true>(s_vals, s_meta, R, C, act, T, ep, out, nullptr, m.p, s);
+    launch_cfg<2, 2, 2, 2, true>(s_vals, s_meta, R, C, act, T, ep, out, part, m.p, s);
   }
 #undef SRA_MA
   if (part) finish_split(m.p, part, R, T, out, s);
