@@ -27,8 +27,6 @@
 // result is deterministic.  Workgroup ids are remapped so each XCD runs a contiguous range of
 // tiles, ordered in groups of 8 row tiles so concurrent workgroups share both operands in L2.
 
-
-
 #include <algorithm>
 
 #include "common.h"
@@ -850,9 +848,11 @@ hipError_t launch_spmm24_bf16(const uint16_t* s_vals, const uint32_t* s_meta, in
   return hipGetLastError();
 }
 
-// Many adapters.  The tile follows the one-adapter rule of plan_for on the tile counts: 256x256
-// once those fill the GPU twice, 256x128 once those fill it, else 128x64 (C % 128 == 0, metadata in
-// super-stages) or 256x64; C % 64 == 32 takes the register-staged 128x128.  Up to 128 tiles
+// Many adapters.  256x256 tiles once those fill the GPU twice; else 128x64 (C % 128 == 0, metadata in
+// super-stages; two workgroups to a CU) or 256x64 (one) as long as they all run at once, 512 or 256 of
+// them, and 256x128 beyond: 2119 tokens of 16 adapters side by side, N = 3200, K = 1024 / 4096, r = 64: 75 /
+// 143 us where the small tiles took 100 / 190; at 512 small tiles (2048 tokens, N = 2048) those take 64 where
+// the large ones take 70.  C % 64 == 32 takes the register-staged 128x128.  Up to 128 tiles
 // split a long reduction (whole 8-stage super-stages per split, so a split of the streaming layout starts
 // on a metadata block) into about 256 workgroups, and the splits share the adapters: forward of 64
 // tokens of 32 adapters, streaming layout, r = 16, whole / split: K = N = 4096 40.3 / 27.0 us, K = 8192,
@@ -878,12 +878,12 @@ MultiPlan multi_plan(int64_t R, int64_t C, int64_t T) {
     }
     return m;
   }
-  m.bt = tiles(256, 256) >= 512 ? 256 : tiles(256, 128) >= 240 ? 128 : 64;
+  m.bt = tiles(256, 256) >= 512 ? 256 : tiles(256, 128) > 128 ? 128 : 64;
   const int64_t n = tiles(C % 128 == 0 ? 128 : 256, 64);
   if (m.bt == 64 && n <= 128) {
     const int nC = (int)(C / 64);
     int s = (int)((256 + n - 1) / n);
-    if (s > nC / 8) s = nC / 8;  // keep >= 8 stages per split
+    if (s > (nC + 7) / 8) s = (nC + 7) / 8;  // 8 stages per split but the last
     if (s > 1) {
       m.p.stages_per_split = ((nC + s - 1) / s + 7) / 8 * 8;
       m.p.splits = (nC + m.p.stages_per_split - 1) / m.p.stages_per_split;

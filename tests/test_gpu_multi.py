@@ -137,6 +137,21 @@ def test_large_tiles(gpu):
     run(gpu, 100, 4096, 128, 16, 9, "mixed")
 
 
+@pytest.mark.parametrize("kind", ["mixed", "requests"])
+@pytest.mark.parametrize("T,K,N,r,n,tiled", [(17, 2048, 128, 16, 12, True), (64, 1024, 256, 40, 30, True),
+                                             (50, 768, 640, 4, 35, True), (100, 1600, 128, 8, 9, False),
+                                             (28, 544, 160, 128, 18, False), (130, 1056, 96, 10, 3, False)])
+def test_split_reduction(gpu, T, K, N, r, n, tiled, kind):
+    """Few tiles: the reduction is split and the splits share the adapters (more adapters than splits, and
+    fewer), in both layouts, with a short last split, and on the tile of reductions of 64 i + 32."""
+    run(gpu, T, K, N, r, n, kind, tiled=tiled)
+
+
+def test_middle_tiles(gpu):
+    """More than 128 tiles of 256 x 128 and fewer than fill the GPU."""
+    run(gpu, 1300, 128, 4096, 40, 5, "mixed")
+
+
 def test_many_adapters(gpu):
     run(gpu, 200, 64, 64, 4, 1023, "mixed")
     run(gpu, 1500, 64, 32, 4, 700, "mixed")
