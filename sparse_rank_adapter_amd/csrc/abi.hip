@@ -1137,7 +1137,7 @@ sra_status check_ids(const int32_t* ids, bool needed) {
 
 struct MultiPlan {
   size_t u_off = 0, du_off = 0, rows_off = 0, spmm_off = 0, meta_off = 0, v24_off = 0, x_off = 0;
-  size_t gblk_off = 0, perm_off = 0, grads_off = 0, wt_off = 0, at_off = 0, total = 0;
+  size_t gblk_off = 0, perm_off = 0, grads_off = 0, wt_off = 0, at_off = 0, pad_off = 0, total = 0;
 };
 void multi_weight_bytes(const sra_sparse* S, int64_t T, Arena* a, MultiPlan* p) {
   if (is12(S)) p->meta_off = a->take(meta_bytes(S));
@@ -1185,6 +1185,7 @@ size_t multi_bwd_plan(const sra_sparse* P, int64_t T, int32_t n, int32_t r, uint
     if (db) jobs[nj++].M = N;
     if (da) jobs[nj++].M = K;
     p.grads_off = a.take(sra::multi_grads_ws(jobs, nj, T, n, r));
+    if (da && !sra::multi_grad_fits(K, !have_x, r)) p.pad_off = a.take((size_t)T * sra::multi_pad_ld(K) * 2);
   }
   if (dx) multi_weight_bytes(P, T, &a, &p);
   p.total = a.used;
@@ -1348,6 +1349,14 @@ sra_status sra_multi_lora_bwd(const sra_sparse* P, const void* dY, const void* X
     jobs[nj].act = (const uint16_t*)X;
     jobs[nj].codes = X_codes;
     jobs[nj].exps = X_exps;
+    if (!sra::multi_grad_fits(K, X_codes != nullptr, r)) {  // rows that the kernels' loads do not fit
+      uint16_t* const pad = (uint16_t*)(wsb + plan.pad_off);
+      SRA_TRY(hip_done(sra::launch_multi_pad((const uint16_t*)X, X_codes, X_exps, T, K, pad, s), s, "multi bwd X rows"));
+      jobs[nj].act = pad;
+      jobs[nj].codes = nullptr;
+      jobs[nj].exps = nullptr;
+      jobs[nj].ld = sra::multi_pad_ld(K);
+    }
     jobs[nj].V = dU;
     jobs[nj].out = dA;
     jobs[nj].M = K;

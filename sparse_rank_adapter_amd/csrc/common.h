@@ -429,8 +429,10 @@ bool multi_rows_w_t(int64_t T, int64_t C, int r);
 size_t multi_rows_ws(int64_t T, int64_t C, int n, int r);
 hipError_t launch_multi_rows(const uint16_t* act, int64_t T, int64_t C, const uint16_t* w, bool w_t, int r,
                              const int32_t* ids, int n, float* out, void* ws, hipStream_t s);
-// One or two grouped products out_g = sum over g's tokens of act[t][:] V[t][:] (M % 8 == 0): act in
-// bf16, or as a checkpoint (act == nullptr); out [n][M][r], or [n][r][M] when out_t.
+// One or two grouped products out_g = sum over g's tokens of act[t][:] V[t][:]: act in bf16, or as a
+// checkpoint (act == nullptr); out [n][M][r], or [n][r][M] when out_t.  The kernels load whole vectors
+// of a row, so act's row length has to satisfy multi_grad_fits; launch_multi_pad makes rows that do
+// (bf16, ld columns, zeros past M) of any others.
 struct MultiGrad {
   const uint16_t* act = nullptr;
   const int8_t* codes = nullptr;
@@ -438,8 +440,13 @@ struct MultiGrad {
   const float* V = nullptr;
   float* out = nullptr;
   int64_t M = 0;
+  int64_t ld = 0;  // act's row length where it is not M
   bool out_t = false;
 };
+bool multi_grad_fits(int64_t row, bool ckpt, int r);
+int64_t multi_pad_ld(int64_t M);
+hipError_t launch_multi_pad(const uint16_t* act, const int8_t* codes, const uint8_t* exps, int64_t T, int64_t M,
+                            uint16_t* out, hipStream_t s);
 size_t multi_grads_ws(const MultiGrad* g, int n_jobs, int64_t T, int n, int r);
 hipError_t launch_multi_grads(const MultiGrad* g, int n_jobs, int64_t T, const int32_t* gblk, const int32_t* perm, int n,
                               int r, void* ws, hipStream_t s);

@@ -272,7 +272,7 @@ struct GradJob {
   const float* V;        // [T][r]
   uint16_t* vt;          // its parts [block][3][rp][32], ranks above 32
   float* out;            // [n][r][M] (out_t) or [n][M][r]; with slices, partials of slice 0
-  int64_t M;
+  int64_t M, ld;         // columns, act's row length (multi_grad_fits)
   int mb;                // column tiles
   bool out_t;
 };
@@ -364,17 +364,17 @@ __global__ __launch_bounds__(64 * NW) void k_multi_grads_few(GradArgs ga) {
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool second = (int)blockIdx.x >= ga.job[0].mb;
   const GradJob job = second ? ga.job[1] : ga.job[0];
-  const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * MT, M = job.M;
+  const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * MT, ld = job.ld;
   const int z = blockIdx.z, r = ga.r;
   int b0, b1;
   const int g = slice_of(ga, blockIdx.y, z, b0, b1);
-  const int64_t nblk = (M + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
+  const int64_t nblk = (ld + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
   uint8_t* const tile = lds + w * TILE;
 
   // a lane's share of a block: chunk l % 8 of rows l / 8 + 8 i, and V of adapter column l % 16 at the
   // tokens 8 (l / 16) + e
   const int c8 = l & 7, r8 = l >> 3;
-  const int64_t mc = min(m0 + 8 * c8, M - 8);  // past the row: any columns, their sums are not stored
+  const int64_t mc = min(m0 + 8 * c8, ld - 8);  // past the row (ld % 8 == 0): any columns, their sums are not stored
   u32x4 ar[4];
   float vr[JT][8];
   uint32_t a_ok = 0, v_ok = 0;  // bit: the row (token) is no padding.  Clearing waits for the data, so it
@@ -391,11 +391,11 @@ __global__ __launch_bounds__(64 * NW) void k_multi_grads_few(GradArgs ga) {
     }
     if (job.act) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ar[i] = *reinterpret_cast<const u32x4*>(job.act + tok[i] * M + mc);
+      for (int i = 0; i < 4; ++i) ar[i] = *reinterpret_cast<const u32x4*>(job.act + tok[i] * ld + mc);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const u32x2 q = *reinterpret_cast<const u32x2*>(job.codes + tok[i] * M + mc);
+        const u32x2 q = *reinterpret_cast<const u32x2*>(job.codes + tok[i] * ld + mc);
         ar[i] = u32x4{q[0], q[1], job.exps[tok[i] * nblk + mc / sra_row::kCkBlock], 0};
       }
     }
@@ -519,7 +519,7 @@ __global__ __launch_bounds__(512, 2) void k_multi_grads(GradArgs ga) {
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wj = w % WJ, wm = w / WJ;
   const bool second = (int)blockIdx.x >= ga.job[0].mb;
   const GradJob& job = ga.job[second ? 1 : 0];
-  const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * MT, M = job.M;
+  const int64_t m0 = ((int64_t)blockIdx.x - (second ? ga.job[0].mb : 0)) * MT, ld = job.ld;
   const int njt = (ga.r + JR - 1) / JR, j0 = ((int)blockIdx.z % njt) * JR, z = (int)blockIdx.z / njt;
   int b0, b1;
   const int g = slice_of(ga, blockIdx.y, z, b0, b1);
@@ -529,9 +529,9 @@ __global__ __launch_bounds__(512, 2) void k_multi_grads(GradArgs ga) {
   // (not stored), padding reads token 0 and is cleared on the way to LDS.
   const bool bf = job.act != nullptr;
   const int t0 = bf ? tid >> 5 : tid >> 4, cc = bf ? tid & 31 : tid & 15;
-  const int64_t mc = min(m0 + (bf ? 8 : 16) * cc, M - (bf ? 8 : 16));
+  const int64_t mc = min(m0 + (bf ? 8 : 16) * cc, ld - (bf ? 8 : 16));  // ld is a multiple of 8, or of 16
   const uint8_t* const col = bf ? reinterpret_cast<const uint8_t*>(job.act + mc) : reinterpret_cast<const uint8_t*>(job.codes + mc);
-  const int64_t rowb = bf ? 2 * M : M, nblk = (M + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
+  const int64_t rowb = bf ? 2 * ld : ld, nblk = (ld + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
   // (bf16: the exponent's load stays, one per step for either kind, and reads Act's first byte)
   const uint8_t* const ecol = bf ? reinterpret_cast<const uint8_t*>(job.act) : job.exps + mc / sra_row::kCkBlock;
   struct Act {
@@ -646,6 +646,30 @@ __global__ __launch_bounds__(512, 2) void k_multi_grads(GradArgs ga) {
 #pragma unroll
     for (int f = 0; f < MF; ++f)
       grad_store(ga, job, g, z, j0 + 64 * wj + 16 * a, m0 + (wm * MF + f) * 16, acc[a][f], l16, q4);
+}
+
+// Rows of M columns as bf16 rows of ld >= M (ld % 8 == 0), zeros past M: for the few row lengths that the
+// gradient kernels' loads do not fit.  A thread writes eight columns; T * ld / 8 of them, walked by the grid.
+__global__ __launch_bounds__(256) void k_multi_pad(const uint16_t* __restrict__ act, const int8_t* __restrict__ codes,
+                                                   const uint8_t* __restrict__ exps, int64_t T, int64_t M, int64_t ld,
+                                                   uint16_t* __restrict__ out) {
+  const int64_t per = ld / 8, nblk = (M + sra_row::kCkBlock - 1) / sra_row::kCkBlock;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < T * per; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / per, m = i % per * 8;
+    union { uint16_t h[8]; u32x4 v; } o;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      o.h[k] = 0;
+      if (m + k >= M) continue;
+      if (act) {
+        o.h[k] = act[t * M + m + k];
+      } else {  // q 2^e is exact in bf16: the high half of the fp32 value
+        const float s = __uint_as_float((uint32_t)exps[t * nblk + (m + k) / sra_row::kCkBlock] << 23);
+        o.h[k] = (uint16_t)(__float_as_uint((float)codes[t * M + m + k] * s) >> 16);
+      }
+    }
+    *reinterpret_cast<u32x4*>(out + t * ld + m) = o.v;
+  }
 }
 
 // out[i] = sum of the S slices' partials in slice order; both jobs' outputs one after the other (5.5 us
@@ -937,6 +961,7 @@ hipError_t launch_multi_prep(const MultiPrep& p, hipStream_t s) {
 }
 
 namespace {
+constexpr int kFewRank = 32;  // ranks up to this: k_multi_grads_few
 struct GradPlan {
   bool few;
   int mt, wj, S, njt;
@@ -946,7 +971,7 @@ struct GradPlan {
 // batch spread evenly over the adapters.
 GradPlan grad_plan(const MultiGrad* g, int n_jobs, int64_t T, int n, int r) {
   GradPlan p{};
-  p.few = r <= 32;
+  p.few = r <= kFewRank;
   p.mt = p.few ? 64 : 256;
   p.wj = r <= 64 ? 1 : 2;
   p.njt = p.few ? 1 : (int)cdiv64(r, 64 * p.wj);
@@ -964,6 +989,18 @@ GradPlan grad_plan(const MultiGrad* g, int n_jobs, int64_t T, int n, int r) {
 }
 }  // namespace
 
+// 16-byte loads of bf16, 8-byte loads of codes, and above kFewRank 16-byte loads of codes
+bool multi_grad_fits(int64_t row, bool ckpt, int r) { return row % (ckpt && r > kFewRank ? 16 : 8) == 0; }
+int64_t multi_pad_ld(int64_t M) { return cdiv64(M, 32) * 32; }
+hipError_t launch_multi_pad(const uint16_t* act, const int8_t* codes, const uint8_t* exps, int64_t T, int64_t M,
+                            uint16_t* out, hipStream_t s) {
+  const int64_t ld = multi_pad_ld(M);
+  if (T <= 0 || M <= 0) return hipSuccess;
+  const unsigned grid = (unsigned)std::min<int64_t>(cdiv64(T * (ld / 8), 256), 1 << 16);
+  hipLaunchKernelGGL(k_multi_pad, dim3(grid), dim3(256), 0, s, act, codes, exps, T, M, ld, out);
+  return hipGetLastError();
+}
+
 size_t multi_grads_ws(const MultiGrad* g, int n_jobs, int64_t T, int n, int r) {
   const GradPlan p = grad_plan(g, n_jobs, T, n, r);
   return (size_t)(((p.vt + 255) / 256 * 256) * n_jobs + (p.S > 1 ? p.S * p.slice * 4 : 0));
@@ -972,6 +1009,10 @@ size_t multi_grads_ws(const MultiGrad* g, int n_jobs, int64_t T, int n, int r) {
 hipError_t launch_multi_grads(const MultiGrad* g, int n_jobs, int64_t T, const int32_t* gblk, const int32_t* perm, int n,
                               int r, void* ws, hipStream_t s) {
   if (n_jobs <= 0 || r <= 0 || n <= 0) return hipSuccess;
+  for (int i = 0; i < n_jobs; ++i) {
+    const int64_t ld = g[i].ld ? g[i].ld : g[i].M;
+    if (ld < g[i].M || !multi_grad_fits(ld, !g[i].act, r)) return hipErrorInvalidValue;
+  }
   const GradPlan p = grad_plan(g, n_jobs, T, n, r);
   GradArgs ga{};
   ga.gblk = gblk;
@@ -995,6 +1036,7 @@ hipError_t launch_multi_grads(const MultiGrad* g, int n_jobs, int64_t T, const i
     j.out = p.S > 1 ? part + done : g[i].out;
     done += (int64_t)n * r * g[i].M;
     j.M = g[i].M;
+    j.ld = g[i].ld ? g[i].ld : g[i].M;
     j.mb = (int)cdiv64(g[i].M, p.mt);
     j.out_t = g[i].out_t;
     mb += j.mb;
