@@ -1261,7 +1261,10 @@ sra_status sra_multi_bwd_workspace(const sra_sparse* P, int64_t T, int32_t n_ada
   if (flags & ~15u) return fail(SRA_ERR_INVALID_ARG, "unknown flag bits 0x%x", flags);
   if (flags & SRA_GRAD_DX) SRA_TRY(check_multi_product(P, T));
   if (!bytes) return fail(SRA_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = multi_bwd_plan(P, T, n_adapters, r, flags, false, false, false, nullptr);
+  // enough for every call with these flags: a call may ask for dU, which then has to be computed, or not,
+  // and then the call may need a place for it
+  *bytes = std::max(multi_bwd_plan(P, T, n_adapters, r, flags, false, false, false, nullptr),
+                    multi_bwd_plan(P, T, n_adapters, r, flags, false, false, true, nullptr));
   return SRA_OK;
 }
 
