@@ -405,6 +405,7 @@ sra_status sra_nm_axpby(const void* a_values, float beta, const void* b_values, 
  * bit.  It is read for dA, and for U when U is NULL and dB is asked for.  P may have any number of rows
  * K; where K is no multiple of 8 (of 16 for a checkpoint and r > 32), dA reads X through a copy of whole
  * rows in the workspace.  Sums over tokens run in a fixed order.  T = 0: the forward is a no-op, the backward writes zeros to dA and dB.
+ * ids (like A and B) may be NULL where nothing asked for needs it: dX with SRA_DX_NO_ADAPTER.
  * The backward's workspace size is enough for every call with its flags, with or without U, dU_out and a
  * checkpoint.
  * Supported: 1 <= r <= 256, 1 <= n_adapters <= 1023, T < 2^26, N * r and K * r (rounded up to 8)

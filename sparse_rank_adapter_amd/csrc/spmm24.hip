@@ -903,7 +903,7 @@ hipError_t launch_spmm24_multi_bf16(bool tiled, const uint16_t* s_vals, const ui
                                     int64_t C, const uint16_t* act, int64_t T, const Epilogue& ep, uint16_t* out,
                                     void* ws, hipStream_t s) {
   if (T == 0 || R == 0) return hipSuccess;
-  if (ep.G || !ep.ai.ids || !epilogue_ok(ep, R)) return hipErrorInvalidValue;
+  if (ep.G || (ep.r > 0 && !ep.ai.ids) || !epilogue_ok(ep, R)) return hipErrorInvalidValue;
   if (T <= 16) return launch_decode24_bf16(s_vals, s_meta, R, C, act, T, ep, out, s, tiled);
   if (tiled && C % 128 != 0) return hipErrorInvalidValue;
   const MultiPlan m = multi_plan(R, C, T);
