@@ -242,6 +242,8 @@ __global__ __launch_bounds__(1024) void k_ln_params(const float* __restrict__ pa
 // rows of up to 16384), in as many whole waves as the row then needs.
 int ept_for(int64_t H) { return H <= 2048 ? 8 : 16; }
 int threads_for(int64_t H, int ept) { return 64 * (int)((H + 64 * ept - 1) / (64 * ept)); }
+// Rows of one forward launch: a launch has fewer than 2^32 threads, and a row takes up to 1024 of them
+constexpr int64_t kFwdRows = (int64_t)1 << 21;
 int bwd_groups(int64_t T) { return (int)std::min<int64_t>(T, 512); }
 
 }  // namespace
@@ -271,20 +273,30 @@ hipError_t launch_layer_norm_fwd(int dtype, const void* x, const void* gamma, co
                                  int64_t H, void* y, float* mean, float* rstd, int8_t* codes, uint8_t* exps,
                                  hipStream_t s) {
   if (T <= 0 || H <= 0) return hipSuccess;
-  const dim3 grid((unsigned)T), block((unsigned)threads_for(H, ept_for(H)));
-#define SRA_LN_FWD(E, VEC, EPT)                                                                                   \
-  do {                                                                                                            \
-    if (codes)                                                                                                    \
-      launch(SRA_KERNEL_LAYER_NORM, k_ln_fwd<E, VEC, EPT, true>, grid, block, 0, s, (const E*)x, (const E*)gamma, \
-             (const E*)beta, eps, H, (E*)y, mean, rstd, codes, exps);                                             \
-    else                                                                                                          \
-      launch(SRA_KERNEL_LAYER_NORM, k_ln_fwd<E, VEC, EPT, false>, grid, block, 0, s, (const E*)x, (const E*)gamma, \
-             (const E*)beta, eps, H, (E*)y, mean, rstd, codes, exps);                                             \
+  const dim3 block((unsigned)threads_for(H, ept_for(H)));
+  const int64_t blocks_per_row = (H + kCkBlock - 1) / kCkBlock, esz = dtype == SRA_BF16 ? 2 : 4;
+  for (int64_t t0 = 0; t0 < T; t0 += kFwdRows) {
+    const dim3 grid((unsigned)std::min<int64_t>(kFwdRows, T - t0));
+    const void* const xt = (const uint8_t*)x + t0 * H * esz;
+    void* const yt = (uint8_t*)y + t0 * H * esz;
+    int8_t* const ct = codes ? codes + t0 * H : nullptr;
+    uint8_t* const et = codes ? exps + t0 * blocks_per_row : nullptr;
+#define SRA_LN_FWD(E, VEC, EPT)                                                                                    \
+  do {                                                                                                             \
+    if (codes)                                                                                                     \
+      launch(SRA_KERNEL_LAYER_NORM, k_ln_fwd<E, VEC, EPT, true>, grid, block, 0, s, (const E*)xt, (const E*)gamma, \
+             (const E*)beta, eps, H, (E*)yt, mean + t0, rstd + t0, ct, et);                                        \
+    else                                                                                                           \
+      launch(SRA_KERNEL_LAYER_NORM, k_ln_fwd<E, VEC, EPT, false>, grid, block, 0, s, (const E*)xt, (const E*)gamma, \
+             (const E*)beta, eps, H, (E*)yt, mean + t0, rstd + t0, ct, et);                                        \
   } while (0)
-  if (dtype == SRA_BF16) SRA_LN_PICK(uint16_t, SRA_LN_FWD);
-  else SRA_LN_PICK(float, SRA_LN_FWD);
+    if (dtype == SRA_BF16) SRA_LN_PICK(uint16_t, SRA_LN_FWD);
+    else SRA_LN_PICK(float, SRA_LN_FWD);
 #undef SRA_LN_FWD
-  return hipGetLastError();
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_layer_norm_bwd(int dtype, const void* dy, const void* x, const void* gamma, const float* mean,
