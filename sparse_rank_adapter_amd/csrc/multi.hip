@@ -917,6 +917,8 @@ hipError_t launch_multi_rows(const uint16_t* act, int64_t T, int64_t C, const ui
   // adapter: 41 / 42 and 39 / 41)
   const int64_t wgs = cdiv64(T, 128) * cdiv64(r, p.jr) * p.S;
   ai.passes = (int)std::min<int64_t>(n, std::max<int64_t>(8, std::min<int64_t>(32, 1024 / wgs)));
+  // a launch has fewer than 2^32 threads (of 512 a workgroup): two column tiles of nearly 2^26 tokens leave seven
+  ai.passes = (int)std::min<int64_t>(ai.passes, (((int64_t)1 << 23) - 1) / wgs);
   float* part = p.S > 1 ? (float*)ws : nullptr;
   const dim3 grid((unsigned)(cdiv64(T, 128) * cdiv64(r, p.jr) * p.S * ai.passes));
 #define SRA_MR(JR, TWV) \
