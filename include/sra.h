@@ -454,7 +454,8 @@ sra_status sra_ckpt_decode(const int8_t* codes, const uint8_t* exps, int64_t T, 
  * written in the same pass (what sra_ckpt_encode(Y) gives, bit for bit).
  * The backward takes the forward's mean and rstd, and a workspace of sra_layer_norm_bwd_workspace
  * bytes; its sums over tokens run in a fixed order.  T = 0: the forward is a no-op, the backward
- * writes zeros to dgamma and dbeta.  eps must be finite and >= 0.  Supported: H <= 16384, T < 2^31.
+ * writes zeros to dgamma and dbeta.  H = 0: mean and rstd, where given, are
+ * NaN (no terms to average).  eps must be finite and >= 0.  Supported: H <= 16384, T < 2^31.
  */
 sra_status sra_layer_norm_fwd(const void* X, const void* gamma, const void* beta, float eps,
                               int32_t dtype, int64_t T, int64_t H, void* Y, float* mean,
