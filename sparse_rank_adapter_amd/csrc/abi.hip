@@ -654,8 +654,8 @@ sra_status sra_layer_norm_fwd(const void* X, const void* gamma, const void* beta
   SRA_TRY(check_ptr(gamma, any, "gamma"));
   SRA_TRY(check_ptr(beta, any, "beta"));
   SRA_TRY(check_ptr(Y, any, "Y"));
-  SRA_TRY(check_ptr(mean, any, "mean"));
-  SRA_TRY(check_ptr(rstd, any, "rstd"));
+  SRA_TRY(check_ptr(mean, any || (mean && T > 0), "mean"));  // rows of no columns: where given
+  SRA_TRY(check_ptr(rstd, any || (rstd && T > 0), "rstd"));
   if (codes) SRA_TRY(check_ckpt(codes, exps, T, H));
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_layer_norm_fwd(dtype, X, gamma, beta, eps, T, H, Y, mean, rstd, codes, exps, s), s,
