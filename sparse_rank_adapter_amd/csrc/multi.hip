@@ -604,18 +604,20 @@ __global__ __launch_bounds__(512, 2) void k_multi_grads(GradArgs ga) {
       }
   };
 
-  // Step b: its Act goes from registers to LDS; its transfers have landed when at most what step
-  // b + 1 issued is outstanding (two loads of tokens, three of Act, the V transfers); one barrier, after
-  // which every wave is past step b - 1's reads, so the loads of step b + 2 may go to its buffers;
-  // then it multiplies.  Loads past the last block repeat it, so every step issues the same number.
+  // Step b: its Act goes from registers to LDS; its transfers have landed when at most what was issued
+  // after them is outstanding (two loads of tokens, three of Act, the V transfers: what step b - 1 issues,
+  // and what the first step finds issued ahead of it); one barrier, after which every wave is past step
+  // b - 1's reads, so the loads of step b + 2 may go to its buffers; then it multiplies.  Loads past the
+  // last block repeat it, so every step issues the same number.  (The compiler's wait for step b's Act, which
+  // is older than its transfers, does not know of the transfers and so waits for at least as much.)
   Act s0, s1;
   Toks tk{0, 0};
   if (b0 < b1) {
     const Toks ta = toks(b0), tb = toks(b0 + 1);
-    tk = toks(b0 + 2);
     load_act(ta, s0);
     issue_v(b0);
     __builtin_amdgcn_sched_barrier(0);
+    tk = toks(b0 + 2);  // after step b0's transfers, as in every later step
     load_act(tb, s1);
     issue_v(b0 + 1);
     __builtin_amdgcn_sched_barrier(0);
