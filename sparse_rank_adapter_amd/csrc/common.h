@@ -139,8 +139,10 @@ SRA_DEV dma_rsrc_t dma_rsrc(const void* base, uint32_t bytes) {  // uniform; off
 }
 SRA_DEV void lds_dma(const dma_rsrc_t& rs, uint32_t block, uint32_t off, int soff) {
   // the nops cover what the compiler would insert around its own form: one wait state after M0 is
-  // written, five after a vector instruction writes a scalar register that the transfer reads.  M0 is
-  // reserved: nothing else in a kernel that uses this may depend on it (no builtin transfer).
+  // written, five after a vector instruction writes a scalar register that the transfer reads.  The
+  // compiler does not know that M0 changes: it is a reserved register, which the clobber list may not name
+  // (-Winline-asm: undefined).  On gfx950 it uses M0 itself for its own transfers into LDS and for nothing
+  // else that these kernels do, so a source file that calls this has no builtin transfer (a test looks).
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane((int)block)), "v"(off), "s"(rs), "s"(soff)
