@@ -398,13 +398,17 @@ sra_status sra_nm_axpby(const void* a_values, float beta, const void* b_values, 
  * canonical arrays or the streaming layout); other formats and fp32 are SRA_ERR_UNSUPPORTED.
  * U_out / U / dU_out [T,r], dA [n_adapters,r,K] and dB [n_adapters,N,r] are fp32; an adapter with
  * no token gets zero gradients.  Flags as for sra_sparse_lora_bwd.
+ * dA and dB are fp32 sums, and so are U and dU where r > 32, T >= 256 and the reduction is a multiple of 64
+ * (else fp64), while the one-adapter calls sum in fp64: with one adapter, this call's gradients keep
+ * fewer digits of sums that cancel.
  * Requests stay apart: infinities or NaN in one adapter, or in its tokens, change nothing for other
  * adapters' tokens and gradients.
  * The backward reads the layer's input from X, or, when X is NULL, from its 8-bit checkpoint
  * X_codes / X_exps (sra_ckpt_encode); the results equal those from the decoded bf16 values bit for
  * bit.  It is read for dA, and for U when U is NULL and dB is asked for.  P may have any number of rows
  * K; where K is no multiple of 8 (of 16 for a checkpoint and r > 32), dA reads X through a copy of whole
- * rows in the workspace.  Sums over tokens run in a fixed order.  T = 0: the forward is a no-op, the backward writes zeros to dA and dB.
+ * rows in the workspace.  Sums over tokens run in a fixed order.  T = 0: the forward is a no-op, the
+ * backward writes zeros to dA and dB.
  * ids (like A and B) may be NULL where nothing asked for needs it: dX with SRA_DX_NO_ADAPTER.
  * The backward's workspace size is enough for every call with its flags, with or without U, dU_out and a
  * checkpoint.
@@ -433,7 +437,8 @@ sra_status sra_multi_lora_bwd(const sra_sparse* P /* host */, const void* dY, co
  * biased exponent e + 127 of its scale 2^e, with e the smallest integer for which a <= 127 * 2^e,
  * clamped to [-126, 121] (an all-zero block: -126), and per element the code
  * q = clamp(round_half_even(x / 2^e), -127, 127).  The decoded value q * 2^e is exact in bf16 and
- * fp32, so it differs from x by at most 2^(e-1) (2^e at most where the clamp at 127 acts).
+ * fp32, so it differs from x by at most 2^(e-1) (2^e at most where the clamp at 127 acts).  X should be
+ * finite: an infinity is kept as 127 * 2^121 (and hides the rest of its block), a NaN as some finite value.
  *   codes: int8 [T,K];  exps: uint8 [T, ceil(K/32)].
  * The backward calls that take a checkpoint compute exactly what they would compute from the
  * decoded bf16 activations.
@@ -446,7 +451,8 @@ sra_status sra_ckpt_decode(const int8_t* codes, const uint8_t* exps, int64_t T, 
 /*
  * layer_norm -- Y = (X - mean) * rstd * gamma + beta over the rows of X [T,H], the norm ahead of a
  * projection, and its gradients.  X, gamma, beta, Y, dY, dX have one dtype (bf16 or fp32); mean,
- * rstd [T], dgamma and dbeta [H] are fp32, as is all arithmetic; every output is rounded once.
+ * rstd [T], dgamma and dbeta [H] are fp32.  Terms are fp32; a row's sums are fp32 within a thread (up to
+ * 16 terms) and fp64 across threads, dgamma's and dbeta's fp32 over the rows.
  *   mean = sum(x) / H;  rstd = 1 / sqrt(sum((x - mean)^2) / H + eps)
  *   dX = rstd * (g - mean(g) - xh * mean(g * xh)) with g = dY * gamma, xh = (X - mean) * rstd;
  *   dgamma = sum_t dY * xh;  dbeta = sum_t dY
@@ -454,8 +460,7 @@ sra_status sra_ckpt_decode(const int8_t* codes, const uint8_t* exps, int64_t T, 
  * written in the same pass (what sra_ckpt_encode(Y) gives, bit for bit).
  * The backward takes the forward's mean and rstd, and a workspace of sra_layer_norm_bwd_workspace
  * bytes; its sums over tokens run in a fixed order.  T = 0: the forward is a no-op, the backward
- * writes zeros to dgamma and dbeta.  H = 0: mean and rstd, where given, are
- * NaN (no terms to average).  eps must be finite and >= 0.  Supported: H <= 16384, T < 2^31.
+ * writes zeros to dgamma and dbeta.  H = 0: mean and rstd, where given, are NaN (no terms to average).  eps must be finite and >= 0.  Supported: H <= 16384, T < 2^31.
  */
 sra_status sra_layer_norm_fwd(const void* X, const void* gamma, const void* beta, float eps,
                               int32_t dtype, int64_t T, int64_t H, void* Y, float* mean,

@@ -731,7 +731,8 @@ CKPT_BLOCK = 32  # columns of a checkpoint that share one scale
 @dataclass
 class Ckpt8:
     """8-bit checkpoint of a [T, K] activation: int8 codes [T, K] and uint8 scale exponents
-    [T, ceil(K / 32)]; value = code * 2^(exponent - 127).  `dtype` is that of the activation."""
+    [T, ceil(K / 32)]; value = code * 2^(exponent - 127).  `dtype` is that of the activation.  Infinities and
+    NaN are not kept: they become finite values."""
     codes: torch.Tensor
     exps: torch.Tensor
     dtype: torch.dtype = torch.bfloat16

@@ -37,6 +37,9 @@
 // adapters, rank 128, K = 5120 (a checkpoint), N = 20480: 161 GFLOP of the three parts at 0.88
 // PFLOP/s, where a large bf16 matrix product reaches 1.34; the matrix cores are busy for 40% of the
 // cycles and the 800 workgroups take unequal shares of the tokens.
+//
+// Both load whole 16-byte pieces of Act's rows (8-byte ones of codes up to rank 32): rows of any other
+// length are copied to whole ones first (k_multi_pad).
 #include <algorithm>
 
 #include "rowvec.h"

@@ -938,9 +938,10 @@ __global__ __launch_bounds__(64 * WR * WT, (QTile<FR, FT, WR, WT, NS, MS, UG, DN
     // many adapters: the E fragments of CH steps (adapter, 32 columns) are in flight together, a step's
     // slot refilled once its products are out (the largest wave tile has registers for two steps).
     // The loads are bare: clearing the entries past r right after each load made every load wait for
-    // itself (36.3 us against 23.1 at OPT-350M fc1 where 16 adapters met in each 128-token tile, before
-    // other steps), so that happens at the products.  With 16 adapters a tile the kernel takes 25.7 us now,
-    // with one 22.4: a step costs about 150 instructions beside its products.
+    // itself (36.3 us against 23.1 for a batch of mixed requests at OPT-350M fc1, before other steps), so that
+    // happens at the products.  A step costs about 150 instructions beside its products: 1999 tokens there,
+    // r 16, take 22.6 / 24.0 / 25.9 / 29.5 / 34.4 / 37.5 / 41.6 us with 1 / 2 / 4 / 8 / 16 / 24 / 40 adapters side by
+    // side, and 25.7 in requests of 24 adapters.
     constexpr int CH = MA ? (FR * FT >= 32 ? 2 : 6) : 1;
     union EF { u32x4 v; bf16x8 b; };
     EF en[CH][MA ? FR : 1];
