@@ -471,6 +471,87 @@ sra_status sra_layer_norm_bwd(const void* dY, const void* X, const void* gamma, 
                               float* dgamma, float* dbeta, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * rms_norm -- Y = H * rstd * gamma over the rows of H = X + R [T,H], the root-mean-square norm ahead of a
+ * projection with the residual's addition, and its gradients:
+ *   rstd = 1 / sqrt(sum(h^2) / H + eps)
+ *   dX = rstd * (g - xh * mean(g * xh)) + dH with g = dY * gamma, xh = h * rstd;  dgamma = sum_t dY * xh
+ * X, R, gamma, H_out, Y, dY, dH, dX have one dtype (bf16 or fp32); rstd [T] and dgamma [H] are fp32.
+ * R may be NULL (then H = X and H_out is not written); else H_out receives X + R, and may be X's or R's own
+ * buffer.  The norm is taken of the sum in fp32; H_out, Y and the codes are each rounded once.
+ * Outputs: Y, or its 8-bit form codes / exps (sra_quant_encode with SRA_FP8_E4M3 and blocks of one row, of the
+ * values before Y's rounding), or both; NULL leaves one out.
+ * The backward's H is the forward's H_out (X without R); dH, the gradient that reaches H past the norm, may
+ * be NULL.  dX is the gradient of X and of R alike, and may be dY's, dH's or H's own buffer.  Its sums over
+ * tokens run in a fixed order.  A row's sum is fp32 within a thread (up to 16 terms) and fp64 across threads,
+ * dgamma's fp32 over the rows.  T = 0: the forward is a no-op, the backward writes zeros to dgamma.  H = 0:
+ * rstd is NaN.  eps must be finite and >= 0.  Supported: H <= 16384, T < 2^31.
+ */
+sra_status sra_rms_norm_fwd(const void* X, const void* R, const void* gamma, float eps, int32_t dtype,
+                            int64_t T, int64_t H, void* H_out, void* Y, float* rstd, uint8_t* codes,
+                            uint8_t* exps, void* stream);
+sra_status sra_rms_norm_bwd_workspace(int64_t T, int64_t H, size_t* bytes /* host */);
+sra_status sra_rms_norm_bwd(const void* dY, const void* H_in, const void* gamma, const float* rstd,
+                            const void* dH, int32_t dtype, int64_t T, int64_t H, void* dX, float* dgamma,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * quant -- matrices in 8-bit floating point with a power-of-two scale for each block of 128 columns, and their
+ * product.  (SQuAsh project update: fine-tuning adapters over a base weight held in few bits; SLoPe
+ * paperlayer summary, results: the memory of training is what limits the model.)
+ *
+ * A matrix [rows, cols] is held as codes [rows, ld], ld = cols rounded up to a multiple of 128 (the columns
+ * past `cols` hold zero codes; the product relies on it), and exps uint8
+ * [ceil(rows / block_rows), ld / 128]: block_rows = 1 gives each row its own scales, block_rows = 128 one
+ * scale to each 128 x 128 block.  A block with largest finite magnitude a stores e + 127 with e the smallest
+ * integer for which a <= lim * 2^e, lim = 448 (SRA_FP8_E4M3, the finite-only OCP type) or 57344
+ * (SRA_FP8_E5M2), clamped to [-126, 119] or [-126, 112] (an all-zero block: -126); a code is x / 2^e rounded
+ * to nearest even, at most lim in magnitude.  An infinity or NaN becomes the code NaN and takes no part in its
+ * block's scale.  A decoded value is code * 2^e rounded to dtype: exact in fp32, and in bf16 from 2^-133 up.
+ * encode: X [rows, cols] (bf16 or fp32) -> codes / exps, and codes_t / exps_t, the same of X's transpose
+ * ([cols, rows rounded up], blocks of 128 rows of X): either pair may be NULL.  With block_rows = 128 the
+ * transpose holds the same values; with block_rows = 1 it is scaled along its own rows.
+ */
+enum { SRA_FP8_E4M3 = 0, SRA_FP8_E5M2 = 1 };
+typedef struct sra_fp8 {
+  int32_t kind;       /* SRA_FP8_E4M3 or SRA_FP8_E5M2 */
+  int32_t block_rows; /* 1 or 128 */
+  int64_t rows, cols;
+  uint8_t* codes;
+  uint8_t* exps;
+} sra_fp8;
+/* out, out_t: caller-filled descriptors of the outputs (either may be NULL, not both): out->rows x out->cols is
+ * X's shape, out_t's the transpose; kind and block_rows agree. */
+sra_status sra_quant_encode(const void* X, int32_t dtype, int64_t rows, int64_t cols,
+                          const sra_fp8* out /* host */, const sra_fp8* out_t /* host */, void* stream);
+sra_status sra_quant_decode(const sra_fp8* F /* host */, int32_t dtype, void* X, void* stream);
+/*
+ * quant_matmul -- Out = a b^T, [a->rows, b->rows], both reduced over cols (a->cols == b->cols): a projection
+ * (a = the activations, b = the weight), its input gradient (a = dY, b = the weight's transpose) and its
+ * weight gradient (a = dY's transpose, b = X's).  Any kinds and block_rows.  Out has out_dtype (bf16 or fp32),
+ * rounded once; sums are fp32.  A NaN code or scale makes NaN of its own row's results alone.  cols = 0 writes
+ * zeros.  The workspace (sra_quant_matmul_workspace bytes, 0 for most shapes) holds partial products of a split
+ * reduction, joined in a fixed order.  Supported: a->rows < 2^31, b->rows < 2^26, cols <= 2^22, and
+ * a->rows * b->rows < 2^40.
+ */
+sra_status sra_quant_matmul_workspace(int64_t M, int64_t N, int64_t K, size_t* bytes /* host */);
+sra_status sra_quant_matmul(const sra_fp8* a /* host */, const sra_fp8* b /* host */, int32_t out_dtype, void* Out,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * orthogonalize -- n updates [rows, cols] (adapter gradients: dA [n,r,K], dB [n,N,r]) orthogonalised by Newton-Schulz
+ * steps: X_0 = G / (|G| + eps) with |G| the root of the sum of squares, then `steps` times
+ * X <- a X + (b A + c A^2) X with A = X X^T (X^T X where rows > cols).  G and O have one dtype (bf16 or fp32)
+ * and do not overlap; everything between is fp64, with one rounding at the end.  Each matrix stands alone: an
+ * infinity or NaN in one changes nothing in another.  A zero matrix gives zeros where eps > 0.
+ * Supported: min(rows, cols) <= 256, n <= 65535, max(rows, cols) < 2^31, 1 <= steps <= 64; a, b, c finite,
+ * eps finite and >= 0.
+ */
+sra_status sra_orthogonalize_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes /* host */);
+sra_status sra_orthogonalize(const void* G, int32_t dtype, int64_t n, int64_t rows, int64_t cols, int32_t steps,
+                             double a, double b, double c, double eps, void* O, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/*
  * Tuning knobs of the calling thread, for benchmarks and tests (not needed for computing anything;
  * every knob's default is the library's own choice, and results stay within the stated tolerance
  * under any setting).  Returns SRA_ERR_INVALID_ARG for an unknown key or a value out of range.
@@ -524,7 +605,11 @@ enum {
   SRA_KERNEL_WEIGHT_GRAD = 8,  /* bf16 masked weight gradient (sra_masked_weight_grad) */
   SRA_KERNEL_NM_UPDATE = 9,    /* beta A + gamma B on shared-pattern values (sra_nm_axpby) */
   SRA_KERNEL_LAYER_NORM = 10,  /* layer norm forward or backward (not the backward's final sum) */
-  SRA_KERNEL_CKPT = 11         /* 8-bit checkpoint encode or decode */
+  SRA_KERNEL_CKPT = 11,        /* 8-bit checkpoint encode or decode */
+  SRA_KERNEL_RMS_NORM = 12,    /* root-mean-square norm forward or backward (not the backward's final sum) */
+  SRA_KERNEL_FP8_CODE = 13,    /* 8-bit floating point encode or decode */
+  SRA_KERNEL_FP8_MM = 14,      /* product of 8-bit floating point matrices (not a split's final sum) */
+  SRA_KERNEL_ORTH = 15         /* Newton-Schulz: Gram product, last product (one launch each) */
 };
 
 /*

@@ -10,4 +10,6 @@ from .api import (SparseMatrix, bwd_workspace, ffa_bwd_workspace, ffa_fwd_worksp
                   sparse_lora_bwd_ffa, sparse_lora_fwd, sparse_lora_fwd_ffa, time_next_kernel,
                   set_tuning, reset_tuning, tuned,
                   multi_lora_fwd, multi_lora_bwd, Ckpt8, ckpt8_encode, ckpt8_decode, layer_norm_fwd, layer_norm_bwd,
+                  rms_norm_fwd, rms_norm_bwd, Fp8Matrix, fp8_encode, fp8_encode_t, fp8_encode_pair, fp8_decode, fp8_matmul,
+                  orthogonalize, rms_norm_bwd_workspace, fp8_matmul_workspace, orthogonalize_workspace,
                   SRA_FMT_NM, SRA_FMT_NM_TILED)

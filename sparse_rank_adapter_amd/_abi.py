@@ -3,7 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsra.so")
 
@@ -31,12 +31,17 @@ EXPORTS = (
     "sra_multi_fwd_workspace", "sra_multi_lora_fwd", "sra_multi_bwd_workspace", "sra_multi_lora_bwd",
     "sra_ckpt_encode", "sra_ckpt_decode",
     "sra_layer_norm_fwd", "sra_layer_norm_bwd_workspace", "sra_layer_norm_bwd",
+    "sra_rms_norm_fwd", "sra_rms_norm_bwd_workspace", "sra_rms_norm_bwd",
+    "sra_quant_encode", "sra_quant_decode", "sra_quant_matmul_workspace", "sra_quant_matmul",
+    "sra_orthogonalize_workspace", "sra_orthogonalize",
     "sra_time_next_kernel", "sra_set_tuning",
 )
 SRA_KERNEL_COMPRESS, SRA_KERNEL_DOUBLE_PRUNE, SRA_KERNEL_SPMM24 = 1, 2, 3
 SRA_KERNEL_ADAPTER, SRA_KERNEL_DECODE24, SRA_KERNEL_SPMM_FFI = 4, 5, 6
 SRA_KERNEL_FFI_DENSIFY, SRA_KERNEL_WEIGHT_GRAD, SRA_KERNEL_NM_UPDATE = 7, 8, 9
 SRA_KERNEL_LAYER_NORM, SRA_KERNEL_CKPT = 10, 11
+SRA_KERNEL_RMS_NORM, SRA_KERNEL_FP8_CODE, SRA_KERNEL_FP8_MM, SRA_KERNEL_ORTH = 12, 13, 14, 15
+SRA_FP8_E4M3, SRA_FP8_E5M2 = 0, 1
 
 
 class SraSparse(ctypes.Structure):
@@ -45,6 +50,11 @@ class SraSparse(ctypes.Structure):
         ("n", c_int32), ("m", c_int32), ("k", c_int32), ("nnz", c_int64),
         ("values", c_void_p), ("meta", c_void_p), ("index", c_void_p), ("row_ptr", c_void_p),
     ]
+
+
+class SraFp8(ctypes.Structure):
+    _fields_ = [("kind", c_int32), ("block_rows", c_int32), ("rows", c_int64), ("cols", c_int64),
+                ("codes", c_void_p), ("exps", c_void_p)]
 
 
 _lib = None
@@ -60,7 +70,7 @@ def load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is not built: run `python -m sparse_rank_adapter_amd.build`")
     lib = ctypes.CDLL(path)
-    P = POINTER(SraSparse)
+    P, F = POINTER(SraSparse), POINTER(SraFp8)
     sig = {
         "sra_abi_version": (c_int32, []),
         "sra_last_error": (c_char_p, []),
@@ -114,6 +124,18 @@ def load(path: str = LIB_PATH):
         "sra_layer_norm_bwd": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int64,
                                          c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                          c_void_p]),
+        "sra_rms_norm_fwd": (c_int32, [c_void_p, c_void_p, c_void_p, c_float, c_int32, c_int64, c_int64, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "sra_rms_norm_bwd_workspace": (c_int32, [c_int64, c_int64, POINTER(c_size_t)]),
+        "sra_rms_norm_bwd": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64,
+                                       c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "sra_quant_encode": (c_int32, [c_void_p, c_int32, c_int64, c_int64, F, F, c_void_p]),
+        "sra_quant_decode": (c_int32, [F, c_int32, c_void_p, c_void_p]),
+        "sra_quant_matmul_workspace": (c_int32, [c_int64, c_int64, c_int64, POINTER(c_size_t)]),
+        "sra_quant_matmul": (c_int32, [F, F, c_int32, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "sra_orthogonalize_workspace": (c_int32, [c_int64, c_int64, c_int64, POINTER(c_size_t)]),
+        "sra_orthogonalize": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_int32, c_double, c_double,
+                                        c_double, c_double, c_void_p, c_void_p, c_size_t, c_void_p]),
         "sra_time_next_kernel": (c_int32, [c_int32, c_void_p, c_void_p]),
         "sra_set_tuning": (c_int32, [c_int32, c_int32]),
     }

@@ -6,16 +6,16 @@ kernels.  Nothing here computes a result on the host.
 from __future__ import annotations
 
 import ctypes
-from contextlib import contextmanager
+from contextlib import contextmanager, nullcontext
 from dataclasses import dataclass
 from functools import lru_cache
 
 import torch
 
 from . import _abi
-from ._abi import (SRA_BF16, SRA_DX_NO_ADAPTER, SRA_F32, SRA_FMT_CSR, SRA_FMT_ELL, SRA_FMT_NM,
+from ._abi import (SRA_BF16, SRA_DX_NO_ADAPTER, SRA_F32, SRA_FP8_E4M3, SRA_FP8_E5M2, SRA_FMT_CSR, SRA_FMT_ELL, SRA_FMT_NM,
                    SRA_FMT_NM_TILED, SRA_FMT_FFI_TILED,
-                   SRA_GRAD_DA, SRA_GRAD_DB, SRA_GRAD_DX, SraSparse, check, load)
+                   SRA_GRAD_DA, SRA_GRAD_DB, SRA_GRAD_DX, SraFp8, SraSparse, check, load)
 
 _DT = {torch.bfloat16: SRA_BF16, torch.float32: SRA_F32}
 
@@ -845,6 +845,274 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor, mean:
         dY.data_ptr(), X.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _DT[X.dtype], T, H,
         dX.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)))
     return dX, dgamma, dbeta
+
+
+@lru_cache(maxsize=1024)
+def rms_norm_bwd_workspace(T: int, H: int) -> int:
+    """Workspace bytes of rms_norm_bwd over [T, H]."""
+    nbytes = ctypes.c_size_t()
+    check("sra_rms_norm_bwd_workspace", load().sra_rms_norm_bwd_workspace(T, H, ctypes.byref(nbytes)))
+    return nbytes.value
+
+
+@lru_cache(maxsize=1024)
+def fp8_matmul_workspace(M: int, N: int, K: int) -> int:
+    """Workspace bytes of fp8_matmul of [M, K] and [N, K] (0 for most shapes)."""
+    nbytes = ctypes.c_size_t()
+    check("sra_quant_matmul_workspace", load().sra_quant_matmul_workspace(M, N, K, ctypes.byref(nbytes)))
+    return nbytes.value
+
+
+@lru_cache(maxsize=1024)
+def orthogonalize_workspace(n: int, rows: int, cols: int) -> int:
+    """Workspace bytes of orthogonalize of n matrices [rows, cols]."""
+    nbytes = ctypes.c_size_t()
+    check("sra_orthogonalize_workspace", load().sra_orthogonalize_workspace(n, rows, cols, ctypes.byref(nbytes)))
+    return nbytes.value
+
+
+_SAME_DEVICE = nullcontext()
+
+
+def _on(dev):
+    """Makes the device whose stream a call launches on the current one, where it is not."""
+    return _SAME_DEVICE if dev.index is None or dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+FP8_BLOCK = 128  # columns of an 8-bit floating point matrix that share one scale
+_FP8_KIND = {torch.float8_e4m3fn: SRA_FP8_E4M3, torch.float8_e5m2: SRA_FP8_E5M2}
+
+
+@dataclass
+class Fp8Matrix:
+    """A [rows, cols] matrix in 8-bit floating point: codes (float8_e4m3fn or float8_e5m2) [rows, cols rounded up to
+    whole blocks of 128, the rest zeros] and uint8 scale exponents [ceil(rows / block_rows), ceil(cols / 128)], one for
+    each block of 128 columns of a row (block_rows = 1) or of 128 rows (block_rows = 128);
+    value = code * 2^(exponent - 127).  Where cols is a multiple of 128 the codes are a plain tensor of the shape."""
+    codes: torch.Tensor
+    exps: torch.Tensor
+    rows: int
+    cols: int
+    block_rows: int = 1
+
+    @property
+    def shape(self):
+        return torch.Size((self.rows, self.cols))
+
+    @property
+    def dtype(self):
+        return self.codes.dtype
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def desc(self) -> SraFp8:
+        return SraFp8(_FP8_KIND[self.codes.dtype], self.block_rows, self.rows, self.cols, self.codes.data_ptr(),
+                      self.exps.data_ptr())
+
+
+def _check_fp8(F: Fp8Matrix, name: str, shape: tuple | None = None, device=None, kind=None, block_rows=None):
+    if not isinstance(F, Fp8Matrix):
+        raise TypeError(f"{name} must be an Fp8Matrix")
+    if F.block_rows not in (1, FP8_BLOCK):
+        raise ValueError(f"{name}: block_rows {F.block_rows} is not 1 or {FP8_BLOCK}")
+    if not isinstance(F.codes, torch.Tensor) or F.codes.dtype not in _FP8_KIND:
+        raise ValueError(f"{name}.codes must be a tensor of float8_e4m3fn or float8_e5m2")
+    if shape is not None and (F.rows, F.cols) != shape:
+        raise ValueError(f"{name} is {F.rows} x {F.cols}, expected {shape[0]} x {shape[1]}")
+    if F.rows < 0 or F.cols < 0:
+        raise ValueError(f"{name} has a negative shape")
+    if kind is not None and F.codes.dtype != kind:
+        raise ValueError(f"{name} has dtype {F.codes.dtype}, expected {kind}")
+    if block_rows is not None and F.block_rows != block_rows:
+        raise ValueError(f"{name} has block_rows {F.block_rows}, expected {block_rows}")
+    blocks = -(-F.cols // FP8_BLOCK)
+    _arg(F.codes, f"{name}.codes", (F.rows, blocks * FP8_BLOCK), F.codes.dtype, device)
+    _arg(F.exps, f"{name}.exps", (-(-F.rows // F.block_rows), blocks), torch.uint8, F.codes.device)
+
+
+def _new_fp8(rows: int, cols: int, dtype, block_rows: int, device) -> Fp8Matrix:
+    blocks = -(-cols // FP8_BLOCK)
+    return Fp8Matrix(torch.empty((rows, blocks * FP8_BLOCK), dtype=dtype, device=device),
+                     torch.empty((-(-rows // block_rows), blocks), dtype=torch.uint8, device=device), rows, cols,
+                     block_rows)
+
+
+def _fp8_encode(X, dtype, block_rows: int, rows_form, transpose):
+    """rows_form / transpose: False (not wanted), None (new) or an Fp8Matrix to fill."""
+    lib = load()
+    R, C = _mat(X, "X")
+    if dtype not in _FP8_KIND:
+        raise ValueError(f"dtype {dtype} is not float8_e4m3fn or float8_e5m2")
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError(f"block_rows {block_rows} is not 1 or {FP8_BLOCK}")
+    dev, made = X.device, []
+    for F, name, shape in ((rows_form, "out", (R, C)), (transpose, "out_t", (C, R))):
+        if F is None:
+            F = _new_fp8(*shape, dtype, block_rows, dev)
+        elif F is not False:
+            _check_fp8(F, name, shape, dev, dtype, block_rows)
+        made.append(F)
+    a, b = (None if F is False else F for F in made)
+    with _on(dev):
+        check("sra_quant_encode", lib.sra_quant_encode(_p(X), _dt(X), R, C, ctypes.byref(a.desc()) if a else None,
+                                                   ctypes.byref(b.desc()) if b else None, _stream(dev)))
+    return a, b
+
+
+def fp8_encode(X: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, block_rows: int = 1,
+               out: Fp8Matrix | None = None) -> Fp8Matrix:
+    """X [rows, cols] (bf16 or fp32) in 8-bit floating point, into `out`'s buffers if given."""
+    return _fp8_encode(X, dtype, block_rows, out, False)[0]
+
+
+def fp8_encode_t(X: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, block_rows: int = 1,
+                 out: Fp8Matrix | None = None) -> Fp8Matrix:
+    """X's transpose [cols, rows] in 8-bit floating point, its scales along its own rows."""
+    return _fp8_encode(X, dtype, block_rows, False, out)[1]
+
+
+def fp8_encode_pair(X: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, block_rows: int = 1,
+                    out: tuple | None = None):
+    """(fp8_encode(X), fp8_encode_t(X)) in one pass over X; `out` = (F, F_t) reuses buffers."""
+    F, Ft = out if out is not None else (None, None)
+    return _fp8_encode(X, dtype, block_rows, F, Ft)
+
+
+def fp8_decode(F: Fp8Matrix, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values F stands for, in bf16 or fp32."""
+    lib = load()
+    _check_fp8(F, "F")
+    if out is None:
+        if dtype not in _DT:
+            raise ValueError(f"dtype {dtype} is not bfloat16 or float32")
+        out = torch.empty((F.rows, F.cols), dtype=dtype, device=F.device)
+    _dt(out)
+    _arg(out, "out", (F.rows, F.cols), out.dtype, F.device)
+    with _on(F.device):
+        check("sra_quant_decode", lib.sra_quant_decode(ctypes.byref(F.desc()), _dt(out), _p(out), _stream(F.device)))
+    return out
+
+
+def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+               ws: torch.Tensor | None = None) -> torch.Tensor:
+    """a b^T [a.rows, b.rows], in bf16 or fp32 (`out`'s dtype where it is given).
+
+    A projection (a = X, b = W), its input gradient (a = dY, b = W^T) and its weight gradient (a = dY^T, b = X^T)."""
+    lib = load()
+    _check_fp8(a, "a")
+    dev = a.device
+    _check_fp8(b, "b", device=dev)
+    if a.cols != b.cols:
+        raise ValueError(f"a has {a.cols} columns, b {b.cols}")
+    M, N = a.rows, b.rows
+    if out is None:
+        if out_dtype not in _DT:
+            raise ValueError(f"out_dtype {out_dtype} is not bfloat16 or float32")
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        _dt(out)
+        _arg(out, "out", (M, N), out.dtype, dev)
+    nbytes = fp8_matmul_workspace(M, N, a.cols)
+    if nbytes:
+        ws = _workspace(ws, nbytes, dev)
+    with _on(dev):
+        check("sra_quant_matmul", lib.sra_quant_matmul(ctypes.byref(a.desc()), ctypes.byref(b.desc()), _DT[out.dtype],
+                                                   out.data_ptr(), ws.data_ptr() if nbytes else None,
+                                                   ws.numel() if nbytes else 0, _stream(dev)))
+    return out
+
+
+def rms_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                 fp8: torch.dtype | Fp8Matrix | None = None, want_y: bool = True, Y: torch.Tensor | None = None,
+                 H: torch.Tensor | None = None):
+    """Y = h rstd gamma over the rows of h = X + residual.  Returns (Y, H, rstd, F): H = X + residual in X's dtype
+    (X itself without a residual), rstd fp32 [T], and F the 8-bit form of Y (blocks of one row), None unless ``fp8``
+    is torch.float8_e4m3fn (or an Fp8Matrix whose buffers it goes into).  ``want_y=False`` leaves Y out (None).
+    ``H`` may be X or the residual itself: the sum then replaces it."""
+    lib = load()
+    T, W = _mat(X, "X")
+    dev = X.device
+    _arg(gamma, "gamma", (W,), X.dtype, dev)
+    if residual is not None:
+        _arg(residual, "residual", (T, W), X.dtype, dev)
+        if H is None:
+            H = torch.empty_like(X)
+        else:
+            _arg(H, "H", (T, W), X.dtype, dev)
+    elif H is not None:
+        raise ValueError("H is given without a residual")
+    if not want_y:
+        if Y is not None:
+            raise ValueError("Y is given, but not wanted")
+        if fp8 is None:
+            raise ValueError("neither Y nor its 8-bit form is wanted")
+    elif Y is None:
+        Y = torch.empty_like(X)
+    else:
+        _arg(Y, "Y", (T, W), X.dtype, dev)
+    F = None
+    if isinstance(fp8, Fp8Matrix):
+        F = fp8
+        _check_fp8(F, "fp8", (T, W), dev, torch.float8_e4m3fn, 1)
+    elif fp8 is not None:
+        if fp8 is not torch.float8_e4m3fn:
+            raise ValueError(f"fp8 {fp8} is not torch.float8_e4m3fn")
+        F = _new_fp8(T, W, fp8, 1, dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    with _on(dev):
+        check("sra_rms_norm_fwd", lib.sra_rms_norm_fwd(
+            X.data_ptr(), _p(residual), gamma.data_ptr(), float(eps), _DT[X.dtype], T, W, _p(H), _p(Y), rstd.data_ptr(),
+            F.codes.data_ptr() if F else None, F.exps.data_ptr() if F else None, _stream(dev)))
+    return Y, X if residual is None else H, rstd, F
+
+
+def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor,
+                 dH: torch.Tensor | None = None, dX: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """Gradients of rms_norm_fwd from its H (X without a residual) and rstd; ``dH`` is the gradient that reaches H
+    past the norm.  Returns (dX, dgamma): dX is the gradient of X and of the residual, dgamma fp32 [width]."""
+    lib = load()
+    T, W = _mat(H, "H")
+    dev = H.device
+    _arg(dY, "dY", (T, W), H.dtype, dev)
+    _arg(gamma, "gamma", (W,), H.dtype, dev)
+    _arg(rstd, "rstd", (T,), torch.float32, dev)
+    if dH is not None:
+        _arg(dH, "dH", (T, W), H.dtype, dev)
+    if dX is None:
+        dX = torch.empty_like(H)
+    else:
+        _arg(dX, "dX", (T, W), H.dtype, dev)
+    dgamma = torch.empty(W, dtype=torch.float32, device=dev)
+    ws = _workspace(ws, rms_norm_bwd_workspace(T, W), dev)
+    with _on(dev):
+        check("sra_rms_norm_bwd", lib.sra_rms_norm_bwd(
+            dY.data_ptr(), H.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), _p(dH), _DT[H.dtype], T, W, dX.data_ptr(),
+            dgamma.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)))
+    return dX, dgamma
+
+
+def orthogonalize(G: torch.Tensor, steps: int = 5, coeffs: tuple = (3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                  out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Updates G [n, rows, cols] or [rows, cols] (an adapter's dA or dB) orthogonalised by Newton-Schulz steps:
+    X = G / (|G| + eps), then X <- a X + (b A + c A^2) X with A = X X^T, (a, b, c) = coeffs.
+    min(rows, cols) <= 256; ``out`` must not overlap G."""
+    lib = load()
+    if not isinstance(G, torch.Tensor) or G.dim() not in (2, 3):
+        raise ValueError("G must be a 2-D or 3-D tensor")
+    dt, dev = _dt(G), _dev(G, "G").device
+    n, R, C = G.shape if G.dim() == 3 else (1, *G.shape)
+    a, b, c = (float(v) for v in coeffs)
+    if out is None:
+        out = torch.empty_like(G)
+    else:
+        _arg(out, "out", tuple(G.shape), G.dtype, dev)
+    ws = _workspace(ws, orthogonalize_workspace(n, R, C), dev)
+    with _on(dev):
+        check("sra_orthogonalize", lib.sra_orthogonalize(G.data_ptr(), dt, n, R, C, int(steps), a, b, c, float(eps),
+                                                         out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)))
+    return out
 
 
 _ENGINES = {"smfmac": 0, "dense_mfma": 1}

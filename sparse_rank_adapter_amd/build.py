@@ -31,6 +31,10 @@ SOURCES = [
     "multi.hip",
     "ckpt.hip",
     "layer_norm.hip",
+    "rms_norm.hip",
+    "fp8.hip",
+    "fp8_mm.hip",
+    "orth.hip",
 ]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -65,6 +65,13 @@ sra_status check_ptr(const void* p, bool needed, const char* name) {
   return SRA_OK;
 }
 
+sra_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(SRA_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", need, ws ? ws_bytes : (size_t)0);
+  if (need > 0 && !al16(ws)) return fail(SRA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  return SRA_OK;
+}
+
 sra_status check_nm(int64_t rows, int64_t cols, int n, int m) {
   if (rows < 0 || cols < 0) return fail(SRA_ERR_INVALID_ARG, "negative shape");
   if (n < 1 || m < n || (m > 4 && m != 8)) return fail(SRA_ERR_INVALID_ARG, "invalid N:M %d:%d", n, m);
@@ -369,7 +376,7 @@ sra_status sra_time_next_kernel(int32_t which, void* start, void* stop) {
     g_time_which = 0;
     return SRA_OK;
   }
-  if (which < SRA_KERNEL_COMPRESS || which > SRA_KERNEL_CKPT)
+  if (which < SRA_KERNEL_COMPRESS || which > SRA_KERNEL_ORTH)
     return fail(SRA_ERR_INVALID_ARG, "unknown kernel class %d", which);
   if (!start || !stop) return fail(SRA_ERR_INVALID_ARG, "start and stop events are required");
   g_time_which = which;
@@ -689,6 +696,174 @@ sra_status sra_layer_norm_bwd(const void* dY, const void* X, const void* gamma, 
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_layer_norm_bwd(dtype, dY, X, gamma, mean, rstd, T, H, dX, dgamma, dbeta, ws, s), s,
                   "layer_norm_bwd");
+}
+
+static sra_status check_eps(float eps) {
+  if (!(eps >= 0.f) || eps > 3.0e38f) return fail(SRA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  return SRA_OK;
+}
+static sra_status check_rms(int32_t dtype, int64_t T, int64_t H) {
+  SRA_TRY(check_dtype(dtype));
+  if (T < 0 || H < 0) return fail(SRA_ERR_INVALID_ARG, "negative shape");
+  if (!sra::rms_norm_ok(H)) return fail(SRA_ERR_UNSUPPORTED, "rms norm needs H <= 16384 (H = %lld)", (long long)H);
+  if (T >= ((int64_t)1 << 31)) return fail(SRA_ERR_UNSUPPORTED, "rms norm needs T < 2^31");
+  return SRA_OK;
+}
+
+sra_status sra_rms_norm_fwd(const void* X, const void* R, const void* gamma, float eps, int32_t dtype, int64_t T,
+                            int64_t H, void* H_out, void* Y, float* rstd, uint8_t* codes, uint8_t* exps,
+                            void* stream) {
+  SRA_TRY(check_rms(dtype, T, H));
+  SRA_TRY(check_eps(eps));
+  if ((codes == nullptr) != (exps == nullptr))
+    return fail(SRA_ERR_INVALID_ARG, "codes and exps must both be given or both be NULL");
+  const bool any = T > 0 && H > 0;
+  if (any && !Y && !codes) return fail(SRA_ERR_INVALID_ARG, "neither Y nor codes is given");
+  SRA_TRY(check_ptr(X, any, "X"));
+  SRA_TRY(check_ptr(R, any && R, "R"));
+  SRA_TRY(check_ptr(gamma, any, "gamma"));
+  SRA_TRY(check_ptr(H_out, any && R, "H_out"));
+  SRA_TRY(check_ptr(Y, any && Y, "Y"));
+  SRA_TRY(check_ptr(rstd, T > 0, "rstd"));
+  SRA_TRY(check_ptr(codes, any && codes, "codes"));
+  SRA_TRY(check_ptr(exps, any && codes, "exps"));
+  const hipStream_t s = (hipStream_t)stream;
+  return hip_done(sra::launch_rms_norm_fwd(dtype, X, R, gamma, eps, T, H, H_out, Y, rstd, codes, exps, s), s,
+                  "rms_norm_fwd");
+}
+
+sra_status sra_rms_norm_bwd_workspace(int64_t T, int64_t H, size_t* bytes) {
+  SRA_TRY(check_rms(SRA_BF16, T, H));
+  if (!bytes) return fail(SRA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = sra::rms_norm_bwd_ws(T, H);
+  return SRA_OK;
+}
+
+sra_status sra_rms_norm_bwd(const void* dY, const void* H_in, const void* gamma, const float* rstd, const void* dH,
+                            int32_t dtype, int64_t T, int64_t H, void* dX, float* dgamma, void* ws, size_t ws_bytes,
+                            void* stream) {
+  SRA_TRY(check_rms(dtype, T, H));
+  const bool any = T > 0 && H > 0;
+  SRA_TRY(check_ptr(dY, any, "dY"));
+  SRA_TRY(check_ptr(H_in, any, "H_in"));
+  SRA_TRY(check_ptr(gamma, any, "gamma"));
+  SRA_TRY(check_ptr(rstd, any, "rstd"));
+  SRA_TRY(check_ptr(dH, any && dH, "dH"));
+  SRA_TRY(check_ptr(dX, any, "dX"));
+  SRA_TRY(check_ptr(dgamma, H > 0, "dgamma"));
+  SRA_TRY(check_ws(ws, ws_bytes, sra::rms_norm_bwd_ws(T, H)));
+  const hipStream_t s = (hipStream_t)stream;
+  return hip_done(sra::launch_rms_norm_bwd(dtype, dY, H_in, gamma, rstd, dH, T, H, dX, dgamma, ws, s), s,
+                  "rms_norm_bwd");
+}
+
+static sra_status check_fp8(const sra_fp8* F, const char* name) {
+  if (!F) return fail(SRA_ERR_INVALID_ARG, "%s descriptor is NULL", name);
+  if (F->kind != SRA_FP8_E4M3 && F->kind != SRA_FP8_E5M2) return fail(SRA_ERR_INVALID_ARG, "%s: kind %d", name, F->kind);
+  if (F->block_rows != 1 && F->block_rows != 128)
+    return fail(SRA_ERR_INVALID_ARG, "%s: block_rows %d is not 1 or 128", name, F->block_rows);
+  if (F->rows < 0 || F->cols < 0) return fail(SRA_ERR_INVALID_ARG, "%s has a negative shape", name);
+  if (F->rows >= ((int64_t)1 << 40) || F->cols >= ((int64_t)1 << 40))
+    return fail(SRA_ERR_UNSUPPORTED, "%s has 2^40 or more rows or columns", name);
+  const bool any = F->rows > 0 && F->cols > 0;
+  SRA_TRY(check_ptr(F->codes, any, "codes"));
+  return check_ptr(F->exps, any, "exps");
+}
+
+sra_status sra_quant_encode(const void* X, int32_t dtype, int64_t rows, int64_t cols, const sra_fp8* out,
+                          const sra_fp8* out_t, void* stream) {
+  SRA_TRY(check_dtype(dtype));
+  if (!out && !out_t) return fail(SRA_ERR_INVALID_ARG, "neither out nor out_t is given");
+  if (out) SRA_TRY(check_fp8(out, "out"));
+  if (out_t) SRA_TRY(check_fp8(out_t, "out_t"));
+  const sra_fp8* const f = out ? out : out_t;
+  if ((out && (out->rows != rows || out->cols != cols)) || (out_t && (out_t->rows != cols || out_t->cols != rows)))
+    return fail(SRA_ERR_INVALID_ARG, "the outputs do not have X's shape %lld x %lld", (long long)rows, (long long)cols);
+  if (out && out_t && (out->kind != out_t->kind || out->block_rows != out_t->block_rows))
+    return fail(SRA_ERR_INVALID_ARG, "out and out_t differ in kind or block_rows");
+  SRA_TRY(check_ptr(X, rows > 0 && cols > 0, "X"));
+  const hipStream_t s = (hipStream_t)stream;
+  return hip_done(sra::launch_fp8_encode(dtype, f->kind, X, rows, cols, f->block_rows, out ? out->codes : nullptr,
+                                         out ? out->exps : nullptr, out_t ? out_t->codes : nullptr,
+                                         out_t ? out_t->exps : nullptr, s),
+                  s, "fp8_encode");
+}
+
+sra_status sra_quant_decode(const sra_fp8* F, int32_t dtype, void* X, void* stream) {
+  SRA_TRY(check_dtype(dtype));
+  SRA_TRY(check_fp8(F, "F"));
+  SRA_TRY(check_ptr(X, F->rows > 0 && F->cols > 0, "X"));
+  const hipStream_t s = (hipStream_t)stream;
+  return hip_done(sra::launch_fp8_decode(dtype, F->kind, F->codes, F->exps, F->rows, F->cols, F->block_rows, X, s), s,
+                  "fp8_decode");
+}
+
+static sra_status check_fp8_mm(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0) return fail(SRA_ERR_INVALID_ARG, "negative shape");
+  if (M >= ((int64_t)1 << 31) || N >= ((int64_t)1 << 26) || K > ((int64_t)1 << 22) || M * N >= ((int64_t)1 << 40))
+    return fail(SRA_ERR_UNSUPPORTED, "fp8_matmul of %lld x %lld over %lld is too large", (long long)M, (long long)N, (long long)K);
+  return SRA_OK;
+}
+
+sra_status sra_quant_matmul_workspace(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  SRA_TRY(check_fp8_mm(M, N, K));
+  if (!bytes) return fail(SRA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = sra::fp8_matmul_ws(M, N, K);
+  return SRA_OK;
+}
+
+sra_status sra_quant_matmul(const sra_fp8* a, const sra_fp8* b, int32_t out_dtype, void* Out, void* ws, size_t ws_bytes,
+                          void* stream) {
+  SRA_TRY(check_dtype(out_dtype));
+  SRA_TRY(check_fp8(a, "a"));
+  SRA_TRY(check_fp8(b, "b"));
+  if (a->cols != b->cols)
+    return fail(SRA_ERR_INVALID_ARG, "a has %lld columns, b %lld", (long long)a->cols, (long long)b->cols);
+  SRA_TRY(check_fp8_mm(a->rows, b->rows, a->cols));
+  SRA_TRY(check_ptr(Out, a->rows > 0 && b->rows > 0, "Out"));
+  SRA_TRY(check_ws(ws, ws_bytes, sra::fp8_matmul_ws(a->rows, b->rows, a->cols)));
+  const hipStream_t s = (hipStream_t)stream;
+  const sra::Fp8Operand x{a->codes, a->exps, a->kind, a->block_rows}, y{b->codes, b->exps, b->kind, b->block_rows};
+  return hip_done(sra::launch_fp8_matmul(x, y, a->rows, b->rows, a->cols, out_dtype == SRA_F32, Out, ws, s), s,
+                  "fp8_matmul");
+}
+
+static sra_status check_orth(int64_t n, int64_t rows, int64_t cols) {
+  if (n < 0 || rows < 0 || cols < 0) return fail(SRA_ERR_INVALID_ARG, "negative shape");
+  if (!sra::orth_ok(rows, cols))
+    return fail(SRA_ERR_UNSUPPORTED, "orthogonalize needs min(rows, cols) <= 256 (%lld x %lld)", (long long)rows, (long long)cols);
+  if (n > 65535 || std::max(rows, cols) >= ((int64_t)1 << 31))
+    return fail(SRA_ERR_UNSUPPORTED, "orthogonalize of %lld matrices of %lld x %lld is too large", (long long)n,
+                (long long)rows, (long long)cols);
+  return SRA_OK;
+}
+
+sra_status sra_orthogonalize_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes) {
+  SRA_TRY(check_orth(n, rows, cols));
+  if (!bytes) return fail(SRA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = sra::orth_ws(n, rows, cols);
+  return SRA_OK;
+}
+
+sra_status sra_orthogonalize(const void* G, int32_t dtype, int64_t n, int64_t rows, int64_t cols, int32_t steps,
+                             double a, double b, double c, double eps, void* O, void* ws, size_t ws_bytes, void* stream) {
+  SRA_TRY(check_dtype(dtype));
+  SRA_TRY(check_orth(n, rows, cols));
+  if (!(eps >= 0. && eps <= 1e300)) return fail(SRA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (steps < 1 || steps > 64) return fail(SRA_ERR_INVALID_ARG, "steps %d is not between 1 and 64", steps);
+  for (double v : {a, b, c})
+    if (!(v >= -1e300 && v <= 1e300)) return fail(SRA_ERR_INVALID_ARG, "a, b and c must be finite");
+  const bool any = n > 0 && rows > 0 && cols > 0;
+  SRA_TRY(check_ptr(G, any, "G"));
+  SRA_TRY(check_ptr(O, any, "O"));
+  if (any) {
+    const uintptr_t g = (uintptr_t)G, o = (uintptr_t)O, size = (uintptr_t)n * rows * cols * esize(dtype);
+    if (g < o + size && o < g + size) return fail(SRA_ERR_INVALID_ARG, "G and O overlap");
+  }
+  SRA_TRY(check_ws(ws, ws_bytes, sra::orth_ws(n, rows, cols)));
+  const double abc[3] = {a, b, c};
+  const hipStream_t s = (hipStream_t)stream;
+  return hip_done(sra::launch_orth(dtype, G, n, rows, cols, steps, abc, eps, O, ws, s), s, "orthogonalize");
 }
 
 sra_status sra_nm_tile_bytes(int64_t rows, int64_t cols, int32_t n, int32_t m, size_t* value_bytes,
@@ -1191,12 +1366,6 @@ size_t multi_bwd_plan(const sra_sparse* P, int64_t T, int32_t n, int32_t r, uint
   p.total = a.used;
   if (plan) *plan = p;
   return p.total;
-}
-sra_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
-  if (need > 0 && (!ws || ws_bytes < need))
-    return fail(SRA_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", need, ws ? ws_bytes : (size_t)0);
-  if (need > 0 && !al16(ws)) return fail(SRA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
-  return SRA_OK;
 }
 // Y or dX: the shared product with the adapters' epilogue (ep.r = 0: without)
 sra_status multi_product(const sra_sparse* S, const void* act, int64_t T, const sra::Epilogue& ep, void* out, void* ws,

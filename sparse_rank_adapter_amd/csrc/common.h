@@ -470,6 +470,36 @@ hipError_t launch_ckpt_encode(int dtype, const void* x, int64_t T, int64_t K, in
 hipError_t launch_ckpt_decode(int dtype, const int8_t* codes, const uint8_t* exps, int64_t T, int64_t K, void* x,
                               hipStream_t s);
 
+// Matrices in 8-bit floating point (fp8.hip): codes [R][fp8_ld(C)], exps [ceil(R / block_rows)][ceil(C / 128)];
+// codes / exps and codes_t / exps_t (the transpose's): either pair may be null.
+int64_t fp8_ld(int64_t cols);
+hipError_t launch_fp8_encode(int dtype, int kind, const void* x, int64_t R, int64_t C, int block_rows, uint8_t* codes,
+                             uint8_t* exps, uint8_t* codes_t, uint8_t* exps_t, hipStream_t s);
+hipError_t launch_fp8_decode(int dtype, int kind, const uint8_t* codes, const uint8_t* exps, int64_t R, int64_t C,
+                             int block_rows, void* x, hipStream_t s);
+// Their product a b^T (fp8_mm.hip); the workspace holds the splits' partial products
+struct Fp8Operand {
+  const uint8_t* codes;
+  const uint8_t* exps;
+  int kind, block_rows;
+};
+size_t fp8_matmul_ws(int64_t M, int64_t N, int64_t K);
+hipError_t launch_fp8_matmul(const Fp8Operand& a, const Fp8Operand& b, int64_t M, int64_t N, int64_t K, bool out_f32,
+                             void* out, void* ws, hipStream_t s);
+// Root-mean-square norm over rows (rms_norm.hip), H <= 16384 (rms_norm_ok); y or codes may be null, r and h
+// both may be
+bool rms_norm_ok(int64_t H);
+size_t rms_norm_bwd_ws(int64_t T, int64_t H);
+hipError_t launch_rms_norm_fwd(int dtype, const void* x, const void* r, const void* gamma, float eps, int64_t T,
+                               int64_t H, void* h, void* y, float* rstd, uint8_t* codes, uint8_t* exps, hipStream_t s);
+hipError_t launch_rms_norm_bwd(int dtype, const void* dy, const void* h, const void* gamma, const float* rstd,
+                               const void* dh, int64_t T, int64_t H, void* dx, float* dgamma, void* ws, hipStream_t s);
+// Newton-Schulz steps on n matrices (orth.hip), min(rows, cols) <= 256 (orth_ok); abc: three host doubles
+bool orth_ok(int64_t rows, int64_t cols);
+size_t orth_ws(int64_t n, int64_t rows, int64_t cols);
+hipError_t launch_orth(int dtype, const void* G, int64_t n, int64_t rows, int64_t cols, int steps, const double* abc,
+                       double eps, void* O, void* ws, hipStream_t s);
+
 bool adapter_grads_ok(const AdapterGrad* g, int n, int64_t T, int r);
 size_t adapter_grads_ws(const AdapterGrad* g, int n, int64_t T, int r);
 hipError_t launch_adapter_grads(const AdapterGrad* g, int n, int64_t T, int r, void* ws,

@@ -1,0 +1,390 @@
+// Products of 8-bit floating point matrices with a power-of-two scale for each block of 128 columns
+// (fp8.h): Out[m][n] = sum_k a[m][k] b[n][k], both operands reduced along their rows.
+//
+// The scaled matrix instruction v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 x 128 by 128 x 16 codes
+// and applies one E8M0 byte per row and 32 columns; a block's byte is given for all four of its quarters.
+// The sum over the whole reduction stays in its fp32 accumulators.  The order of the 128 codes inside a
+// step does not matter as long as both operands use the same: a lane (row l % 16) takes 16-byte chunks
+// l / 16 and l / 16 + 4 of its row's 128 bytes.
+//
+// Scales of four consecutive blocks are one dword of a row's exponents; the instruction's op_sel picks
+// the byte, so they cost one load per row and 512 columns.
+#include <algorithm>
+
+#include "fp8.h"
+
+namespace {
+using namespace sra_f8;
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+struct Mat {
+  const uint8_t* codes;
+  const uint8_t* exps;
+  int64_t rows, ld, nblk;  // ld = 128 nblk bytes a row
+  int shift;               // log2 of the rows that share a scale (0 or 7)
+};
+struct Out {
+  void* p;
+  int64_t M, N;
+  bool f32;
+};
+
+union Frag {
+  u32x4 h[2];
+  v8i v;
+};
+
+// s_waitcnt vmcnt(N) alone (expcnt / lgkmcnt at their maxima)
+template <int N>
+SRA_DEV void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// 16-byte buffer -> LDS transfer: lane i's bytes from offset off + soff land at block + 16 i
+SRA_DEV void dma(__amdgpu_buffer_rsrc_t rs, uint8_t* block, uint32_t off, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)block, 16, off, soff, 0, 0);
+}
+
+// exponents of blocks kb .. kb + 3 of `row` (those past the row's end are of no use to the caller);
+// nothing past the array's end is read
+SRA_DEV uint32_t scales4(const Mat& m, int64_t row, int64_t kb) {
+  const int64_t total = ((m.rows - 1) >> m.shift) * m.nblk + m.nblk;
+  const int64_t at = (min(row, m.rows - 1) >> m.shift) * m.nblk + kb;
+  uint32_t v = 0;
+  if (total >= 4) {
+    const int64_t o = min(at, total - 4);
+    __builtin_memcpy(&v, m.exps + o, 4);
+    v >>= 8 * (int)(at - o);
+  } else {
+    for (int i = 0; i < 4; ++i)
+      if (at + i < total) v |= (uint32_t)m.exps[at + i] << (8 * i);
+  }
+  return v;
+}
+
+// j (a constant once unrolled): which byte of the scale dwords
+template <int KX, int KY>
+SRA_DEV f32x4 mfma(const Frag& x, const Frag& y, f32x4 c, uint32_t sx, uint32_t sy, int j) {
+  if (j == 0) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, c, KX, KY, 0, (int)sx, 0, (int)sy);
+  if (j == 1) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, c, KX, KY, 1, (int)sx, 1, (int)sy);
+  if (j == 2) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, c, KX, KY, 2, (int)sx, 2, (int)sy);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, c, KX, KY, 3, (int)sx, 3, (int)sy);
+}
+
+SRA_DEV void store_out(const Out& o, int64_t m, int64_t n, float v) {
+  if (o.f32) reinterpret_cast<float*>(o.p)[m * o.N + n] = v;
+  else {
+    float one[1] = {v};
+    sra_row::RowVec<uint16_t, 1>::store(reinterpret_cast<uint16_t*>(o.p) + m * o.N + n, one);
+  }
+}
+
+// ---- few rows of a (up to 16 MT): b streams once from memory into registers.
+// A workgroup owns 16 rows of b; its waves share the reduction in contiguous parts and join in LDS.
+template <int KA, int KB, int MT, int NW>
+__global__ __launch_bounds__(64 * NW) void k_fp8_few(Mat a, Mat b, Out out) {
+  __shared__ float red[NW][MT * 256];
+  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t nrow = min(n0 + (l & 15), b.rows - 1);
+  const uint8_t* const bp = b.codes + nrow * b.ld + 16 * q;
+  const uint8_t* ap[MT];
+#pragma unroll
+  for (int f = 0; f < MT; ++f) ap[f] = a.codes + min((int64_t)(16 * f + (l & 15)), a.rows - 1) * a.ld + 16 * q;
+  f32x4 acc[MT];
+#pragma unroll
+  for (int f = 0; f < MT; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t lo = b.nblk * w / NW, hi = b.nblk * (w + 1) / NW;
+  for (int64_t kb = lo; kb < hi; kb += 4) {
+    Frag fb[4], fa[4][MT];
+    uint32_t sa[MT];
+    const int left = (int)min(hi - kb, (int64_t)4);
+    const uint32_t sb = scales4(b, nrow, kb);
+#pragma unroll
+    for (int f = 0; f < MT; ++f) sa[f] = scales4(a, 16 * f + (l & 15), kb);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t at = (kb + min(j, left - 1)) * kBlock;  // past the part's end: a block that is read anyway
+      fb[j].h[0] = *reinterpret_cast<const u32x4*>(bp + at);
+      fb[j].h[1] = *reinterpret_cast<const u32x4*>(bp + at + 64);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t at = (kb + min(j, left - 1)) * kBlock;
+#pragma unroll
+      for (int f = 0; f < MT; ++f) {
+        fa[j][f].h[0] = *reinterpret_cast<const u32x4*>(ap[f] + at);
+        fa[j][f].h[1] = *reinterpret_cast<const u32x4*>(ap[f] + at + 64);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j < left) {
+#pragma unroll
+        for (int f = 0; f < MT; ++f) acc[f] = mfma<KB, KA>(fb[j], fa[j][f], acc[f], sb, sa[f], j);
+      }
+    }
+  }
+  // acc[f][v]: row 16 f + l % 16 of a, row n0 + 4 q + v of b
+#pragma unroll
+  for (int f = 0; f < MT; ++f)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[w][f * 256 + (l & 15) * 16 + 4 * q + v] = acc[f][v];
+  __syncthreads();
+  for (int i = threadIdx.x; i < MT * 256; i += 64 * NW) {
+    float s = red[0][i];
+#pragma unroll
+    for (int k = 1; k < NW; ++k) s += red[k][i];
+    const int64_t m = i >> 4, n = n0 + (i & 15);
+    if (m < out.M && n < out.N) store_out(out, m, n, s);
+  }
+}
+
+// ---- tiles of BM x BN, WM x WN waves, a ring of ST stages of 128 columns in LDS.
+// Rows are 128 bytes; chunk c of row i lies at (c ^ key(i)), key = i % 8 for a and (i / FN) % 8 for b, whose
+// fragments take rows FN (l % 16) + g, so that a lane's FN accumulators are neighbouring columns of Out.
+template <int BM, int BN, int WM, int WN, int ST>
+struct Cfg {
+  static constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
+  static constexpr int stage = (BM + BN) * kBlock;
+  static constexpr int DA = BM / 8 / NW, DB = BN / 8 / NW;  // transfers of a wave per stage
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole transfers");
+  static constexpr int bytes = ST * stage;
+};
+
+// Workgroup ids go round-robin over the 8 XCDs: give each XCD a contiguous range of tiles, and order the
+// tiles in groups of 8 row tiles so that the workgroups of one XCD share operands in its L2.
+SRA_DEV void tile_of(int bid, int n, int nm, int nn, int& tm, int& tn) {
+  const int full = n & ~7;
+  const int t = bid >= full ? bid : (bid & 7) * (full >> 3) + (bid >> 3);
+  constexpr int G = 8;
+  const int per = G * nn, g = t / per, gs = min(G, nm - g * G), in = t - g * per;
+  tm = g * G + in % gs;
+  tn = in / gs;
+}
+
+template <int KA, int KB, int BM, int BN, int WM, int WN, int ST>
+__global__ __launch_bounds__(64 * WM * WN) void k_fp8_tiles(Mat a, Mat b, Out out, int nm, int nn, float* part) {
+  using C = Cfg<BM, BN, WM, WN, ST>;
+  constexpr int FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB;
+  __shared__ __align__(1024) uint8_t smem[C::bytes];
+  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i16 = l & 15;
+  int tm, tn;
+  tile_of(blockIdx.x, nm * nn, nm, nn, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int wm = (w / WN) * (BM / WM), wn = (w % WN) * (BN / WN);
+  // this split's blocks of the reduction
+  const int64_t k0 = a.nblk * blockIdx.y / gridDim.y, k1 = a.nblk * (blockIdx.y + 1) / gridDim.y;
+  const int n_kb = (int)(k1 - k0);
+  const int rows_a = (int)min((int64_t)BM, a.rows - m0), rows_b = (int)min((int64_t)BN, b.rows - n0);
+  // rows past the end lie past the resource's size: they read zeros
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(a.codes + m0 * a.ld), 0, (int)(rows_a * a.ld), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)(b.codes + n0 * b.ld), 0, (int)(rows_b * b.ld), 0x00020000);
+  uint32_t va[DA], vb[DB];
+#pragma unroll
+  for (int d = 0; d < DA; ++d) {
+    const int row = 8 * (w * DA + d) + (l >> 3);
+    va[d] = (uint32_t)(row * a.ld) + 16 * ((l & 7) ^ (row & 7));
+  }
+#pragma unroll
+  for (int d = 0; d < DB; ++d) {
+    const int row = 8 * (w * DB + d) + (l >> 3);
+    vb[d] = (uint32_t)(row * b.ld) + 16 * ((l & 7) ^ ((row / FN) & 7));
+  }
+  auto issue = [&](int kb) {
+    uint8_t* const st = smem + (kb % ST) * C::stage;
+    const int so = (int)((k0 + kb) * kBlock);
+#pragma unroll
+    for (int d = 0; d < DA; ++d)
+      dma(ra, st + 1024 * (w * DA + d), va[d], so);
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+      dma(rb, st + BM * kBlock + 1024 * (w * DB + d), vb[d], so);
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int f = 0; f < FM; ++f)
+#pragma unroll
+    for (int g = 0; g < FN; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint32_t sa[FM], sb[FN], na[FM], nb[FN];
+  auto scales = [&](int kb) {
+#pragma unroll
+    for (int f = 0; f < FM; ++f) na[f] = scales4(a, m0 + wm + 16 * f + i16, k0 + kb);
+#pragma unroll
+    for (int g = 0; g < FN; ++g) nb[g] = scales4(b, n0 + wn + FN * i16 + g, k0 + kb);
+  };
+  auto step = [&](int kb, int j) {
+    if (ST > 2 && kb + 1 < n_kb) wait_vm<DA + DB>();  // the newer stage may still be in flight
+    else wait_vm<0>();
+    ring_barrier();  // the stage is there for every wave, and every wave has read the one before it
+    if (j == 0 && kb + 4 < n_kb) scales(kb + 4);
+    if (kb + ST - 1 < n_kb) issue(kb + ST - 1);
+    const uint8_t* const st = smem + (kb % ST) * C::stage;
+    Frag fb[FN];
+#pragma unroll
+    for (int g = 0; g < FN; ++g) {
+      const int row = wn + FN * i16 + g, key = (row / FN) & 7;
+      const uint8_t* const p = st + (BM + row) * kBlock;
+      fb[g].h[0] = *reinterpret_cast<const u32x4*>(p + 16 * (q ^ key));
+      fb[g].h[1] = *reinterpret_cast<const u32x4*>(p + 16 * ((q + 4) ^ key));
+    }
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      const int row = wm + 16 * f + i16, key = row & 7;
+      const uint8_t* const p = st + row * kBlock;
+      Frag fa;
+      fa.h[0] = *reinterpret_cast<const u32x4*>(p + 16 * (q ^ key));
+      fa.h[1] = *reinterpret_cast<const u32x4*>(p + 16 * ((q + 4) ^ key));
+#pragma unroll
+      for (int g = 0; g < FN; ++g) acc[f][g] = mfma<KA, KB>(fa, fb[g], acc[f][g], sa[f], sb[g], j);
+    }
+  };
+  if (n_kb > 0) {
+    scales(0);
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i)
+      if (i < n_kb) issue(i);
+  }
+  for (int kb = 0; kb < n_kb; kb += 4) {
+#pragma unroll
+    for (int f = 0; f < FM; ++f) sa[f] = na[f];
+#pragma unroll
+    for (int g = 0; g < FN; ++g) sb[g] = nb[g];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (kb + j < n_kb) step(kb + j, j);
+  }
+  // acc[f][g][v]: row 16 f + 4 q + v, column FN (l % 16) + g of the wave's part
+  const bool f32 = part || out.f32;
+  float* const fo = part ? part + (int64_t)blockIdx.y * out.M * out.N : (float*)out.p;
+  const int64_t n = n0 + wn + FN * i16;
+#pragma unroll
+  for (int f = 0; f < FM; ++f)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t m = m0 + wm + 16 * f + 4 * q + v;
+      if (m >= out.M) continue;
+      if (FN == 4 && out.N % 4 == 0) {
+        if (n >= out.N) continue;
+        const float e[4] = {acc[f][0][v], acc[f][1 % FN][v], acc[f][2 % FN][v], acc[f][3 % FN][v]};
+        if (f32) {
+          *reinterpret_cast<f32x4*>(fo + m * out.N + n) = f32x4{e[0], e[1], e[2], e[3]};
+        } else {
+          union { __bf16 h[4]; u32x2 w; } o;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o.h[k] = (__bf16)e[k];
+          *reinterpret_cast<u32x2*>((uint16_t*)out.p + m * out.N + n) = o.w;
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < FN; ++g) {
+          if (n + g >= out.N) continue;
+          if (f32) fo[m * out.N + n + g] = acc[f][g][v];
+          else store_out(out, m, n + g, acc[f][g][v]);
+        }
+      }
+    }
+}
+
+// sum of the splits' partial products, in order
+__global__ __launch_bounds__(256) void k_fp8_join(const float* __restrict__ part, int S, Out out) {
+  const int64_t n = out.M * out.N, step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+    float s = part[i];
+    for (int k = 1; k < S; ++k) s += part[k * n + i];
+    store_out(out, 0, i, s);
+  }
+}
+
+// ---- the choice of kernel
+enum { kFew, kBig, kMid, kSmall };
+struct Plan {
+  int kernel;
+  int splits;
+};
+Plan plan_of(int64_t M, int64_t N, int64_t nblk) {
+  if (M <= 64) return {kFew, 1};
+  const auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  if (tiles(256, 256) >= 256) return {kBig, 1};
+  if (tiles(128, 128) >= 192) return {kMid, 1};
+  const int64_t t = tiles(64, 128);
+  int s = 1;
+  while (t * s < 192 && nblk >= 8 * s) s *= 2;  // at least 4 blocks a split
+  return {kSmall, s};
+}
+
+}  // namespace
+
+namespace sra {
+
+size_t fp8_matmul_ws(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0) return 0;
+  const Plan p = plan_of(M, N, blocks_of(K));
+  return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(float) : 0;
+}
+
+template <int KA, int KB>
+static hipError_t matmul(const Mat& a, const Mat& b, const Out& out, const Plan& p, float* ws, hipStream_t s) {
+  if (p.kernel == kFew) {
+    const dim3 grid((unsigned)((out.N + 15) / 16));
+    const bool wide = grid.x < 1024;  // few workgroups: more waves share the reduction
+    const int mt = (int)((out.M + 15) / 16);
+#define SRA_FEW(MT)                                                                                                   \
+  do {                                                                                                                \
+    if (wide) launch(SRA_KERNEL_FP8_MM, k_fp8_few<KA, KB, MT, 8>, grid, dim3(512), 0, s, a, b, out);                  \
+    else launch(SRA_KERNEL_FP8_MM, k_fp8_few<KA, KB, MT, 4>, grid, dim3(256), 0, s, a, b, out);                       \
+  } while (0)
+    if (mt <= 1) SRA_FEW(1);
+    else if (mt == 2) SRA_FEW(2);
+    else SRA_FEW(4);
+#undef SRA_FEW
+    return hipGetLastError();
+  }
+#define SRA_TILES(BM, BN, WM, WN, ST)                                                                               \
+  do {                                                                                                              \
+    const int nm = (int)((out.M + BM - 1) / BM), nn = (int)((out.N + BN - 1) / BN);                                 \
+    launch(SRA_KERNEL_FP8_MM, k_fp8_tiles<KA, KB, BM, BN, WM, WN, ST>, dim3((unsigned)(nm * nn), (unsigned)p.splits), \
+           dim3(64 * WM * WN), 0, s, a, b, out, nm, nn, p.splits > 1 ? ws : nullptr);                               \
+  } while (0)
+  if (p.kernel == kBig) SRA_TILES(256, 256, 2, 4, 2);
+  else if (p.kernel == kMid) SRA_TILES(128, 128, 2, 2, 3);
+  else SRA_TILES(64, 128, 2, 2, 3);
+#undef SRA_TILES
+  hipError_t err = hipGetLastError();
+  if (err == hipSuccess && p.splits > 1) {
+    const int64_t n = out.M * out.N;
+    hipLaunchKernelGGL(k_fp8_join, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4096)), dim3(256), 0, s, ws, p.splits, out);
+    err = hipGetLastError();
+  }
+  return err;
+}
+
+hipError_t launch_fp8_matmul(const Fp8Operand& x, const Fp8Operand& y, int64_t M, int64_t N, int64_t K, bool out_f32,
+                             void* o, void* ws, hipStream_t s) {
+  if (M <= 0 || N <= 0) return hipSuccess;
+  const int64_t nblk = blocks_of(K);
+  const Plan p = plan_of(M, N, nblk);
+  // a launch has fewer than 2^32 threads: at most 2^22 tiles of 512 each, by rows of a (N < 2^26)
+  const int64_t rows = p.kernel == kBig ? ((int64_t)1 << 22) / ((N + 255) / 256) * 256 : M;
+  for (int64_t m0 = 0; m0 < M; m0 += rows) {
+    // m0 is a multiple of 256: whole blocks of exponents
+    const Mat a{x.codes + m0 * nblk * kBlock, x.exps + (x.block_rows == 1 ? m0 : m0 / 128) * nblk, std::min(rows, M - m0),
+                nblk * kBlock, nblk, x.block_rows == 1 ? 0 : 7};
+    const Mat b{y.codes, y.exps, N, nblk * kBlock, nblk, y.block_rows == 1 ? 0 : 7};
+    const Out out{(uint8_t*)o + m0 * N * (out_f32 ? 4 : 2), a.rows, N, out_f32};
+    hipError_t err;
+    if (x.kind == SRA_FP8_E4M3)
+      err = y.kind == SRA_FP8_E4M3 ? matmul<SRA_FP8_E4M3, SRA_FP8_E4M3>(a, b, out, p, (float*)ws, s)
+                                   : matmul<SRA_FP8_E4M3, SRA_FP8_E5M2>(a, b, out, p, (float*)ws, s);
+    else
+      err = y.kind == SRA_FP8_E4M3 ? matmul<SRA_FP8_E5M2, SRA_FP8_E4M3>(a, b, out, p, (float*)ws, s)
+                                   : matmul<SRA_FP8_E5M2, SRA_FP8_E5M2>(a, b, out, p, (float*)ws, s);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+}  // namespace sra

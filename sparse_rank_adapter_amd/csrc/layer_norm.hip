@@ -26,60 +26,6 @@
 namespace {
 using namespace sra_row;
 
-// Sum over the wave in fp64 by DPP row shifts and broadcasts (lane 63 ends with it), the same value in
-// every lane, with no LDS round trips (lane exchanges through LDS: 52 us against 48-50 at 8192 x 5120);
-// fp32 sums here moved the statistics by enough to flip over half as many codes of a checkpoint again.
-template <int CTRL, int ROWS>
-SRA_DEV double dpp_add(double x) {
-  const uint64_t u = (uint64_t)__double_as_longlong(x);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
-  return x + __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
-}
-SRA_DEV double wave_sum(double x) {
-  x = dpp_add<0x111, 0xf>(x);  // row_shr 1, 2, 4, 8: lane 15 of each row of 16 holds the row's sum
-  x = dpp_add<0x112, 0xf>(x);
-  x = dpp_add<0x114, 0xf>(x);
-  x = dpp_add<0x118, 0xf>(x);
-  x = dpp_add<0x142, 0xa>(x);  // row_bcast 15 into rows 1 and 3
-  x = dpp_add<0x143, 0xc>(x);  // row_bcast 31 into rows 2 and 3
-  const uint64_t u = (uint64_t)__double_as_longlong(x);
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
-  return __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
-}
-// Sums over the workgroup (up to 16 waves, added in fp64), the same values in every thread.  `red` is
-// LDS that no wave still reads: calls alternate between two areas, so one barrier each is enough.
-template <int N>
-SRA_DEV void block_sum(const float (&v)[N], double (&out)[N], double* red) {
-  double s[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) s[k] = wave_sum((double)v[k]);
-  const int nw = blockDim.x >> 6;
-  if (nw == 1) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) out[k] = s[k];
-    return;
-  }
-  const int w = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) red[w * N + k] = s[k];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < N; ++k) out[k] = 0.0;
-  for (int i = 0; i < nw; ++i)
-#pragma unroll
-    for (int k = 0; k < N; ++k) out[k] += red[i * N + k];
-}
-
-// sum of N terms as a tree
-template <int N>
-SRA_DEV float tree_sum(const float* v) {
-  if constexpr (N == 1) return v[0];
-  else return tree_sum<N / 2>(v) + tree_sum<N - N / 2>(v + N / 2);
-}
-
 // one workgroup per row
 template <typename E, int VEC, int EPT, bool CK>
 __global__ __launch_bounds__(EPT == 8 ? 256 : 1024) void k_ln_fwd(const E* __restrict__ x, const E* __restrict__ gamma,
