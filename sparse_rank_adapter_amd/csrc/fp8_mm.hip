@@ -8,8 +8,14 @@
 // l / 16 and l / 16 + 4 of its row's 128 bytes.
 //
 // Scales of four consecutive blocks are one dword of a row's exponents; the instruction's op_sel picks
-// the byte, so they cost one load per row and 512 columns.
+// the byte, so they cost one read per row and 512 columns.
+//
+// Inside one instruction the products are added with about 17 bits below the largest of them (measured: results 1e-5 to
+// 4e-5 off over one block, the plain fp8 instructions the same), which is far below a bf16 result's rounding but not
+// below fp32's.  fp32 results (EX) therefore go over bf16: every code is exact in bf16, v_mfma_f32_16x16x32_bf16 adds
+// with full fp32 accuracy, and each block's sum enters the accumulator over its scale, an exact ldexp.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8.h"
 
@@ -48,21 +54,53 @@ SRA_DEV void dma(__amdgpu_buffer_rsrc_t rs, uint8_t* block, uint32_t off, int so
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)block, 16, off, soff, 0, 0);
 }
 
-// exponents of blocks kb .. kb + 3 of `row` (those past the row's end are of no use to the caller);
-// nothing past the array's end is read
-SRA_DEV uint32_t scales4(const Mat& m, int64_t row, int64_t kb) {
-  const int64_t total = ((m.rows - 1) >> m.shift) * m.nblk + m.nblk;
+// exponents of blocks kb .. kb + 3 of `row` (those past the row's end are of no use to the caller); nothing past
+// the array's end is read.  `whole`: the array has four bytes at least.
+SRA_DEV int64_t exps_total(const Mat& m) { return (((m.rows - 1) >> m.shift) + 1) * m.nblk; }
+SRA_DEV uint32_t scales4(const Mat& m, int64_t row, int64_t kb, int64_t total, bool whole) {
   const int64_t at = (min(row, m.rows - 1) >> m.shift) * m.nblk + kb;
   uint32_t v = 0;
-  if (total >= 4) {
+  if (whole) {
     const int64_t o = min(at, total - 4);
     __builtin_memcpy(&v, m.exps + o, 4);
-    v >>= 8 * (int)(at - o);
-  } else {
-    for (int i = 0; i < 4; ++i)
-      if (at + i < total) v |= (uint32_t)m.exps[at + i] << (8 * i);
+    return v >> (8 * (int)(at - o));
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v |= (uint32_t)m.exps[min(at + i, total - 1)] << (8 * i);
   return v;
+}
+SRA_DEV int byte_of(uint32_t w, int j) { return (int)((w >> (8 * j)) & 0xffu); }
+
+// 32 codes as bf16, exactly: fragment s holds the 8 codes of dwords 2 s and 2 s + 1
+struct Wide {
+  bf16x8 s[4];
+};
+template <int K>
+SRA_DEV Wide widen(const Frag& f) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  Wide o;
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    bf16x2 lo, hi;
+    if constexpr (K == SRA_FP8_E4M3) {
+      lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f.v[d], 1.f, false);
+      hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f.v[d], 1.f, true);
+    } else {
+      lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)f.v[d], 1.f, false);
+      hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)f.v[d], 1.f, true);
+    }
+    o.s[d / 2][4 * (d % 2)] = lo[0];
+    o.s[d / 2][4 * (d % 2) + 1] = lo[1];
+    o.s[d / 2][4 * (d % 2) + 2] = hi[0];
+    o.s[d / 2][4 * (d % 2) + 3] = hi[1];
+  }
+  return o;
+}
+SRA_DEV f32x4 mfma_wide(const Wide& x, const Wide& y) {
+  f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.s[s], y.s[s], c, 0, 0, 0);
+  return c;
 }
 
 // j (a constant once unrolled): which byte of the scale dwords
@@ -84,7 +122,7 @@ SRA_DEV void store_out(const Out& o, int64_t m, int64_t n, float v) {
 
 // ---- few rows of a (up to 16 MT): b streams once from memory into registers.
 // A workgroup owns 16 rows of b; its waves share the reduction in contiguous parts and join in LDS.
-template <int KA, int KB, int MT, int NW>
+template <int KA, int KB, int MT, int NW, bool EX>
 __global__ __launch_bounds__(64 * NW) void k_fp8_few(Mat a, Mat b, Out out) {
   __shared__ float red[NW][MT * 256];
   const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4;
@@ -97,14 +135,23 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_few(Mat a, Mat b, Out out) {
   f32x4 acc[MT];
 #pragma unroll
   for (int f = 0; f < MT; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint32_t poison = 0;  // EX: scales of 255 met, bit v for row 4 q + v of b, bit 4 + f for a's
+  const int64_t ta = exps_total(a), tb = exps_total(b);
+  const bool whole = ta >= 4 && tb >= 4;
+  constexpr int SB = EX ? 4 : 1;  // b's rows whose scales a lane holds: those of its results, or that of its operand
   const int64_t lo = b.nblk * w / NW, hi = b.nblk * (w + 1) / NW;
   for (int64_t kb = lo; kb < hi; kb += 4) {
     Frag fb[4], fa[4][MT];
-    uint32_t sa[MT];
+    uint32_t sa[MT], sb[SB];
     const int left = (int)min(hi - kb, (int64_t)4);
-    const uint32_t sb = scales4(b, nrow, kb);
+    const auto scales = [&](bool ok) {
 #pragma unroll
-    for (int f = 0; f < MT; ++f) sa[f] = scales4(a, 16 * f + (l & 15), kb);
+      for (int v = 0; v < SB; ++v) sb[v] = scales4(b, EX ? n0 + 4 * q + v : nrow, kb, tb, ok);
+#pragma unroll
+      for (int f = 0; f < MT; ++f) sa[f] = scales4(a, 16 * f + (l & 15), kb, ta, ok);
+    };
+    if (whole) scales(true);
+    else scales(false);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t at = (kb + min(j, left - 1)) * kBlock;  // past the part's end: a block that is read anyway
@@ -122,9 +169,22 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_few(Mat a, Mat b, Out out) {
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (j < left) {
+      if (j >= left) continue;
+      if constexpr (!EX) {
 #pragma unroll
-        for (int f = 0; f < MT; ++f) acc[f] = mfma<KB, KA>(fb[j], fa[j][f], acc[f], sb, sa[f], j);
+        for (int f = 0; f < MT; ++f) acc[f] = mfma<KB, KA>(fb[j], fa[j][f], acc[f], sb[0], sa[f], j);
+      } else {
+        const Wide wb = widen<KB>(fb[j]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) poison |= byte_of(sb[v], j) == 255 ? 1u << v : 0u;
+#pragma unroll
+        for (int f = 0; f < MT; ++f) {
+          const f32x4 p = mfma_wide(wb, widen<KA>(fa[j][f]));
+          const int ea = byte_of(sa[f], j);
+          poison |= ea == 255 ? 16u << f : 0u;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[f][v] += __builtin_amdgcn_ldexpf(p[v], byte_of(sb[v], j) + ea - 254);
+        }
       }
     }
   }
@@ -132,7 +192,10 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_few(Mat a, Mat b, Out out) {
 #pragma unroll
   for (int f = 0; f < MT; ++f)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) red[w][f * 256 + (l & 15) * 16 + 4 * q + v] = acc[f][v];
+    for (int v = 0; v < 4; ++v) {
+      if (EX && (poison & (1u << v | 16u << f))) acc[f][v] = __uint_as_float(0x7fc00000u);
+      red[w][f * 256 + (l & 15) * 16 + 4 * q + v] = acc[f][v];
+    }
   __syncthreads();
   for (int i = threadIdx.x; i < MT * 256; i += 64 * NW) {
     float s = red[0][i];
@@ -143,7 +206,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_few(Mat a, Mat b, Out out) {
   }
 }
 
-// ---- tiles of BM x BN, WM x WN waves, a ring of ST stages of 128 columns in LDS.
+// ---- tiles of BM x BN, WM x WN waves, a ring of ST = 2 or 4 stages of 128 columns in LDS.
 // Rows are 128 bytes; chunk c of row i lies at (c ^ key(i)), key = i % 8 for a and (i / FN) % 8 for b, whose
 // fragments take rows FN (l % 16) + g, so that a lane's FN accumulators are neighbouring columns of Out.
 template <int BM, int BN, int WM, int WN, int ST>
@@ -152,6 +215,7 @@ struct Cfg {
   static constexpr int stage = (BM + BN) * kBlock;
   static constexpr int DA = BM / 8 / NW, DB = BN / 8 / NW;  // transfers of a wave per stage
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole transfers");
+  static_assert(ST == 2 || ST == 4, "slots by the step modulo four");
   static constexpr int bytes = ST * stage;
 };
 
@@ -166,116 +230,28 @@ SRA_DEV void tile_of(int bid, int n, int nm, int nn, int& tm, int& tn) {
   tn = in / gs;
 }
 
-template <int KA, int KB, int BM, int BN, int WM, int WN, int ST>
-__global__ __launch_bounds__(64 * WM * WN) void k_fp8_tiles(Mat a, Mat b, Out out, int nm, int nn, float* part) {
-  using C = Cfg<BM, BN, WM, WN, ST>;
-  constexpr int FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB;
-  __shared__ __align__(1024) uint8_t smem[C::bytes];
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i16 = l & 15;
-  int tm, tn;
-  tile_of(blockIdx.x, nm * nn, nm, nn, tm, tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const int wm = (w / WN) * (BM / WM), wn = (w % WN) * (BN / WN);
-  // this split's blocks of the reduction
-  const int64_t k0 = a.nblk * blockIdx.y / gridDim.y, k1 = a.nblk * (blockIdx.y + 1) / gridDim.y;
-  const int n_kb = (int)(k1 - k0);
-  const int rows_a = (int)min((int64_t)BM, a.rows - m0), rows_b = (int)min((int64_t)BN, b.rows - n0);
-  // rows past the end lie past the resource's size: they read zeros
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(a.codes + m0 * a.ld), 0, (int)(rows_a * a.ld), 0x00020000);
-  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)(b.codes + n0 * b.ld), 0, (int)(rows_b * b.ld), 0x00020000);
-  uint32_t va[DA], vb[DB];
-#pragma unroll
-  for (int d = 0; d < DA; ++d) {
-    const int row = 8 * (w * DA + d) + (l >> 3);
-    va[d] = (uint32_t)(row * a.ld) + 16 * ((l & 7) ^ (row & 7));
-  }
-#pragma unroll
-  for (int d = 0; d < DB; ++d) {
-    const int row = 8 * (w * DB + d) + (l >> 3);
-    vb[d] = (uint32_t)(row * b.ld) + 16 * ((l & 7) ^ ((row / FN) & 7));
-  }
-  auto issue = [&](int kb) {
-    uint8_t* const st = smem + (kb % ST) * C::stage;
-    const int so = (int)((k0 + kb) * kBlock);
-#pragma unroll
-    for (int d = 0; d < DA; ++d)
-      dma(ra, st + 1024 * (w * DA + d), va[d], so);
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-      dma(rb, st + BM * kBlock + 1024 * (w * DB + d), vb[d], so);
-  };
-  f32x4 acc[FM][FN];
-#pragma unroll
-  for (int f = 0; f < FM; ++f)
-#pragma unroll
-    for (int g = 0; g < FN; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint32_t sa[FM], sb[FN], na[FM], nb[FN];
-  auto scales = [&](int kb) {
-#pragma unroll
-    for (int f = 0; f < FM; ++f) na[f] = scales4(a, m0 + wm + 16 * f + i16, k0 + kb);
-#pragma unroll
-    for (int g = 0; g < FN; ++g) nb[g] = scales4(b, n0 + wn + FN * i16 + g, k0 + kb);
-  };
-  auto step = [&](int kb, int j) {
-    if (ST > 2 && kb + 1 < n_kb) wait_vm<DA + DB>();  // the newer stage may still be in flight
-    else wait_vm<0>();
-    ring_barrier();  // the stage is there for every wave, and every wave has read the one before it
-    if (j == 0 && kb + 4 < n_kb) scales(kb + 4);
-    if (kb + ST - 1 < n_kb) issue(kb + ST - 1);
-    const uint8_t* const st = smem + (kb % ST) * C::stage;
-    Frag fb[FN];
-#pragma unroll
-    for (int g = 0; g < FN; ++g) {
-      const int row = wn + FN * i16 + g, key = (row / FN) & 7;
-      const uint8_t* const p = st + (BM + row) * kBlock;
-      fb[g].h[0] = *reinterpret_cast<const u32x4*>(p + 16 * (q ^ key));
-      fb[g].h[1] = *reinterpret_cast<const u32x4*>(p + 16 * ((q + 4) ^ key));
-    }
-#pragma unroll
-    for (int f = 0; f < FM; ++f) {
-      const int row = wm + 16 * f + i16, key = row & 7;
-      const uint8_t* const p = st + row * kBlock;
-      Frag fa;
-      fa.h[0] = *reinterpret_cast<const u32x4*>(p + 16 * (q ^ key));
-      fa.h[1] = *reinterpret_cast<const u32x4*>(p + 16 * ((q + 4) ^ key));
-#pragma unroll
-      for (int g = 0; g < FN; ++g) acc[f][g] = mfma<KA, KB>(fa, fb[g], acc[f][g], sa[f], sb[g], j);
-    }
-  };
-  if (n_kb > 0) {
-    scales(0);
-#pragma unroll
-    for (int i = 0; i < ST - 1; ++i)
-      if (i < n_kb) issue(i);
-  }
-  for (int kb = 0; kb < n_kb; kb += 4) {
-#pragma unroll
-    for (int f = 0; f < FM; ++f) sa[f] = na[f];
-#pragma unroll
-    for (int g = 0; g < FN; ++g) sb[g] = nb[g];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (kb + j < n_kb) step(kb + j, j);
-  }
-  // acc[f][g][v]: row 16 f + 4 q + v, column FN (l % 16) + g of the wave's part
+// acc[f][g][v]: row m0 + 16 f + 4 q + v, column n0 + FN (l % 16) + g of Out, or of this split's fp32 partial product
+template <int FM, int FN>
+SRA_DEV void store_tile(const f32x4 (&acc)[FM][FN], const Out& out, float* part, int64_t m0, int64_t n0) {
+  static_assert(FN == 4, "16-byte stores");
+  const int l = threadIdx.x & 63, q = l >> 4, i16 = l & 15;
   const bool f32 = part || out.f32;
   float* const fo = part ? part + (int64_t)blockIdx.y * out.M * out.N : (float*)out.p;
-  const int64_t n = n0 + wn + FN * i16;
+  const int64_t n = n0 + FN * i16;
+  if (n >= out.N) return;
 #pragma unroll
   for (int f = 0; f < FM; ++f)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int64_t m = m0 + wm + 16 * f + 4 * q + v;
+      const int64_t m = m0 + 16 * f + 4 * q + v;
       if (m >= out.M) continue;
-      if (FN == 4 && out.N % 4 == 0) {
-        if (n >= out.N) continue;
-        const float e[4] = {acc[f][0][v], acc[f][1 % FN][v], acc[f][2 % FN][v], acc[f][3 % FN][v]};
+      if (out.N % 4 == 0) {
         if (f32) {
-          *reinterpret_cast<f32x4*>(fo + m * out.N + n) = f32x4{e[0], e[1], e[2], e[3]};
+          *reinterpret_cast<f32x4*>(fo + m * out.N + n) = f32x4{acc[f][0][v], acc[f][1][v], acc[f][2][v], acc[f][3][v]};
         } else {
           union { __bf16 h[4]; u32x2 w; } o;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o.h[k] = (__bf16)e[k];
+          for (int k = 0; k < 4; ++k) o.h[k] = (__bf16)acc[f][k][v];
           *reinterpret_cast<u32x2*>((uint16_t*)out.p + m * out.N + n) = o.w;
         }
       } else {
@@ -287,6 +263,293 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_tiles(Mat a, Mat b, Out ou
         }
       }
     }
+}
+
+// Scales of a tile's rows, 16 blocks at a time: thread t keeps row t (a's BM rows, then b's BN)
+struct ScaleRow {
+  const uint8_t* exps;
+  int64_t at, total;
+  SRA_DEV u32x4 load(int chunk) const {
+    const int64_t o = at + 16 * chunk;
+    u32x4 v;
+    if (o + 16 <= total) {
+      __builtin_memcpy(&v, exps + o, 16);
+    } else {  // the array's last bytes
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i / 4] |= (uint32_t)exps[min(o + i, total - 1)] << (8 * (i % 4));
+      v = u32x4{w[0], w[1], w[2], w[3]};
+    }
+    return v;
+  }
+};
+constexpr int kScaleLd = 20;  // bytes between rows of a chunk in LDS: 16 rows fall on different banks
+
+template <int KA, int KB, int BM, int BN, int WM, int WN, int ST, bool EX>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tiles(Mat a, Mat b, Out out, int nm, int nn, float* part) {
+  using C = Cfg<BM, BN, WM, WN, ST>;
+  constexpr int FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB;
+  __shared__ __align__(1024) uint8_t smem[C::bytes];
+  __shared__ __align__(16) uint8_t scal[2][(BM + BN) * kScaleLd];
+  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i16 = l & 15;
+  int tm, tn;
+  tile_of(blockIdx.x, nm * nn, nm, nn, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int wm = (w / WN) * (BM / WM), wn = (w % WN) * (BN / WN);
+  // this split's blocks of the reduction
+  const int64_t k0 = a.nblk * blockIdx.y / gridDim.y, k1 = a.nblk * (blockIdx.y + 1) / gridDim.y;
+  const int n_kb = (int)(k1 - k0);
+  const int rows_a = (int)min((int64_t)BM, a.rows - m0), rows_b = (int)min((int64_t)BN, b.rows - n0);
+  // rows past the end lie past the resource's size: they read zeros
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(a.codes + m0 * a.ld), (short)0, (int)(rows_a * a.ld), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)(b.codes + n0 * b.ld), (short)0, (int)(rows_b * b.ld), 0x00020000);
+  uint32_t va[DA], vb[DB];
+#pragma unroll
+  for (int d = 0; d < DA; ++d) {
+    const int row = 8 * (w * DA + d) + (l >> 3);
+    va[d] = (uint32_t)(row * a.ld) + 16 * ((l & 7) ^ (row & 7));
+  }
+#pragma unroll
+  for (int d = 0; d < DB; ++d) {
+    const int row = 8 * (w * DB + d) + (l >> 3);
+    vb[d] = (uint32_t)(row * b.ld) + 16 * ((l & 7) ^ ((row / FN) & 7));
+  }
+  auto issue = [&](int kb, int slot) {
+    uint8_t* const st = smem + slot * C::stage;
+    const int so = (int)((k0 + kb) * kBlock);
+#pragma unroll
+    for (int d = 0; d < DA; ++d) dma(ra, st + 1024 * (w * DA + d), va[d], so);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) dma(rb, st + BM * kBlock + 1024 * (w * DB + d), vb[d], so);
+  };
+  const int t = threadIdx.x;
+  const bool has_row = t < BM + BN;
+  const Mat& sm = t < BM ? a : b;
+  const int64_t srow = min(t < BM ? m0 + t : n0 + t - BM, sm.rows - 1);
+  const ScaleRow sr{sm.exps, (srow >> sm.shift) * sm.nblk + k0, exps_total(sm)};
+  u32x4 sreg = {0, 0, 0, 0};
+  auto put_scales = [&](int chunk) {  // sreg, loaded before, into the chunk's half
+    if (has_row) {
+      uint32_t* const p = reinterpret_cast<uint32_t*>(scal[chunk & 1] + t * kScaleLd);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = sreg[i];
+    }
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int f = 0; f < FM; ++f)
+#pragma unroll
+    for (int g = 0; g < FN; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint32_t poison = 0;            // EX: scales of 255 met, bit 4 f + v for a's row of acc[..][v], bit 4 FM + g for b's
+  constexpr int SA = EX ? 4 : 1;  // a's rows per fragment whose scales a lane holds: its results', or its operand's
+  uint32_t sa[FM][SA], sb[FN];
+  // a lane's chunks of its first row of each operand; its other rows lie at fixed distances with the same key
+  const uint8_t* const pa0 = smem + (wm + i16) * kBlock + 16 * (q ^ (i16 & 7));
+  const uint8_t* const pa1 = smem + (wm + i16) * kBlock + 16 * ((q + 4) ^ (i16 & 7));
+  const uint8_t* const pb0 = smem + (BM + wn + FN * i16) * kBlock + 16 * (q ^ (i16 & 7));
+  const uint8_t* const pb1 = smem + (BM + wn + FN * i16) * kBlock + 16 * ((q + 4) ^ (i16 & 7));
+  auto step = [&](int kb, int j) {  // kb % 4 == j, so the ring's slots are constants
+    if (ST == 4 && kb + 2 < n_kb) wait_vm<2 * (DA + DB)>();  // the newer stages may still be in flight
+    else if (ST == 4 && kb + 1 < n_kb) wait_vm<DA + DB>();
+    else wait_vm<0>();
+    ring_barrier();  // the stage is there for every wave, and every wave has read the one before it
+    if (kb + ST - 1 < n_kb) issue(kb + ST - 1, (j + ST - 1) % ST);
+    const int st = j % ST * C::stage;
+    if (j == 0) {
+      const uint8_t* const sc = scal[(kb >> 4) & 1] + (kb & 12);
+#pragma unroll
+      for (int f = 0; f < FM; ++f)
+#pragma unroll
+        for (int v = 0; v < SA; ++v)
+          sa[f][v] = *reinterpret_cast<const uint32_t*>(sc + (wm + 16 * f + (EX ? 4 * q + v : i16)) * kScaleLd);
+#pragma unroll
+      for (int g = 0; g < FN; ++g) sb[g] = *reinterpret_cast<const uint32_t*>(sc + (BM + wn + FN * i16 + g) * kScaleLd);
+    }
+    Frag fb[FN];
+#pragma unroll
+    for (int g = 0; g < FN; ++g) {
+      fb[g].h[0] = *reinterpret_cast<const u32x4*>(pb0 + st + g * kBlock);
+      fb[g].h[1] = *reinterpret_cast<const u32x4*>(pb1 + st + g * kBlock);
+    }
+    Wide wb[EX ? FN : 1];
+    if constexpr (EX) {
+#pragma unroll
+      for (int g = 0; g < FN; ++g) {
+        wb[g] = widen<KB>(fb[g]);
+        poison |= byte_of(sb[g], j) == 255 ? 1u << (4 * FM + g) : 0u;
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      Frag fa;
+      fa.h[0] = *reinterpret_cast<const u32x4*>(pa0 + st + 16 * f * kBlock);
+      fa.h[1] = *reinterpret_cast<const u32x4*>(pa1 + st + 16 * f * kBlock);
+      if constexpr (!EX) {
+#pragma unroll
+        for (int g = 0; g < FN; ++g) acc[f][g] = mfma<KA, KB>(fa, fb[g], acc[f][g], sa[f][0], sb[g], j);
+      } else {
+        const Wide wa = widen<KA>(fa);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) poison |= byte_of(sa[f][v], j) == 255 ? 1u << (4 * f + v) : 0u;
+#pragma unroll
+        for (int g = 0; g < FN; ++g) {
+          const f32x4 p = mfma_wide(wa, wb[g]);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            acc[f][g][v] += __builtin_amdgcn_ldexpf(p[v], byte_of(sa[f][v], j) + byte_of(sb[g], j) - 254);
+        }
+      }
+    }
+  };
+  if (n_kb > 0) {
+    if (has_row) sreg = sr.load(0);
+    put_scales(0);
+    if (has_row && n_kb > 16) sreg = sr.load(1);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i)
+      if (i < n_kb) issue(i, i);
+  }
+  for (int kb = 0; kb < n_kb; kb += 4) {
+    if ((kb & 15) == 8 && (kb | 15) + 1 < n_kb) {  // the next chunk's half was last read before this chunk began
+      put_scales((kb >> 4) + 1);
+      if (has_row && (kb | 15) + 17 < n_kb) sreg = sr.load((kb >> 4) + 2);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): written before the barriers that follow
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (kb + j < n_kb) step(kb + j, j);
+  }
+  if constexpr (EX) {
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+#pragma unroll
+      for (int g = 0; g < FN; ++g)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (poison & (1u << (4 * f + v) | 1u << (4 * FM + g))) acc[f][g][v] = __uint_as_float(0x7fc00000u);
+  }
+  store_tile<FM, FN>(acc, out, part, m0 + wm, n0 + wn);
+}
+
+// ---- 256 x 256 tiles by two groups of four waves that take turns: while one group's 32 matrix instructions a wave run
+// (1024 cycles), the other reads its next operands from LDS (96 KB, 768 cycles), so each SIMD's matrix unit always has
+// a wave to serve.  Phases alternate at barriers; group 0 reads stage k in phase 2 k and computes in 2 k + 1, group 1
+// one phase later.  Stage k + 1 goes where stage k - 1 was from phase 2 k on and has to be there by phase 2 k + 2.
+template <int KA, int KB>
+__global__ __launch_bounds__(512) void k_fp8_turns(Mat a, Mat b, Out out, int nm, int nn) {
+  constexpr int BM = 256, BN = 256;
+  using C = Cfg<BM, BN, 2, 4, 2>;
+  constexpr int FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB;
+  __shared__ __align__(1024) uint8_t smem[C::bytes];
+  __shared__ __align__(16) uint8_t scal[2][(BM + BN) * kScaleLd];
+  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i16 = l & 15;
+  int tm, tn;
+  tile_of(blockIdx.x, nm * nn, nm, nn, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const bool late = w >= 4;  // waves 0-3 and 4-7: one of each group on every SIMD
+  const int wm = (w >> 2) * 128, wn = (w & 3) * 64;
+  const int n_kb = (int)a.nblk;
+  const int rows_a = (int)min((int64_t)BM, a.rows - m0), rows_b = (int)min((int64_t)BN, b.rows - n0);
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(a.codes + m0 * a.ld), (short)0, (int)(rows_a * a.ld), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)(b.codes + n0 * b.ld), (short)0, (int)(rows_b * b.ld), 0x00020000);
+  uint32_t va[DA], vb[DB];
+#pragma unroll
+  for (int d = 0; d < DA; ++d) {
+    const int row = 8 * (w * DA + d) + (l >> 3);
+    va[d] = (uint32_t)(row * a.ld) + 16 * ((l & 7) ^ (row & 7));
+  }
+#pragma unroll
+  for (int d = 0; d < DB; ++d) {
+    const int row = 8 * (w * DB + d) + (l >> 3);
+    vb[d] = (uint32_t)(row * b.ld) + 16 * ((l & 7) ^ ((row / FN) & 7));
+  }
+  auto issue = [&](int kb, int slot) {
+    if (kb >= n_kb) return;
+    uint8_t* const st = smem + slot * C::stage;
+    const int so = kb * kBlock;
+#pragma unroll
+    for (int d = 0; d < DA; ++d) dma(ra, st + 1024 * (w * DA + d), va[d], so);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) dma(rb, st + BM * kBlock + 1024 * (w * DB + d), vb[d], so);
+  };
+  const int t = threadIdx.x;
+  const Mat& sm = t < BM ? a : b;
+  const int64_t srow = min(t < BM ? m0 + t : n0 + t - BM, sm.rows - 1);
+  const ScaleRow sr{sm.exps, (srow >> sm.shift) * sm.nblk, exps_total(sm)};
+  u32x4 sreg;
+  auto put_scales = [&](int chunk) {
+    uint32_t* const p = reinterpret_cast<uint32_t*>(scal[chunk & 1] + t * kScaleLd);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = sreg[i];
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int f = 0; f < FM; ++f)
+#pragma unroll
+    for (int g = 0; g < FN; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint8_t* const pa0 = smem + (wm + i16) * kBlock + 16 * (q ^ (i16 & 7));
+  const uint8_t* const pa1 = smem + (wm + i16) * kBlock + 16 * ((q + 4) ^ (i16 & 7));
+  const uint8_t* const pb0 = smem + (BM + wn + FN * i16) * kBlock + 16 * (q ^ (i16 & 7));
+  const uint8_t* const pb1 = smem + (BM + wn + FN * i16) * kBlock + 16 * ((q + 4) ^ (i16 & 7));
+  uint32_t sa[FM], sb[FN];
+  Frag fa[FM], fb[FN];
+  auto read = [&](int kb, int j) {
+    const int st = j % 2 * C::stage;
+#pragma unroll
+    for (int g = 0; g < FN; ++g) {
+      fb[g].h[0] = *reinterpret_cast<const u32x4*>(pb0 + st + g * kBlock);
+      fb[g].h[1] = *reinterpret_cast<const u32x4*>(pb1 + st + g * kBlock);
+    }
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      fa[f].h[0] = *reinterpret_cast<const u32x4*>(pa0 + st + 16 * f * kBlock);
+      fa[f].h[1] = *reinterpret_cast<const u32x4*>(pa1 + st + 16 * f * kBlock);
+    }
+    if (j == 0) {
+      const uint8_t* const sc = scal[(kb >> 4) & 1] + (kb & 12);
+#pragma unroll
+      for (int f = 0; f < FM; ++f) sa[f] = *reinterpret_cast<const uint32_t*>(sc + (wm + 16 * f + i16) * kScaleLd);
+#pragma unroll
+      for (int g = 0; g < FN; ++g) sb[g] = *reinterpret_cast<const uint32_t*>(sc + (BM + wn + FN * i16 + g) * kScaleLd);
+    }
+  };
+  sreg = sr.load(0);
+  put_scales(0);
+  if (n_kb > 16) sreg = sr.load(1);
+  issue(0, 0);
+  wait_vm<0>();
+  __syncthreads();
+  if (late) {  // phase 0
+    issue(1, 1);
+    ring_barrier();
+  }
+  for (int kb = 0; kb < n_kb; kb += 4) {
+    if ((kb & 15) == 8 && (kb | 15) + 1 < n_kb) {  // the next chunk's half was last read before this chunk began
+      put_scales((kb >> 4) + 1);
+      if ((kb | 15) + 17 < n_kb) sreg = sr.load((kb >> 4) + 2);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (kb + j >= n_kb) break;
+      if (!late) issue(kb + j + 1, (j + 1) % 2);
+      read(kb + j, j);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this stage's slot is filled again after the next barriers
+      if (late) wait_vm<0>();
+      ring_barrier();
+      if (late) issue(kb + j + 2, j % 2);
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int f = 0; f < FM; ++f)
+#pragma unroll
+        for (int g = 0; g < FN; ++g) acc[f][g] = mfma<KA, KB>(fa[f], fb[g], acc[f][g], sa[f], sb[g], j);
+      __builtin_amdgcn_s_setprio(0);
+      if (!late) wait_vm<0>();
+      ring_barrier();
+    }
+  }
+  if (!late) ring_barrier();
+  store_tile<FM, FN>(acc, out, nullptr, m0 + wm, n0 + wn);
 }
 
 // sum of the splits' partial products, in order
@@ -308,7 +571,7 @@ struct Plan {
 Plan plan_of(int64_t M, int64_t N, int64_t nblk) {
   if (M <= 64) return {kFew, 1};
   const auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 256) return {kBig, 1};
+  if (tiles(256, 256) >= 256) return {kBig, 1};  // (EX: the middle tiles, whose accumulators leave room for the widened codes)
   if (tiles(128, 128) >= 192) return {kMid, 1};
   const int64_t t = tiles(64, 128);
   int s = 1;
@@ -326,7 +589,7 @@ size_t fp8_matmul_ws(int64_t M, int64_t N, int64_t K) {
   return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(float) : 0;
 }
 
-template <int KA, int KB>
+template <int KA, int KB, bool EX>
 static hipError_t matmul(const Mat& a, const Mat& b, const Out& out, const Plan& p, float* ws, hipStream_t s) {
   if (p.kernel == kFew) {
     const dim3 grid((unsigned)((out.N + 15) / 16));
@@ -334,8 +597,8 @@ static hipError_t matmul(const Mat& a, const Mat& b, const Out& out, const Plan&
     const int mt = (int)((out.M + 15) / 16);
 #define SRA_FEW(MT)                                                                                                   \
   do {                                                                                                                \
-    if (wide) launch(SRA_KERNEL_FP8_MM, k_fp8_few<KA, KB, MT, 8>, grid, dim3(512), 0, s, a, b, out);                  \
-    else launch(SRA_KERNEL_FP8_MM, k_fp8_few<KA, KB, MT, 4>, grid, dim3(256), 0, s, a, b, out);                       \
+    if (wide) launch(SRA_KERNEL_FP8_MM, k_fp8_few<KA, KB, MT, 8, EX>, grid, dim3(512), 0, s, a, b, out);              \
+    else launch(SRA_KERNEL_FP8_MM, k_fp8_few<KA, KB, MT, 4, EX>, grid, dim3(256), 0, s, a, b, out);                   \
   } while (0)
     if (mt <= 1) SRA_FEW(1);
     else if (mt == 2) SRA_FEW(2);
@@ -346,12 +609,17 @@ static hipError_t matmul(const Mat& a, const Mat& b, const Out& out, const Plan&
 #define SRA_TILES(BM, BN, WM, WN, ST)                                                                               \
   do {                                                                                                              \
     const int nm = (int)((out.M + BM - 1) / BM), nn = (int)((out.N + BN - 1) / BN);                                 \
-    launch(SRA_KERNEL_FP8_MM, k_fp8_tiles<KA, KB, BM, BN, WM, WN, ST>, dim3((unsigned)(nm * nn), (unsigned)p.splits), \
+    launch(SRA_KERNEL_FP8_MM, k_fp8_tiles<KA, KB, BM, BN, WM, WN, ST, EX>, dim3((unsigned)(nm * nn), (unsigned)p.splits), \
            dim3(64 * WM * WN), 0, s, a, b, out, nm, nn, p.splits > 1 ? ws : nullptr);                               \
   } while (0)
-  if (p.kernel == kBig) SRA_TILES(256, 256, 2, 4, 2);
-  else if (p.kernel == kMid) SRA_TILES(128, 128, 2, 2, 3);
-  else SRA_TILES(64, 128, 2, 2, 3);
+  if (p.kernel == kSmall) {
+    SRA_TILES(64, 128, 2, 2, 2);
+  } else if (EX || p.kernel == kMid) {
+    SRA_TILES(128, 128, 2, 2, 2);
+  } else if constexpr (!EX) {
+    const int nm = (int)((out.M + 255) / 256), nn = (int)((out.N + 255) / 256);
+    launch(SRA_KERNEL_FP8_MM, k_fp8_turns<KA, KB>, dim3((unsigned)(nm * nn)), dim3(512), 0, s, a, b, out, nm, nn);
+  }
 #undef SRA_TILES
   hipError_t err = hipGetLastError();
   if (err == hipSuccess && p.splits > 1) {
@@ -367,21 +635,22 @@ hipError_t launch_fp8_matmul(const Fp8Operand& x, const Fp8Operand& y, int64_t M
   if (M <= 0 || N <= 0) return hipSuccess;
   const int64_t nblk = blocks_of(K);
   const Plan p = plan_of(M, N, nblk);
-  // a launch has fewer than 2^32 threads: at most 2^22 tiles of 512 each, by rows of a (N < 2^26)
-  const int64_t rows = p.kernel == kBig ? ((int64_t)1 << 22) / ((N + 255) / 256) * 256 : M;
+  // a launch has fewer than 2^32 threads: at most 2^22 tiles of 128 x 128 or more, by rows of a (N < 2^26)
+  const int64_t rows = p.kernel == kBig ? ((int64_t)1 << 20) / ((N + 127) / 128) * 256 : M;
   for (int64_t m0 = 0; m0 < M; m0 += rows) {
     // m0 is a multiple of 256: whole blocks of exponents
     const Mat a{x.codes + m0 * nblk * kBlock, x.exps + (x.block_rows == 1 ? m0 : m0 / 128) * nblk, std::min(rows, M - m0),
                 nblk * kBlock, nblk, x.block_rows == 1 ? 0 : 7};
     const Mat b{y.codes, y.exps, N, nblk * kBlock, nblk, y.block_rows == 1 ? 0 : 7};
     const Out out{(uint8_t*)o + m0 * N * (out_f32 ? 4 : 2), a.rows, N, out_f32};
-    hipError_t err;
-    if (x.kind == SRA_FP8_E4M3)
-      err = y.kind == SRA_FP8_E4M3 ? matmul<SRA_FP8_E4M3, SRA_FP8_E4M3>(a, b, out, p, (float*)ws, s)
-                                   : matmul<SRA_FP8_E4M3, SRA_FP8_E5M2>(a, b, out, p, (float*)ws, s);
-    else
-      err = y.kind == SRA_FP8_E4M3 ? matmul<SRA_FP8_E5M2, SRA_FP8_E4M3>(a, b, out, p, (float*)ws, s)
-                                   : matmul<SRA_FP8_E5M2, SRA_FP8_E5M2>(a, b, out, p, (float*)ws, s);
+    const auto run = [&](auto ka, auto kb) {
+      return out_f32 ? matmul<ka.value, kb.value, true>(a, b, out, p, (float*)ws, s)
+                     : matmul<ka.value, kb.value, false>(a, b, out, p, (float*)ws, s);
+    };
+    const std::integral_constant<int, SRA_FP8_E4M3> e4{};
+    const std::integral_constant<int, SRA_FP8_E5M2> e5{};
+    const hipError_t err = x.kind == SRA_FP8_E4M3 ? (y.kind == SRA_FP8_E4M3 ? run(e4, e4) : run(e4, e5))
+                                                  : (y.kind == SRA_FP8_E4M3 ? run(e5, e4) : run(e5, e5));
     if (err != hipSuccess) return err;
   }
   return hipSuccess;
