@@ -23,7 +23,6 @@ namespace {
 using namespace sra_f8;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 struct Mat {
   const uint8_t* codes;
@@ -49,9 +48,20 @@ SRA_DEV void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// 16-byte buffer -> LDS transfer: lane i's bytes from offset off + soff land at block + 16 i
-SRA_DEV void dma(__amdgpu_buffer_rsrc_t rs, uint8_t* block, uint32_t off, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)block, 16, off, soff, 0, 0);
+// Buffer -> LDS transfers as lds_dma makes them (unseen by the compiler, which would put a wait for all of them before
+// any LDS read), with scalar operands given as such: a readfirstlane of what is scalar already costs vector registers,
+// and these kernels have none to spare.  base and bytes are uniform; offsets past `bytes` read zeros.
+SRA_DEV dma_rsrc_t rows_rsrc(const uint8_t* base, int rows, int ld) {
+  const uint64_t p = (uint64_t)(uintptr_t)base;
+  return dma_rsrc_t{(int)(uint32_t)p, (int)((uint32_t)(p >> 32) & 0xffff), max(0, rows) * ld, 0x00020000};
+}
+SRA_DEV void dma(const dma_rsrc_t& rs, uint32_t block, uint32_t off, int soff) {
+  // one wait state after M0 is written, five after a vector instruction writes a scalar register that is read here; M0 is
+  // reserved and may not be in the clobber list: this file has no builtin transfer, which keeps its target there
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(block), "v"(off), "s"(rs), "s"(soff)
+               : "memory");
 }
 
 // exponents of blocks kb .. kb + 3 of `row` (those past the row's end are of no use to the caller); nothing past
@@ -267,17 +277,26 @@ SRA_DEV void store_tile(const f32x4 (&acc)[FM][FN], const Out& out, float* part,
 
 // Scales of a tile's rows, 16 blocks at a time: thread t keeps row t (a's BM rows, then b's BN)
 struct ScaleRow {
-  const uint8_t* exps;
-  int64_t at, total;
+  const uint8_t* p;  // the row's first byte of this reduction
+  int left;          // bytes from there to the array's end, where that is less than 2^30
+  SRA_DEV ScaleRow(const Mat& m, int64_t row, int64_t k0) {
+    const int64_t at = (min(row, m.rows - 1) >> m.shift) * m.nblk + k0;
+    p = m.exps + at;
+    left = (int)min(exps_total(m) - at, (int64_t)1 << 30);
+  }
   SRA_DEV u32x4 load(int chunk) const {
-    const int64_t o = at + 16 * chunk;
+    const int o = 16 * chunk;
     u32x4 v;
-    if (o + 16 <= total) {
-      __builtin_memcpy(&v, exps + o, 16);
+    if (o + 16 <= left) {
+      __builtin_memcpy(&v, p + o, 16);
     } else {  // the array's last bytes
       uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll 1
+      for (int i = 0; i < 16 && o + i < left; ++i) {
+        const uint32_t e = (uint32_t)p[o + i] << (8 * (i % 4));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i / 4] |= (uint32_t)exps[min(o + i, total - 1)] << (8 * (i % 4));
+        for (int k = 0; k < 4; ++k) w[k] |= i / 4 == k ? e : 0u;
+      }
       v = u32x4{w[0], w[1], w[2], w[3]};
     }
     return v;
@@ -291,7 +310,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tiles(Mat a, Mat b, Out
   constexpr int FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB;
   __shared__ __align__(1024) uint8_t smem[C::bytes];
   __shared__ __align__(16) uint8_t scal[2][(BM + BN) * kScaleLd];
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i16 = l & 15;
+  const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), q = l >> 4, i16 = l & 15;
   int tm, tn;
   tile_of(blockIdx.x, nm * nn, nm, nn, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
@@ -299,34 +318,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tiles(Mat a, Mat b, Out
   // this split's blocks of the reduction
   const int64_t k0 = a.nblk * blockIdx.y / gridDim.y, k1 = a.nblk * (blockIdx.y + 1) / gridDim.y;
   const int n_kb = (int)(k1 - k0);
-  const int rows_a = (int)min((int64_t)BM, a.rows - m0), rows_b = (int)min((int64_t)BN, b.rows - n0);
-  // rows past the end lie past the resource's size: they read zeros
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(a.codes + m0 * a.ld), (short)0, (int)(rows_a * a.ld), 0x00020000);
-  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)(b.codes + n0 * b.ld), (short)0, (int)(rows_b * b.ld), 0x00020000);
-  uint32_t va[DA], vb[DB];
+  // A wave's transfer d of an operand fills 8 rows from 8 (w D + d) on; rows past the resource's end (the matrix's) read
+  // zeros.  The transfers are issued unseen by the compiler, which would wait for all of them before any LDS read.
+  const int ld = (int)a.ld;
+  const int left_a = (int)min((int64_t)BM, a.rows - m0) - 8 * w * DA, left_b = (int)min((int64_t)BN, b.rows - n0) - 8 * w * DB;
+  const uint8_t *const ga = a.codes + (m0 + 8 * w * DA) * a.ld, *const gb = b.codes + (n0 + 8 * w * DB) * b.ld;
+  const uint32_t va = (uint32_t)((l >> 3) * ld) + 16 * ((l & 7) ^ (l >> 3));
+  uint32_t vb[DB];
 #pragma unroll
-  for (int d = 0; d < DA; ++d) {
-    const int row = 8 * (w * DA + d) + (l >> 3);
-    va[d] = (uint32_t)(row * a.ld) + 16 * ((l & 7) ^ (row & 7));
-  }
-#pragma unroll
-  for (int d = 0; d < DB; ++d) {
-    const int row = 8 * (w * DB + d) + (l >> 3);
-    vb[d] = (uint32_t)(row * b.ld) + 16 * ((l & 7) ^ ((row / FN) & 7));
-  }
+  for (int d = 0; d < DB; ++d) vb[d] = (uint32_t)((l >> 3) * ld) + 16 * ((l & 7) ^ (((8 * (w * DB + d) + (l >> 3)) / FN) & 7));
   auto issue = [&](int kb, int slot) {
-    uint8_t* const st = smem + slot * C::stage;
+    const uint32_t st = lds_offset(smem) + slot * C::stage;
     const int so = (int)((k0 + kb) * kBlock);
 #pragma unroll
-    for (int d = 0; d < DA; ++d) dma(ra, st + 1024 * (w * DA + d), va[d], so);
+    for (int d = 0; d < DA; ++d)
+      dma(rows_rsrc(ga + (int64_t)(8 * d) * ld, left_a - 8 * d, ld), st + 1024 * (w * DA + d), va, so);
 #pragma unroll
-    for (int d = 0; d < DB; ++d) dma(rb, st + BM * kBlock + 1024 * (w * DB + d), vb[d], so);
+    for (int d = 0; d < DB; ++d)
+      dma(rows_rsrc(gb + (int64_t)(8 * d) * ld, left_b - 8 * d, ld), st + BM * kBlock + 1024 * (w * DB + d), vb[d], so);
   };
   const int t = threadIdx.x;
   const bool has_row = t < BM + BN;
-  const Mat& sm = t < BM ? a : b;
-  const int64_t srow = min(t < BM ? m0 + t : n0 + t - BM, sm.rows - 1);
-  const ScaleRow sr{sm.exps, (srow >> sm.shift) * sm.nblk + k0, exps_total(sm)};
+  const ScaleRow sr(t < BM ? a : b, t < BM ? m0 + t : n0 + t - BM, k0);
   u32x4 sreg = {0, 0, 0, 0};
   auto put_scales = [&](int chunk) {  // sreg, loaded before, into the chunk's half
     if (has_row) {
@@ -437,74 +450,62 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tiles(Mat a, Mat b, Out
 // a wave to serve.  Phases alternate at barriers; group 0 reads stage k in phase 2 k and computes in 2 k + 1, group 1
 // one phase later.  Stage k + 1 goes where stage k - 1 was from phase 2 k on and has to be there by phase 2 k + 2.
 template <int KA, int KB>
-__global__ __launch_bounds__(512) void k_fp8_turns(Mat a, Mat b, Out out, int nm, int nn) {
-  constexpr int BM = 256, BN = 256;
-  using C = Cfg<BM, BN, 2, 4, 2>;
-  constexpr int FM = C::FM, FN = C::FN, DA = C::DA, DB = C::DB;
-  __shared__ __align__(1024) uint8_t smem[C::bytes];
+__global__ __launch_bounds__(512, 2) void k_fp8_turns(Mat a, Mat b, Out out, int nm, int nn) {
+  constexpr int BM = 256, BN = 256, FM = 8, FN = 4, D = 4;  // D transfers of each operand per wave and stage
+  constexpr int kSlot = BM * kBlock;                        // a's two slots, then b's: all reads within 64 KB of a base
+  __shared__ __align__(1024) uint8_t smem[4 * kSlot];
   __shared__ __align__(16) uint8_t scal[2][(BM + BN) * kScaleLd];
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i16 = l & 15;
+  const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), q = l >> 4, i16 = l & 15;
   int tm, tn;
   tile_of(blockIdx.x, nm * nn, nm, nn, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const bool late = w >= 4;  // waves 0-3 and 4-7: one of each group on every SIMD
   const int wm = (w >> 2) * 128, wn = (w & 3) * 64;
-  const int n_kb = (int)a.nblk;
-  const int rows_a = (int)min((int64_t)BM, a.rows - m0), rows_b = (int)min((int64_t)BN, b.rows - n0);
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(a.codes + m0 * a.ld), (short)0, (int)(rows_a * a.ld), 0x00020000);
-  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)(b.codes + n0 * b.ld), (short)0, (int)(rows_b * b.ld), 0x00020000);
-  uint32_t va[DA], vb[DB];
-#pragma unroll
-  for (int d = 0; d < DA; ++d) {
-    const int row = 8 * (w * DA + d) + (l >> 3);
-    va[d] = (uint32_t)(row * a.ld) + 16 * ((l & 7) ^ (row & 7));
-  }
-#pragma unroll
-  for (int d = 0; d < DB; ++d) {
-    const int row = 8 * (w * DB + d) + (l >> 3);
-    vb[d] = (uint32_t)(row * b.ld) + 16 * ((l & 7) ^ ((row / FN) & 7));
-  }
+  const int n_kb = (int)a.nblk, ld = (int)a.ld;
+  // A wave's transfer d fills rows 32 w + 8 d .. + 7; its resource starts at the first of them and ends with the matrix,
+  // so rows past the end read zeros.  b's key (row / 4) % 8 of those rows is 2 d + l / 32.
+  const int left_a = (int)min((int64_t)BM, a.rows - m0) - 32 * w, left_b = (int)min((int64_t)BN, b.rows - n0) - 32 * w;
+  const uint8_t *const ga = a.codes + (m0 + 32 * w) * a.ld, *const gb = b.codes + (n0 + 32 * w) * b.ld;
+  const uint32_t va = (uint32_t)((l >> 3) * ld) + 16 * ((l & 7) ^ (l >> 3));
+  const uint32_t vb = (uint32_t)((l >> 3) * ld) + 16 * ((l & 7) ^ (l >> 5));
   auto issue = [&](int kb, int slot) {
     if (kb >= n_kb) return;
-    uint8_t* const st = smem + slot * C::stage;
-    const int so = kb * kBlock;
+    const uint32_t st = lds_offset(smem) + slot * kSlot + 32 * kBlock * w;
 #pragma unroll
-    for (int d = 0; d < DA; ++d) dma(ra, st + 1024 * (w * DA + d), va[d], so);
+    for (int d = 0; d < D; ++d)
+      dma(rows_rsrc(ga + (int64_t)(8 * d) * ld, left_a - 8 * d, ld), st + 1024 * d, va, kb * kBlock);
 #pragma unroll
-    for (int d = 0; d < DB; ++d) dma(rb, st + BM * kBlock + 1024 * (w * DB + d), vb[d], so);
+    for (int d = 0; d < D; ++d)
+      dma(rows_rsrc(gb + (int64_t)(8 * d) * ld, left_b - 8 * d, ld), st + 2 * kSlot + 1024 * d, vb ^ (32 * d),
+              kb * kBlock);
   };
   const int t = threadIdx.x;
-  const Mat& sm = t < BM ? a : b;
-  const int64_t srow = min(t < BM ? m0 + t : n0 + t - BM, sm.rows - 1);
-  const ScaleRow sr{sm.exps, (srow >> sm.shift) * sm.nblk, exps_total(sm)};
-  u32x4 sreg;
-  auto put_scales = [&](int chunk) {
+  const ScaleRow sr(t < BM ? a : b, t < BM ? m0 + t : n0 + t - BM, 0);
+  auto put_scales = [&](int chunk, const u32x4& v) {
     uint32_t* const p = reinterpret_cast<uint32_t*>(scal[chunk & 1] + t * kScaleLd);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = sreg[i];
+    for (int i = 0; i < 4; ++i) p[i] = v[i];
   };
   f32x4 acc[FM][FN];
 #pragma unroll
   for (int f = 0; f < FM; ++f)
 #pragma unroll
     for (int g = 0; g < FN; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const uint8_t* const pa0 = smem + (wm + i16) * kBlock + 16 * (q ^ (i16 & 7));
-  const uint8_t* const pa1 = smem + (wm + i16) * kBlock + 16 * ((q + 4) ^ (i16 & 7));
-  const uint8_t* const pb0 = smem + (BM + wn + FN * i16) * kBlock + 16 * (q ^ (i16 & 7));
-  const uint8_t* const pb1 = smem + (BM + wn + FN * i16) * kBlock + 16 * ((q + 4) ^ (i16 & 7));
+  const uint8_t* const pa = smem + (wm + i16) * kBlock + 16 * (q ^ (i16 & 7));
+  const uint8_t* const pb = smem + 2 * kSlot + (wn + FN * i16) * kBlock + 16 * (q ^ (i16 & 7));
+  const int other = (q ^ (i16 & 7)) & 4 ? -64 : 64;  // from chunk q ^ key to chunk (q + 4) ^ key
   uint32_t sa[FM], sb[FN];
   Frag fa[FM], fb[FN];
   auto read = [&](int kb, int j) {
-    const int st = j % 2 * C::stage;
+    const int st = j % 2 * kSlot;
 #pragma unroll
     for (int g = 0; g < FN; ++g) {
-      fb[g].h[0] = *reinterpret_cast<const u32x4*>(pb0 + st + g * kBlock);
-      fb[g].h[1] = *reinterpret_cast<const u32x4*>(pb1 + st + g * kBlock);
+      fb[g].h[0] = *reinterpret_cast<const u32x4*>(pb + st + g * kBlock);
+      fb[g].h[1] = *reinterpret_cast<const u32x4*>(pb + other + st + g * kBlock);
     }
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
-      fa[f].h[0] = *reinterpret_cast<const u32x4*>(pa0 + st + 16 * f * kBlock);
-      fa[f].h[1] = *reinterpret_cast<const u32x4*>(pa1 + st + 16 * f * kBlock);
+      fa[f].h[0] = *reinterpret_cast<const u32x4*>(pa + st + 16 * f * kBlock);
+      fa[f].h[1] = *reinterpret_cast<const u32x4*>(pa + other + st + 16 * f * kBlock);
     }
     if (j == 0) {
       const uint8_t* const sc = scal[(kb >> 4) & 1] + (kb & 12);
@@ -514,41 +515,44 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Mat a, Mat b, Out out, int nm
       for (int g = 0; g < FN; ++g) sb[g] = *reinterpret_cast<const uint32_t*>(sc + (BM + wn + FN * i16 + g) * kScaleLd);
     }
   };
-  sreg = sr.load(0);
-  put_scales(0);
-  if (n_kb > 16) sreg = sr.load(1);
+  put_scales(0, sr.load(0));
   issue(0, 0);
   wait_vm<0>();
   __syncthreads();
-  if (late) {  // phase 0
-    issue(1, 1);
-    ring_barrier();
-  }
-  for (int kb = 0; kb < n_kb; kb += 4) {
-    if ((kb & 15) == 8 && (kb | 15) + 1 < n_kb) {  // the next chunk's half was last read before this chunk began
-      put_scales((kb >> 4) + 1);
-      if ((kb | 15) + 17 < n_kb) sreg = sr.load((kb >> 4) + 2);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (kb + j >= n_kb) break;
-      if (!late) issue(kb + j + 1, (j + 1) % 2);
-      read(kb + j, j);
-      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this stage's slot is filled again after the next barriers
-      if (late) wait_vm<0>();
-      ring_barrier();
-      if (late) issue(kb + j + 2, j % 2);
-      __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-      for (int f = 0; f < FM; ++f)
-#pragma unroll
-        for (int g = 0; g < FN; ++g) acc[f][g] = mfma<KA, KB>(fa[f], fb[g], acc[f][g], sa[f], sb[g], j);
-      __builtin_amdgcn_s_setprio(0);
-      if (!late) wait_vm<0>();
+  auto loop = [&](auto late_c) {
+    constexpr bool late = decltype(late_c)::value;
+    if (late) {  // phase 0
+      issue(1, 1);
       ring_barrier();
     }
-  }
-  if (!late) ring_barrier();
+    for (int kb = 0; kb < n_kb; kb += 4) {
+      // the next chunk of scales: its half was last read before this chunk began
+      if ((kb & 15) == 8 && (kb | 15) + 1 < n_kb) put_scales((kb >> 4) + 1, sr.load((kb >> 4) + 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (kb + j >= n_kb) break;
+        if (!late) issue(kb + j + 1, (j + 1) % 2);
+        read(kb + j, j);
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this stage's slot is filled again after the next barriers
+        if (late) wait_vm<0>();
+        ring_barrier();
+        if (late) issue(kb + j + 2, j % 2);
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+#pragma unroll
+          for (int g = 0; g < FN; ++g) acc[f][g] = mfma<KA, KB>(fa[f], fb[g], acc[f][g], sa[f], sb[g], j);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (!late) wait_vm<0>();
+        ring_barrier();
+      }
+    }
+    if (!late) ring_barrier();
+  };
+  if (w >= 4) loop(std::true_type{});  // waves 0-3 and 4-7: one of each group on every SIMD
+  else loop(std::false_type{});
   store_tile<FM, FN>(acc, out, nullptr, m0 + wm, n0 + wn);
 }
 
