@@ -243,26 +243,37 @@ SRA_DEV void tile_of(int bid, int n, int nm, int nn, int& tm, int& tn) {
 // acc[f][g][v]: row m0 + 16 f + 4 q + v, column n0 + FN (l % 16) + g of Out, or of this split's fp32 partial product
 template <int FM, int FN>
 SRA_DEV void store_tile(const f32x4 (&acc)[FM][FN], const Out& out, float* part, int64_t m0, int64_t n0) {
-  static_assert(FN == 4, "16-byte stores");
+  static_assert(FN % 4 == 0, "stores of four columns");
   const int l = threadIdx.x & 63, q = l >> 4, i16 = l & 15;
   const bool f32 = part || out.f32;
   float* const fo = part ? part + (int64_t)blockIdx.y * out.M * out.N : (float*)out.p;
+  uint16_t* const ho = (uint16_t*)out.p;
   const int64_t n = n0 + FN * i16;
-  if (n >= out.N) return;
 #pragma unroll
   for (int f = 0; f < FM; ++f)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int64_t m = m0 + 16 * f + 4 * q + v;
       if (m >= out.M) continue;
-      if (out.N % 4 == 0) {
-        if (f32) {
-          *reinterpret_cast<f32x4*>(fo + m * out.N + n) = f32x4{acc[f][0][v], acc[f][1][v], acc[f][2][v], acc[f][3][v]};
-        } else {
-          union { __bf16 h[4]; u32x2 w; } o;
+      if (FN == 8 && !f32 && out.N % 8 == 0) {
+        if (n >= out.N) continue;
+        union { __bf16 h[8]; u32x4 w; } o;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o.h[k] = (__bf16)acc[f][k][v];
-          *reinterpret_cast<u32x2*>((uint16_t*)out.p + m * out.N + n) = o.w;
+        for (int k = 0; k < 8; ++k) o.h[k] = (__bf16)acc[f][k % FN][v];
+        *reinterpret_cast<u32x4*>(ho + m * out.N + n) = o.w;
+      } else if (out.N % 4 == 0) {
+#pragma unroll
+        for (int g = 0; g < FN; g += 4) {
+          if (n + g >= out.N) continue;
+          if (f32) {
+            *reinterpret_cast<f32x4*>(fo + m * out.N + n + g) =
+                f32x4{acc[f][g][v], acc[f][g + 1][v], acc[f][g + 2][v], acc[f][g + 3][v]};
+          } else {
+            union { __bf16 h[4]; u32x2 w; } o;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o.h[k] = (__bf16)acc[f][g + k][v];
+            *reinterpret_cast<u32x2*>(ho + m * out.N + n + g) = o.w;
+          }
         }
       } else {
 #pragma unroll
@@ -278,26 +289,34 @@ SRA_DEV void store_tile(const f32x4 (&acc)[FM][FN], const Out& out, float* part,
 // Scales of a tile's rows, 16 blocks at a time: thread t keeps row t (a's BM rows, then b's BN)
 struct ScaleRow {
   const uint8_t* p;  // the row's first byte of this reduction
-  int left;          // bytes from there to the array's end, where that is less than 2^30
-  SRA_DEV ScaleRow(const Mat& m, int64_t row, int64_t k0) {
+  int n, left;       // its blocks; bytes from p to the array's end, where that is less than 2^30
+  SRA_DEV ScaleRow(const Mat& m, int64_t row, int64_t k0, int n_kb) {
     const int64_t at = (min(row, m.rows - 1) >> m.shift) * m.nblk + k0;
     p = m.exps + at;
+    n = n_kb;
     left = (int)min(exps_total(m) - at, (int64_t)1 << 30);
   }
-  SRA_DEV u32x4 load(int chunk) const {
+  SRA_DEV u32x4 load(int chunk) const {  // 127 (a scale of one) past the reduction's end
     const int o = 16 * chunk;
     u32x4 v;
     if (o + 16 <= left) {
       __builtin_memcpy(&v, p + o, 16);
     } else {  // the array's last bytes
-      uint32_t w[4] = {0, 0, 0, 0};
+      v = u32x4{0, 0, 0, 0};
 #pragma unroll 1
       for (int i = 0; i < 16 && o + i < left; ++i) {
         const uint32_t e = (uint32_t)p[o + i] << (8 * (i % 4));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] |= i / 4 == k ? e : 0u;
+        for (int k = 0; k < 4; ++k) v[k] |= i / 4 == k ? e : 0u;
       }
-      v = u32x4{w[0], w[1], w[2], w[3]};
+    }
+    if (o + 16 > n) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int keep = min(max(n - o - 4 * k, 0), 4);  // bytes of this dword inside the reduction
+        const uint32_t mask = keep == 4 ? ~0u : (1u << (8 * keep)) - 1u;
+        v[k] = (v[k] & mask) | (0x7f7f7f7fu & ~mask);
+      }
     }
     return v;
   }
@@ -339,7 +358,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tiles(Mat a, Mat b, Out
   };
   const int t = threadIdx.x;
   const bool has_row = t < BM + BN;
-  const ScaleRow sr(t < BM ? a : b, t < BM ? m0 + t : n0 + t - BM, k0);
+  const ScaleRow sr(t < BM ? a : b, t < BM ? m0 + t : n0 + t - BM, k0, n_kb);
   u32x4 sreg = {0, 0, 0, 0};
   auto put_scales = [&](int chunk) {  // sreg, loaded before, into the chunk's half
     if (has_row) {
@@ -445,115 +464,172 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tiles(Mat a, Mat b, Out
   store_tile<FM, FN>(acc, out, part, m0 + wm, n0 + wn);
 }
 
-// ---- 256 x 256 tiles by two groups of four waves that take turns: while one group's 32 matrix instructions a wave run
-// (1024 cycles), the other reads its next operands from LDS (96 KB, 768 cycles), so each SIMD's matrix unit always has
-// a wave to serve.  Phases alternate at barriers; group 0 reads stage k in phase 2 k and computes in 2 k + 1, group 1
-// one phase later.  Stage k + 1 goes where stage k - 1 was from phase 2 k on and has to be there by phase 2 k + 2.
+// ---- 256 x 256 tiles, four waves of 128 x 128, one to a SIMD: half the LDS traffic of eight waves of 128 x 64 (per 128
+// columns 128 KB read and 64 KB written, 1536 cycles of 128 bytes, beside 2048 cycles of matrix instructions).  A step's
+// 64 matrix instructions run in four quarters of 16; the operands of a quarter are read from LDS during the one before
+// it, so the matrix unit does not wait for LDS:
+//   a_lo b_lo (reads b_hi) | a_lo b_hi (reads a_hi) | barrier | a_hi b_lo (reads the next a_lo) | a_hi b_hi (the next b_lo)
+// At the barrier in the middle of step k stage k has been read by every wave and stage k + 1 is there; stage k + 2 then
+// goes into stage k's slot.  Rows are 128 bytes with chunk c at c ^ (position / 2 % 8), which spreads 16 rows over 64
+// banks; b's row 8 i + g of a wave's 128 lies at position 16 g + i, so a lane's 8 columns are neighbours in Out.
+//
+// The accumulators fill the 256 accumulation registers; left to itself the compiler keeps operands there too and spills
+// (186 registers), so the instruction is written out with its operands' classes.  It then does not know the
+// instruction's latency: every read of a result has 63 others between (or the wait at the end), and operands written
+// by vector instructions (scales) have a wait behind them.
+SRA_DEV void wait_states() {  // 32 of them, with nothing moved across
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
 template <int KA, int KB>
-__global__ __launch_bounds__(512, 2) void k_fp8_turns(Mat a, Mat b, Out out, int nm, int nn) {
-  constexpr int BM = 256, BN = 256, FM = 8, FN = 4, D = 4;  // D transfers of each operand per wave and stage
-  constexpr int kSlot = BM * kBlock;                        // a's two slots, then b's: all reads within 64 KB of a base
+SRA_DEV void mfma_acc(const Frag& x, const Frag& y, f32x4& c, uint32_t sx, uint32_t sy, int j) {
+#define SRA_MFMA_ACC(LO, HI)                                                                                             \
+  asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" LO "," LO ",0] op_sel_hi:[" HI "," HI ",0] cbsz:%5 blgp:%6" \
+      : "+a"(c)                                                                                                          \
+      : "v"(x.v), "v"(y.v), "v"(sx), "v"(sy), "n"(KA), "n"(KB))
+  if (j == 0) SRA_MFMA_ACC("0", "0");
+  else if (j == 1) SRA_MFMA_ACC("1", "0");
+  else if (j == 2) SRA_MFMA_ACC("0", "1");
+  else SRA_MFMA_ACC("1", "1");
+#undef SRA_MFMA_ACC
+}
+template <int KA, int KB>
+__global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int nm, int nn) {
+  constexpr int BM = 256, BN = 256, F = 8, D = 8;  // fragments a side, transfers of each operand per wave and stage
+  constexpr int kSlot = BM * kBlock;               // a's two slots, then b's: all reads within 64 KB of a base
   __shared__ __align__(1024) uint8_t smem[4 * kSlot];
   __shared__ __align__(16) uint8_t scal[2][(BM + BN) * kScaleLd];
-  const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), q = l >> 4, i16 = l & 15;
+  const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), q = l >> 4, i16 = l & 15;
   int tm, tn;
   tile_of(blockIdx.x, nm * nn, nm, nn, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const int wm = (w >> 2) * 128, wn = (w & 3) * 64;
+  const int wm = (w >> 1) * 128, wn = (w & 1) * 128;
   const int n_kb = (int)a.nblk, ld = (int)a.ld;
-  // A wave's transfer d fills rows 32 w + 8 d .. + 7; its resource starts at the first of them and ends with the matrix,
-  // so rows past the end read zeros.  b's key (row / 4) % 8 of those rows is 2 d + l / 32.
-  const int left_a = (int)min((int64_t)BM, a.rows - m0) - 32 * w, left_b = (int)min((int64_t)BN, b.rows - n0) - 32 * w;
-  const uint8_t *const ga = a.codes + (m0 + 32 * w) * a.ld, *const gb = b.codes + (n0 + 32 * w) * b.ld;
-  const uint32_t va = (uint32_t)((l >> 3) * ld) + 16 * ((l & 7) ^ (l >> 3));
-  const uint32_t vb = (uint32_t)((l >> 3) * ld) + 16 * ((l & 7) ^ (l >> 5));
-  auto issue = [&](int kb, int slot) {
-    if (kb >= n_kb) return;
-    const uint32_t st = lds_offset(smem) + slot * kSlot + 32 * kBlock * w;
+  const int left_a = (int)min((int64_t)BM, a.rows - m0), left_b = (int)min((int64_t)BN, b.rows - n0);
+  const uint8_t *const ga = a.codes + m0 * a.ld, *const gb = b.codes + n0 * b.ld;
+  uint32_t va[D], vb[D];  // rows past the end lie past the resource's size: they read zeros
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-      dma(rows_rsrc(ga + (int64_t)(8 * d) * ld, left_a - 8 * d, ld), st + 1024 * d, va, kb * kBlock);
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-      dma(rows_rsrc(gb + (int64_t)(8 * d) * ld, left_b - 8 * d, ld), st + 2 * kSlot + 1024 * d, vb ^ (32 * d),
-              kb * kBlock);
+  for (int d = 0; d < D; ++d) {
+    const int pos = 64 * w + 8 * d + (l >> 3), chunk = 16 * ((l & 7) ^ ((pos >> 1) & 7));
+    va[d] = (uint32_t)(pos * ld) + chunk;
+    vb[d] = (uint32_t)(((pos & 128) + 8 * (pos & 15) + ((pos >> 4) & 7)) * ld) + chunk;
+  }
+  const uint32_t lds = lds_offset(smem) + 64 * kBlock * w;
+  // transfer d of stage kb; past the last stage it reads zeros
+  auto fill_a = [&](int kb, int slot, int d) {
+    dma(rows_rsrc(ga, kb < n_kb ? left_a : 0, ld), lds + slot * kSlot + 1024 * d, va[d], kb * kBlock);
   };
-  const int t = threadIdx.x;
-  const ScaleRow sr(t < BM ? a : b, t < BM ? m0 + t : n0 + t - BM, 0);
-  auto put_scales = [&](int chunk, const u32x4& v) {
+  auto fill_b = [&](int kb, int slot, int d) {
+    dma(rows_rsrc(gb, kb < n_kb ? left_b : 0, ld), lds + (2 + slot) * kSlot + 1024 * d, vb[d], kb * kBlock);
+  };
+  const ScaleRow ra(a, m0 + t, 0, n_kb), rb(b, n0 + t, 0, n_kb);
+  u32x4 ca, cb;
+  auto put_scales = [&](int chunk) {
     uint32_t* const p = reinterpret_cast<uint32_t*>(scal[chunk & 1] + t * kScaleLd);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = v[i];
-  };
-  f32x4 acc[FM][FN];
-#pragma unroll
-  for (int f = 0; f < FM; ++f)
-#pragma unroll
-    for (int g = 0; g < FN; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const uint8_t* const pa = smem + (wm + i16) * kBlock + 16 * (q ^ (i16 & 7));
-  const uint8_t* const pb = smem + 2 * kSlot + (wn + FN * i16) * kBlock + 16 * (q ^ (i16 & 7));
-  const int other = (q ^ (i16 & 7)) & 4 ? -64 : 64;  // from chunk q ^ key to chunk (q + 4) ^ key
-  uint32_t sa[FM], sb[FN];
-  Frag fa[FM], fb[FN];
-  auto read = [&](int kb, int j) {
-    const int st = j % 2 * kSlot;
-#pragma unroll
-    for (int g = 0; g < FN; ++g) {
-      fb[g].h[0] = *reinterpret_cast<const u32x4*>(pb + st + g * kBlock);
-      fb[g].h[1] = *reinterpret_cast<const u32x4*>(pb + other + st + g * kBlock);
-    }
-#pragma unroll
-    for (int f = 0; f < FM; ++f) {
-      fa[f].h[0] = *reinterpret_cast<const u32x4*>(pa + st + 16 * f * kBlock);
-      fa[f].h[1] = *reinterpret_cast<const u32x4*>(pa + other + st + 16 * f * kBlock);
-    }
-    if (j == 0) {
-      const uint8_t* const sc = scal[(kb >> 4) & 1] + (kb & 12);
-#pragma unroll
-      for (int f = 0; f < FM; ++f) sa[f] = *reinterpret_cast<const uint32_t*>(sc + (wm + 16 * f + i16) * kScaleLd);
-#pragma unroll
-      for (int g = 0; g < FN; ++g) sb[g] = *reinterpret_cast<const uint32_t*>(sc + (BM + wn + FN * i16 + g) * kScaleLd);
+    for (int i = 0; i < 4; ++i) {
+      p[i] = ca[i];
+      p[BM * kScaleLd / 4 + i] = cb[i];
     }
   };
-  put_scales(0, sr.load(0));
-  issue(0, 0);
-  wait_vm<0>();
-  __syncthreads();
-  auto loop = [&](auto late_c) {
-    constexpr bool late = decltype(late_c)::value;
-    if (late) {  // phase 0
-      issue(1, 1);
-      ring_barrier();
+  const int key = (i16 >> 1) & 7, other = (q ^ key) & 4 ? -64 : 64;  // from chunk q ^ key to chunk (q + 4) ^ key
+  const uint8_t* const pa = smem + (wm + i16) * kBlock + 16 * (q ^ key);
+  const uint8_t* const pb = smem + 2 * kSlot + (wn + i16) * kBlock + 16 * (q ^ key);
+  Frag fa[F], fb[F];
+  auto read_a = [&](int slot, int f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) fa[f].h[h] = *reinterpret_cast<const u32x4*>(pa + h * other + slot * kSlot + 16 * f * kBlock);
+  };
+  auto read_b = [&](int slot, int g) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) fb[g].h[h] = *reinterpret_cast<const u32x4*>(pb + h * other + slot * kSlot + 16 * g * kBlock);
+  };
+  uint32_t sa[F], sb[F], na[F], nb[F];
+  auto read_scales = [&](int kb) {
+    const uint8_t* const sc = scal[(kb >> 4) & 1] + (kb & 12);
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      na[f] = *reinterpret_cast<const uint32_t*>(sc + (wm + 16 * f + i16) * kScaleLd);
+      nb[f] = *reinterpret_cast<const uint32_t*>(sc + (BM + wn + 8 * i16 + f) * kScaleLd);
     }
-    for (int kb = 0; kb < n_kb; kb += 4) {
-      // the next chunk of scales: its half was last read before this chunk began
-      if ((kb & 15) == 8 && (kb | 15) + 1 < n_kb) put_scales((kb >> 4) + 1, sr.load((kb >> 4) + 1));
+  };
+  f32x4 acc[F][F];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (kb + j >= n_kb) break;
-        if (!late) issue(kb + j + 1, (j + 1) % 2);
-        read(kb + j, j);
-        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this stage's slot is filled again after the next barriers
-        if (late) wait_vm<0>();
-        ring_barrier();
-        if (late) issue(kb + j + 2, j % 2);
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(1);
+  for (int f = 0; f < F; ++f)
 #pragma unroll
-        for (int f = 0; f < FM; ++f)
+    for (int g = 0; g < F; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // 16 matrix instructions on fragments f0 .. and g0 .., and after each two of them more(x), x = 0 .. 7
+  auto quarter = [&](int f0, int g0, int j, auto more) {
 #pragma unroll
-          for (int g = 0; g < FN; ++g) acc[f][g] = mfma<KA, KB>(fa[f], fb[g], acc[f][g], sa[f], sb[g], j);
-        __builtin_amdgcn_s_setprio(0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (!late) wait_vm<0>();
-        ring_barrier();
+    for (int x = 0; x < 8; ++x) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int f = f0 + x / 2, g = g0 + 2 * (x % 2) + y;
+        mfma_acc<KA, KB>(fa[f], fb[g], acc[f][g], sa[f], sb[g], j);
       }
+      more(x);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (!late) ring_barrier();
   };
-  if (w >= 4) loop(std::true_type{});  // waves 0-3 and 4-7: one of each group on every SIMD
-  else loop(std::false_type{});
-  store_tile<FM, FN>(acc, out, nullptr, m0 + wm, n0 + wn);
+  ca = ra.load(0);
+  cb = rb.load(0);
+  put_scales(0);
+#pragma unroll
+  for (int d = 0; d < D; ++d) fill_a(0, 0, d);
+#pragma unroll
+  for (int d = 0; d < D; ++d) fill_b(0, 0, d);
+#pragma unroll
+  for (int d = 0; d < D; ++d) fill_a(1, 1, d);
+#pragma unroll
+  for (int d = 0; d < D; ++d) fill_b(1, 1, d);
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  wait_vm<2 * D>();
+  ring_barrier();
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    read_a(0, x);
+    read_b(0, x);
+  }
+  read_scales(0);
+  // whole groups of four steps: stages past the last are zeros, under scales of one
+  for (int kb = 0; kb < n_kb; kb += 4) {
+    // the next chunk of scales: its half was last read before this chunk began
+    if ((kb & 15) == 4 && (kb | 15) + 1 < n_kb) {
+      ca = ra.load((kb >> 4) + 1);
+      cb = rb.load((kb >> 4) + 1);
+    }
+    if ((kb & 15) == 8 && (kb | 15) + 1 < n_kb) put_scales((kb >> 4) + 1);
+#pragma unroll
+    for (int f = 0; f < F; ++f) sa[f] = na[f], sb[f] = nb[f];
+    wait_states();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int slot = j % 2;
+      // a quarter's reads go out in its first half, so that they are back before the next begins
+      quarter(0, 0, j, [&](int x) {
+        if (x < 4) read_b(slot, 4 + x);
+      });
+      quarter(0, 4, j, [&](int x) {
+        if (x < 4) read_a(slot, 4 + x);
+      });
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+      wait_vm<0>();
+      ring_barrier();
+      quarter(4, 0, j, [&](int x) {
+        if (x < 4) read_a(1 - slot, x);  // after the last step: of no use
+        fill_a(kb + j + 2, slot, x);
+      });
+      quarter(4, 4, j, [&](int x) {
+        if (x < 4) read_b(1 - slot, x);
+        fill_b(kb + j + 2, slot, x);
+        if (j == 3 && x == 4) read_scales(kb + 4);
+      });
+    }
+  }
+  wait_vm<0>();  // no transfer may be under way when the workgroup's LDS is given up
+  wait_states();  // the last matrix instructions' results
+  store_tile<F, F>(acc, out, nullptr, m0 + wm, n0 + wn);
 }
 
 // sum of the splits' partial products, in order
@@ -622,7 +698,7 @@ static hipError_t matmul(const Mat& a, const Mat& b, const Out& out, const Plan&
     SRA_TILES(128, 128, 2, 2, 2);
   } else if constexpr (!EX) {
     const int nm = (int)((out.M + 255) / 256), nn = (int)((out.N + 255) / 256);
-    launch(SRA_KERNEL_FP8_MM, k_fp8_turns<KA, KB>, dim3((unsigned)(nm * nn)), dim3(512), 0, s, a, b, out, nm, nn);
+    launch(SRA_KERNEL_FP8_MM, k_fp8_big<KA, KB>, dim3((unsigned)(nm * nn)), dim3(256), 0, s, a, b, out, nm, nn);
   }
 #undef SRA_TILES
   hipError_t err = hipGetLastError();
