@@ -240,50 +240,53 @@ SRA_DEV void tile_of(int bid, int n, int nm, int nn, int& tm, int& tn) {
   tn = in / gs;
 }
 
-// acc[f][g][v]: row m0 + 16 f + 4 q + v, column n0 + FN (l % 16) + g of Out, or of this split's fp32 partial product
-template <int FM, int FN>
-SRA_DEV void store_tile(const f32x4 (&acc)[FM][FN], const Out& out, float* part, int64_t m0, int64_t n0) {
+// acc[g][v]: row m0 + 4 q + v, column n0 + FN (l % 16) + g of Out, or of this split's fp32 partial product
+template <int FN, bool F32>
+SRA_DEV void store_row16(const f32x4 (&acc)[FN], void* o, const Out& out, int64_t m0, int64_t n0) {
   static_assert(FN % 4 == 0, "stores of four columns");
   const int l = threadIdx.x & 63, q = l >> 4, i16 = l & 15;
-  const bool f32 = part || out.f32;
-  float* const fo = part ? part + (int64_t)blockIdx.y * out.M * out.N : (float*)out.p;
-  uint16_t* const ho = (uint16_t*)out.p;
   const int64_t n = n0 + FN * i16;
 #pragma unroll
-  for (int f = 0; f < FM; ++f)
+  for (int v = 0; v < 4; ++v) {
+    const int64_t m = m0 + 4 * q + v, at = m * out.N + n;
+    const int have = m < out.M ? (int)min(max(out.N - n, (int64_t)0), (int64_t)FN) : 0;  // columns inside
+    if constexpr (F32) {
+      float* const p = (float*)o + at;
+      if (have == FN && out.N % 4 == 0) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t m = m0 + 16 * f + 4 * q + v;
-      if (m >= out.M) continue;
-      if (FN == 8 && !f32 && out.N % 8 == 0) {
-        if (n >= out.N) continue;
-        union { __bf16 h[8]; u32x4 w; } o;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o.h[k] = (__bf16)acc[f][k % FN][v];
-        *reinterpret_cast<u32x4*>(ho + m * out.N + n) = o.w;
-      } else if (out.N % 4 == 0) {
-#pragma unroll
-        for (int g = 0; g < FN; g += 4) {
-          if (n + g >= out.N) continue;
-          if (f32) {
-            *reinterpret_cast<f32x4*>(fo + m * out.N + n + g) =
-                f32x4{acc[f][g][v], acc[f][g + 1][v], acc[f][g + 2][v], acc[f][g + 3][v]};
-          } else {
-            union { __bf16 h[4]; u32x2 w; } o;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o.h[k] = (__bf16)acc[f][g + k][v];
-            *reinterpret_cast<u32x2*>(ho + m * out.N + n + g) = o.w;
-          }
-        }
+        for (int g = 0; g < FN; g += 4)
+          *reinterpret_cast<f32x4*>(p + g) = f32x4{acc[g][v], acc[g + 1][v], acc[g + 2][v], acc[g + 3][v]};
       } else {
 #pragma unroll
-        for (int g = 0; g < FN; ++g) {
-          if (n + g >= out.N) continue;
-          if (f32) fo[m * out.N + n + g] = acc[f][g][v];
-          else store_out(out, m, n + g, acc[f][g][v]);
-        }
+        for (int g = 0; g < FN; ++g)
+          if (g < have) p[g] = acc[g][v];
+      }
+    } else {
+      union { __bf16 h[FN]; uint16_t e[FN]; u32x2 w[FN / 4]; u32x4 x[(FN + 7) / 8]; } c;
+#pragma unroll
+      for (int g = 0; g < FN; ++g) c.h[g] = (__bf16)acc[g][v];
+      uint16_t* const p = (uint16_t*)o + at;
+      if (have == FN && out.N % FN == 0) {
+        if constexpr (FN == 8) __builtin_nontemporal_store(c.x[0], reinterpret_cast<u32x4*>(p));
+        else *reinterpret_cast<u32x2*>(p) = c.w[0];
+      } else {
+#pragma unroll
+        for (int g = 0; g < FN; ++g)
+          if (g < have) p[g] = c.e[g];
       }
     }
+  }
+}
+template <int FM, int FN>
+SRA_DEV void store_tile(const f32x4 (&acc)[FM][FN], const Out& out, float* part, int64_t m0, int64_t n0) {
+  if (part || out.f32) {
+    void* const o = part ? part + (int64_t)blockIdx.y * out.M * out.N : out.p;
+#pragma unroll
+    for (int f = 0; f < FM; ++f) store_row16<FN, true>(acc[f], o, out, m0 + 16 * f, n0);
+  } else {
+#pragma unroll
+    for (int f = 0; f < FM; ++f) store_row16<FN, false>(acc[f], out.p, out, m0 + 16 * f, n0);
+  }
 }
 
 // Scales of a tile's rows, 16 blocks at a time: thread t keeps row t (a's BM rows, then b's BN)
@@ -475,25 +478,48 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tiles(Mat a, Mat b, Out
 //
 // The accumulators fill the 256 accumulation registers; left to itself the compiler keeps operands there too and spills
 // (186 registers), so the instruction is written out with its operands' classes.  It then does not know the
-// instruction's latency: every read of a result has 63 others between (or the wait at the end), and operands written
+// instruction's latency: every read of a result has 62 others between (or the wait at the end), and operands written
 // by vector instructions (scales) have a wait behind them.
 SRA_DEV void wait_states() {  // 32 of them, with nothing moved across
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
+#define SRA_MFMA_TEXT(C, X, Y, SX, SY, LO, HI) \
+  "v_mfma_scale_f32_16x16x128_f8f6f4 " C ", " X ", " Y ", " C ", " SX ", " SY " op_sel:[" LO "," LO ",0] op_sel_hi:[" HI "," HI ",0] cbsz:%8 blgp:%9"
+// two matrix instructions on one fragment of a and two of b
 template <int KA, int KB>
-SRA_DEV void mfma_acc(const Frag& x, const Frag& y, f32x4& c, uint32_t sx, uint32_t sy, int j) {
-#define SRA_MFMA_ACC(LO, HI)                                                                                             \
-  asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" LO "," LO ",0] op_sel_hi:[" HI "," HI ",0] cbsz:%5 blgp:%6" \
-      : "+a"(c)                                                                                                          \
-      : "v"(x.v), "v"(y.v), "v"(sx), "v"(sy), "n"(KA), "n"(KB))
-  if (j == 0) SRA_MFMA_ACC("0", "0");
-  else if (j == 1) SRA_MFMA_ACC("1", "0");
-  else if (j == 2) SRA_MFMA_ACC("0", "1");
-  else SRA_MFMA_ACC("1", "1");
-#undef SRA_MFMA_ACC
+SRA_DEV void mfma_pair(const Frag& x, const Frag& y0, const Frag& y1, f32x4& c0, f32x4& c1, uint32_t sx, uint32_t sy0,
+                       uint32_t sy1, int j) {
+#define SRA_PAIR(LO, HI)                                                                                            \
+  asm(SRA_MFMA_TEXT("%0", "%2", "%3", "%5", "%6", LO, HI) "\n\t" SRA_MFMA_TEXT("%1", "%2", "%4", "%5", "%7", LO, HI) \
+      : "+a"(c0), "+a"(c1)                                                                                          \
+      : "v"(x.v), "v"(y0.v), "v"(y1.v), "v"(sx), "v"(sy0), "v"(sy1), "n"(KA), "n"(KB))
+  if (j == 0) SRA_PAIR("0", "0");
+  else if (j == 1) SRA_PAIR("1", "0");
+  else if (j == 2) SRA_PAIR("0", "1");
+  else SRA_PAIR("1", "1");
+#undef SRA_PAIR
 }
+// The same with a transfer behind them, M0 set in front: the second instruction starts 8 wait states after the first, which
+// covers what M0 and scalar registers written by vector instructions need before the transfer reads them.
+template <int KA, int KB>
+SRA_DEV void mfma_pair_dma(const Frag& x, const Frag& y0, const Frag& y1, f32x4& c0, f32x4& c1, uint32_t sx, uint32_t sy0,
+                           uint32_t sy1, int j, const dma_rsrc_t& rs, uint32_t block, int more, uint32_t off, int soff) {
+#define SRA_PAIR(LO, HI)                                                                                               \
+  asm volatile("s_add_u32 m0, %10, %11\n\t" SRA_MFMA_TEXT("%0", "%2", "%3", "%5", "%6", LO, HI) "\n\t"                 \
+               SRA_MFMA_TEXT("%1", "%2", "%4", "%5", "%7", LO, HI) "\n\tbuffer_load_dwordx4 %12, %13, %14 offen lds"   \
+               : "+a"(c0), "+a"(c1)                                                                                    \
+               : "v"(x.v), "v"(y0.v), "v"(y1.v), "v"(sx), "v"(sy0), "v"(sy1), "n"(KA), "n"(KB), "s"(block), "i"(more), \
+                 "v"(off), "s"(rs), "s"(soff)                                                                          \
+               : "memory", "scc")
+  if (j == 0) SRA_PAIR("0", "0");
+  else if (j == 1) SRA_PAIR("1", "0");
+  else if (j == 2) SRA_PAIR("0", "1");
+  else SRA_PAIR("1", "1");
+#undef SRA_PAIR
+}
+#undef SRA_MFMA_TEXT
 template <int KA, int KB>
 __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int nm, int nn) {
   constexpr int BM = 256, BN = 256, F = 8, D = 8;  // fragments a side, transfers of each operand per wave and stage
@@ -501,13 +527,25 @@ __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int n
   __shared__ __align__(1024) uint8_t smem[4 * kSlot];
   __shared__ __align__(16) uint8_t scal[2][(BM + BN) * kScaleLd];
   const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), q = l >> 4, i16 = l & 15;
-  int tm, tn;
-  tile_of(blockIdx.x, nm * nn, nm, nn, tm, tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int wm = (w >> 1) * 128, wn = (w & 1) * 128;
-  const int n_kb = (int)a.nblk, ld = (int)a.ld;
-  const int left_a = (int)min((int64_t)BM, a.rows - m0), left_b = (int)min((int64_t)BN, b.rows - n0);
-  const uint8_t *const ga = a.codes + m0 * a.ld, *const gb = b.codes + n0 * b.ld;
+  const int n_kb = (int)a.nblk, n_steps = (n_kb + 3) & ~3, n_chunks = (n_steps + 15) >> 4, ld = (int)a.ld;
+  const int tiles = nm * nn;
+  struct Tile {
+    int64_t m0, n0;
+    const uint8_t *ga, *gb;
+    int left_a, left_b;  // rows of the operands that are there; none past the last tile
+  };
+  auto tile_at = [&](int id) {
+    int tm, tn;
+    tile_of(min(id, tiles - 1), tiles, nm, nn, tm, tn);
+    Tile x;
+    x.m0 = (int64_t)tm * BM, x.n0 = (int64_t)tn * BN;
+    x.ga = a.codes + x.m0 * a.ld, x.gb = b.codes + x.n0 * b.ld;
+    x.left_a = id < tiles ? (int)min((int64_t)BM, a.rows - x.m0) : 0;
+    x.left_b = id < tiles ? (int)min((int64_t)BN, b.rows - x.n0) : 0;
+    return x;
+  };
+  Tile cur = tile_at(blockIdx.x), nxt = tile_at(blockIdx.x + gridDim.x);
   uint32_t va[D], vb[D];  // rows past the end lie past the resource's size: they read zeros
 #pragma unroll
   for (int d = 0; d < D; ++d) {
@@ -516,17 +554,28 @@ __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int n
     vb[d] = (uint32_t)(((pos & 128) + 8 * (pos & 15) + ((pos >> 4) & 7)) * ld) + chunk;
   }
   const uint32_t lds = lds_offset(smem) + 64 * kBlock * w;
-  // transfer d of stage kb; past the last stage it reads zeros
-  auto fill_a = [&](int kb, int slot, int d) {
-    dma(rows_rsrc(ga, kb < n_kb ? left_a : 0, ld), lds + slot * kSlot + 1024 * d, va[d], kb * kBlock);
+  // where step s comes from: zeros from the reduction's end to the group's, then the next tile's first stages
+  struct Source {
+    dma_rsrc_t a, b;
+    int off;
   };
-  auto fill_b = [&](int kb, int slot, int d) {
-    dma(rows_rsrc(gb, kb < n_kb ? left_b : 0, ld), lds + (2 + slot) * kSlot + 1024 * d, vb[d], kb * kBlock);
+  auto source = [&](int s) {
+    const bool on = s >= n_steps;
+    Source x;
+    x.a = rows_rsrc(on ? nxt.ga : cur.ga, on ? nxt.left_a : s < n_kb ? cur.left_a : 0, ld);
+    x.b = rows_rsrc(on ? nxt.gb : cur.gb, on ? nxt.left_b : s < n_kb ? cur.left_b : 0, ld);
+    x.off = (on ? s - n_steps : s) * kBlock;
+    return x;
   };
-  const ScaleRow ra(a, m0 + t, 0, n_kb), rb(b, n0 + t, 0, n_kb);
+  auto fill_a = [&](const Source& x, int slot, int d) { dma(x.a, lds + slot * kSlot + 1024 * d, va[d], x.off); };
+  auto fill_b = [&](const Source& x, int slot, int d) { dma(x.b, lds + (2 + slot) * kSlot + 1024 * d, vb[d], x.off); };
   u32x4 ca, cb;
-  auto put_scales = [&](int chunk) {
-    uint32_t* const p = reinterpret_cast<uint32_t*>(scal[chunk & 1] + t * kScaleLd);
+  auto load_scales = [&](const Tile& x, int chunk) {
+    ca = ScaleRow(a, x.m0 + t, 0, n_kb).load(chunk);
+    cb = ScaleRow(b, x.n0 + t, 0, n_kb).load(chunk);
+  };
+  auto put_scales = [&](int half) {
+    uint32_t* const p = reinterpret_cast<uint32_t*>(scal[half] + t * kScaleLd);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       p[i] = ca[i];
@@ -546,8 +595,8 @@ __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int n
     for (int h = 0; h < 2; ++h) fb[g].h[h] = *reinterpret_cast<const u32x4*>(pb + h * other + slot * kSlot + 16 * g * kBlock);
   };
   uint32_t sa[F], sb[F], na[F], nb[F];
-  auto read_scales = [&](int kb) {
-    const uint8_t* const sc = scal[(kb >> 4) & 1] + (kb & 12);
+  auto read_scales = [&](int half, int kb) {
+    const uint8_t* const sc = scal[half] + (kb & 12);
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       na[f] = *reinterpret_cast<const uint32_t*>(sc + (wm + 16 * f + i16) * kScaleLd);
@@ -555,34 +604,42 @@ __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int n
     }
   };
   f32x4 acc[F][F];
-#pragma unroll
-  for (int f = 0; f < F; ++f)
-#pragma unroll
-    for (int g = 0; g < F; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
   // 16 matrix instructions on fragments f0 .. and g0 .., and after each two of them more(x), x = 0 .. 7
   auto quarter = [&](int f0, int g0, int j, auto more) {
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int f = f0 + x / 2, g = g0 + 2 * (x % 2) + y;
-        mfma_acc<KA, KB>(fa[f], fb[g], acc[f][g], sa[f], sb[g], j);
-      }
+      const int f = f0 + x / 2, g = g0 + 2 * (x % 2);
+      mfma_pair<KA, KB>(fa[f], fb[g], fb[g + 1], acc[f][g], acc[f][g + 1], sa[f], sb[g], sb[g + 1], j);
       more(x);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  ca = ra.load(0);
-  cb = rb.load(0);
+  // the same with one transfer of a stage behind each two: of a's (part 0) or b's (part 2)
+  auto quarter_fill = [&](int f0, int g0, int j, const Source& from, int part, int slot, auto more) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int f = f0 + x / 2, g = g0 + 2 * (x % 2);
+      if (part == 0)
+        mfma_pair_dma<KA, KB>(fa[f], fb[g], fb[g + 1], acc[f][g], acc[f][g + 1], sa[f], sb[g], sb[g + 1], j, from.a, lds,
+                              slot * kSlot + 1024 * x, va[x], from.off);
+      else
+        mfma_pair_dma<KA, KB>(fa[f], fb[g], fb[g + 1], acc[f][g], acc[f][g + 1], sa[f], sb[g], sb[g + 1], j, from.b, lds,
+                              (2 + slot) * kSlot + 1024 * x, vb[x], from.off);
+      more(x);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int half = 0;  // where the current chunk of scales lies
+  load_scales(cur, 0);
   put_scales(0);
 #pragma unroll
-  for (int d = 0; d < D; ++d) fill_a(0, 0, d);
+  for (int s = 0; s < 2; ++s) {
+    const Source from = source(s);
 #pragma unroll
-  for (int d = 0; d < D; ++d) fill_b(0, 0, d);
+    for (int d = 0; d < D; ++d) fill_a(from, s, d);
 #pragma unroll
-  for (int d = 0; d < D; ++d) fill_a(1, 1, d);
-#pragma unroll
-  for (int d = 0; d < D; ++d) fill_b(1, 1, d);
+    for (int d = 0; d < D; ++d) fill_b(from, s, d);
+  }
   __builtin_amdgcn_s_waitcnt(0xc07f);
   wait_vm<2 * D>();
   ring_barrier();
@@ -591,45 +648,63 @@ __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int n
     read_a(0, x);
     read_b(0, x);
   }
-  read_scales(0);
-  // whole groups of four steps: stages past the last are zeros, under scales of one
-  for (int kb = 0; kb < n_kb; kb += 4) {
-    // the next chunk of scales: its half was last read before this chunk began
-    if ((kb & 15) == 4 && (kb | 15) + 1 < n_kb) {
-      ca = ra.load((kb >> 4) + 1);
-      cb = rb.load((kb >> 4) + 1);
-    }
-    if ((kb & 15) == 8 && (kb | 15) + 1 < n_kb) put_scales((kb >> 4) + 1);
+  read_scales(0, 0);
 #pragma unroll
-    for (int f = 0; f < F; ++f) sa[f] = na[f], sb[f] = nb[f];
-    wait_states();
+  for (int f = 0; f < F; ++f)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int slot = j % 2;
-      // a quarter's reads go out in its first half, so that they are back before the next begins
-      quarter(0, 0, j, [&](int x) {
-        if (x < 4) read_b(slot, 4 + x);
-      });
-      quarter(0, 4, j, [&](int x) {
-        if (x < 4) read_a(slot, 4 + x);
-      });
-      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-      wait_vm<0>();
-      ring_barrier();
-      quarter(4, 0, j, [&](int x) {
-        if (x < 4) read_a(1 - slot, x);  // after the last step: of no use
-        fill_a(kb + j + 2, slot, x);
-      });
-      quarter(4, 4, j, [&](int x) {
-        if (x < 4) read_b(1 - slot, x);
-        fill_b(kb + j + 2, slot, x);
-        if (j == 3 && x == 4) read_scales(kb + 4);
-      });
+    for (int g = 0; g < F; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int id = blockIdx.x; id < tiles; id += gridDim.x) {
+    // whole groups of four steps: stages past the reduction's end are zeros, under scales of one
+    for (int kb = 0; kb < n_steps; kb += 4) {
+      // the next chunk of scales (this tile's, or the next tile's first) is fetched in a chunk's first group and put down
+      // in its last; its half was last read before this chunk began
+      const bool first = (kb & 15) == 0, last = (kb & 15) == 12 || kb + 4 == n_steps;
+      if (first) {
+        const int c = (kb >> 4) + 1;
+        if (c < n_chunks) load_scales(cur, c);
+        else load_scales(nxt, 0);
+      }
+      if (last) put_scales(half ^ 1);
+#pragma unroll
+      for (int f = 0; f < F; ++f) sa[f] = na[f], sb[f] = nb[f];
+      wait_states();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int slot = j % 2;
+        const Source from = source(kb + j + 2);
+        // a quarter's reads go out in its first half, so that they are back before the next begins
+        quarter(0, 0, j, [&](int x) {
+          if (x < 4) read_b(slot, 4 + x);
+        });
+        quarter(0, 4, j, [&](int x) {
+          if (x < 4) read_a(slot, 4 + x);
+        });
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+        wait_vm<0>();
+        ring_barrier();
+        quarter_fill(4, 0, j, from, 0, slot, [&](int x) {
+          if (x < 4) read_a(1 - slot, x);
+        });
+        quarter_fill(4, 4, j, from, 2, slot, [&](int x) {
+          if (x < 4) read_b(1 - slot, x);
+          if (j == 3 && x == 4) read_scales(last ? half ^ 1 : half, last ? 0 : kb + 4);
+        });
+      }
+      if (last) half ^= 1;
     }
+    wait_states();  // the last matrix instructions' results
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      store_row16<F, false>(acc[f], out.p, out, cur.m0 + wm + 16 * f, cur.n0 + wn);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int g = 0; g < F; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    cur = nxt;
+    nxt = tile_at(id + 2 * gridDim.x);
   }
   wait_vm<0>();  // no transfer may be under way when the workgroup's LDS is given up
-  wait_states();  // the last matrix instructions' results
-  store_tile<F, F>(acc, out, nullptr, m0 + wm, n0 + wn);
 }
 
 // sum of the splits' partial products, in order
@@ -698,7 +773,7 @@ static hipError_t matmul(const Mat& a, const Mat& b, const Out& out, const Plan&
     SRA_TILES(128, 128, 2, 2, 2);
   } else if constexpr (!EX) {
     const int nm = (int)((out.M + 255) / 256), nn = (int)((out.N + 255) / 256);
-    launch(SRA_KERNEL_FP8_MM, k_fp8_big<KA, KB>, dim3((unsigned)(nm * nn)), dim3(256), 0, s, a, b, out, nm, nn);
+    launch(SRA_KERNEL_FP8_MM, k_fp8_big<KA, KB>, dim3((unsigned)std::min(nm * nn, 256)), dim3(256), 0, s, a, b, out, nm, nn);
   }
 #undef SRA_TILES
   hipError_t err = hipGetLastError();
