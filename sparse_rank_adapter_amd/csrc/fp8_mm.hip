@@ -131,32 +131,36 @@ SRA_DEV void store_out(const Out& o, int64_t m, int64_t n, float v) {
 }
 
 // ---- few rows of a (up to 16 MT): b streams once from memory into registers.
-// A workgroup owns 16 rows of b; its waves share the reduction in contiguous parts and join in LDS.
-template <int KA, int KB, int MT, int NW, bool EX>
+// A workgroup owns 16 RT rows of b; its waves take groups of four blocks of the reduction in turn, so that together they
+// read on along the rows, and join in LDS.  a comes from the caches: RT row tiles share what a wave loads of it.
+template <int KA, int KB, int MT, int RT, int NW, bool EX>
 __global__ __launch_bounds__(64 * NW) void k_fp8_few(Mat a, Mat b, Out out) {
-  __shared__ float red[NW][MT * 256];
+  __shared__ float red[NW][RT * MT * 256];
   const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int64_t nrow = min(n0 + (l & 15), b.rows - 1);
-  const uint8_t* const bp = b.codes + nrow * b.ld + 16 * q;
-  const uint8_t* ap[MT];
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+  const uint8_t *bp[RT], *ap[MT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) bp[r] = b.codes + min(n0 + 16 * r + (l & 15), b.rows - 1) * b.ld + 16 * q;
 #pragma unroll
   for (int f = 0; f < MT; ++f) ap[f] = a.codes + min((int64_t)(16 * f + (l & 15)), a.rows - 1) * a.ld + 16 * q;
-  f32x4 acc[MT];
+  f32x4 acc[RT][MT];
 #pragma unroll
-  for (int f = 0; f < MT; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint32_t poison = 0;  // EX: scales of 255 met, bit v for row 4 q + v of b, bit 4 + f for a's
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int f = 0; f < MT; ++f) acc[r][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint32_t poison = 0;  // EX: scales of 255 met, bit 4 r + v for row 16 r + 4 q + v of b, bit 4 RT + f for a's
   const int64_t ta = exps_total(a), tb = exps_total(b);
   const bool whole = ta >= 4 && tb >= 4;
   constexpr int SB = EX ? 4 : 1;  // b's rows whose scales a lane holds: those of its results, or that of its operand
-  const int64_t lo = b.nblk * w / NW, hi = b.nblk * (w + 1) / NW;
-  for (int64_t kb = lo; kb < hi; kb += 4) {
-    Frag fb[4], fa[4][MT];
-    uint32_t sa[MT], sb[SB];
-    const int left = (int)min(hi - kb, (int64_t)4);
+  for (int64_t kb = 4 * w; kb < b.nblk; kb += 4 * NW) {
+    Frag fb[4][RT], fa[4][MT];
+    uint32_t sa[MT], sb[RT][SB];
+    const int left = (int)min(b.nblk - kb, (int64_t)4);
     const auto scales = [&](bool ok) {
 #pragma unroll
-      for (int v = 0; v < SB; ++v) sb[v] = scales4(b, EX ? n0 + 4 * q + v : nrow, kb, tb, ok);
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int v = 0; v < SB; ++v) sb[r][v] = scales4(b, n0 + 16 * r + (EX ? 4 * q + v : l & 15), kb, tb, ok);
 #pragma unroll
       for (int f = 0; f < MT; ++f) sa[f] = scales4(a, 16 * f + (l & 15), kb, ta, ok);
     };
@@ -164,9 +168,12 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_few(Mat a, Mat b, Out out) {
     else scales(false);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t at = (kb + min(j, left - 1)) * kBlock;  // past the part's end: a block that is read anyway
-      fb[j].h[0] = *reinterpret_cast<const u32x4*>(bp + at);
-      fb[j].h[1] = *reinterpret_cast<const u32x4*>(bp + at + 64);
+      const int64_t at = (kb + min(j, left - 1)) * kBlock;  // past the row's end: a block that is read anyway
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        fb[j][r].h[0] = *reinterpret_cast<const u32x4*>(bp[r] + at);
+        fb[j][r].h[1] = *reinterpret_cast<const u32x4*>(bp[r] + at + 64);
+      }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -182,36 +189,44 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_few(Mat a, Mat b, Out out) {
       if (j >= left) continue;
       if constexpr (!EX) {
 #pragma unroll
-        for (int f = 0; f < MT; ++f) acc[f] = mfma<KB, KA>(fb[j], fa[j][f], acc[f], sb[0], sa[f], j);
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int f = 0; f < MT; ++f) acc[r][f] = mfma<KB, KA>(fb[j][r], fa[j][f], acc[r][f], sb[r][0], sa[f], j);
       } else {
-        const Wide wb = widen<KB>(fb[j]);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) poison |= byte_of(sb[v], j) == 255 ? 1u << v : 0u;
+        for (int f = 0; f < MT; ++f) poison |= byte_of(sa[f], j) == 255 ? 1u << (4 * RT + f) : 0u;
 #pragma unroll
-        for (int f = 0; f < MT; ++f) {
-          const f32x4 p = mfma_wide(wb, widen<KA>(fa[j][f]));
-          const int ea = byte_of(sa[f], j);
-          poison |= ea == 255 ? 16u << f : 0u;
+        for (int r = 0; r < RT; ++r) {
+          const Wide wb = widen<KB>(fb[j][r]);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[f][v] += __builtin_amdgcn_ldexpf(p[v], byte_of(sb[v], j) + ea - 254);
+          for (int v = 0; v < 4; ++v) poison |= byte_of(sb[r][v], j) == 255 ? 1u << (4 * r + v) : 0u;
+#pragma unroll
+          for (int f = 0; f < MT; ++f) {
+            const f32x4 p = mfma_wide(wb, widen<KA>(fa[j][f]));
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              acc[r][f][v] += __builtin_amdgcn_ldexpf(p[v], byte_of(sb[r][v], j) + byte_of(sa[f], j) - 254);
+          }
         }
       }
     }
   }
-  // acc[f][v]: row 16 f + l % 16 of a, row n0 + 4 q + v of b
+  // acc[r][f][v]: row 16 f + l % 16 of a, row n0 + 16 r + 4 q + v of b
 #pragma unroll
-  for (int f = 0; f < MT; ++f)
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (EX && (poison & (1u << v | 16u << f))) acc[f][v] = __uint_as_float(0x7fc00000u);
-      red[w][f * 256 + (l & 15) * 16 + 4 * q + v] = acc[f][v];
-    }
+    for (int f = 0; f < MT; ++f)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (EX && (poison & (1u << (4 * r + v) | 1u << (4 * RT + f)))) acc[r][f][v] = __uint_as_float(0x7fc00000u);
+        red[w][(16 * f + (l & 15)) * (16 * RT) + 16 * r + 4 * q + v] = acc[r][f][v];
+      }
   __syncthreads();
-  for (int i = threadIdx.x; i < MT * 256; i += 64 * NW) {
+  for (int i = threadIdx.x; i < RT * MT * 256; i += 64 * NW) {
     float s = red[0][i];
 #pragma unroll
     for (int k = 1; k < NW; ++k) s += red[k][i];
-    const int64_t m = i >> 4, n = n0 + (i & 15);
+    const int64_t m = i / (16 * RT), n = n0 + i % (16 * RT);
     if (m < out.M && n < out.N) store_out(out, m, n, s);
   }
 }
@@ -718,46 +733,76 @@ __global__ __launch_bounds__(256) void k_fp8_join(const float* __restrict__ part
 }
 
 // ---- the choice of kernel
+// Row tiles of b per workgroup with few rows of a.  More of them share a's loads, fewer spread better over the 256 CUs: the
+// estimate is the tiles of the busiest CU, a quarter more where a workgroup has a single one.  9216 x 36864 by 16 rows
+// (2304 tiles): three 70 us, two 78, one 88.
+int few_tiles(int64_t N, int mt) {
+  const int64_t tiles = (N + 15) / 16;
+  int best = 1;
+  int64_t cost = 5 * ((tiles + 255) / 256);
+  for (int r = 2; r <= (mt == 1 ? 3 : 2); ++r) {
+    const int64_t c = 4 * r * ((tiles + 256 * r - 1) / (256 * r));
+    if (c <= cost) best = r, cost = c;
+  }
+  return best;
+}
 enum { kFew, kBig, kMid, kSmall };
 struct Plan {
   int kernel;
   int splits;
 };
-Plan plan_of(int64_t M, int64_t N, int64_t nblk) {
-  if (M <= 64) return {kFew, 1};
-  const auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 256) return {kBig, 1};  // (EX: the middle tiles, whose accumulators leave room for the widened codes)
-  if (tiles(128, 128) >= 192) return {kMid, 1};
-  const int64_t t = tiles(64, 128);
+// Up to 32 rows of a: b streams.  Else the tiles with the least estimated time, in units of 10 ns, from what a step of 128
+// columns was measured to take on the busiest CU: 256 x 256 tiles 1.55 us; 128 x 128 tiles 0.72 us alone on a CU (a ring of
+// four stages), 1.39 us for two at once (of two stages); 64 x 64 tiles 0.40 us alone, 0.53 us for two.  Where the small
+// tiles are few they split the reduction, at least 4 blocks a split, and a second launch (3 us) joins the parts.
+// Against it, at 512 x 5120 x 20480: 160 large tiles 64 us, 640 middle ones 96; 128 x 5120 x 20480: 160 middle tiles 36 us,
+// 640 small ones 42; 2047 x 4096 x 1024: 512 small tiles 17 us, 128 middle ones 24.
+Plan plan_of(int64_t M, int64_t N, int64_t nblk, bool ex) {
+  if (M <= 32) return {kFew, 1};
+  const auto tiles = [&](int64_t side) { return ((M + side - 1) / side) * ((N + side - 1) / side); };
+  const auto rounds = [](int64_t t, int64_t one, int64_t two) {  // two workgroups a CU
+    const int64_t r = t % 512;
+    return t / 512 * two + (r == 0 ? 0 : r <= 256 ? one : two);
+  };
+  const int64_t big = (tiles(256) + 255) / 256 * 155 * ((nblk + 3) / 4 * 4), mid = rounds(tiles(128), 72, 139) * nblk;
+  const int64_t t = tiles(64);
   int s = 1;
-  while (t * s < 192 && nblk >= 8 * s) s *= 2;  // at least 4 blocks a split
-  return {kSmall, s};
+  while (t * s < 192 && nblk >= 8 * s) s *= 2;
+  const int64_t small = rounds(t * s, 40, 53) * ((nblk + s - 1) / s) + (s > 1 ? 300 : 0);
+  if (!ex && big < mid && big < small) return {kBig, 1};
+  return mid <= small ? Plan{kMid, 1} : Plan{kSmall, s};
 }
 
 }  // namespace
 
 namespace sra {
 
-size_t fp8_matmul_ws(int64_t M, int64_t N, int64_t K) {
+static size_t ws_of(int64_t M, int64_t N, int64_t K, bool ex) {
   if (M <= 0 || N <= 0) return 0;
-  const Plan p = plan_of(M, N, blocks_of(K));
+  const Plan p = plan_of(M, N, blocks_of(K), ex);
   return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(float) : 0;
 }
+
+// enough for either type of the result
+size_t fp8_matmul_ws(int64_t M, int64_t N, int64_t K) { return std::max(ws_of(M, N, K, false), ws_of(M, N, K, true)); }
 
 template <int KA, int KB, bool EX>
 static hipError_t matmul(const Mat& a, const Mat& b, const Out& out, const Plan& p, float* ws, hipStream_t s) {
   if (p.kernel == kFew) {
-    const dim3 grid((unsigned)((out.N + 15) / 16));
-    const bool wide = grid.x < 1024;  // few workgroups: more waves share the reduction
-    const int mt = (int)((out.M + 15) / 16);
-#define SRA_FEW(MT)                                                                                                   \
-  do {                                                                                                                \
-    if (wide) launch(SRA_KERNEL_FP8_MM, k_fp8_few<KA, KB, MT, 8, EX>, grid, dim3(512), 0, s, a, b, out);              \
-    else launch(SRA_KERNEL_FP8_MM, k_fp8_few<KA, KB, MT, 4, EX>, grid, dim3(256), 0, s, a, b, out);                   \
-  } while (0)
-    if (mt <= 1) SRA_FEW(1);
-    else if (mt == 2) SRA_FEW(2);
-    else SRA_FEW(4);
+    const int mt = (int)((out.M + 15) / 16), rt = EX ? 1 : few_tiles(out.N, mt);
+#define SRA_FEW(MT, RT, NW)                                                                                              \
+  launch(SRA_KERNEL_FP8_MM, k_fp8_few<KA, KB, MT, RT, NW, EX>, dim3((unsigned)((out.N + 16 * RT - 1) / (16 * RT))), dim3(64 * NW), \
+         0, s, a, b, out)
+    if (mt <= 1) {
+      if (rt == 1) SRA_FEW(1, 1, 8);
+      else if constexpr (!EX) {
+        if (rt == 2) SRA_FEW(1, 2, 4);
+        else SRA_FEW(1, 3, 4);
+      }
+    } else {
+      if (rt == 1) SRA_FEW(2, 1, 8);
+      else if constexpr (!EX) SRA_FEW(2, 2, 4);
+    }
 #undef SRA_FEW
     return hipGetLastError();
   }
@@ -768,9 +813,11 @@ static hipError_t matmul(const Mat& a, const Mat& b, const Out& out, const Plan&
            dim3(64 * WM * WN), 0, s, a, b, out, nm, nn, p.splits > 1 ? ws : nullptr);                               \
   } while (0)
   if (p.kernel == kSmall) {
-    SRA_TILES(64, 128, 2, 2, 2);
-  } else if (EX || p.kernel == kMid) {
+    SRA_TILES(64, 64, 4, 1, 4);
+  } else if (EX || (p.kernel == kMid && ((out.M + 127) / 128) * ((out.N + 127) / 128) > 256)) {
     SRA_TILES(128, 128, 2, 2, 2);
+  } else if (p.kernel == kMid) {
+    SRA_TILES(128, 128, 2, 2, 4);
   } else if constexpr (!EX) {
     const int nm = (int)((out.M + 255) / 256), nn = (int)((out.N + 255) / 256);
     launch(SRA_KERNEL_FP8_MM, k_fp8_big<KA, KB>, dim3((unsigned)std::min(nm * nn, 256)), dim3(256), 0, s, a, b, out, nm, nn);
@@ -789,9 +836,10 @@ hipError_t launch_fp8_matmul(const Fp8Operand& x, const Fp8Operand& y, int64_t M
                              void* o, void* ws, hipStream_t s) {
   if (M <= 0 || N <= 0) return hipSuccess;
   const int64_t nblk = blocks_of(K);
-  const Plan p = plan_of(M, N, nblk);
-  // a launch has fewer than 2^32 threads: at most 2^22 tiles of 128 x 128 or more, by rows of a (N < 2^26)
-  const int64_t rows = p.kernel == kBig ? ((int64_t)1 << 20) / ((N + 127) / 128) * 256 : M;
+  const Plan p = plan_of(M, N, nblk, out_f32);
+  // a launch has fewer than 2^32 threads: at most 2^23 tiles of 256 each, by rows of a in whole blocks (N < 2^26)
+  const int64_t side = p.kernel == kSmall ? 64 : 128;
+  const int64_t rows = p.kernel == kFew ? M : std::max<int64_t>(256, ((int64_t)1 << 23) / ((N + side - 1) / side) * side & ~(int64_t)255);
   for (int64_t m0 = 0; m0 < M; m0 += rows) {
     // m0 is a multiple of 256: whole blocks of exponents
     const Mat a{x.codes + m0 * nblk * kBlock, x.exps + (x.block_rows == 1 ? m0 : m0 / 128) * nblk, std::min(rows, M - m0),
