@@ -22,47 +22,30 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef double f64x2 __attribute__((ext_vector_type(2)));
 
 SRA_DEV f64x4 mfma(double a, double b, f64x4 c) { return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0); }
+// (Kernels are bound to two waves a SIMD at least: with a wave's 512 registers allowed the compiler keeps accumulators in
+// accumulation registers and copies them to and fro in every step.)
 SRA_DEV int drow(int q, int v) { return 4 * v + q; }  // row of a result's element v in lane group q
 
-// N consecutive elements at p, `left` of which are inside the row (VEC: aligned, and a whole vector is in or out)
+// N consecutive elements at base + at, `left` of which are inside the row (VEC: aligned, and a whole vector is in or out); zeros
+// past it.  No branch: what is outside is read from the matrix's first elements, so that loads go out together.
 template <int N, bool VEC, typename E>
-SRA_DEV void load_n(const E* __restrict__ p, int64_t left, float (&f)[N]) {
-#pragma unroll
-  for (int k = 0; k < N; ++k) f[k] = 0.f;
-  if constexpr (VEC && sizeof(E) == 4 && N == 4) {
-    if (left > 0) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(p);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) f[k] = v[k];
-    }
-  } else if constexpr (VEC && sizeof(E) == 4) {
-    if (left > 0) {
-      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-      f[0] = __uint_as_float(v[0]), f[1] = __uint_as_float(v[1]);
-    }
-  } else if constexpr (VEC) {
-    if (left > 0) {
-      uint32_t w[N / 2];
-      if constexpr (N == 4) {
-        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-        w[0] = v[0], w[1] = v[1];
-      } else {
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
-      }
-#pragma unroll
-      for (int k = 0; k < N / 2; ++k) {
-        f[2 * k] = __uint_as_float(w[k] << 16);
-        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-      }
-    }
+SRA_DEV void load_n(const E* __restrict__ base, int64_t at, int64_t left, float (&f)[N]) {
+  union { E e[N]; uint32_t w[(N * sizeof(E) + 3) / 4]; u32x2 d; u32x4 q; } c;
+  if constexpr (VEC) {
+    const E* const p = base + (left > 0 ? at : 0);
+    if constexpr (N * sizeof(E) == 16) c.q = *reinterpret_cast<const u32x4*>(p);
+    else if constexpr (N * sizeof(E) == 8) c.d = *reinterpret_cast<const u32x2*>(p);
+    else c.w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else {
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (k < left) {
-        float one[1];
-        RowVec<E, 1>::load(p + k, one);
-        f[k] = one[0];
-      }
+    for (int k = 0; k < N; ++k) c.e[k] = base[k < left ? at + k : 0];
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    float v;
+    if constexpr (sizeof(E) == 4) v = c.e[k];
+    else v = bf16_to_f32(c.e[k]);
+    f[k] = (VEC ? left > 0 : k < left) ? v : 0.f;
   }
 }
 template <int N, bool VEC, typename E>
@@ -101,14 +84,14 @@ struct GramArgs {
 template <typename E, bool TALL, bool VEC>
 struct GramBlock {  // a block of 32 rows of X over a chunk of 16 columns, as the lane's operands
   float f[2][4];
-  SRA_DEV void load(const E* __restrict__ G, int64_t L, int d, int row0, int64_t chunk, int64_t end) {
+  SRA_DEV void load(const E* __restrict__ G, int64_t L, int d, int row0, int64_t chunk) {
     const int l = threadIdx.x & 63, q = l >> 4, i = l & 15;
     if constexpr (!TALL) {  // rows row0 + 16 x + i; columns 16 chunk + 4 q + j
       const int64_t k = chunk * 16 + 4 * q;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int row = row0 + 16 * x + i;
-        load_n<4, VEC, E>(G + (int64_t)row * L + k, row < d ? min(end, L) - k : 0, f[x]);
+        load_n<4, VEC, E>(G, (int64_t)row * L + k, row < d ? L - k : 0, f[x]);
       }
     } else {  // rows row0 + 2 i + x; columns 16 chunk + 4 j + q
 #pragma unroll
@@ -116,7 +99,7 @@ struct GramBlock {  // a block of 32 rows of X over a chunk of 16 columns, as th
         const int64_t k = chunk * 16 + 4 * j + q;
         const int row = row0 + 2 * i;
         float two[2];
-        load_n<2, VEC, E>(G + k * d + row, k < min(end, L) ? d - row : 0, two);
+        load_n<2, VEC, E>(G, k * d + row, k < L ? d - row : 0, two);
         f[0][j] = two[0], f[1][j] = two[1];
       }
     }
@@ -125,7 +108,7 @@ struct GramBlock {  // a block of 32 rows of X over a chunk of 16 columns, as th
 };
 
 template <typename E, bool TALL, bool VEC>
-__global__ __launch_bounds__(256) void k_orth_gram(GramArgs g) {
+__global__ __launch_bounds__(256, 2) void k_orth_gram(GramArgs g) {
   __shared__ double red[4][32 * 33];
   const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i = l & 15;
   int bi = 0, pair = blockIdx.x;  // pairs (bi, bj), bj <= bi, row after row
@@ -141,33 +124,47 @@ __global__ __launch_bounds__(256) void k_orth_gram(GramArgs g) {
     for (int y = 0; y < 2; ++y) acc[x][y] = f64x4{0., 0., 0., 0.};
   using B = GramBlock<E, TALL, VEC>;
   B a, b, an, bn;
-  const bool diag = bi == bj;
-  int64_t c = c0 + w;
-  if (c < c1) {
-    a.load(G, g.L, g.d, 32 * bi, c, g.L);
-    if (!diag) b.load(G, g.L, g.d, 32 * bj, c, g.L);
-  }
-  for (; c < c1; c += 4) {
-    if (c + 4 < c1) {
-      an.load(G, g.L, g.d, 32 * bi, c + 4, g.L);
-      if (!diag) bn.load(G, g.L, g.d, 32 * bj, c + 4, g.L);
-    }
-    if (diag) b = a;
+  // the next chunk's loads go out before this one's products; past the slice the last chunk again, not used
+  const auto sum = [&](const B& x, const B& y, bool diag) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) acc[x][y] = mfma((double)a.f[x][j], (double)b.f[y][j], acc[x][y]);
-    a = an;
-    b = bn;
+        for (int r = 0; r < 2; ++r)
+          if (!diag || r <= p) acc[p][r] = mfma((double)x.f[p][j], (double)y.f[r][j], acc[p][r]);
+  };
+  int64_t c = c0 + w;
+  if (bi == bj) {
+    if (c < c1) a.load(G, g.L, g.d, 32 * bi, c);
+    for (; c < c1; c += 4) {
+      an.load(G, g.L, g.d, 32 * bi, min(c + 4, c1 - 1));
+      sum(a, a, true);
+      a = an;
+    }
+  } else {
+    if (c < c1) {
+      a.load(G, g.L, g.d, 32 * bi, c);
+      b.load(G, g.L, g.d, 32 * bj, c);
+    }
+    for (; c < c1; c += 4) {
+      an.load(G, g.L, g.d, 32 * bi, min(c + 4, c1 - 1));
+      bn.load(G, g.L, g.d, 32 * bj, min(c + 4, c1 - 1));
+      sum(a, b, false);
+      a = an;
+      b = bn;
+    }
   }
 #pragma unroll
   for (int x = 0; x < 2; ++x)
 #pragma unroll
     for (int y = 0; y < 2; ++y)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) red[w][B::at(x, drow(q, v)) * 33 + B::at(y, i)] = acc[x][y][v];
+      for (int v = 0; v < 4; ++v) {
+        const int r = B::at(x, drow(q, v)), c = B::at(y, i);
+        if (bi != bj || y <= x) red[w][r * 33 + c] = acc[x][y][v];
+        if (bi == bj && y < x) red[w][c * 33 + r] = acc[x][y][v];  // a diagonal block's fourth tile mirrors this one
+      }
   __syncthreads();
   double* const out = g.part + (((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * g.S + blockIdx.y) * 1024;
   for (int e = threadIdx.x; e < 1024; e += 256) {
@@ -175,13 +172,23 @@ __global__ __launch_bounds__(256) void k_orth_gram(GramArgs g) {
     out[e] = (red[0][at] + red[1][at]) + (red[2][at] + red[3][at]);
   }
 }
-SRA_DEV double gram_at(const double* part, int S, int r, int c) {  // element (r, c) of A_0 from the slices, in order
+// A_0 [n][D][D] from the slices, in order, zeros past d (D = 16: a corner of the only block)
+__global__ __launch_bounds__(256) void k_orth_join(const double* __restrict__ part, int S, int D, double* __restrict__ A) {
+  const int t = (D + 31) / 32, pairs = t * (t + 1) / 2;
+  const int e = blockIdx.x * 256 + threadIdx.x, r = e / D, c = e % D;
   const int hi = max(r, c), lo = min(r, c), bi = hi >> 5, bj = lo >> 5;
   // inside a diagonal block both triangles are there, equal up to rounding: take the lower
-  const double* p = part + ((int64_t)(bi * (bi + 1) / 2 + bj) * S) * 1024 + (hi & 31) * 32 + (lo & 31);
+  const double* p = part + ((int64_t)(blockIdx.y * pairs + bi * (bi + 1) / 2 + bj) * S) * 1024 + (hi & 31) * 32 + (lo & 31);
+  constexpr int U = 8;  // loads in flight
   double s = 0.;
-  for (int k = 0; k < S; ++k) s += p[(int64_t)k * 1024];
-  return s;
+  for (int k = 0; k < S; k += U) {
+    double v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = p[(int64_t)min(k + u, S - 1) * 1024];
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += k + u < S ? v[u] : 0.;
+  }
+  A[(int64_t)blockIdx.y * D * D + e] = s;
 }
 
 struct Steps {
@@ -189,8 +196,9 @@ struct Steps {
   int n;
 };
 
-// ---- d <= 64: all steps of one matrix in one workgroup, its matrices in LDS.  Wave w owns the 16 x 16 tile
-// (w / T, w % T) of every product.  Rows are D + 4 doubles apart, so 16 rows x 4 columns spread over the banks.
+// ---- d <= 64: all steps of one matrix in one workgroup, its matrices in LDS.  All of them are symmetric (polynomials of
+// A_0): wave w owns one 16 x 16 tile on or below the diagonal of every product and writes it on both sides.  Rows are
+// D + 4 doubles apart, so 16 rows x 4 columns spread over the banks.
 template <int D>
 SRA_DEV f64x4 lds_mm(const double* A, const double* B, int ti, int tj) {  // tile (ti, tj) of A B, B symmetric
   constexpr int LD = D + 4;
@@ -202,62 +210,64 @@ SRA_DEV f64x4 lds_mm(const double* A, const double* B, int ti, int tj) {  // til
   return acc;
 }
 template <int D>
-__global__ __launch_bounds__(D * D / 4) void k_orth_small(const double* __restrict__ part, int S, int d, Steps st,
-                                                          double* __restrict__ Q) {
-  constexpr int LD = D + 4, T = D / 16;
+__global__ __launch_bounds__(64 * (D / 16) * (D / 16 + 1) / 2, 2) void k_orth_small(const double* __restrict__ A0, int d, Steps st,
+                                                                              double* __restrict__ Q) {
+  constexpr int LD = D + 4, NT = 64 * (D / 16) * (D / 16 + 1) / 2;
   __shared__ double lds[4 * D * LD];
   double *const A = lds, *const P = A + D * LD, *const W = P + D * LD, *const X = W + D * LD;
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i = l & 15, ti = w / T, tj = w % T;
-  constexpr int pairs = (D / 32) * (D / 32 + 1) / 2;
-  part += (int64_t)blockIdx.x * pairs * S * 1024;
-  for (int e = threadIdx.x; e < D * D; e += blockDim.x) A[(e / D) * LD + e % D] = gram_at(part, S, e / D, e % D);
-  __syncthreads();
+  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i = l & 15;
+  int ti = 0, tj = w;  // tiles (ti, tj), tj <= ti, row after row
+  while (tj > ti) tj -= ++ti;
+  A0 += (int64_t)blockIdx.x * D * D;
   double tr = 0.;
-  for (int k = 0; k < d; ++k) tr += A[k * LD + k];
+  for (int k = l; k < d; k += 64) tr += A0[k * (D + 1)];
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) tr += __shfl_xor(tr, m, 64);
   const double s = 1. / (sqrt(tr) + st.eps);
-  __syncthreads();
-  for (int e = threadIdx.x; e < D * D; e += blockDim.x) A[(e / D) * LD + e % D] *= s * s;
+  for (int e = threadIdx.x; e < D * D; e += NT) A[(e / D) * LD + e % D] = A0[e] * (s * s);
   __syncthreads();
   const int col = 16 * tj + i;
+  const auto put = [&](double* M, const f64x4& v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = 16 * ti + drow(q, k);
+      M[row * LD + col] = v[k];
+      if (ti != tj) M[col * LD + row] = v[k];
+    }
+  };
   for (int k = 0; k < st.n; ++k) {
     f64x4 p = lds_mm<D>(A, A, ti, tj);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int row = 16 * ti + drow(q, v);
       p[v] = (row == col ? st.a : 0.) + st.b * A[row * LD + col] + st.c * p[v];
-      P[row * LD + col] = p[v];
     }
+    put(P, p);
     __syncthreads();
     f64x4 x = p;
     if (k > 0) x = lds_mm<D>(P, X, ti, tj);
     if (k + 1 == st.n) {
       double* const o = Q + (int64_t)blockIdx.x * D * D;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) o[(16 * ti + drow(q, v)) * D + col] = s * x[v];
+      for (int v = 0; v < 4; ++v) {
+        const int row = 16 * ti + drow(q, v);
+        o[row * D + col] = s * x[v];
+        if (ti != tj) o[col * D + row] = s * x[v];
+      }
       break;
     }
-    const f64x4 t = lds_mm<D>(P, A, ti, tj);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) W[(16 * ti + drow(q, v)) * LD + col] = t[v];
+    put(W, lds_mm<D>(P, A, ti, tj));
     __syncthreads();  // P A is there, and A and X have been read
     const f64x4 n = lds_mm<D>(P, W, ti, tj);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      A[(16 * ti + drow(q, v)) * LD + col] = n[v];
-      X[(16 * ti + drow(q, v)) * LD + col] = x[v];
-    }
+    put(A, n);
+    put(X, x);
     __syncthreads();
   }
 }
 
-// ---- d > 64: A_0 from its slices, then every product of a step as a launch of its own, 32 x 32 of the result a
-// workgroup (one workgroup would take 14 us a product at d = 128, its CU's share of the fp64 rate).
-__global__ __launch_bounds__(256) void k_orth_join(const double* __restrict__ part, int S, int D, double* __restrict__ A) {
-  const int pairs = (D / 32) * (D / 32 + 1) / 2;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  A[(int64_t)blockIdx.y * D * D + e] =
-      gram_at(part + (int64_t)blockIdx.y * pairs * S * 1024, S, (int)(e / D), (int)(e % D));
-}
+// ---- d > 64: every product of a step as a launch of its own (one workgroup would take 14 us a product at d = 128, its CU's
+// share of the fp64 rate).  A workgroup has a 16 x 16 tile on or below the diagonal and writes it on both sides, its waves a quarter of the reduction each, all of whose
+// operands are loaded at once: a launch is bound by that latency.
 // job z: C_z = u I + v A_z + w (A_z B_z), B_z symmetric; u, v and w are multiplied by the powers pu, pv and pw
 // of s = 1 / (sqrt(trace of `norm`) + eps)
 struct MmJob {
@@ -269,51 +279,61 @@ struct MmJob {
 struct MmArgs {
   MmJob job[2];
   const double* norm;
-  int D, d;
+  int D, d, n;
   double eps;
 };
-__global__ __launch_bounds__(256) void k_orth_mm(MmArgs g) {
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i = l & 15, D = g.D, T = D / 32;
-  const int mat = blockIdx.y, r0 = 32 * (blockIdx.x / T) + 16 * (w >> 1), c0 = 32 * (blockIdx.x % T) + 16 * (w & 1);
-  const MmJob& j = g.job[blockIdx.z];
+__global__ __launch_bounds__(256, 2) void k_orth_mm(MmArgs g) {
+  __shared__ double part[4][256], scale;
+  const int t = threadIdx.x, l = t & 63, w = t >> 6, q = l >> 4, i = l & 15, D = g.D, KW = D / 4;
+  // the matrix in the low digits: with eight of them (or 16, ...) each stays on one XCD, whose L2 holds it
+  const int mat = blockIdx.x % g.n;
+  int ti = 0, tj = blockIdx.x / g.n;  // tiles (ti, tj), tj <= ti, row after row
+  while (tj > ti) tj -= ++ti;
+  const int r0 = 16 * ti, c0 = 16 * tj;
+  const MmJob& j = g.job[blockIdx.y];
   const int64_t at = (int64_t)mat * D * D;
-  double s = 1.;
-  if (j.pu | j.pv | j.pw) {
+  const double *const pa = j.A + at + (int64_t)(r0 + i) * D + KW * w + 2 * q, *const pb = j.B + at + (int64_t)(c0 + i) * D + KW * w + 2 * q;
+  f64x2 a[8], b[8];  // KW <= 64: everything the wave needs, in flight at once
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int k8 = min(8 * k, KW - 8);  // past the end: not used
+    a[k] = *reinterpret_cast<const f64x2*>(pa + k8);
+    b[k] = *reinterpret_cast<const f64x2*>(pb + k8);
+  }
+  const int row = r0 + (t >> 4), col = c0 + (t & 15);  // this thread's element of the result
+  const double own = j.v != 0. ? j.A[at + (int64_t)row * D + col] : 0.;
+  if ((j.pu | j.pv | j.pw) && w == 0) {
     double tr = 0.;
     for (int k = l; k < g.d; k += 64) tr += g.norm[at + (int64_t)k * (D + 1)];
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) tr += __shfl_xor(tr, m, 64);
-    s = 1. / (sqrt(tr) + g.eps);
+    if (l == 0) scale = 1. / (sqrt(tr) + g.eps);
   }
   f64x4 acc = {0., 0., 0., 0.};
-  const double *pa = j.A + at + (int64_t)(r0 + i) * D + 4 * q, *pb = j.B + at + (int64_t)(c0 + i) * D + 4 * q;
-#pragma unroll 4
-  for (int k = 0; k < D; k += 16) {
-    const f64x2 a0 = *reinterpret_cast<const f64x2*>(pa + k), a1 = *reinterpret_cast<const f64x2*>(pa + k + 2);
-    const f64x2 b0 = *reinterpret_cast<const f64x2*>(pb + k), b1 = *reinterpret_cast<const f64x2*>(pb + k + 2);
-    acc = mfma(a0[0], b0[0], acc);
-    acc = mfma(a0[1], b0[1], acc);
-    acc = mfma(a1[0], b1[0], acc);
-    acc = mfma(a1[1], b1[1], acc);
-  }
-  double u = j.u, v = j.v, wt = j.w;
-  for (int k = 0; k < j.pu; ++k) u *= s;
-  for (int k = 0; k < j.pv; ++k) v *= s;
-  for (int k = 0; k < j.pw; ++k) wt *= s;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int row = r0 + drow(q, e), col = c0 + i;
-    double o = wt * acc[e];
-    if (j.v != 0.) o += v * j.A[at + (int64_t)row * D + col];
-    if (row == col) o += u;
-    j.C[at + (int64_t)row * D + col] = o;
+  for (int k = 0; k < 8; ++k) {
+    if (8 * k < KW) {
+      acc = mfma(a[k][0], b[k][0], acc);
+      acc = mfma(a[k][1], b[k][1], acc);
+    }
   }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) part[w][drow(q, v) * 16 + i] = acc[v];
+  __syncthreads();
+  double u = j.u, v = j.v, wt = j.w;
+  for (int k = 0; k < j.pu; ++k) u *= scale;
+  for (int k = 0; k < j.pv; ++k) v *= scale;
+  for (int k = 0; k < j.pw; ++k) wt *= scale;
+  const double sum = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
+  const double r = wt * sum + v * own + (row == col ? u : 0.);
+  j.C[at + (int64_t)row * D + col] = r;
+  if (ti != tj) j.C[at + (int64_t)col * D + row] = r;
 }
 
 // ---- O = Q X.  A wave owns 16 FR rows of Q against 64 columns of X (rows of the tall matrix); the waves of a
 // workgroup take neighbouring rows of Q, so they share X in the CU's cache.  Q [n][D][D] is symmetric.
 template <typename E, bool TALL, bool VEC, int FR>
-__global__ __launch_bounds__(256) void k_orth_apply(const double* __restrict__ Q, const E* __restrict__ G, int64_t L, int d,
+__global__ __launch_bounds__(256, 2) void k_orth_apply(const double* __restrict__ Q, const E* __restrict__ G, int64_t L, int d,
                                                     int D, E* __restrict__ O) {
   const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i = l & 15;
   const int nrb = (d + 16 * FR - 1) / (16 * FR);
@@ -329,37 +349,43 @@ __global__ __launch_bounds__(256) void k_orth_apply(const double* __restrict__ Q
   for (int x = 0; x < FR; ++x)
 #pragma unroll
     for (int g = 0; g < 4; ++g) acc[x][g] = f64x4{0., 0., 0., 0.};
-  for (int k0 = 0; k0 < d; k0 += 16) {
-    double a[FR][4];  // Q's rows: wide r0 + 16 x + i, tall r0 + FR i + x; columns k0 + 4 q + j
+  struct Step {  // the operands of 16 of the reduction
+    f64x2 a[FR][2];  // Q's rows: wide r0 + 16 x + i, tall r0 + FR i + x; columns k0 + 4 q ..
+    float f[4][4];   // wide f[j][g] = X[k0 + 4 q + j][cb + 4 i + g]; tall f[g][j] = G[cb + 16 g + i][k0 + 4 q + j]
+  };
+  const auto load = [&](int k0, Step& s) {
 #pragma unroll
     for (int x = 0; x < FR; ++x) {
       const double* p = Q + (int64_t)(r0 + (TALL ? FR * i + x : 16 * x + i)) * D + k0 + 4 * q;
-      const f64x2 lo = *reinterpret_cast<const f64x2*>(p), hi = *reinterpret_cast<const f64x2*>(p + 2);
-      a[x][0] = lo[0], a[x][1] = lo[1], a[x][2] = hi[0], a[x][3] = hi[1];
+      s.a[x][0] = *reinterpret_cast<const f64x2*>(p);
+      s.a[x][1] = *reinterpret_cast<const f64x2*>(p + 2);
     }
-    float f[4][4];
-    if constexpr (!TALL) {  // f[j][g] = X[k0 + 4 q + j][cb + 4 i + g]
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = k0 + 4 * q + j;
-        load_n<4, VEC, E>(G + (int64_t)k * L + cb + 4 * i, k < d ? L - cb - 4 * i : 0, f[j]);
-      }
-    } else {  // f[g][j] = X[cb + 16 g + i][k0 + 4 q + j], X as it lies, L x d
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int64_t c = cb + 16 * g + i;
-        load_n<4, VEC, E>(G + c * d + k0 + 4 * q, c < L ? d - k0 - 4 * q : 0, f[g]);
+    for (int y = 0; y < 4; ++y) {
+      if constexpr (!TALL) {
+        const int k = k0 + 4 * q + y;
+        load_n<4, VEC, E>(G, (int64_t)k * L + cb + 4 * i, k < d ? L - cb - 4 * i : 0, s.f[y]);
+      } else {
+        const int64_t c = cb + 16 * y + i;
+        load_n<4, VEC, E>(G, c * d + k0 + 4 * q, c < L ? d - k0 - 4 * q : 0, s.f[y]);
       }
     }
+  };
+  Step cur, nxt;
+  load(0, cur);
+  for (int k0 = 0; k0 < d; k0 += 16) {
+    load(min(k0 + 16, (d - 1) & ~15), nxt);  // the last time: not used
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int x = 0; x < FR; ++x)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          if constexpr (!TALL) acc[x][g] = mfma(a[x][j], (double)f[j][g], acc[x][g]);
-          else acc[x][g] = mfma((double)f[g][j], a[x][j], acc[x][g]);
+          const double a = cur.a[x][j / 2][j % 2];
+          if constexpr (!TALL) acc[x][g] = mfma(a, (double)cur.f[j][g], acc[x][g]);
+          else acc[x][g] = mfma((double)cur.f[g][j], a, acc[x][g]);
         }
+    cur = nxt;
   }
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
@@ -388,7 +414,7 @@ int slices_of(int64_t n, int pairs, int64_t L) {
   const int64_t chunks = (L + 15) / 16;
   return (int)std::max<int64_t>(1, std::min<int64_t>(chunks / 8, 512 / std::max<int64_t>(1, n * pairs)));
 }
-int dim_of(int64_t d) { return (int)((d + 31) / 32 * 32); }
+int dim_of(int64_t d) { return d <= 16 ? 16 : (int)((d + 31) / 32 * 32); }
 struct Layout {
   int d, D, pairs, S;
   int64_t L;
@@ -399,7 +425,7 @@ Layout layout_of(int64_t n, int64_t rows, int64_t cols) {
   y.d = (int)std::min(rows, cols);
   y.L = std::max(rows, cols);
   y.D = dim_of(y.d);
-  const int t = y.D / 32;
+  const int t = (y.D + 31) / 32;
   y.pairs = t * (t + 1) / 2;
   y.S = slices_of(n, y.pairs, y.L);
   y.part = (size_t)n * y.pairs * y.S * 1024 * sizeof(double);
@@ -412,11 +438,11 @@ Layout layout_of(int64_t n, int64_t rows, int64_t cols) {
 namespace sra {
 
 bool orth_ok(int64_t rows, int64_t cols) { return std::min(rows, cols) <= 256; }
-// slices of the Gram matrix, Q, and above d = 64 also the Gram matrix, A twice, P, P A and a second Q
+// slices of the Gram matrix, the Gram matrix, Q, and above d = 64 also A twice, P, P A and a second Q
 size_t orth_ws(int64_t n, int64_t rows, int64_t cols) {
   if (n <= 0 || rows <= 0 || cols <= 0) return 0;
   const Layout y = layout_of(n, rows, cols);
-  return y.part + y.mat * (y.D <= 64 ? 1 : 7);
+  return y.part + y.mat * (y.D <= 64 ? 2 : 7);
 }
 
 template <typename E, bool TALL>
@@ -428,19 +454,21 @@ static hipError_t orth(const E* G, int64_t n, const Layout& y, const Steps& st, 
   const dim3 gg((unsigned)y.pairs, (unsigned)y.S, (unsigned)n);
   if (TALL ? y.d % 2 == 0 : y.L % 4 == 0) launch(SRA_KERNEL_ORTH, k_orth_gram<E, TALL, true>, gg, dim3(256), 0, s, g);
   else launch(SRA_KERNEL_ORTH, k_orth_gram<E, TALL, false>, gg, dim3(256), 0, s, g);
-  const double* Q = m0;
-  if (y.D == 32) {
-    hipLaunchKernelGGL(k_orth_small<32>, dim3((unsigned)n), dim3(256), 0, s, part, y.S, y.d, st, m0);
+  double* const a0 = m0;
+  double* q0 = m0 + me;
+  hipLaunchKernelGGL(k_orth_join, dim3((unsigned)(y.D * y.D / 256), (unsigned)n), dim3(256), 0, s, part, y.S, y.D, a0);
+  if (y.D == 16) {
+    hipLaunchKernelGGL(k_orth_small<16>, dim3((unsigned)n), dim3(64), 0, s, a0, y.d, st, q0);
+  } else if (y.D == 32) {
+    hipLaunchKernelGGL(k_orth_small<32>, dim3((unsigned)n), dim3(192), 0, s, a0, y.d, st, q0);
   } else if (y.D == 64) {
-    hipLaunchKernelGGL(k_orth_small<64>, dim3((unsigned)n), dim3(1024), 0, s, part, y.S, y.d, st, m0);
+    hipLaunchKernelGGL(k_orth_small<64>, dim3((unsigned)n), dim3(640), 0, s, a0, y.d, st, q0);
   } else {
-    double *q0 = m0, *q1 = m0 + me, *const a0 = m0 + 2 * me, *a = m0 + 3 * me, *an = m0 + 4 * me, *const p = m0 + 5 * me,
-           *const w = m0 + 6 * me;
-    hipLaunchKernelGGL(k_orth_join, dim3((unsigned)(y.D * y.D / 256), (unsigned)n), dim3(256), 0, s, part, y.S, y.D, a0);
-    const unsigned tiles = (unsigned)((y.D / 32) * (y.D / 32));
+    double *q1 = m0 + 2 * me, *a = m0 + 3 * me, *an = m0 + 4 * me, *const p = m0 + 5 * me, *const w = m0 + 6 * me;
+    const unsigned tiles = (unsigned)(y.D / 16 * (y.D / 16 + 1) / 2);
     MmArgs m{};
-    m.norm = a0, m.D = y.D, m.d = y.d, m.eps = st.eps;
-    const auto run = [&](unsigned jobs) { hipLaunchKernelGGL(k_orth_mm, dim3(tiles, (unsigned)n, jobs), dim3(256), 0, s, m); };
+    m.norm = a0, m.D = y.D, m.d = y.d, m.n = (int)n, m.eps = st.eps;
+    const auto run = [&](unsigned jobs) { hipLaunchKernelGGL(k_orth_mm, dim3(tiles * (unsigned)n, jobs), dim3(256), 0, s, m); };
     const double* cur = a0;  // A of this step; the first is A_0 itself, with the norm's powers in the factors
     for (int k = 0; k < st.n; ++k) {
       const bool first = k == 0, last = k + 1 == st.n;
@@ -460,9 +488,10 @@ static hipError_t orth(const E* G, int64_t n, const Layout& y, const Steps& st, 
       std::swap(a, an);
       cur = a;
     }
-    Q = q0;
   }
-  const int fr = y.d <= 16 ? 1 : 2;
+  const double* const Q = q0;
+  // 32 rows of Q a wave, or 16 where that leaves fewer than 1024 waves
+  const int fr = y.d <= 16 || n * ((y.L + 63) / 64) * ((y.d + 31) / 32) < 1024 ? 1 : 2;
   const int nrb = (y.d + 16 * fr - 1) / (16 * fr);
   const int64_t jobs = (y.L + 63) / 64 * nrb;
   const dim3 ga((unsigned)((jobs + 3) / 4), (unsigned)n);
