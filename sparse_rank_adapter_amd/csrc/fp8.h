@@ -151,6 +151,35 @@ SRA_DEV void store_row(E* __restrict__ p, int64_t left, const float (&f)[VEC]) {
     }
   }
 }
+// The same in two steps, for loads that are to be in flight together: as stored (of what lies outside, the first elements
+// of the row), and as floats with zeros outside
+template <typename E, int VEC>
+struct Stored {
+  union { E e[VEC]; u32x4 q[VEC * sizeof(E) / 16 + 1]; };
+};
+template <typename E, int VEC>
+SRA_DEV Stored<E, VEC> fetch(const E* __restrict__ row, int64_t c, int64_t len) {
+  Stored<E, VEC> o;
+  if constexpr (VEC == 8) {
+    const E* const p = row + (c < len ? c : 0);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(E) / 2; ++i) o.q[i] = reinterpret_cast<const u32x4*>(p)[i];
+  } else {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) o.e[k] = row[c + k < len ? c + k : 0];
+  }
+  return o;
+}
+template <typename E, int VEC>
+SRA_DEV void as_floats(const Stored<E, VEC>& s, int64_t left, float (&f)[VEC]) {
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) {
+    float v;
+    if constexpr (sizeof(E) == 4) v = s.e[k];
+    else v = bf16_to_f32(s.e[k]);
+    f[k] = (VEC == 8 ? left > 0 : k < left) ? v : 0.f;
+  }
+}
 inline bool vec8(int64_t len) { return len % 8 == 0; }
 
 }  // namespace sra_f8
