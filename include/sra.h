@@ -579,6 +579,9 @@ sra_status sra_orthogonalize(const void* G, int32_t dtype, int64_t n, int64_t ro
  *   SRA_TUNE_DECODE_ROWS   decode workgroup row tiles of 16 rows: 3, 4 or 9 (0 = the planner's)
  *   SRA_TUNE_ROWS_SLICES   reduction slices of the rank > 32 U / dU kernel (0 = the planner's)
  *   SRA_TUNE_GRADS_SLICES  token slices of the dA / dB kernel (0 = the planner's)
+ *   SRA_TUNE_FP8_TILE      tiles of sra_quant_matmul: 64, 128 (a ring of two stages), 132 (of four) or 256 (bf16 results
+ *                          alone; 128 for fp32), at any number of rows; 0 = the planner's.  The reduction is split only
+ *                          where the planner splits it
  */
 enum {
   SRA_TUNE_RESET = 0,
@@ -588,7 +591,8 @@ enum {
   SRA_TUNE_ENGINE = 4,
   SRA_TUNE_DECODE_ROWS = 5,
   SRA_TUNE_ROWS_SLICES = 6,
-  SRA_TUNE_GRADS_SLICES = 7
+  SRA_TUNE_GRADS_SLICES = 7,
+  SRA_TUNE_FP8_TILE = 8
 };
 enum { SRA_ENGINE_SMFMAC = 0, SRA_ENGINE_DENSE_MFMA = 1 };
 sra_status sra_set_tuning(int32_t key, int32_t value);

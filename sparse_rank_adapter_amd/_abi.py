@@ -15,7 +15,7 @@ SRA_FMT_NM, SRA_FMT_ELL, SRA_FMT_CSR, SRA_FMT_NM_TILED, SRA_FMT_FFI_TILED = 0, 1
 SRA_GRAD_DX, SRA_GRAD_DA, SRA_GRAD_DB, SRA_DX_NO_ADAPTER = 1, 2, 4, 8
 SRA_NOALLOC_SCRATCH_BYTES = 64 << 20
 SRA_TUNE_KEYS = {"spmm_config": 1, "spmm_splits": 2, "spmm_fuse": 3, "engine": 4, "decode_rows": 5,
-                 "rows_slices": 6, "grads_slices": 7}
+                 "rows_slices": 6, "grads_slices": 7, "fp8_tile": 8}
 SRA_ENGINE_SMFMAC, SRA_ENGINE_DENSE_MFMA = 0, 1
 
 # every symbol include/sra.h declares

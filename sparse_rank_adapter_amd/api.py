@@ -1120,7 +1120,7 @@ _ENGINES = {"smfmac": 0, "dense_mfma": 1}
 
 def set_tuning(**knobs) -> None:
     """Tuning knobs of the calling thread (sra_set_tuning): spmm_config, spmm_splits, spmm_fuse,
-    engine ("smfmac" or "dense_mfma"), decode_rows, rows_slices, grads_slices."""
+    engine ("smfmac" or "dense_mfma"), decode_rows, rows_slices, grads_slices, fp8_tile."""
     lib = load()
     for k, v in knobs.items():
         if k not in _abi.SRA_TUNE_KEYS:

@@ -416,6 +416,11 @@ sra_status sra_set_tuning(int32_t key, int32_t value) {
       if (value < 0 || value > 1024) return fail(SRA_ERR_INVALID_ARG, "slices %d out of range", value);
       (key == SRA_TUNE_ROWS_SLICES ? g_tune.rows_slices : g_tune.grads_slices) = value;
       return SRA_OK;
+    case SRA_TUNE_FP8_TILE:
+      if (value != 0 && value != 64 && value != 128 && value != 132 && value != 256)
+        return fail(SRA_ERR_INVALID_ARG, "fp8 tiles must be 0, 64, 128, 132 or 256");
+      g_tune.fp8_tile = value;
+      return SRA_OK;
     default: return fail(SRA_ERR_INVALID_ARG, "unknown tuning key %d", key);
   }
 }

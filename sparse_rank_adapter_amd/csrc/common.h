@@ -171,6 +171,7 @@ struct Tuning {
   int decode_rows = 0;  // decode row tiles per workgroup (3, 4 or 9)
   int rows_slices = 0;  // reduction slices of the rank > 32 rows kernel
   int grads_slices = 0; // token slices of the adapter gradient kernel
+  int fp8_tile = 0;     // forced tiles of the 8-bit floating point product
 };
 const Tuning& tuning();
 

@@ -493,11 +493,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tiles(Mat a, Mat b, Out
 //
 // The accumulators fill the 256 accumulation registers; left to itself the compiler keeps operands there too and spills
 // (186 registers), so the instruction is written out with its operands' classes.  It then does not know the
-// instruction's latency: every read of a result has 62 others between (or the wait at the end), and operands written
-// by vector instructions (scales) have a wait behind them.
-SRA_DEV void wait_states() {  // 32 of them, with nothing moved across
+// instruction's latency: every read of a result has 62 others between, or the wait at the end.  The other operands come from
+// LDS, whose waits the compiler does put in.
+// 32 wait states behind the last matrix instructions of a group of steps, in the loop's own block, since the compiler may copy
+// accumulators as soon as the loop is left.  The last ones pass through; the others were written 8 instructions, 64 wait
+// states, earlier.  (A test looks for reads in the assembly that come too early.)
+SRA_DEV void results_settle(f32x4 (&x)[8], f32x4 (&y)[8]) {
   __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  asm volatile("s_nop 15\n\ts_nop 15"
+               : "+a"(x[4]), "+a"(x[5]), "+a"(x[6]), "+a"(x[7]), "+a"(y[4]), "+a"(y[5]), "+a"(y[6]), "+a"(y[7])::"memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 #define SRA_MFMA_TEXT(C, X, Y, SX, SY, LO, HI) \
@@ -569,7 +573,8 @@ __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int n
     vb[d] = (uint32_t)(((pos & 128) + 8 * (pos & 15) + ((pos >> 4) & 7)) * ld) + chunk;
   }
   const uint32_t lds = lds_offset(smem) + 64 * kBlock * w;
-  // where step s comes from: zeros from the reduction's end to the group's, then the next tile's first stages
+  // where step s comes from: zeros from the reduction's end to the group's, then the next tile's first two stages (the
+  // reduction has two blocks at least)
   struct Source {
     dma_rsrc_t a, b;
     int off;
@@ -609,13 +614,13 @@ __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int n
 #pragma unroll
     for (int h = 0; h < 2; ++h) fb[g].h[h] = *reinterpret_cast<const u32x4*>(pb + h * other + slot * kSlot + 16 * g * kBlock);
   };
-  uint32_t sa[F], sb[F], na[F], nb[F];
+  uint32_t sa[F], sb[F];
   auto read_scales = [&](int half, int kb) {
     const uint8_t* const sc = scal[half] + (kb & 12);
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      na[f] = *reinterpret_cast<const uint32_t*>(sc + (wm + 16 * f + i16) * kScaleLd);
-      nb[f] = *reinterpret_cast<const uint32_t*>(sc + (BM + wn + 8 * i16 + f) * kScaleLd);
+      sa[f] = *reinterpret_cast<const uint32_t*>(sc + (wm + 16 * f + i16) * kScaleLd);
+      sb[f] = *reinterpret_cast<const uint32_t*>(sc + (BM + wn + 8 * i16 + f) * kScaleLd);
     }
   };
   f32x4 acc[F][F];
@@ -663,7 +668,6 @@ __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int n
     read_a(0, x);
     read_b(0, x);
   }
-  read_scales(0, 0);
 #pragma unroll
   for (int f = 0; f < F; ++f)
 #pragma unroll
@@ -680,9 +684,7 @@ __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int n
         else load_scales(nxt, 0);
       }
       if (last) put_scales(half ^ 1);
-#pragma unroll
-      for (int f = 0; f < F; ++f) sa[f] = na[f], sb[f] = nb[f];
-      wait_states();
+      read_scales(half, kb);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int slot = j % 2;
@@ -702,12 +704,11 @@ __global__ __launch_bounds__(256, 1) void k_fp8_big(Mat a, Mat b, Out out, int n
         });
         quarter_fill(4, 4, j, from, 2, slot, [&](int x) {
           if (x < 4) read_b(1 - slot, x);
-          if (j == 3 && x == 4) read_scales(last ? half ^ 1 : half, last ? 0 : kb + 4);
         });
       }
+      results_settle(acc[6], acc[7]);
       if (last) half ^= 1;
     }
-    wait_states();  // the last matrix instructions' results
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       store_row16<F, false>(acc[f], out.p, out, cur.m0 + wm + 16 * f, cur.n0 + wn);
@@ -746,7 +747,7 @@ int few_tiles(int64_t N, int mt) {
   }
   return best;
 }
-enum { kFew, kBig, kMid, kSmall };
+enum { kFew, kBig, kMid, kDeep, kSmall };  // kMid: 128 x 128 tiles, two stages; kDeep: four
 struct Plan {
   int kernel;
   int splits;
@@ -757,7 +758,7 @@ struct Plan {
 // tiles are few they split the reduction, at least 4 blocks a split, and a second launch (3 us) joins the parts.
 // Against it, at 512 x 5120 x 20480: 160 large tiles 64 us, 640 middle ones 96; 128 x 5120 x 20480: 160 middle tiles 36 us,
 // 640 small ones 42; 2047 x 4096 x 1024: 512 small tiles 17 us, 128 middle ones 24.
-Plan plan_of(int64_t M, int64_t N, int64_t nblk, bool ex) {
+Plan own_plan(int64_t M, int64_t N, int64_t nblk, bool ex) {
   if (M <= 32) return {kFew, 1};
   const auto tiles = [&](int64_t side) { return ((M + side - 1) / side) * ((N + side - 1) / side); };
   const auto rounds = [](int64_t t, int64_t one, int64_t two) {  // two workgroups a CU
@@ -769,8 +770,19 @@ Plan plan_of(int64_t M, int64_t N, int64_t nblk, bool ex) {
   int s = 1;
   while (t * s < 192 && nblk >= 8 * s) s *= 2;
   const int64_t small = rounds(t * s, 40, 53) * ((nblk + s - 1) / s) + (s > 1 ? 300 : 0);
-  if (!ex && big < mid && big < small) return {kBig, 1};
-  return mid <= small ? Plan{kMid, 1} : Plan{kSmall, s};
+  if (!ex && nblk >= 2 && big < mid && big < small) return {kBig, 1};
+  if (mid > small) return {kSmall, s};
+  return {ex || tiles(128) > 256 ? kMid : kDeep, 1};
+}
+Plan plan_of(int64_t M, int64_t N, int64_t nblk, bool ex) {
+  const Plan p = own_plan(M, N, nblk, ex);
+  switch (sra::tuning().fp8_tile) {
+    case 64: return {kSmall, p.kernel == kSmall ? p.splits : 1};
+    case 128: return {kMid, 1};
+    case 132: return {ex ? kMid : kDeep, 1};
+    case 256: return {ex || nblk < 2 ? kMid : kBig, 1};
+    default: return p;
+  }
 }
 
 }  // namespace
@@ -814,11 +826,13 @@ static hipError_t matmul(const Mat& a, const Mat& b, const Out& out, const Plan&
   } while (0)
   if (p.kernel == kSmall) {
     SRA_TILES(64, 64, 4, 1, 4);
-  } else if (EX || (p.kernel == kMid && ((out.M + 127) / 128) * ((out.N + 127) / 128) > 256)) {
-    SRA_TILES(128, 128, 2, 2, 2);
   } else if (p.kernel == kMid) {
-    SRA_TILES(128, 128, 2, 2, 4);
+    SRA_TILES(128, 128, 2, 2, 2);
   } else if constexpr (!EX) {
+    if (p.kernel == kDeep) {
+      SRA_TILES(128, 128, 2, 2, 4);
+      return hipGetLastError();
+    }
     const int nm = (int)((out.M + 255) / 256), nn = (int)((out.N + 255) / 256);
     launch(SRA_KERNEL_FP8_MM, k_fp8_big<KA, KB>, dim3((unsigned)std::min(nm * nn, 256)), dim3(256), 0, s, a, b, out, nm, nn);
   }
