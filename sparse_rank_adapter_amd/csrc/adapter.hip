@@ -765,6 +765,10 @@ struct GradTile {
 };
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
+// An offset past every V^T buffer (under 2 GiB each): the transfer writes zeros.  V^T's chunks past the
+// slice are taken there, though Act's zeros meet them: what follows a row in the buffer is the next row,
+// and behind the last adapter row one that nothing has written, whose NaN times zero is NaN.
+constexpr uint32_t kNoRow = 0x7ffffff0u;
 
 template <int JT, int KG>
 SRA_DEV void adapter_grads_body(const sra::AdapterGradArgs& ga) {
@@ -788,7 +792,8 @@ SRA_DEV void adapter_grads_body(const sra::AdapterGradArgs& ga) {
   const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
       (void*)job.vt, 0, (int)((int64_t)job.parts * ga.rp * ga.Tp * 2), 0x00020000);
   uint32_t a_off[GT::LA], v_off[GT::LV];
-  int a_dst[GT::LA], v_dst[GT::LV];
+  int a_dst[GT::LA], v_dst[GT::LV], v_tok[GT::LV];
+  const int n_tok = (int)(te - tb);
 #pragma unroll
   for (int k = 0; k < GT::LA; ++k) {  // 1 KB = 8 token rows of 128 bytes
     const int b = k * GT::NW + w, x = 8 * b + (lane >> 3), c = (lane & 7) ^ (((x >> 3) & 3) << 1);
@@ -801,6 +806,7 @@ SRA_DEV void adapter_grads_body(const sra::AdapterGradArgs& ga) {
     const int c = (lane % VCH) ^ ((x >> (VCH == 8 ? 1 : 0)) & (VCH - 1));
     const int p = min(x / JR, job.parts - 1), jj = x % JR;  // parts past the job's repeat its last
     v_off[k] = (uint32_t)((((int64_t)p * ga.rp + j0 + jj) * ga.Tp + tb + c * 8) * 2);
+    v_tok[k] = c * 8;
     v_dst[k] = GT::A_BYTES + b * 1024;
   }
   auto issue = [&](int st, int buf) {
@@ -812,7 +818,8 @@ SRA_DEV void adapter_grads_body(const sra::AdapterGradArgs& ga) {
 #pragma unroll
     for (int k = 0; k < GT::LV; ++k)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr_t)(base + v_dst[k]), 16,
-                                               v_off[k] + (uint32_t)(st * ST * 2), 0, 0, 0);
+                                               v_tok[k] + st * ST < n_tok ? v_off[k] + (uint32_t)(st * ST * 2) : kNoRow,
+                                               0, 0, 0);
   };
 
   // two accumulator sets, alternating by stage: the other (previous stage's) set moves to fp64
@@ -975,7 +982,8 @@ SRA_DEV void adapter_grads_wide_body(const sra::AdapterGradArgs& ga, const sra::
   const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
       (void*)job.vt, 0, (int)((int64_t)P * ga.rp * ga.Tp * 2), 0x00020000);
   uint32_t a_off[GW::LA], v_off[GW::LVM];
-  int a_dst[GW::LA], v_dst[GW::LVM];
+  int a_dst[GW::LA], v_dst[GW::LVM], v_tok[GW::LVM];
+  const int n_tok = (int)(te - tb);
 #pragma unroll
   for (int k = 0; k < GW::LA; ++k) {  // 1 KB = 64 / CPR token rows of 2 MW bytes
     const int b = k * NW + w, x = b * (64 / GW::CPR) + lane / GW::CPR;
@@ -991,6 +999,7 @@ SRA_DEV void adapter_grads_wide_body(const sra::AdapterGradArgs& ga, const sra::
     const int c = (lane & 3) ^ ((x >> 2) & 3);
     const int p = x / JR, jj = x % JR;
     v_off[k] = (uint32_t)((((int64_t)p * ga.rp + j0 + jj) * ga.Tp + tb + c * 8) * 2);
+    v_tok[k] = c * 8;
     v_dst[k] = GW::A_BYTES + b * 1024;
   }
   auto issue = [&](int st, int buf) {
@@ -1003,7 +1012,8 @@ SRA_DEV void adapter_grads_wide_body(const sra::AdapterGradArgs& ga, const sra::
     for (int k = 0; k < GW::LVM; ++k)
       if (k < GW::LVM - 1 || full_v)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr_t)(base + v_dst[k]), 16,
-                                                 v_off[k] + (uint32_t)(st * ST * 2), 0, 0, 0);
+                                                 v_tok[k] + st * ST < n_tok ? v_off[k] + (uint32_t)(st * ST * 2) : kNoRow,
+                                                 0, 0, 0);
   };
 
   f32x4 acc[2][2][4];
