@@ -26,26 +26,38 @@ SRA_DEV f64x4 mfma(double a, double b, f64x4 c) { return __builtin_amdgcn_mfma_f
 // accumulation registers and copies them to and fro in every step.)
 SRA_DEV int drow(int q, int v) { return 4 * v + q; }  // row of a result's element v in lane group q
 
-// N consecutive elements at base + at, `left` of which are inside the row (VEC: aligned, and a whole vector is in or out); zeros
-// past it.  No branch: what is outside is read from the matrix's first elements, so that loads go out together.
-template <int N, bool VEC, typename E>
-SRA_DEV void load_n(const E* __restrict__ base, int64_t at, int64_t left, float (&f)[N]) {
-  union { E e[N]; uint32_t w[(N * sizeof(E) + 3) / 4]; u32x2 d; u32x4 q; } c;
-  if constexpr (VEC) {
-    const E* const p = base + (left > 0 ? at : 0);
-    if constexpr (N * sizeof(E) == 16) c.q = *reinterpret_cast<const u32x4*>(p);
-    else if constexpr (N * sizeof(E) == 8) c.d = *reinterpret_cast<const u32x2*>(p);
-    else c.w[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else {
+// Operands come from a matrix through a buffer resource (under 2 GiB): one 32-bit addition an address, and what is outside
+// reads as zero by the resource's length, or by an offset past it (kOut).  With 64-bit addresses and zeros selected for every
+// element the vector instructions between the fp64 products took about as long as the products, which they do not run beside.
+constexpr uint32_t kOut = 0x80000000u;
+template <int N, typename E>
+SRA_DEV void load_n(__amdgpu_buffer_rsrc_t r, uint32_t at, float (&f)[N]) {
+  union { E e[N]; uint32_t w; u32x2 d; u32x4 q; } c;
+  if constexpr (N * sizeof(E) == 16) c.q = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+  else if constexpr (N * sizeof(E) == 8) c.d = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+  else c.w = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
 #pragma unroll
-    for (int k = 0; k < N; ++k) c.e[k] = base[k < left ? at + k : 0];
+  for (int k = 0; k < N; ++k) {
+    if constexpr (sizeof(E) == 4) f[k] = c.e[k];
+    else f[k] = bf16_to_f32(c.e[k]);
   }
+}
+SRA_DEV __amdgpu_buffer_rsrc_t matrix(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
+}
+// Without that (odd rows, longer matrices): N consecutive elements at base + at, `left` of which are inside the row; what is
+// outside is read from the matrix's first elements and replaced by zeros, so that loads still go out together.
+template <int N, typename E>
+SRA_DEV void load_each(const E* __restrict__ base, int64_t at, int64_t left, float (&f)[N]) {
+  E e[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) e[k] = base[k < left ? at + k : 0];
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     float v;
-    if constexpr (sizeof(E) == 4) v = c.e[k];
-    else v = bf16_to_f32(c.e[k]);
-    f[k] = (VEC ? left > 0 : k < left) ? v : 0.f;
+    if constexpr (sizeof(E) == 4) v = e[k];
+    else v = bf16_to_f32(e[k]);
+    f[k] = k < left ? v : 0.f;
   }
 }
 template <int N, bool VEC, typename E>
@@ -81,25 +93,50 @@ struct GramArgs {
   int d, S;
   double* part;
 };
-template <typename E, bool TALL, bool VEC>
-struct GramBlock {  // a block of 32 rows of X over a chunk of 16 columns, as the lane's operands
-  float f[2][4];
-  SRA_DEV void load(const E* __restrict__ G, int64_t L, int d, int row0, int64_t chunk) {
+template <typename E, bool TALL, bool BUF>
+struct GramRows {  // a block of 32 rows of X, of which a chunk of 16 columns makes the lane's operands f[row][4]
+  const E* G;
+  int64_t L;
+  int d, row0;
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t off[TALL ? 4 : 2];
+  SRA_DEV GramRows(const E* G_, int64_t L_, int d_, int row0_) : G(G_), L(L_), d(d_), row0(row0_) {
+    if constexpr (BUF) {
+      const int l = threadIdx.x & 63, q = l >> 4, i = l & 15, E_ = (int)sizeof(E);
+      r = matrix(TALL ? G : G + (int64_t)row0 * L, (TALL ? d : d - row0) * L * E_);
+      if constexpr (TALL) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) off[j] = row0 + 2 * i < d ? (uint32_t)(((4 * j + q) * d + row0 + 2 * i) * E_) : kOut;
+      } else {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) off[x] = row0 + 16 * x + i < d ? (uint32_t)(((16 * x + i) * L + 4 * q) * E_) : kOut;
+      }
+    }
+  }
+  SRA_DEV void load(int64_t chunk, float (&f)[2][4]) const {
     const int l = threadIdx.x & 63, q = l >> 4, i = l & 15;
     if constexpr (!TALL) {  // rows row0 + 16 x + i; columns 16 chunk + 4 q + j
       const int64_t k = chunk * 16 + 4 * q;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int row = row0 + 16 * x + i;
-        load_n<4, VEC, E>(G, (int64_t)row * L + k, row < d ? L - k : 0, f[x]);
+        if constexpr (BUF) {
+          load_n<4, E>(r, (int)chunk * 16 < (int)L - 4 * q ? off[x] + (uint32_t)chunk * (16 * sizeof(E)) : kOut, f[x]);
+        } else {
+          const int row = row0 + 16 * x + i;
+          load_each<4, E>(G, (int64_t)row * L + k, row < d ? L - k : 0, f[x]);
+        }
       }
     } else {  // rows row0 + 2 i + x; columns 16 chunk + 4 j + q
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t k = chunk * 16 + 4 * j + q;
-        const int row = row0 + 2 * i;
         float two[2];
-        load_n<2, VEC, E>(G, k * d + row, k < L ? d - row : 0, two);
+        if constexpr (BUF) {
+          load_n<2, E>(r, off[j] + (uint32_t)chunk * (uint32_t)(16 * d * sizeof(E)), two);
+        } else {
+          const int64_t k = chunk * 16 + 4 * j + q;
+          const int row = row0 + 2 * i;
+          load_each<2, E>(G, k * d + row, k < L ? d - row : 0, two);
+        }
         f[0][j] = two[0], f[1][j] = two[1];
       }
     }
@@ -107,10 +144,45 @@ struct GramBlock {  // a block of 32 rows of X over a chunk of 16 columns, as th
   static SRA_DEV int at(int x, int i) { return TALL ? 2 * i + x : 16 * x + i; }  // operand row (x, i) in the block
 };
 
-template <typename E, bool TALL, bool VEC>
-__global__ __launch_bounds__(256, 2) void k_orth_gram(GramArgs g) {
-  __shared__ double red[4][32 * 33];
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i = l & 15;
+template <typename E, bool TALL, bool BUF, bool DIAG>
+SRA_DEV void gram_slice(const GramRows<E, TALL, BUF>& ra, const GramRows<E, TALL, BUF>& rb, int64_t c, int64_t c1, f64x4 (&acc)[2][2]) {
+  float a[2][2][4], b[2][2][4];
+  const auto load = [&](int64_t at, int k) {
+    ra.load(at, a[k]);
+    if constexpr (!DIAG) rb.load(at, b[k]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const auto sum = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (!DIAG || r <= p) acc[p][r] = mfma((double)a[k][p][j], (double)(DIAG ? a : b)[k][r][j], acc[p][r]);
+  };
+  if (c >= c1) return;
+  // the next chunk's loads go out before this one's products (and every load is used on every path: the compiler moves one
+  // that is not behind the products)
+  load(c, 0);
+  for (; c + 8 < c1; c += 8) {
+    load(c + 4, 1);
+    sum(0);
+    load(c + 8, 0);
+    sum(1);
+  }
+  if (c + 4 < c1) {
+    load(c + 4, 1);
+    sum(0);
+    sum(1);
+  } else {
+    sum(0);
+  }
+}
+
+template <typename E, bool TALL, bool BUF>
+SRA_DEV void gram_body(const GramArgs& g, double (&red)[4][32 * 33]) {
+  const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = l >> 4, i = l & 15;
   int bi = 0, pair = blockIdx.x;  // pairs (bi, bj), bj <= bi, row after row
   while (pair > bi) pair -= ++bi;
   const int bj = pair;
@@ -122,39 +194,10 @@ __global__ __launch_bounds__(256, 2) void k_orth_gram(GramArgs g) {
   for (int x = 0; x < 2; ++x)
 #pragma unroll
     for (int y = 0; y < 2; ++y) acc[x][y] = f64x4{0., 0., 0., 0.};
-  using B = GramBlock<E, TALL, VEC>;
-  B a, b, an, bn;
-  // the next chunk's loads go out before this one's products; past the slice the last chunk again, not used
-  const auto sum = [&](const B& x, const B& y, bool diag) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (!diag || r <= p) acc[p][r] = mfma((double)x.f[p][j], (double)y.f[r][j], acc[p][r]);
-  };
-  int64_t c = c0 + w;
-  if (bi == bj) {
-    if (c < c1) a.load(G, g.L, g.d, 32 * bi, c);
-    for (; c < c1; c += 4) {
-      an.load(G, g.L, g.d, 32 * bi, min(c + 4, c1 - 1));
-      sum(a, a, true);
-      a = an;
-    }
-  } else {
-    if (c < c1) {
-      a.load(G, g.L, g.d, 32 * bi, c);
-      b.load(G, g.L, g.d, 32 * bj, c);
-    }
-    for (; c < c1; c += 4) {
-      an.load(G, g.L, g.d, 32 * bi, min(c + 4, c1 - 1));
-      bn.load(G, g.L, g.d, 32 * bj, min(c + 4, c1 - 1));
-      sum(a, b, false);
-      a = an;
-      b = bn;
-    }
-  }
+  using B = GramRows<E, TALL, BUF>;
+  const B ra(G, g.L, g.d, 32 * bi), rb(G, g.L, g.d, 32 * bj);
+  if (bi == bj) gram_slice<E, TALL, BUF, true>(ra, rb, c0 + w, c1, acc);
+  else gram_slice<E, TALL, BUF, false>(ra, rb, c0 + w, c1, acc);
 #pragma unroll
   for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -171,6 +214,11 @@ __global__ __launch_bounds__(256, 2) void k_orth_gram(GramArgs g) {
     const int at = (e >> 5) * 33 + (e & 31);
     out[e] = (red[0][at] + red[1][at]) + (red[2][at] + red[3][at]);
   }
+}
+template <typename E, bool TALL, bool BUF>
+__global__ __launch_bounds__(256, 2) void k_orth_gram(GramArgs g) {
+  __shared__ double red[4][32 * 33];
+  gram_body<E, TALL, BUF>(g, red);
 }
 // A_0 [n][D][D] from the slices, in order, zeros past d (D = 16: a corner of the only block)
 __global__ __launch_bounds__(256) void k_orth_join(const double* __restrict__ part, int S, int D, double* __restrict__ A) {
@@ -332,18 +380,28 @@ __global__ __launch_bounds__(256, 2) void k_orth_mm(MmArgs g) {
 
 // ---- O = Q X.  A wave owns 16 FR rows of Q against 64 columns of X (rows of the tall matrix); the waves of a
 // workgroup take neighbouring rows of Q, so they share X in the CU's cache.  Q [n][D][D] is symmetric.
-template <typename E, bool TALL, bool VEC, int FR>
-__global__ __launch_bounds__(256, 2) void k_orth_apply(const double* __restrict__ Q, const E* __restrict__ G, int64_t L, int d,
-                                                    int D, E* __restrict__ O) {
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i = l & 15;
+template <typename E, bool TALL, bool BUF, int FR>
+SRA_DEV void apply_body(const double* __restrict__ Q, const E* __restrict__ G, int64_t L, int d, int D, E* __restrict__ O) {
+  const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = l >> 4, i = l & 15, E_ = (int)sizeof(E);
   const int nrb = (d + 16 * FR - 1) / (16 * FR);
   const int64_t job = (int64_t)blockIdx.x * 4 + w, cb = job / nrb * 64;
   const int r0 = (int)(job % nrb) * 16 * FR;
   if (cb >= L) return;
   const int64_t at = (int64_t)blockIdx.y * d * L;
-  Q += (int64_t)blockIdx.y * D * D;
   G += at;
   O += at;
+  const __amdgpu_buffer_rsrc_t rq = matrix(Q + (int64_t)blockIdx.y * D * D, (int64_t)D * D * 8);
+  const __amdgpu_buffer_rsrc_t rg = matrix(TALL ? G + cb * d : G, (TALL ? (L - cb) * d : (int64_t)d * L) * E_);
+  uint32_t qo[FR], go[4];  // the lane's first operands
+#pragma unroll
+  for (int x = 0; x < FR; ++x) qo[x] = (uint32_t)(((r0 + (TALL ? FR * i + x : 16 * x + i)) * D + 4 * q) * 8);
+  if constexpr (BUF) {
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      if constexpr (TALL) go[y] = (uint32_t)(((16 * y + i) * d + 4 * q) * E_);
+      else go[y] = cb + 4 * i < L ? (uint32_t)(((4 * q + y) * L + cb + 4 * i) * E_) : kOut;
+    }
+  }
   f64x4 acc[FR][4];
 #pragma unroll
   for (int x = 0; x < FR; ++x)
@@ -355,37 +413,60 @@ __global__ __launch_bounds__(256, 2) void k_orth_apply(const double* __restrict_
   };
   const auto load = [&](int k0, Step& s) {
 #pragma unroll
-    for (int x = 0; x < FR; ++x) {
-      const double* p = Q + (int64_t)(r0 + (TALL ? FR * i + x : 16 * x + i)) * D + k0 + 4 * q;
-      s.a[x][0] = *reinterpret_cast<const f64x2*>(p);
-      s.a[x][1] = *reinterpret_cast<const f64x2*>(p + 2);
-    }
+    for (int x = 0; x < FR; ++x)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        union { u32x4 w; f64x2 d; } c;
+        c.w = __builtin_amdgcn_raw_buffer_load_b128(rq, qo[x] + (uint32_t)k0 * 8 + 16 * h, 0, 0);
+        s.a[x][h] = c.d;
+      }
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
       if constexpr (!TALL) {
-        const int k = k0 + 4 * q + y;
-        load_n<4, VEC, E>(G, (int64_t)k * L + cb + 4 * i, k < d ? L - cb - 4 * i : 0, s.f[y]);
+        if constexpr (BUF) {
+          load_n<4, E>(rg, go[y] + (uint32_t)k0 * (uint32_t)(L * E_), s.f[y]);
+        } else {
+          const int k = k0 + 4 * q + y;
+          load_each<4, E>(G, (int64_t)k * L + cb + 4 * i, k < d ? L - cb - 4 * i : 0, s.f[y]);
+        }
       } else {
-        const int64_t c = cb + 16 * y + i;
-        load_n<4, VEC, E>(G, c * d + k0 + 4 * q, c < L ? d - k0 - 4 * q : 0, s.f[y]);
+        if constexpr (BUF) {
+          load_n<4, E>(rg, k0 < d - 4 * q ? go[y] + (uint32_t)(k0 * E_) : kOut, s.f[y]);
+        } else {
+          const int64_t c = cb + 16 * y + i;
+          load_each<4, E>(G, c * d + k0 + 4 * q, c < L ? d - k0 - 4 * q : 0, s.f[y]);
+        }
       }
     }
+    __builtin_amdgcn_sched_barrier(0);  // as above: before the products
   };
-  Step cur, nxt;
-  load(0, cur);
-  for (int k0 = 0; k0 < d; k0 += 16) {
-    load(min(k0 + 16, (d - 1) & ~15), nxt);  // the last time: not used
+  const auto sum = [&](const Step& s) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int x = 0; x < FR; ++x)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const double a = cur.a[x][j / 2][j % 2];
-          if constexpr (!TALL) acc[x][g] = mfma(a, (double)cur.f[j][g], acc[x][g]);
-          else acc[x][g] = mfma((double)cur.f[g][j], a, acc[x][g]);
+          const double a = s.a[x][j / 2][j % 2];
+          if constexpr (!TALL) acc[x][g] = mfma(a, (double)s.f[j][g], acc[x][g]);
+          else acc[x][g] = mfma((double)s.f[g][j], a, acc[x][g]);
         }
-    cur = nxt;
+  };
+  Step s0, s1;
+  int k0 = 0;
+  load(0, s0);
+  for (; k0 + 32 < d; k0 += 32) {
+    load(k0 + 16, s1);
+    sum(s0);
+    load(k0 + 32, s0);
+    sum(s1);
+  }
+  if (k0 + 16 < d) {
+    load(k0 + 16, s1);
+    sum(s0);
+    sum(s1);
+  } else {
+    sum(s0);
   }
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
@@ -394,7 +475,7 @@ __global__ __launch_bounds__(256, 2) void k_orth_apply(const double* __restrict_
       for (int x = 0; x < FR; ++x) {
         const int row = r0 + 16 * x + drow(q, v);
         const double o[4] = {acc[x][0][v], acc[x][1][v], acc[x][2][v], acc[x][3][v]};
-        store_n<4, VEC, E>(O + (int64_t)row * L + cb + 4 * i, row < d ? L - cb - 4 * i : 0, o);
+        store_n<4, BUF, E>(O + (int64_t)row * L + cb + 4 * i, row < d ? L - cb - 4 * i : 0, o);
       }
     } else {  // rows cb + 16 g + drow of the tall matrix, columns r0 + FR i + x
 #pragma unroll
@@ -403,10 +484,15 @@ __global__ __launch_bounds__(256, 2) void k_orth_apply(const double* __restrict_
         double o[FR];
 #pragma unroll
         for (int x = 0; x < FR; ++x) o[x] = acc[x][g][v];
-        store_n<FR, VEC && FR == 2, E>(O + c * d + r0 + FR * i, c < L ? d - r0 - FR * i : 0, o);
+        store_n<FR, BUF && FR == 2, E>(O + c * d + r0 + FR * i, c < L ? d - r0 - FR * i : 0, o);
       }
     }
   }
+}
+template <typename E, bool TALL, bool BUF, int FR>
+__global__ __launch_bounds__(256, 2) void k_orth_apply(const double* __restrict__ Q, const E* __restrict__ G, int64_t L, int d,
+                                                    int D, E* __restrict__ O) {
+  apply_body<E, TALL, BUF, FR>(Q, G, L, d, D, O);
 }
 
 // slices of L: about 512 workgroups over the matrices and pairs, each with 8 chunks of 16 at least
@@ -452,7 +538,9 @@ static hipError_t orth(const E* G, int64_t n, const Layout& y, const Steps& st, 
   const size_t me = y.mat / sizeof(double);
   const GramArgs g{G, y.L, y.d, y.S, part};
   const dim3 gg((unsigned)y.pairs, (unsigned)y.S, (unsigned)n);
-  if (TALL ? y.d % 2 == 0 : y.L % 4 == 0) launch(SRA_KERNEL_ORTH, k_orth_gram<E, TALL, true>, gg, dim3(256), 0, s, g);
+  // whole vectors in a row, and 32-bit offsets up to the 16 rows past the last that a step of the reduction may ask for
+  const bool small = ((int64_t)y.d + 16) * y.L * (int64_t)sizeof(E) < ((int64_t)1 << 31);
+  if (small && (TALL ? y.d % 2 == 0 : y.L % 4 == 0)) launch(SRA_KERNEL_ORTH, k_orth_gram<E, TALL, true>, gg, dim3(256), 0, s, g);
   else launch(SRA_KERNEL_ORTH, k_orth_gram<E, TALL, false>, gg, dim3(256), 0, s, g);
   double* const a0 = m0;
   double* q0 = m0 + me;
@@ -495,7 +583,7 @@ static hipError_t orth(const E* G, int64_t n, const Layout& y, const Steps& st, 
   const int nrb = (y.d + 16 * fr - 1) / (16 * fr);
   const int64_t jobs = (y.L + 63) / 64 * nrb;
   const dim3 ga((unsigned)((jobs + 3) / 4), (unsigned)n);
-  const bool vec = TALL ? y.d % 4 == 0 : y.L % 4 == 0;
+  const bool vec = small && (TALL ? y.d % 4 == 0 : y.L % 4 == 0);
 #define SRA_APPLY(V, FR) launch(SRA_KERNEL_ORTH, k_orth_apply<E, TALL, V, FR>, ga, dim3(256), 0, s, Q, G, y.L, y.d, y.D, O)
   if (fr == 1) {
     if (vec) SRA_APPLY(true, 1);
