@@ -789,9 +789,10 @@ Plan plan_of(int64_t M, int64_t N, int64_t nblk, bool ex) {
 
 namespace sra {
 
+// the planner's, whatever the knob says: a knob's tiles split no further, and a size that was asked for stays enough
 static size_t ws_of(int64_t M, int64_t N, int64_t K, bool ex) {
   if (M <= 0 || N <= 0) return 0;
-  const Plan p = plan_of(M, N, blocks_of(K), ex);
+  const Plan p = own_plan(M, N, blocks_of(K), ex);
   return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * sizeof(float) : 0;
 }
 
