@@ -477,7 +477,7 @@ sra_status sra_layer_norm_bwd(const void* dY, const void* X, const void* gamma, 
  *   dX = rstd * (g - xh * mean(g * xh)) + dH with g = dY * gamma, xh = h * rstd;  dgamma = sum_t dY * xh
  * X, R, gamma, H_out, Y, dY, dH, dX have one dtype (bf16 or fp32); rstd [T] and dgamma [H] are fp32.
  * R may be NULL (then H = X and H_out is not written); else H_out receives X + R, and may be X's or R's own
- * buffer.  The norm is taken of the sum in fp32; H_out, Y and the codes are each rounded once.
+ * buffer.  Y and codes overlap no other tensor.  The norm is taken of the sum in fp32; H_out, Y and the codes are each rounded once.
  * Outputs: Y, or its 8-bit form codes / exps (sra_quant_encode with SRA_FP8_E4M3 and blocks of one row, of the
  * values before Y's rounding), or both; NULL leaves one out.
  * The backward's H is the forward's H_out (X without R); dH, the gradient that reaches H past the norm, may
@@ -508,7 +508,7 @@ sra_status sra_rms_norm_bwd(const void* dY, const void* H_in, const void* gamma,
  * to nearest even, at most lim in magnitude.  An infinity or NaN becomes the code NaN and takes no part in its
  * block's scale.  A decoded value is code * 2^e rounded to dtype: exact in fp32, and in bf16 from 2^-133 up.
  * encode: X [rows, cols] (bf16 or fp32) -> codes / exps, and codes_t / exps_t, the same of X's transpose
- * ([cols, rows rounded up], blocks of 128 rows of X): either pair may be NULL.  With block_rows = 128 the
+ * ([cols, rows rounded up], blocks of 128 rows of X): either pair may be NULL, and no output overlaps an input.  With block_rows = 128 the
  * transpose holds the same values; with block_rows = 1 it is scaled along its own rows.
  */
 enum { SRA_FP8_E4M3 = 0, SRA_FP8_E5M2 = 1 };

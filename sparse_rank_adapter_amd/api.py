@@ -1030,7 +1030,7 @@ def rms_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residu
     """Y = h rstd gamma over the rows of h = X + residual.  Returns (Y, H, rstd, F): H = X + residual in X's dtype
     (X itself without a residual), rstd fp32 [T], and F the 8-bit form of Y (blocks of one row), None unless ``fp8``
     is torch.float8_e4m3fn (or an Fp8Matrix whose buffers it goes into).  ``want_y=False`` leaves Y out (None).
-    ``H`` may be X or the residual itself: the sum then replaces it."""
+    ``H`` may be X or the residual itself: the sum then replaces it; no other two of these overlap."""
     lib = load()
     T, W = _mat(X, "X")
     dev = X.device
@@ -1071,7 +1071,8 @@ def rms_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residu
 def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor,
                  dH: torch.Tensor | None = None, dX: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """Gradients of rms_norm_fwd from its H (X without a residual) and rstd; ``dH`` is the gradient that reaches H
-    past the norm.  Returns (dX, dgamma): dX is the gradient of X and of the residual, dgamma fp32 [width]."""
+    past the norm.  Returns (dX, dgamma): dX is the gradient of X and of the residual (and may be dY, H or dH itself),
+    dgamma fp32 [width]."""
     lib = load()
     T, W = _mat(H, "H")
     dev = H.device

@@ -703,6 +703,20 @@ sra_status sra_layer_norm_bwd(const void* dY, const void* X, const void* gamma, 
                   "layer_norm_bwd");
 }
 
+// a buffer that a call writes against one that it reads or writes (NULL: none); `same`: they may be one buffer
+struct Span {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+static sra_status check_apart(const Span& out, const Span& in, bool same = false) {
+  const uintptr_t a = (uintptr_t)out.p, b = (uintptr_t)in.p;
+  if (!a || !b || (same && a == b)) return SRA_OK;
+  if (a < b + in.bytes && b < a + out.bytes)
+    return fail(SRA_ERR_INVALID_ARG, "%s and %s overlap", out.name, in.name);
+  return SRA_OK;
+}
+static size_t code_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (size_t)((cols + 127) / 128 * 128); }
 static sra_status check_eps(float eps) {
   if (!(eps >= 0.f) || eps > 3.0e38f) return fail(SRA_ERR_INVALID_ARG, "eps must be finite and >= 0");
   return SRA_OK;
@@ -732,6 +746,13 @@ sra_status sra_rms_norm_fwd(const void* X, const void* R, const void* gamma, flo
   SRA_TRY(check_ptr(rstd, T > 0, "rstd"));
   SRA_TRY(check_ptr(codes, any && codes, "codes"));
   SRA_TRY(check_ptr(exps, any && codes, "exps"));
+  if (any) {
+    const size_t n = (size_t)T * H * esize(dtype);
+    const Span x{X, n, "X"}, r{R, n, "R"}, h{R ? H_out : nullptr, n, "H_out"}, y{Y, n, "Y"}, c{codes, code_bytes(T, H), "codes"};
+    for (const Span& in : {x, r}) SRA_TRY(check_apart(h, in, true));
+    for (const Span& in : {x, r, h}) SRA_TRY(check_apart(y, in));
+    for (const Span& in : {x, r, h, y}) SRA_TRY(check_apart(c, in));
+  }
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_rms_norm_fwd(dtype, X, R, gamma, eps, T, H, H_out, Y, rstd, codes, exps, s), s,
                   "rms_norm_fwd");
@@ -757,6 +778,11 @@ sra_status sra_rms_norm_bwd(const void* dY, const void* H_in, const void* gamma,
   SRA_TRY(check_ptr(dX, any, "dX"));
   SRA_TRY(check_ptr(dgamma, H > 0, "dgamma"));
   SRA_TRY(check_ws(ws, ws_bytes, sra::rms_norm_bwd_ws(T, H)));
+  if (any) {
+    const size_t n = (size_t)T * H * esize(dtype);
+    const Span out{dX, n, "dX"};
+    for (const Span& in : {Span{dY, n, "dY"}, Span{H_in, n, "H_in"}, Span{dH, n, "dH"}}) SRA_TRY(check_apart(out, in, true));
+  }
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_rms_norm_bwd(dtype, dY, H_in, gamma, rstd, dH, T, H, dX, dgamma, ws, s), s,
                   "rms_norm_bwd");
@@ -787,6 +813,13 @@ sra_status sra_quant_encode(const void* X, int32_t dtype, int64_t rows, int64_t 
   if (out && out_t && (out->kind != out_t->kind || out->block_rows != out_t->block_rows))
     return fail(SRA_ERR_INVALID_ARG, "out and out_t differ in kind or block_rows");
   SRA_TRY(check_ptr(X, rows > 0 && cols > 0, "X"));
+  if (rows > 0 && cols > 0) {
+    const Span x{X, (size_t)rows * cols * esize(dtype), "X"}, c{out ? out->codes : nullptr, code_bytes(rows, cols), "out's codes"},
+        t{out_t ? out_t->codes : nullptr, code_bytes(cols, rows), "out_t's codes"};
+    SRA_TRY(check_apart(c, x));
+    SRA_TRY(check_apart(t, x));
+    SRA_TRY(check_apart(t, c));
+  }
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_fp8_encode(dtype, f->kind, X, rows, cols, f->block_rows, out ? out->codes : nullptr,
                                          out ? out->exps : nullptr, out_t ? out_t->codes : nullptr,
@@ -798,6 +831,8 @@ sra_status sra_quant_decode(const sra_fp8* F, int32_t dtype, void* X, void* stre
   SRA_TRY(check_dtype(dtype));
   SRA_TRY(check_fp8(F, "F"));
   SRA_TRY(check_ptr(X, F->rows > 0 && F->cols > 0, "X"));
+  if (F->rows > 0 && F->cols > 0)
+    SRA_TRY(check_apart({X, (size_t)F->rows * F->cols * esize(dtype), "X"}, {F->codes, code_bytes(F->rows, F->cols), "F's codes"}));
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_fp8_decode(dtype, F->kind, F->codes, F->exps, F->rows, F->cols, F->block_rows, X, s), s,
                   "fp8_decode");
@@ -827,6 +862,11 @@ sra_status sra_quant_matmul(const sra_fp8* a, const sra_fp8* b, int32_t out_dtyp
   SRA_TRY(check_fp8_mm(a->rows, b->rows, a->cols));
   SRA_TRY(check_ptr(Out, a->rows > 0 && b->rows > 0, "Out"));
   SRA_TRY(check_ws(ws, ws_bytes, sra::fp8_matmul_ws(a->rows, b->rows, a->cols)));
+  if (a->rows > 0 && b->rows > 0 && a->cols > 0) {
+    const Span o{Out, (size_t)a->rows * b->rows * esize(out_dtype), "Out"};
+    SRA_TRY(check_apart(o, {a->codes, code_bytes(a->rows, a->cols), "a's codes"}));
+    SRA_TRY(check_apart(o, {b->codes, code_bytes(b->rows, b->cols), "b's codes"}));
+  }
   const hipStream_t s = (hipStream_t)stream;
   const sra::Fp8Operand x{a->codes, a->exps, a->kind, a->block_rows}, y{b->codes, b->exps, b->kind, b->block_rows};
   return hip_done(sra::launch_fp8_matmul(x, y, a->rows, b->rows, a->cols, out_dtype == SRA_F32, Out, ws, s), s,
@@ -862,8 +902,8 @@ sra_status sra_orthogonalize(const void* G, int32_t dtype, int64_t n, int64_t ro
   SRA_TRY(check_ptr(G, any, "G"));
   SRA_TRY(check_ptr(O, any, "O"));
   if (any) {
-    const uintptr_t g = (uintptr_t)G, o = (uintptr_t)O, size = (uintptr_t)n * rows * cols * esize(dtype);
-    if (g < o + size && o < g + size) return fail(SRA_ERR_INVALID_ARG, "G and O overlap");
+    const size_t size = (size_t)n * rows * cols * esize(dtype);
+    SRA_TRY(check_apart({O, size, "O"}, {G, size, "G"}));
   }
   SRA_TRY(check_ws(ws, ws_bytes, sra::orth_ws(n, rows, cols)));
   const double abc[3] = {a, b, c};
