@@ -11,7 +11,7 @@
 //
 // Measured: 8 fp32 matrices of 20480 x 128 256 us: A_0 63 us (3.0 GFLOP, bound by the fp64 matrix unit, 38 us at its peak, and
 // by uneven shares: 480 workgroups on 256 CUs), 14 launches of 128 x 128 products 6 us each (latency), Q G 102 us (5.4 GFLOP,
-// 68 us at the peak).  12 of 16 x 1024: 17 us, four launches.  4 of 64 x 8192: 73 us, 45 of them the steps (k_orth_small).
+// 68 us at the peak).  12 of 16 x 1024: 15-18 us, three launches.  4 of 64 x 8192: 73 us, 45 of them the steps (k_orth_small).
 //
 // The fp64 matrix instruction: lane l gives a[l % 16][l / 16] and b[l / 16][l % 16], and holds rows
 // 4 v + l / 16 (v = 0 .. 3) of column l % 16 of the result.
@@ -261,22 +261,60 @@ SRA_DEV f64x4 lds_mm(const double* A, const double* B, int ti, int tj) {  // til
   for (int k = 0; k < D; k += 4) acc = mfma(pa[k], pb[k], acc);
   return acc;
 }
-template <int D>
-__global__ __launch_bounds__(64 * (D / 16) * (D / 16 + 1) / 2, 2) void k_orth_small(const double* __restrict__ A0, int d, Steps st,
-                                                                              double* __restrict__ Q) {
-  constexpr int LD = D + 4, NT = 64 * (D / 16) * (D / 16 + 1) / 2;
+// JOIN: A0 is the slices' sums [n][S][32][32], joined here in k_orth_join's order, up to kJoinSlices of them: 12 x 16 x 1024 with
+// 8 slices 19.6 us with the launch, 18.2 without; at 32 slices 12 x 32 x 4096 takes 31 us with it and 34 without.
+constexpr int kJoinSlices = 16;
+template <int D, bool JOIN>
+__global__ __launch_bounds__(64 * (D / 16) * (D / 16 + 1) / 2, 2) void k_orth_small(const double* __restrict__ A0, int S, int d,
+                                                                              Steps st, double* __restrict__ Q) {
+  constexpr int LD = D + 4, NT = 64 * (D / 16) * (D / 16 + 1) / 2, PER = (D * D + NT - 1) / NT;
   __shared__ double lds[4 * D * LD];
   double *const A = lds, *const P = A + D * LD, *const W = P + D * LD, *const X = W + D * LD;
   const int l = threadIdx.x & 63, w = threadIdx.x >> 6, q = l >> 4, i = l & 15;
   int ti = 0, tj = w;  // tiles (ti, tj), tj <= ti, row after row
   while (tj > ti) tj -= ++ti;
-  A0 += (int64_t)blockIdx.x * D * D;
+  double own[PER];  // this thread's elements of A_0
+  if constexpr (JOIN) {
+    static_assert(D <= 32, "one block of 32 x 32");
+    A0 += (int64_t)blockIdx.x * S * 1024;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) own[k] = 0.;
+    constexpr int U = 8;  // slices in flight
+    for (int c = 0; c < S; c += U) {
+      double v[U][PER];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int e = min((int)threadIdx.x + k * NT, D * D - 1), row = e / D, cl = e % D;
+          v[u][k] = A0[min(c + u, S - 1) * 1024 + max(row, cl) * 32 + min(row, cl)];
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < PER; ++k) own[k] += c + u < S ? v[u][k] : 0.;
+    }
+  } else {
+    A0 += (int64_t)blockIdx.x * D * D;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) own[k] = A0[min((int)threadIdx.x + k * NT, D * D - 1)];
+  }
+  const auto put_own = [&](double f) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int e = threadIdx.x + k * NT;
+      if (e < D * D) A[(e / D) * LD + e % D] = own[k] * f;
+    }
+  };
+  put_own(1.);
+  __syncthreads();
   double tr = 0.;
-  for (int k = l; k < d; k += 64) tr += A0[k * (D + 1)];
+  for (int k = l; k < d; k += 64) tr += A[k * (LD + 1)];
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) tr += __shfl_xor(tr, m, 64);
   const double s = 1. / (sqrt(tr) + st.eps);
-  for (int e = threadIdx.x; e < D * D; e += NT) A[(e / D) * LD + e % D] = A0[e] * (s * s);
+  __syncthreads();
+  put_own(s * s);
   __syncthreads();
   const int col = 16 * tj + i;
   const auto put = [&](double* M, const f64x4& v) {
@@ -548,13 +586,20 @@ static hipError_t orth(const E* G, int64_t n, const Layout& y, const Steps& st, 
   else launch(SRA_KERNEL_ORTH, k_orth_gram<E, TALL, false>, gg, dim3(256), 0, s, g);
   double* const a0 = m0;
   double* q0 = m0 + me;
-  hipLaunchKernelGGL(k_orth_join, dim3((unsigned)(y.D * y.D / 256), (unsigned)n), dim3(256), 0, s, part, y.S, y.D, a0);
+  const bool join = y.D <= 32 && y.S <= kJoinSlices;
+  if (!join)
+    hipLaunchKernelGGL(k_orth_join, dim3((unsigned)(y.D * y.D / 256), (unsigned)n), dim3(256), 0, s, part, y.S, y.D, a0);
+#define SRA_SMALL(D, JOIN, NT) \
+  hipLaunchKernelGGL((k_orth_small<D, JOIN>), dim3((unsigned)n), dim3(NT), 0, s, JOIN ? part : a0, y.S, y.d, st, q0)
   if (y.D == 16) {
-    hipLaunchKernelGGL(k_orth_small<16>, dim3((unsigned)n), dim3(64), 0, s, a0, y.d, st, q0);
+    if (join) SRA_SMALL(16, true, 64);
+    else SRA_SMALL(16, false, 64);
   } else if (y.D == 32) {
-    hipLaunchKernelGGL(k_orth_small<32>, dim3((unsigned)n), dim3(192), 0, s, a0, y.d, st, q0);
+    if (join) SRA_SMALL(32, true, 192);
+    else SRA_SMALL(32, false, 192);
   } else if (y.D == 64) {
-    hipLaunchKernelGGL(k_orth_small<64>, dim3((unsigned)n), dim3(640), 0, s, a0, y.d, st, q0);
+    SRA_SMALL(64, false, 640);
+#undef SRA_SMALL
   } else {
     double *q1 = m0 + 2 * me, *a = m0 + 3 * me, *an = m0 + 4 * me, *const p = m0 + 5 * me, *const w = m0 + 6 * me;
     const unsigned tiles = (unsigned)(y.D / 16 * (y.D / 16 + 1) / 2);
