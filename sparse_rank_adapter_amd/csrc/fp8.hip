@@ -26,16 +26,15 @@ __global__ __launch_bounds__(kThreads) void k_fp8_rows(const E* __restrict__ x, 
   const int64_t nvec = ld / VEC, nblk = ld / kBlock;
   const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kU) + threadIdx.x;
   for (int64_t t = blockIdx.y; t < R; t += gridDim.y) {
-    float f[kU][VEC];
+    Stored<E, VEC> in[kU];  // all loads go out before any is used
+#pragma unroll
+    for (int u = 0; u < kU; ++u) in[u] = fetch<E, VEC>(x + t * C, (i0 + u * kThreads) * VEC, C);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int64_t i = i0 + u * kThreads;
-      load_row<E, VEC>(x + t * C + i * VEC, C - i * VEC, f[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int64_t i = i0 + u * kThreads;
-      const Coded<KIND, VEC> c = encode<KIND, VEC>(f[u]);
+      float f[VEC];
+      as_floats<E, VEC>(in[u], C - i * VEC, f);
+      const Coded<KIND, VEC> c = encode<KIND, VEC>(f);
       if (i < nvec) {
         store_codes<KIND, VEC>(codes + t * ld + i * VEC, c);
         if ((threadIdx.x & (kBlock / VEC - 1)) == 0) exps[t * nblk + i * VEC / kBlock] = (uint8_t)c.exp;
@@ -58,24 +57,27 @@ __global__ __launch_bounds__(kThreads) void k_fp8_tile(const E* __restrict__ x, 
   const int64_t nbc = (C + kBlock - 1) / kBlock, nbr = (R + kBlock - 1) / kBlock;
   for (int64_t tile_r = blockIdx.y; tile_r < nbr; tile_r += gridDim.y) {
     const int64_t r0 = tile_r * kBlock + 8 * a;
+    // every row's load goes out before any is used (in branches of their own each waited for the one before): what is outside
+    // is read from inside, and replaced by zeros
+    Stored<E, 8> in[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const E* const row = x + min(r0 + i, R - 1) * C;
+      if constexpr (VEC) {
+        in[i] = fetch<E, 8>(row, c0, C);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) in[i].e[k] = row[c0 + k < C ? c0 + k : 0];
+      }
+    }
     float f[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      const int64_t left = r0 + i < R ? C - c0 : 0;
+      as_floats<E, 8>(in[i], left, f[i]);
+      if constexpr (!VEC) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[i][k] = 0.f;
-      if (r0 + i < R) {
-        if constexpr (VEC) {
-          load_row<E, 8>(x + (r0 + i) * C + c0, C - c0, f[i]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float one[1];
-            if (c0 + k < C) {
-              sra_row::RowVec<E, 1>::load(x + (r0 + i) * C + c0 + k, one);
-              f[i][k] = one[0];
-            }
-          }
-        }
+        for (int k = 1; k < 8; ++k) f[i][k] = k < left ? f[i][k] : 0.f;
       }
     }
     uint32_t rm[8], cm[8];

@@ -34,18 +34,27 @@ __global__ __launch_bounds__(1024) void k_rms_fwd(const E* x, const E* r, const 
   __shared__ double red[16];
   const int64_t t = blockIdx.x;
   const int nt = blockDim.x;
-  float f[V][VEC];
+  // all loads go out before any is used
+  Stored<E, VEC> xs[V], res[V], gs[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int64_t c = (int64_t)(threadIdx.x + v * nt) * VEC;
-    load_row<E, VEC>(x + t * H + c, H - c, f[v]);
+    xs[v] = fetch<E, VEC>(x + t * H, c, H);
+    gs[v] = fetch<E, VEC>(gamma, c, H);
   }
+  if (r) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) res[v] = fetch<E, VEC>(r + t * H, (int64_t)(threadIdx.x + v * nt) * VEC, H);
+  }
+  float f[V][VEC];
+#pragma unroll
+  for (int v = 0; v < V; ++v) as_floats<E, VEC>(xs[v], H - (int64_t)(threadIdx.x + v * nt) * VEC, f[v]);
   if (r) {  // h may be x or r: a row's elements are read and written by the same thread
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int64_t c = (int64_t)(threadIdx.x + v * nt) * VEC;
       float g[VEC];
-      load_row<E, VEC>(r + t * H + c, H - c, g);
+      as_floats<E, VEC>(res[v], H - c, g);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) f[v][k] += g[k];
       store_row<E, VEC>(h + t * H + c, H - c, f[v]);
@@ -68,7 +77,7 @@ __global__ __launch_bounds__(1024) void k_rms_fwd(const E* x, const E* r, const 
   for (int v = 0; v < V; ++v) {
     const int64_t c = (int64_t)(threadIdx.x + v * nt) * VEC;
     float ga[VEC];
-    load_row<E, VEC>(gamma + c, H - c, ga);
+    as_floats<E, VEC>(gs[v], H - c, ga);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) f[v][k] = f[v][k] * rs * ga[k];
     if constexpr (OUT & 1) store_row<E, VEC>(y + t * H + c, H - c, f[v]);
