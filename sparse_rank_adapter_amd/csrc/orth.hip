@@ -33,6 +33,8 @@ SRA_DEV int drow(int q, int v) { return 4 * v + q; }  // row of a result's eleme
 // Operands come from a matrix through a buffer resource (under 2 GiB): one 32-bit addition an address, and what is outside
 // reads as zero by the resource's length, or by an offset past it (kOut).  With 64-bit addresses and zeros selected for every
 // element the vector instructions between the fp64 products took about as long as the products, which they do not run beside.
+// (BUF = 1: rows of any number of whole words, whose last vector may run on into the next row; BUF = 2: rows of whole vectors.
+// 6 x 250 x 20481 640 us, 20480 columns 584 without the masks and 621 with them.)
 constexpr uint32_t kOut = 0x80000000u;
 template <int N, typename E>
 SRA_DEV void load_n(__amdgpu_buffer_rsrc_t r, uint32_t at, float (&f)[N]) {
@@ -49,7 +51,7 @@ SRA_DEV void load_n(__amdgpu_buffer_rsrc_t r, uint32_t at, float (&f)[N]) {
 SRA_DEV __amdgpu_buffer_rsrc_t matrix(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
 }
-// Without that (odd rows, longer matrices): N consecutive elements at base + at, `left` of which are inside the row; what is
+// Without that (bf16 in odd rows, longer matrices): N consecutive elements at base + at, `left` of which are inside the row; what is
 // outside is read from the matrix's first elements and replaced by zeros, so that loads still go out together.
 template <int N, typename E>
 SRA_DEV void load_each(const E* __restrict__ base, int64_t at, int64_t left, float (&f)[N]) {
@@ -64,20 +66,22 @@ SRA_DEV void load_each(const E* __restrict__ base, int64_t at, int64_t left, flo
     f[k] = k < left ? v : 0.f;
   }
 }
+typedef uint32_t u32x2w __attribute__((ext_vector_type(2), aligned(4)));  // in memory at any whole word
+typedef uint32_t u32x4w __attribute__((ext_vector_type(4), aligned(4)));
+// N elements to p, `left` of which are inside the row.  VEC: p is a whole word's address
 template <int N, bool VEC, typename E>
 SRA_DEV void store_n(E* __restrict__ p, int64_t left, const double (&d)[N]) {
-  if constexpr (VEC) {
-    if (left <= 0) return;
-    if constexpr (sizeof(E) == 4) {
-      if constexpr (N == 4) *reinterpret_cast<f32x4*>(p) = f32x4{(float)d[0], (float)d[1], (float)d[2], (float)d[3]};
-      else *reinterpret_cast<u32x2*>(p) = u32x2{__float_as_uint((float)d[0]), __float_as_uint((float)d[1])};
-    } else {
-      union { __bf16 h[N]; uint32_t w[N / 2]; } o;
+  if (VEC && left >= N) {
+    union { float f[N]; __bf16 h[N]; uint32_t w[N]; } o;
 #pragma unroll
-      for (int k = 0; k < N; ++k) o.h[k] = (__bf16)(float)d[k];
-      if constexpr (N == 4) *reinterpret_cast<u32x2*>(p) = u32x2{o.w[0], o.w[1]};
-      else *reinterpret_cast<uint32_t*>(p) = o.w[0];
+    for (int k = 0; k < N; ++k) {
+      if constexpr (sizeof(E) == 4) o.f[k] = (float)d[k];
+      else o.h[k] = (__bf16)(float)d[k];
     }
+    constexpr int W = N * sizeof(E) / 4;
+    if constexpr (W == 4) *reinterpret_cast<u32x4w*>(p) = u32x4w{o.w[0], o.w[1], o.w[2], o.w[3]};
+    else if constexpr (W == 2) *reinterpret_cast<u32x2w*>(p) = u32x2w{o.w[0], o.w[1]};
+    else *reinterpret_cast<uint32_t*>(p) = o.w[0];
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k)
@@ -97,7 +101,7 @@ struct GramArgs {
   int d, S;
   double* part;
 };
-template <typename E, bool TALL, bool BUF>
+template <typename E, bool TALL, int BUF>
 struct GramRows {  // a block of 32 rows of X, of which a chunk of 16 columns makes the lane's operands f[row][4]
   const E* G;
   int64_t L;
@@ -124,7 +128,12 @@ struct GramRows {  // a block of 32 rows of X, of which a chunk of 16 columns ma
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if constexpr (BUF) {
-          load_n<4, E>(r, (int)chunk * 16 < (int)L - 4 * q ? off[x] + (uint32_t)chunk * (16 * sizeof(E)) : kOut, f[x]);
+          const int inside = (int)L - (int)chunk * 16;  // columns from the chunk's first on
+          load_n<4, E>(r, 4 * q < inside ? off[x] + (uint32_t)chunk * (16 * sizeof(E)) : kOut, f[x]);
+          if (BUF == 1 && inside < 16) {  // the last chunk: what follows the row's end is the next row
+#pragma unroll
+            for (int j = 1; j < 4; ++j) f[x][j] = 4 * q + j < inside ? f[x][j] : 0.f;
+          }
         } else {
           const int row = row0 + 16 * x + i;
           load_each<4, E>(G, (int64_t)row * L + k, row < d ? L - k : 0, f[x]);
@@ -136,6 +145,7 @@ struct GramRows {  // a block of 32 rows of X, of which a chunk of 16 columns ma
         float two[2];
         if constexpr (BUF) {
           load_n<2, E>(r, off[j] + (uint32_t)chunk * (uint32_t)(16 * d * sizeof(E)), two);
+          if (BUF == 1 && row0 + 32 > d) two[1] = row0 + 2 * i + 1 < d ? two[1] : 0.f;
         } else {
           const int64_t k = chunk * 16 + 4 * j + q;
           const int row = row0 + 2 * i;
@@ -148,7 +158,7 @@ struct GramRows {  // a block of 32 rows of X, of which a chunk of 16 columns ma
   static SRA_DEV int at(int x, int i) { return TALL ? 2 * i + x : 16 * x + i; }  // operand row (x, i) in the block
 };
 
-template <typename E, bool TALL, bool BUF, bool DIAG>
+template <typename E, bool TALL, int BUF, bool DIAG>
 SRA_DEV void gram_slice(const GramRows<E, TALL, BUF>& ra, const GramRows<E, TALL, BUF>& rb, int64_t c, int64_t c1, f64x4 (&acc)[2][2]) {
   float a[2][2][4], b[2][2][4];
   const auto load = [&](int64_t at, int k) {
@@ -184,7 +194,7 @@ SRA_DEV void gram_slice(const GramRows<E, TALL, BUF>& ra, const GramRows<E, TALL
   }
 }
 
-template <typename E, bool TALL, bool BUF>
+template <typename E, bool TALL, int BUF>
 SRA_DEV void gram_body(const GramArgs& g, double (&red)[4][32 * 33]) {
   const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = l >> 4, i = l & 15;
   int bi = 0, pair = blockIdx.x;  // pairs (bi, bj), bj <= bi, row after row
@@ -219,7 +229,7 @@ SRA_DEV void gram_body(const GramArgs& g, double (&red)[4][32 * 33]) {
     out[e] = (red[0][at] + red[1][at]) + (red[2][at] + red[3][at]);
   }
 }
-template <typename E, bool TALL, bool BUF>
+template <typename E, bool TALL, int BUF>
 __global__ __launch_bounds__(256, 2) void k_orth_gram(GramArgs g) {
   __shared__ double red[4][32 * 33];
   gram_body<E, TALL, BUF>(g, red);
@@ -422,7 +432,7 @@ __global__ __launch_bounds__(256, 2) void k_orth_mm(MmArgs g) {
 
 // ---- O = Q X.  A wave owns 16 FR rows of Q against 64 columns of X (rows of the tall matrix); the waves of a
 // workgroup take neighbouring rows of Q, so they share X in the CU's cache.  Q [n][D][D] is symmetric.
-template <typename E, bool TALL, bool BUF, int FR>
+template <typename E, bool TALL, int BUF, int FR>
 SRA_DEV void apply_body(const double* __restrict__ Q, const E* __restrict__ G, int64_t L, int d, int D, E* __restrict__ O) {
   const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = l >> 4, i = l & 15, E_ = (int)sizeof(E);
   const int nrb = (d + 16 * FR - 1) / (16 * FR);
@@ -474,6 +484,10 @@ SRA_DEV void apply_body(const double* __restrict__ Q, const E* __restrict__ G, i
       } else {
         if constexpr (BUF) {
           load_n<4, E>(rg, k0 < d - 4 * q ? go[y] + (uint32_t)(k0 * E_) : kOut, s.f[y]);
+          if (BUF == 1 && k0 + 16 > d) {
+#pragma unroll
+            for (int j = 1; j < 4; ++j) s.f[y][j] = k0 + 4 * q + j < d ? s.f[y][j] : 0.f;
+          }
         } else {
           const int64_t c = cb + 16 * y + i;
           load_each<4, E>(G, c * d + k0 + 4 * q, c < L ? d - k0 - 4 * q : 0, s.f[y]);
@@ -517,7 +531,7 @@ SRA_DEV void apply_body(const double* __restrict__ Q, const E* __restrict__ G, i
       for (int x = 0; x < FR; ++x) {
         const int row = r0 + 16 * x + drow(q, v);
         const double o[4] = {acc[x][0][v], acc[x][1][v], acc[x][2][v], acc[x][3][v]};
-        store_n<4, BUF, E>(O + (int64_t)row * L + cb + 4 * i, row < d ? L - cb - 4 * i : 0, o);
+        store_n<4, BUF != 0, E>(O + (int64_t)row * L + cb + 4 * i, row < d ? L - cb - 4 * i : 0, o);
       }
     } else {  // rows cb + 16 g + drow of the tall matrix, columns r0 + FR i + x
 #pragma unroll
@@ -526,12 +540,12 @@ SRA_DEV void apply_body(const double* __restrict__ Q, const E* __restrict__ G, i
         double o[FR];
 #pragma unroll
         for (int x = 0; x < FR; ++x) o[x] = acc[x][g][v];
-        store_n<FR, BUF && FR == 2, E>(O + c * d + r0 + FR * i, c < L ? d - r0 - FR * i : 0, o);
+        store_n<FR, BUF != 0 && FR == 2, E>(O + c * d + r0 + FR * i, c < L ? d - r0 - FR * i : 0, o);
       }
     }
   }
 }
-template <typename E, bool TALL, bool BUF, int FR>
+template <typename E, bool TALL, int BUF, int FR>
 __global__ __launch_bounds__(256, 2) void k_orth_apply(const double* __restrict__ Q, const E* __restrict__ G, int64_t L, int d,
                                                     int D, E* __restrict__ O) {
   apply_body<E, TALL, BUF, FR>(Q, G, L, d, D, O);
@@ -580,10 +594,14 @@ static hipError_t orth(const E* G, int64_t n, const Layout& y, const Steps& st, 
   const size_t me = y.mat / sizeof(double);
   const GramArgs g{G, y.L, y.d, y.S, part};
   const dim3 gg((unsigned)y.pairs, (unsigned)y.S, (unsigned)n);
-  // whole vectors in a row, and 32-bit offsets up to the 16 rows past the last that a step of the reduction may ask for
+  // rows that begin at whole words (loads need no more than that), and 32-bit offsets up to the 16 rows past the last that a step of the reduction may ask for
   const bool small = ((int64_t)y.d + 16) * y.L * (int64_t)sizeof(E) < ((int64_t)1 << 31);
-  if (small && (TALL ? y.d % 2 == 0 : y.L % 4 == 0)) launch(SRA_KERNEL_ORTH, k_orth_gram<E, TALL, true>, gg, dim3(256), 0, s, g);
-  else launch(SRA_KERNEL_ORTH, k_orth_gram<E, TALL, false>, gg, dim3(256), 0, s, g);
+  const bool words = small && (sizeof(E) == 4 || (TALL ? y.d : y.L) % 2 == 0);
+#define SRA_GRAM(BUF) launch(SRA_KERNEL_ORTH, k_orth_gram<E, TALL, BUF>, gg, dim3(256), 0, s, g)
+  if (words && (TALL ? y.d % 2 == 0 : y.L % 4 == 0)) SRA_GRAM(2);
+  else if (words) SRA_GRAM(1);
+  else SRA_GRAM(0);
+#undef SRA_GRAM
   double* const a0 = m0;
   double* q0 = m0 + me;
   const bool join = y.D <= 32 && y.S <= kJoinSlices;
@@ -632,14 +650,16 @@ static hipError_t orth(const E* G, int64_t n, const Layout& y, const Steps& st, 
   const int nrb = (y.d + 16 * fr - 1) / (16 * fr);
   const int64_t jobs = (y.L + 63) / 64 * nrb;
   const dim3 ga((unsigned)((jobs + 3) / 4), (unsigned)n);
-  const bool vec = small && (TALL ? y.d % 4 == 0 : y.L % 4 == 0);
-#define SRA_APPLY(V, FR) launch(SRA_KERNEL_ORTH, k_orth_apply<E, TALL, V, FR>, ga, dim3(256), 0, s, Q, G, y.L, y.d, y.D, O)
+  const int buf = !words ? 0 : (TALL ? y.d : y.L) % 4 == 0 ? 2 : 1;
+#define SRA_APPLY(BUF, FR) launch(SRA_KERNEL_ORTH, k_orth_apply<E, TALL, BUF, FR>, ga, dim3(256), 0, s, Q, G, y.L, y.d, y.D, O)
   if (fr == 1) {
-    if (vec) SRA_APPLY(true, 1);
-    else SRA_APPLY(false, 1);
+    if (buf == 2) SRA_APPLY(2, 1);
+    else if (buf == 1) SRA_APPLY(1, 1);
+    else SRA_APPLY(0, 1);
   } else {
-    if (vec) SRA_APPLY(true, 2);
-    else SRA_APPLY(false, 2);
+    if (buf == 2) SRA_APPLY(2, 2);
+    else if (buf == 1) SRA_APPLY(1, 2);
+    else SRA_APPLY(0, 2);
   }
 #undef SRA_APPLY
   return hipGetLastError();
