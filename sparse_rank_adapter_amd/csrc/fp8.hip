@@ -7,8 +7,8 @@
 // registers (8 x 8 elements a thread), so the matrix is read once for both forms; the transposed codes
 // cross through LDS and leave in whole 128-byte lines.
 //
-// Measured: 20480 x 5120 in bf16 by 128 x 128 blocks with the transpose 94-104 us (419 MB, 4.0-4.5 TB/s), decoded again 49 and
-// 54 us (5.5-6.4 TB/s); 2047 x 4096 by rows with the transpose 14-17 us (34 MB: 512 workgroups of one tile each, so nothing
+// Measured: 20480 x 5120 in bf16 by 128 x 128 blocks with the transpose 75-88 us (419 MB, 4.8-5.6 TB/s), decoded again 49 and
+// 54 us (5.5-6.4 TB/s); 2047 x 4096 by rows with the transpose 13-16 us (34 MB: 512 workgroups of one tile each, so nothing
 // overlaps a tile's loads, maxima and stores), decoded 6.5 us, and 9.4 us where rows of 2047 allow two elements at a time.
 #include <algorithm>
 

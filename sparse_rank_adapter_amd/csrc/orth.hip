@@ -9,7 +9,7 @@
 // (128 x 5120, singular values over three to four decades), so everything from A_0 on is fp64, on
 // v_mfma_f64_16x16x4_f64.  The norm is the square root of A_0's trace.
 //
-// Measured: 8 fp32 matrices of 20480 x 128 256 us: A_0 63 us (3.0 GFLOP, bound by the fp64 matrix unit, 38 us at its peak, and
+// Measured: 8 fp32 matrices of 20480 x 128 253 us: A_0 63 us (3.0 GFLOP, bound by the fp64 matrix unit, 38 us at its peak, and
 // by uneven shares: 480 workgroups on 256 CUs), 14 launches of 128 x 128 products 6 us each (latency), Q G 102 us (5.4 GFLOP,
 // 68 us at the peak).  12 of 16 x 1024: 15-18 us, three launches.  4 of 64 x 8192: 73 us, 45 of them the steps (k_orth_small).
 //
