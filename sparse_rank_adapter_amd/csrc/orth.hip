@@ -366,7 +366,8 @@ __global__ __launch_bounds__(64 * (D / 16) * (D / 16 + 1) / 2, 2) void k_orth_sm
 }
 
 // ---- d > 64: every product of a step as a launch of its own (one workgroup would take 14 us a product at d = 128, its CU's
-// share of the fp64 rate).  A workgroup has a 16 x 16 tile on or below the diagonal and writes it on both sides, its waves a quarter of the reduction each, all of whose
+// share of the fp64 rate).  A workgroup has a 16 x 16 tile on or below the diagonal and writes it on both sides, its waves a
+// quarter of the reduction each, all of whose
 // operands are loaded at once: a launch is bound by that latency.
 // job z: C_z = u I + v A_z + w (A_z B_z), B_z symmetric; u, v and w are multiplied by the powers pu, pv and pw
 // of s = 1 / (sqrt(trace of `norm`) + eps)
@@ -594,7 +595,8 @@ static hipError_t orth(const E* G, int64_t n, const Layout& y, const Steps& st, 
   const size_t me = y.mat / sizeof(double);
   const GramArgs g{G, y.L, y.d, y.S, part};
   const dim3 gg((unsigned)y.pairs, (unsigned)y.S, (unsigned)n);
-  // rows that begin at whole words (loads need no more than that), and 32-bit offsets up to the 16 rows past the last that a step of the reduction may ask for
+  // rows that begin at whole words (loads need no more than that), and 32-bit offsets up to the 16 rows past the last that a
+  // step of the reduction may ask for
   const bool small = ((int64_t)y.d + 16) * y.L * (int64_t)sizeof(E) < ((int64_t)1 << 31);
   const bool words = small && (sizeof(E) == 4 || (TALL ? y.d : y.L) % 2 == 0);
 #define SRA_GRAM(BUF) launch(SRA_KERNEL_ORTH, k_orth_gram<E, TALL, BUF>, gg, dim3(256), 0, s, g)
