@@ -257,6 +257,9 @@ struct Steps {
   double a, b, c, eps;
   int n;
 };
+// 1 / (|G| + eps) from |G|^2.  It is multiplied up to its fifth power, which overflows where eps alone is far below fp32's
+// range: a zero matrix takes 0, which gives its zeros as well.
+SRA_DEV double scale_of(double trace, double eps) { return trace == 0. && eps > 0. ? 0. : 1. / (sqrt(trace) + eps); }
 
 // ---- d <= 64: all steps of one matrix in one workgroup, its matrices in LDS.  All of them are symmetric (polynomials of
 // A_0): wave w owns one 16 x 16 tile on or below the diagonal of every product and writes it on both sides.  Rows are
@@ -322,7 +325,7 @@ __global__ __launch_bounds__(64 * (D / 16) * (D / 16 + 1) / 2, 2) void k_orth_sm
   for (int k = l; k < d; k += 64) tr += A[k * (LD + 1)];
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) tr += __shfl_xor(tr, m, 64);
-  const double s = 1. / (sqrt(tr) + st.eps);
+  const double s = scale_of(tr, st.eps);
   __syncthreads();
   put_own(s * s);
   __syncthreads();
@@ -408,7 +411,7 @@ __global__ __launch_bounds__(256, 2) void k_orth_mm(MmArgs g) {
     for (int k = l; k < g.d; k += 64) tr += g.norm[at + (int64_t)k * (D + 1)];
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) tr += __shfl_xor(tr, m, 64);
-    if (l == 0) scale = 1. / (sqrt(tr) + g.eps);
+    if (l == 0) scale = scale_of(tr, g.eps);
   }
   f64x4 acc = {0., 0., 0., 0.};
 #pragma unroll
