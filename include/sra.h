@@ -477,11 +477,11 @@ sra_status sra_layer_norm_bwd(const void* dY, const void* X, const void* gamma, 
  *   dX = rstd * (g - xh * mean(g * xh)) + dH with g = dY * gamma, xh = h * rstd;  dgamma = sum_t dY * xh
  * X, R, gamma, H_out, Y, dY, dH, dX have one dtype (bf16 or fp32); rstd [T] and dgamma [H] are fp32.
  * R may be NULL (then H = X and H_out is not written); else H_out receives X + R, and may be X's or R's own
- * buffer.  Y and codes overlap no other tensor.  The norm is taken of the sum in fp32; H_out, Y and the codes are each rounded once.
+ * buffer.  No other output overlaps any tensor.  The norm is taken of the sum in fp32; H_out, Y and the codes are each rounded once.
  * Outputs: Y, or its 8-bit form codes / exps (sra_quant_encode with SRA_FP8_E4M3 and blocks of one row, of the
  * values before Y's rounding), or both; NULL leaves one out.
  * The backward's H is the forward's H_out (X without R); dH, the gradient that reaches H past the norm, may
- * be NULL.  dX is the gradient of X and of R alike, and may be dY's, dH's or H's own buffer.  Its sums over
+ * be NULL.  dX is the gradient of X and of R alike, and may be dY's, dH's or H's own buffer; dgamma and the workspace overlap nothing.  Its sums over
  * tokens run in a fixed order.  A row's sum is fp32 within a thread (up to 16 terms) and fp64 across threads,
  * dgamma's fp32 over the rows.  T = 0: the forward is a no-op, the backward writes zeros to dgamma.  H = 0:
  * rstd is NaN.  eps must be finite and >= 0.  Supported: H <= 16384, T < 2^31.
@@ -508,7 +508,7 @@ sra_status sra_rms_norm_bwd(const void* dY, const void* H_in, const void* gamma,
  * to nearest even, at most lim in magnitude.  An infinity or NaN becomes the code NaN and takes no part in its
  * block's scale.  A decoded value is code * 2^e rounded to dtype: exact in fp32, and in bf16 from 2^-133 up.
  * encode: X [rows, cols] (bf16 or fp32) -> codes / exps, and codes_t / exps_t, the same of X's transpose
- * ([cols, rows rounded up], blocks of 128 rows of X): either pair may be NULL, and no output overlaps an input.  With block_rows = 128 the
+ * ([cols, rows rounded up], blocks of 128 rows of X): either pair may be NULL, and no output overlaps X or another output.  With block_rows = 128 the
  * transpose holds the same values; with block_rows = 1 it is scaled along its own rows.
  */
 enum { SRA_FP8_E4M3 = 0, SRA_FP8_E5M2 = 1 };
@@ -530,7 +530,7 @@ sra_status sra_quant_decode(const sra_fp8* F /* host */, int32_t dtype, void* X,
  * weight gradient (a = dY's transpose, b = X's).  Any kinds and block_rows.  Out has out_dtype (bf16 or fp32),
  * rounded once; sums are fp32.  A NaN code or scale makes NaN of its own row's results alone.  cols = 0 writes
  * zeros.  The workspace (sra_quant_matmul_workspace bytes, 0 for most shapes) holds partial products of a split
- * reduction, joined in a fixed order.  Supported: a->rows < 2^31, b->rows < 2^26, cols <= 2^22, and
+ * reduction, joined in a fixed order; neither it nor Out overlaps any other buffer.  Supported: a->rows < 2^31, b->rows < 2^26, cols <= 2^22, and
  * a->rows * b->rows < 2^40.
  */
 sra_status sra_quant_matmul_workspace(int64_t M, int64_t N, int64_t K, size_t* bytes /* host */);
@@ -541,7 +541,7 @@ sra_status sra_quant_matmul(const sra_fp8* a /* host */, const sra_fp8* b /* hos
  * orthogonalize -- n updates [rows, cols] (adapter gradients: dA [n,r,K], dB [n,N,r]) orthogonalised by Newton-Schulz
  * steps: X_0 = G / (|G| + eps) with |G| the root of the sum of squares, then `steps` times
  * X <- a X + (b A + c A^2) X with A = X X^T (X^T X where rows > cols).  G and O have one dtype (bf16 or fp32)
- * and do not overlap; everything between is fp64, with one rounding at the end.  Each matrix stands alone: an
+ * and overlap neither each other nor the workspace; everything between is fp64, with one rounding at the end.  Each matrix stands alone: an
  * infinity or NaN in one changes nothing in another.  A zero matrix gives zeros where eps > 0.
  * Supported: min(rows, cols) <= 256, n <= 65535, max(rows, cols) < 2^31, 1 <= steps <= 64; a, b, c finite,
  * eps finite and >= 0.

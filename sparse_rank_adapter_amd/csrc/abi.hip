@@ -4,6 +4,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -711,12 +712,23 @@ struct Span {
 };
 static sra_status check_apart(const Span& out, const Span& in, bool same = false) {
   const uintptr_t a = (uintptr_t)out.p, b = (uintptr_t)in.p;
-  if (!a || !b || (same && a == b)) return SRA_OK;
+  if (!a || !b || !out.bytes || !in.bytes || (same && a == b)) return SRA_OK;
   if (a < b + in.bytes && b < a + out.bytes)
     return fail(SRA_ERR_INVALID_ARG, "%s and %s overlap", out.name, in.name);
   return SRA_OK;
 }
+// every output against every input and against the other outputs
+static sra_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& in : ins) SRA_TRY(check_apart(*o, in));
+    for (const Span* q = o + 1; q != outs.end(); ++q) SRA_TRY(check_apart(*o, *q));
+  }
+  return SRA_OK;
+}
 static size_t code_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (size_t)((cols + 127) / 128 * 128); }
+static size_t exp_bytes(int64_t rows, int64_t cols, int block_rows) {
+  return (size_t)((rows + block_rows - 1) / block_rows) * (size_t)((cols + 127) / 128);
+}
 static sra_status check_eps(float eps) {
   if (!(eps >= 0.f) || eps > 3.0e38f) return fail(SRA_ERR_INVALID_ARG, "eps must be finite and >= 0");
   return SRA_OK;
@@ -748,10 +760,11 @@ sra_status sra_rms_norm_fwd(const void* X, const void* R, const void* gamma, flo
   SRA_TRY(check_ptr(exps, any && codes, "exps"));
   if (any) {
     const size_t n = (size_t)T * H * esize(dtype);
-    const Span x{X, n, "X"}, r{R, n, "R"}, h{R ? H_out : nullptr, n, "H_out"}, y{Y, n, "Y"}, c{codes, code_bytes(T, H), "codes"};
+    const Span x{X, n, "X"}, r{R, n, "R"}, g{gamma, (size_t)H * esize(dtype), "gamma"}, h{R ? H_out : nullptr, n, "H_out"},
+        y{Y, n, "Y"}, s{rstd, (size_t)T * 4, "rstd"}, c{codes, code_bytes(T, H), "codes"}, e{exps, exp_bytes(T, H, 1), "exps"};
     for (const Span& in : {x, r}) SRA_TRY(check_apart(h, in, true));
-    for (const Span& in : {x, r, h}) SRA_TRY(check_apart(y, in));
-    for (const Span& in : {x, r, h, y}) SRA_TRY(check_apart(c, in));
+    SRA_TRY(check_apart({y, s, c, e}, {x, r, g, h}));
+    SRA_TRY(check_apart(h, g));
   }
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_rms_norm_fwd(dtype, X, R, gamma, eps, T, H, H_out, Y, rstd, codes, exps, s), s,
@@ -780,8 +793,11 @@ sra_status sra_rms_norm_bwd(const void* dY, const void* H_in, const void* gamma,
   SRA_TRY(check_ws(ws, ws_bytes, sra::rms_norm_bwd_ws(T, H)));
   if (any) {
     const size_t n = (size_t)T * H * esize(dtype);
-    const Span out{dX, n, "dX"};
-    for (const Span& in : {Span{dY, n, "dY"}, Span{H_in, n, "H_in"}, Span{dH, n, "dH"}}) SRA_TRY(check_apart(out, in, true));
+    const Span out{dX, n, "dX"}, y{dY, n, "dY"}, h{H_in, n, "H_in"}, d{dH, n, "dH"}, g{gamma, (size_t)H * esize(dtype), "gamma"},
+        s{rstd, (size_t)T * 4, "rstd"}, dg{dgamma, (size_t)H * 4, "dgamma"}, w{ws, sra::rms_norm_bwd_ws(T, H), "the workspace"};
+    for (const Span& in : {y, h, d}) SRA_TRY(check_apart(out, in, true));
+    SRA_TRY(check_apart({dg, w}, {y, h, d, g, s, out}));
+    for (const Span& in : {g, s}) SRA_TRY(check_apart(out, in));
   }
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_rms_norm_bwd(dtype, dY, H_in, gamma, rstd, dH, T, H, dX, dgamma, ws, s), s,
@@ -815,10 +831,10 @@ sra_status sra_quant_encode(const void* X, int32_t dtype, int64_t rows, int64_t 
   SRA_TRY(check_ptr(X, rows > 0 && cols > 0, "X"));
   if (rows > 0 && cols > 0) {
     const Span x{X, (size_t)rows * cols * esize(dtype), "X"}, c{out ? out->codes : nullptr, code_bytes(rows, cols), "out's codes"},
-        t{out_t ? out_t->codes : nullptr, code_bytes(cols, rows), "out_t's codes"};
-    SRA_TRY(check_apart(c, x));
-    SRA_TRY(check_apart(t, x));
-    SRA_TRY(check_apart(t, c));
+        e{out ? out->exps : nullptr, exp_bytes(rows, cols, f->block_rows), "out's exps"},
+        ct{out_t ? out_t->codes : nullptr, code_bytes(cols, rows), "out_t's codes"},
+        et{out_t ? out_t->exps : nullptr, exp_bytes(cols, rows, f->block_rows), "out_t's exps"};
+    SRA_TRY(check_apart({c, e, ct, et}, {x}));
   }
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_fp8_encode(dtype, f->kind, X, rows, cols, f->block_rows, out ? out->codes : nullptr,
@@ -832,7 +848,8 @@ sra_status sra_quant_decode(const sra_fp8* F, int32_t dtype, void* X, void* stre
   SRA_TRY(check_fp8(F, "F"));
   SRA_TRY(check_ptr(X, F->rows > 0 && F->cols > 0, "X"));
   if (F->rows > 0 && F->cols > 0)
-    SRA_TRY(check_apart({X, (size_t)F->rows * F->cols * esize(dtype), "X"}, {F->codes, code_bytes(F->rows, F->cols), "F's codes"}));
+    SRA_TRY(check_apart({{X, (size_t)F->rows * F->cols * esize(dtype), "X"}},
+                        {{F->codes, code_bytes(F->rows, F->cols), "F's codes"}, {F->exps, exp_bytes(F->rows, F->cols, F->block_rows), "F's exps"}}));
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_fp8_decode(dtype, F->kind, F->codes, F->exps, F->rows, F->cols, F->block_rows, X, s), s,
                   "fp8_decode");
@@ -863,9 +880,10 @@ sra_status sra_quant_matmul(const sra_fp8* a, const sra_fp8* b, int32_t out_dtyp
   SRA_TRY(check_ptr(Out, a->rows > 0 && b->rows > 0, "Out"));
   SRA_TRY(check_ws(ws, ws_bytes, sra::fp8_matmul_ws(a->rows, b->rows, a->cols)));
   if (a->rows > 0 && b->rows > 0 && a->cols > 0) {
-    const Span o{Out, (size_t)a->rows * b->rows * esize(out_dtype), "Out"};
-    SRA_TRY(check_apart(o, {a->codes, code_bytes(a->rows, a->cols), "a's codes"}));
-    SRA_TRY(check_apart(o, {b->codes, code_bytes(b->rows, b->cols), "b's codes"}));
+    SRA_TRY(check_apart({{Out, (size_t)a->rows * b->rows * esize(out_dtype), "Out"},
+                         {ws, sra::fp8_matmul_ws(a->rows, b->rows, a->cols), "the workspace"}},
+                        {{a->codes, code_bytes(a->rows, a->cols), "a's codes"}, {a->exps, exp_bytes(a->rows, a->cols, a->block_rows), "a's exps"},
+                         {b->codes, code_bytes(b->rows, b->cols), "b's codes"}, {b->exps, exp_bytes(b->rows, b->cols, b->block_rows), "b's exps"}}));
   }
   const hipStream_t s = (hipStream_t)stream;
   const sra::Fp8Operand x{a->codes, a->exps, a->kind, a->block_rows}, y{b->codes, b->exps, b->kind, b->block_rows};
@@ -901,11 +919,11 @@ sra_status sra_orthogonalize(const void* G, int32_t dtype, int64_t n, int64_t ro
   const bool any = n > 0 && rows > 0 && cols > 0;
   SRA_TRY(check_ptr(G, any, "G"));
   SRA_TRY(check_ptr(O, any, "O"));
+  SRA_TRY(check_ws(ws, ws_bytes, sra::orth_ws(n, rows, cols)));
   if (any) {
     const size_t size = (size_t)n * rows * cols * esize(dtype);
-    SRA_TRY(check_apart({O, size, "O"}, {G, size, "G"}));
+    SRA_TRY(check_apart({{O, size, "O"}, {ws, sra::orth_ws(n, rows, cols), "the workspace"}}, {{G, size, "G"}}));
   }
-  SRA_TRY(check_ws(ws, ws_bytes, sra::orth_ws(n, rows, cols)));
   const double abc[3] = {a, b, c};
   const hipStream_t s = (hipStream_t)stream;
   return hip_done(sra::launch_orth(dtype, G, n, rows, cols, steps, abc, eps, O, ws, s), s, "orthogonalize");
