@@ -18,13 +18,15 @@ namespace {
 using namespace sra_f8;
 
 constexpr int kThreads = 256, kU = 4;
+// A launch has fewer than 2^32 threads: column tiles go out in spans of 2^23, the kernels' `first` the span's first tile.
+constexpr int64_t kSpan = (int64_t)1 << 23;
 
 // blocks of one row; grid: (vector tiles of a filled-up row, rows in steps of gridDim.y)
 template <typename E, int KIND, int VEC>
-__global__ __launch_bounds__(kThreads) void k_fp8_rows(const E* __restrict__ x, int64_t R, int64_t C, int64_t ld,
+__global__ __launch_bounds__(kThreads) void k_fp8_rows(const E* __restrict__ x, int64_t R, int64_t C, int64_t ld, int64_t first,
                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
   const int64_t nvec = ld / VEC, nblk = ld / kBlock;
-  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kU) + threadIdx.x;
+  const int64_t i0 = (first + blockIdx.x) * (kThreads * kU) + threadIdx.x;
   for (int64_t t = blockIdx.y; t < R; t += gridDim.y) {
     Stored<E, VEC> in[kU];  // all loads go out before any is used
 #pragma unroll
@@ -47,13 +49,13 @@ __global__ __launch_bounds__(kThreads) void k_fp8_rows(const E* __restrict__ x, 
 // BLK: one scale for the tile (else one per row, and one per column for the transpose).
 // codes / exps and codes_t / exps_t: either pair may be absent.
 template <typename E, int KIND, bool BLK, bool VEC>
-__global__ __launch_bounds__(kThreads) void k_fp8_tile(const E* __restrict__ x, int64_t R, int64_t C,
+__global__ __launch_bounds__(kThreads) void k_fp8_tile(const E* __restrict__ x, int64_t R, int64_t C, int64_t first,
                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ exps,
                                                        uint8_t* __restrict__ codes_t, uint8_t* __restrict__ exps_t) {
   __shared__ uint32_t red[4][kBlock];
   __shared__ __align__(16) uint8_t turn[kBlock * kBlock];  // the transposed codes: column c's 16-byte chunk q at (q ^ (c / 8 % 8))
   const int a = threadIdx.x >> 4, b = threadIdx.x & 15, w = threadIdx.x >> 6;
-  const int64_t tile_c = blockIdx.x, c0 = tile_c * kBlock + 8 * b;
+  const int64_t tile_c = first + blockIdx.x, c0 = tile_c * kBlock + 8 * b;
   const int64_t nbc = (C + kBlock - 1) / kBlock, nbr = (R + kBlock - 1) / kBlock;
   for (int64_t tile_r = blockIdx.y; tile_r < nbr; tile_r += gridDim.y) {
     const int64_t r0 = tile_r * kBlock + 8 * a;
@@ -164,9 +166,9 @@ __global__ __launch_bounds__(kThreads) void k_fp8_tile(const E* __restrict__ x, 
 template <typename E, int KIND, int VEC>
 __global__ __launch_bounds__(kThreads) void k_fp8_decode(const uint8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ exps, int64_t R, int64_t C,
-                                                         int64_t ld, int blk, E* __restrict__ x) {
+                                                         int64_t ld, int blk, int64_t first, E* __restrict__ x) {
   const int64_t nvec = (C + VEC - 1) / VEC, nblk = ld / kBlock;
-  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kU) + threadIdx.x;
+  const int64_t i0 = (first + blockIdx.x) * (kThreads * kU) + threadIdx.x;
   for (int64_t t = blockIdx.y; t < R; t += gridDim.y) {
     uint32_t c[kU][2], e[kU];
 #pragma unroll
@@ -203,41 +205,47 @@ __global__ __launch_bounds__(kThreads) void k_fp8_decode(const uint8_t* __restri
   }
 }
 
-dim3 grid_of(int64_t R, int64_t nvec) {
-  return dim3((unsigned)((nvec + kThreads * kU - 1) / (kThreads * kU)), (unsigned)std::min<int64_t>(R, 32768));
+// launch_one(first, grid) for each span of `tiles` column tiles, over R rows or row tiles
+template <typename F>
+void in_spans(int64_t tiles, int64_t R, const F& launch_one) {
+  for (int64_t first = 0; first < tiles; first += kSpan)
+    launch_one(first, dim3((unsigned)std::min(kSpan, tiles - first), (unsigned)std::min<int64_t>(R, 32768)));
 }
+int64_t vec_tiles(int64_t nvec) { return (nvec + kThreads * kU - 1) / (kThreads * kU); }
 
 template <typename E, int KIND>
 void encode_rows(const void* x, int64_t R, int64_t C, uint8_t* codes, uint8_t* exps, hipStream_t s) {
   if (C % kBlock == 0) C *= R, R = 1;  // rows of whole blocks follow each other without a gap: one long row
   const int64_t ld = ld_of(C);
-  if (vec8(C))
-    sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_rows<E, KIND, 8>, grid_of(R, ld / 8), dim3(kThreads), 0, s, (const E*)x, R, C,
-                ld, codes, exps);
-  else
-    sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_rows<E, KIND, 2>, grid_of(R, ld / 2), dim3(kThreads), 0, s, (const E*)x, R, C,
-                ld, codes, exps);
+  in_spans(vec_tiles(ld / (vec8(C) ? 8 : 2)), R, [&](int64_t first, dim3 grid) {
+    if (vec8(C))
+      sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_rows<E, KIND, 8>, grid, dim3(kThreads), 0, s, (const E*)x, R, C, ld, first, codes, exps);
+    else
+      sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_rows<E, KIND, 2>, grid, dim3(kThreads), 0, s, (const E*)x, R, C, ld, first, codes, exps);
+  });
 }
 template <typename E, int KIND, bool BLK>
 void encode_tiles(const void* x, int64_t R, int64_t C, uint8_t* codes, uint8_t* exps, uint8_t* codes_t,
                   uint8_t* exps_t, hipStream_t s) {
-  const dim3 grid((unsigned)blocks_of(C), (unsigned)std::min<int64_t>(blocks_of(R), 32768));
-  if (vec8(C))
-    sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_tile<E, KIND, BLK, true>, grid, dim3(kThreads), 0, s, (const E*)x, R, C,
-                codes, exps, codes_t, exps_t);
-  else
-    sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_tile<E, KIND, BLK, false>, grid, dim3(kThreads), 0, s, (const E*)x, R, C,
-                codes, exps, codes_t, exps_t);
+  in_spans(blocks_of(C), blocks_of(R), [&](int64_t first, dim3 grid) {
+    if (vec8(C))
+      sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_tile<E, KIND, BLK, true>, grid, dim3(kThreads), 0, s, (const E*)x, R, C, first,
+                  codes, exps, codes_t, exps_t);
+    else
+      sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_tile<E, KIND, BLK, false>, grid, dim3(kThreads), 0, s, (const E*)x, R, C, first,
+                  codes, exps, codes_t, exps_t);
+  });
 }
 template <typename E, int KIND>
 void decode(const uint8_t* codes, const uint8_t* exps, int64_t R, int64_t C, int block_rows, void* x, hipStream_t s) {
   const int64_t ld = ld_of(C);
-  if (vec8(C))
-    sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_decode<E, KIND, 8>, grid_of(R, C / 8), dim3(kThreads), 0, s, codes, exps, R, C,
-                ld, block_rows == 1 ? 0 : 7, (E*)x);
-  else
-    sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_decode<E, KIND, 2>, grid_of(R, (C + 1) / 2), dim3(kThreads), 0, s, codes,
-                exps, R, C, ld, block_rows == 1 ? 0 : 7, (E*)x);
+  const int blk = block_rows == 1 ? 0 : 7;
+  in_spans(vec_tiles(vec8(C) ? C / 8 : (C + 1) / 2), R, [&](int64_t first, dim3 grid) {
+    if (vec8(C))
+      sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_decode<E, KIND, 8>, grid, dim3(kThreads), 0, s, codes, exps, R, C, ld, blk, first, (E*)x);
+    else
+      sra::launch(SRA_KERNEL_FP8_CODE, k_fp8_decode<E, KIND, 2>, grid, dim3(kThreads), 0, s, codes, exps, R, C, ld, blk, first, (E*)x);
+  });
 }
 
 }  // namespace
