@@ -527,8 +527,12 @@ sra_status sra_quant_decode(const sra_fp8* F /* host */, int32_t dtype, void* X,
 /*
  * quant_matmul -- Out = a b^T, [a->rows, b->rows], both reduced over cols (a->cols == b->cols): a projection
  * (a = the activations, b = the weight), its input gradient (a = dY, b = the weight's transpose) and its
- * weight gradient (a = dY's transpose, b = X's).  Any kinds and block_rows.  Out has out_dtype (bf16 or fp32),
- * rounded once; sums are fp32.  A NaN code or scale makes NaN of its own row's results alone.  cols = 0 writes
+ * weight gradient (a = dY's transpose, b = X's).  Any kinds and block_rows.  Out has out_dtype, rounded once.
+ * With fp32 results every product is exact and sums are fp32.  With bf16 results a product first loses its bits
+ * below 2^(E - 13), E the largest sum of two codes' exponents among the products of its eight columns 8 i .. 8 i + 7
+ * (a code below the kind's smallest normal value counts as that value); what is left is summed in fp32.  Eight
+ * columns are so off by less than 7 * 2^-13 of their largest |a b|, which shows where large products cancel among
+ * them: take fp32 results there.  A NaN code or scale makes NaN of its own row's results alone.  cols = 0 writes
  * zeros.  The workspace (sra_quant_matmul_workspace bytes, 0 for most shapes) holds partial products of a split
  * reduction, joined in a fixed order; neither it nor Out overlaps any other buffer.  Supported: a->rows < 2^31, b->rows < 2^26, cols <= 2^22, and
  * a->rows * b->rows < 2^40.

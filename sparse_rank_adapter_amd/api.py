@@ -999,7 +999,10 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out_dtype: torch.dtype = torch.bfloat
                ws: torch.Tensor | None = None) -> torch.Tensor:
     """a b^T [a.rows, b.rows], in bf16 or fp32 (`out`'s dtype where it is given).
 
-    A projection (a = X, b = W), its input gradient (a = dY, b = W^T) and its weight gradient (a = dY^T, b = X^T)."""
+    A projection (a = X, b = W), its input gradient (a = dY, b = W^T) and its weight gradient (a = dY^T, b = X^T).
+    fp32 results have exact products and fp32 sums.  For bf16 results the products of columns 8 i .. 8 i + 7 are added with 13
+    bits below the largest of the eight, and these sums in fp32: an error below 7 2^-13 of that product for each eight, which
+    shows where large products cancel among them."""
     lib = load()
     _check_fp8(a, "a")
     dev = a.device

@@ -10,10 +10,13 @@
 // Scales of four consecutive blocks are one dword of a row's exponents; the instruction's op_sel picks
 // the byte, so they cost one read per row and 512 columns.
 //
-// Inside one instruction the products are added with about 17 bits below the largest of them (measured: results 1e-5 to
-// 4e-5 off over one block, the plain fp8 instructions the same), which is far below a bf16 result's rounding but not
-// below fp32's.  fp32 results (EX) therefore go over bf16: every code is exact in bf16, v_mfma_f32_16x16x32_bf16 adds
-// with full fp32 accuracy, and each block's sum enters the accumulator over its scale, an exact ldexp.
+// The instruction first adds the products of each eight neighbouring codes, every one truncated to a multiple of 2^(E - 13), E
+// the largest sum of two codes' exponents among them (codes below the smallest normal value count as that), and then these sums
+// and the accumulator in fp32 (measured; the plain fp8 instructions do the same).  A block's sum is so 1e-5 to 4e-5 off for
+// normally distributed values, and by 7 2^-13 of the eights' largest products at worst: less than a bf16 result's rounding
+// unless large products cancel, so bf16 results accept it for the rate (8192 x 20480 over 5120: 619 us, 1826 with fp32
+// results), but not less than fp32's.  fp32 results (EX) go over bf16: every code is exact in bf16, v_mfma_f32_16x16x32_bf16
+// adds with full fp32 accuracy, and each block's sum enters the accumulator over its scale, an exact ldexp.
 #include <algorithm>
 #include <type_traits>
 
