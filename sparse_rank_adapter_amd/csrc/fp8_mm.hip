@@ -759,14 +759,17 @@ struct Plan {
   int kernel;
   int splits;
 };
-// Up to 32 rows of a: b streams.  Else the tiles with the least estimated time, in units of 10 ns, from what a step of 128
+// Up to 32 rows of a: b streams (but see below).  Else the tiles with the least estimated time, in units of 10 ns, from what a step of 128
 // columns was measured to take on the busiest CU: 256 x 256 tiles 1.55 us; 128 x 128 tiles 0.72 us alone on a CU (a ring of
 // four stages), 1.39 us for two at once (of two stages); 64 x 64 tiles 0.40 us alone, 0.53 us for two.  Where the small
 // tiles are few they split the reduction, at least 4 blocks a split, and a second launch (3 us) joins the parts.
 // Against it, at 512 x 5120 x 20480: 160 large tiles 64 us, 640 middle ones 96; 128 x 5120 x 20480: 160 middle tiles 36 us,
 // 640 small ones 42; 2047 x 4096 x 1024: 512 small tiles 17 us, 128 middle ones 24.
+// Where b has few rows too (16 for a CU at most), nothing but its waves shares out the streaming kernel's reduction: a round of 32
+// blocks takes 2.35 us and 0.11 for each row of a.  The split small tiles are taken where they promise half of that, with
+// 0.2 us for each split in the second launch: 32 x 64 over 2^20 1495 us streaming, 80 by tiles; 16 x 256 over 131072 128 and 29;
+// 32 x 2048 over 16384 27 and 13; but 16 x 64 over 16384 18 and 15, streaming.
 Plan own_plan(int64_t M, int64_t N, int64_t nblk, bool ex) {
-  if (M <= 32) return {kFew, 1};
   const auto tiles = [&](int64_t side) { return ((M + side - 1) / side) * ((N + side - 1) / side); };
   const auto rounds = [](int64_t t, int64_t one, int64_t two) {  // two workgroups a CU
     const int64_t r = t % 512;
@@ -777,6 +780,10 @@ Plan own_plan(int64_t M, int64_t N, int64_t nblk, bool ex) {
   int s = 1;
   while (t * s < 192 && nblk >= 8 * s) s *= 2;
   const int64_t small = rounds(t * s, 40, 53) * ((nblk + s - 1) / s) + (s > 1 ? 300 : 0);
+  if (M <= 32) {
+    const int64_t few = (N + 15) / 16 <= 256 ? (nblk + 31) / 32 * (235 + 11 * M) : 0;
+    return few > 2 * (small + 20 * s) ? Plan{kSmall, s} : Plan{kFew, 1};
+  }
   if (!ex && nblk >= 2 && big < mid && big < small) return {kBig, 1};
   if (mid > small) return {kSmall, s};
   return {ex || tiles(128) > 256 ? kMid : kDeep, 1};
