@@ -70,27 +70,37 @@ __global__ __launch_bounds__(kThreads) void k_fp8_tile(const E* __restrict__ x, 
   const int64_t nbc = (C + kBlock - 1) / kBlock, nbr = (R + kBlock - 1) / kBlock;
   for (int64_t tile_r = blockIdx.y; tile_r < nbr; tile_r += gridDim.y) {
     const int64_t r0 = tile_r * kBlock + 8 * a;
-    // every row's load goes out before any is used (in branches of their own each waited for the one before): what is outside
-    // is read from inside, and replaced by zeros
-    Stored<E, 8> in[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const E* const row = x + min(r0 + i, R - 1) * C;
-      if constexpr (VEC) {
-        in[i] = fetch<E, 8>(row, c0, C);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) in[i].e[k] = row[c0 + k < C ? c0 + k : 0];
-      }
-    }
+    // Every row's load goes out before any is used (in branches of their own each waited for the one before).  In tiles at an edge
+    // what is outside is read from inside, and replaced by zeros; doing so in every tile cost an eighth (8192 x 5120 with the
+    // transpose 41 us in fp32 and 32 in bf16, 46 and 39 with it).
     float f[8][8];
+    const bool inside = VEC && (tile_r + 1) * kBlock <= R && (tile_c + 1) * kBlock <= C;
+    if (inside) {
+      Stored<E, 8> in[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t left = r0 + i < R ? C - c0 : 0;
-      as_floats<E, 8>(in[i], left, f[i]);
-      if constexpr (!VEC) {
+      for (int i = 0; i < 8; ++i) in[i] = fetch<E, 8>(x + (r0 + i) * C, c0, INT64_MAX);
 #pragma unroll
-        for (int k = 1; k < 8; ++k) f[i][k] = k < left ? f[i][k] : 0.f;
+      for (int i = 0; i < 8; ++i) as_floats<E, 8>(in[i], 8, f[i]);
+    } else {
+      Stored<E, 8> in[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const E* const row = x + min(r0 + i, R - 1) * C;
+        if constexpr (VEC) {
+          in[i] = fetch<E, 8>(row, c0, C);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) in[i].e[k] = row[c0 + k < C ? c0 + k : 0];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t left = r0 + i < R ? C - c0 : 0;
+        as_floats<E, 8>(in[i], left, f[i]);
+        if constexpr (!VEC) {
+#pragma unroll
+          for (int k = 1; k < 8; ++k) f[i][k] = k < left ? f[i][k] : 0.f;
+        }
       }
     }
     uint32_t rm[8], cm[8];
