@@ -471,9 +471,8 @@ hipError_t launch_ckpt_encode(int dtype, const void* x, int64_t T, int64_t K, in
 hipError_t launch_ckpt_decode(int dtype, const int8_t* codes, const uint8_t* exps, int64_t T, int64_t K, void* x,
                               hipStream_t s);
 
-// Matrices in 8-bit floating point (fp8.hip): codes [R][fp8_ld(C)], exps [ceil(R / block_rows)][ceil(C / 128)];
+// Matrices in 8-bit floating point (fp8.hip): codes [R][C rounded up to 128], exps [ceil(R / block_rows)][ceil(C / 128)];
 // codes / exps and codes_t / exps_t (the transpose's): either pair may be null.
-int64_t fp8_ld(int64_t cols);
 hipError_t launch_fp8_encode(int dtype, int kind, const void* x, int64_t R, int64_t C, int block_rows, uint8_t* codes,
                              uint8_t* exps, uint8_t* codes_t, uint8_t* exps_t, hipStream_t s);
 hipError_t launch_fp8_decode(int dtype, int kind, const uint8_t* codes, const uint8_t* exps, int64_t R, int64_t C,

@@ -273,8 +273,6 @@ void decode(const uint8_t* codes, const uint8_t* exps, int64_t R, int64_t C, int
 
 namespace sra {
 
-int64_t fp8_ld(int64_t cols) { return ld_of(cols); }
-
 hipError_t launch_fp8_encode(int dtype, int kind, const void* x, int64_t R, int64_t C, int block_rows, uint8_t* codes,
                              uint8_t* exps, uint8_t* codes_t, uint8_t* exps_t, hipStream_t s) {
   if (R <= 0 || C <= 0) return hipSuccess;
