@@ -10,6 +10,7 @@
 // Measured: 20480 x 5120 in bf16 by 128 x 128 blocks with the transpose 75-88 us (419 MB, 4.8-5.6 TB/s), decoded again 49 and
 // 54 us (5.5-6.4 TB/s); 2047 x 4096 by rows with the transpose 13-16 us (34 MB: 512 workgroups of one tile each, so nothing
 // overlaps a tile's loads, maxima and stores), decoded 6.5 us, and 9.4 us where rows of 2047 allow two elements at a time.
+// By rows alone 8192 x 5120 takes 22-23 us in bf16 and 31 in fp32 (126 and 210 MB), 8192 x 5121 in bf16 42-44.
 #include <algorithm>
 
 #include "fp8.h"

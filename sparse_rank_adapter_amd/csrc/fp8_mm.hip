@@ -345,6 +345,8 @@ struct ScaleRow {
 };
 constexpr int kScaleLd = 20;  // bytes between rows of a chunk in LDS: 16 rows fall on different banks
 
+// (128 x 128 with four stages: 138 KB of LDS, one workgroup a CU.  The bound of two only keeps its registers to 256 a wave; the
+// compiler says that it is not met.)
 template <int KA, int KB, int BM, int BN, int WM, int WN, int ST, bool EX>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tiles(Mat a, Mat b, Out out, int nm, int nn, float* part) {
   using C = Cfg<BM, BN, WM, WN, ST>;
@@ -486,8 +488,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_fp8_tiles(Mat a, Mat b, Out
   store_tile<FM, FN>(acc, out, part, m0 + wm, n0 + wn);
 }
 
-// 8192 x 20480 over 5120 with scales of 128 x 128 blocks: 608-623 us, 2.8 PFLOP/s (a library product with one scale a matrix
-// 553); the matrix units are then busy 60% of the time at 2.1 GHz, the clock that power allows.
+// 8192 x 20480 over 5120 with scales of 128 x 128 blocks: 600-672 us by box, 2.6-2.9 PFLOP/s (a library product with one scale a
+// matrix 553 where this took 622); the matrix units are then busy 60% of the time at 2.1 GHz, the clock that power allows.
 //
 // ---- 256 x 256 tiles, four waves of 128 x 128, one to a SIMD: half the LDS traffic of eight waves of 128 x 64 (per 128
 // columns 128 KB read and 64 KB written, 1536 cycles of 128 bytes, beside 2048 cycles of matrix instructions).  A step's
@@ -759,12 +761,12 @@ struct Plan {
   int kernel;
   int splits;
 };
-// Up to 32 rows of a: b streams (but see below).  Else the tiles with the least estimated time, in units of 10 ns, from what a step of 128
-// columns was measured to take on the busiest CU: 256 x 256 tiles 1.55 us; 128 x 128 tiles 0.72 us alone on a CU (a ring of
-// four stages), 1.39 us for two at once (of two stages); 64 x 64 tiles 0.40 us alone, 0.53 us for two.  Where the small
+// Up to 32 rows of a b streams, but see below.  Else the tiles with the least estimated time, in units of 10 ns, from what a step
+// of 128 columns was measured to take on the busiest CU: 256 x 256 tiles 1.55 us; 128 x 128 tiles 0.72 us alone on a CU (a ring
+// of four stages), 1.39 us for two at once (of two stages); 64 x 64 tiles 0.40 us alone, 0.53 us for two.  Where the small
 // tiles are few they split the reduction, at least 4 blocks a split, and a second launch (3 us) joins the parts.
-// Against it, at 512 x 5120 x 20480: 160 large tiles 64 us, 640 middle ones 96; 128 x 5120 x 20480: 160 middle tiles 36 us,
-// 640 small ones 42; 2047 x 4096 x 1024: 512 small tiles 17 us, 128 middle ones 24.
+// Against it, at 512 x 20480 over 5120: 160 large tiles 57-61 us, 640 middle ones 63; 128 x 20480 over 5120: 160 middle tiles
+// 30 us, 320 small ones 35; 2047 x 1024 over 4096: 512 small tiles 17 us, 128 middle ones 24.
 // Where b has few rows too (16 for a CU at most), nothing but its waves shares out the streaming kernel's reduction: a round of 32
 // blocks takes 2.35 us and 0.11 for each row of a.  The split small tiles are taken where they promise half of that, with
 // 0.2 us for each split in the second launch: 32 x 64 over 2^20 1495 us streaming, 80 by tiles; 16 x 256 over 131072 128 and 29;

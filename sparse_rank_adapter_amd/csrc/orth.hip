@@ -11,7 +11,8 @@
 //
 // Measured: 8 fp32 matrices of 20480 x 128 253 us: A_0 63 us (3.0 GFLOP, bound by the fp64 matrix unit, 38 us at its peak, and
 // by uneven shares: 480 workgroups on 256 CUs), 14 launches of 128 x 128 products 6 us each (latency), Q G 102 us (5.4 GFLOP,
-// 68 us at the peak).  12 of 16 x 1024: 15-18 us, three launches.  4 of 64 x 8192: 73 us, 45 of them the steps (k_orth_small).
+// 68 us at the peak).  12 of 16 x 1024: 15 us, three launches.  4 of 64 x 8192: 71 us, 45 of them the steps (k_orth_small); in
+// bf16 73, 8 of 20480 x 128 in bf16 276 (half the bytes, but the fp64 unit bounds both).
 //
 // The fp64 matrix instruction: lane l gives a[l % 16][l / 16] and b[l / 16][l % 16], and holds rows
 // 4 v + l / 16 (v = 0 .. 3) of column l % 16 of the result.
@@ -275,7 +276,7 @@ SRA_DEV f64x4 lds_mm(const double* A, const double* B, int ti, int tj) {  // til
   return acc;
 }
 // JOIN: A0 is the slices' sums [n][S][32][32], joined here in k_orth_join's order, up to kJoinSlices of them: 12 x 16 x 1024 with
-// 8 slices 19.6 us with the launch, 18.2 without; at 32 slices 12 x 32 x 4096 takes 31 us with it and 34 without.
+// 8 slices 17.0 us with the launch, 14.9 without; at 32 slices 12 x 32 x 4096 takes 28.4 us with it and 32.7 without.
 constexpr int kJoinSlices = 16;
 template <int D, bool JOIN>
 __global__ __launch_bounds__(64 * (D / 16) * (D / 16 + 1) / 2, 2) void k_orth_small(const double* __restrict__ A0, int S, int d,

@@ -208,7 +208,8 @@ __global__ __launch_bounds__(1024) void k_rms_param(const float* __restrict__ pa
 
 // Elements a thread holds, in at most 1024 threads: the forward 8 up to 2048 columns, 16 above (8192 rows of 5120 in bf16
 // with H, Y and codes: 64 us, with 8 elements 74, each before loads went out ahead), the backward 8 up to 8192 columns, which leaves registers for the
-// next row (8191 rows of 5120 with dH: 69 us, with 16 elements and no row ahead 85)
+// next row (8191 rows of 5120 with dH: 69 us, with 16 elements and no row ahead 85).  Rows above 8192 columns that are no
+// multiple of 8 spill 27 to 54 registers there (2048 rows of 9001 with dH 96 us).
 int fwd_ept(int64_t H) { return H <= 2048 ? 8 : 16; }
 int bwd_ept(int64_t H) { return H <= 8192 ? 8 : 16; }
 int threads_for(int64_t H, int ept) { return 64 * (int)((H + 64 * ept - 1) / (64 * ept)); }
